@@ -11,14 +11,19 @@ Entry points (same names as the C ABI):
     spec_verify_workspace_init, spec_verify_sample, spec_verify_tree,
     spec_verify_last_error, spec_verify_intermediates,
     spec_verify_acceptance, spec_verify_sample_probs, spec_verify_tree_mask,
-    spec_verify_status_string
+    spec_verify_status_string,
+    spec_kv_append, spec_kv_read, spec_attn_workspace_size, spec_attn_tree,
+    spec_attn_shared (the target pass's cache and attention, declared in
+    ``include/spec_attn.h``)
 plus tensor-level helpers ``verify_sample`` / ``verify_sample_probs`` /
-``verify_tree`` / ``acceptance`` that take
+``verify_tree`` / ``acceptance`` / ``kv_append`` / ``kv_read`` /
+``attn_tree`` / ``attn_shared`` that take
 torch CUDA tensors, allocate outputs and a zeroed workspace, and raise on a
 negative status.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import subprocess
@@ -29,13 +34,15 @@ LIB_PATH = os.path.join(_PKG, "libspecverify.so")
 CSRC = os.path.join(_PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("api.cu", "rows.cu", "topp.cu", "final.cu", "noalloc.cu",
-                     "accept.cu", "treemask.cu", "treesample.cu", "select.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh")]
+                     "accept.cu", "treemask.cu", "treesample.cu", "select.cu",
+                     "kvcache.cu", "attn.cu", "attn_api.cu")]
+HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh", "attn.cuh")]
 INCLUDE = os.path.join(_ROOT, "include")
 HEADER = os.path.join(INCLUDE, "spec_verify.h")
+ATTN_HEADER = os.path.join(INCLUDE, "spec_attn.h")
 BUILD_DIR = os.path.join(_PKG, "_build")
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_E4M3 = 0, 1, 2
 SPEC_STOCHASTIC, SPEC_GREEDY = 0, 1
 SPEC_OK = 0
 SPEC_DATA_ROW_NONFINITE = 1 << 1
@@ -44,6 +51,7 @@ SPEC_DATA_TOKEN_RANGE = 1 << 3
 SPEC_DATA_UNIFORM_RANGE = 1 << 4
 SPEC_DATA_TREE_SHAPE = 1 << 5
 SPEC_DATA_PROB_RANGE = 1 << 6
+SPEC_DATA_PAGE_RANGE = 1 << 7
 SPEC_MAX_K = 31
 
 EXPORTED = (
@@ -63,12 +71,24 @@ EXPORTED = (
     "spec_verify_tree_mask",
     "spec_verify_tree_sample_workspace_size",
     "spec_verify_tree_sample",
+    "spec_kv_append",
+    "spec_kv_read",
+    "spec_attn_workspace_size",
+    "spec_attn_tree",
+    "spec_attn_shared",
     "spec_verify_status_string",
 )
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden"]
+
+
+class CacheDescriptor(ctypes.Structure):
+    """struct spec_kv_cache of include/spec_attn.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("page", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -78,7 +98,7 @@ class SpecVerifyError(RuntimeError):
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA sources for sm_103a (one nvcc per translation unit,
     in parallel) and link libspecverify.so in-tree."""
-    newest = max(os.path.getmtime(p) for p in SOURCES + HEADERS + [HEADER])
+    newest = max(os.path.getmtime(p) for p in SOURCES + HEADERS + [HEADER, ATTN_HEADER])
     if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= newest:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -130,6 +150,13 @@ def lib():
         L.spec_verify_tree_sample_workspace_size.argtypes = [I, I, I, ctypes.POINTER(Z)]
         L.spec_verify_tree_sample.argtypes = [P, P, P, P, P, I, I, I, I, F, F, I, I, P, P, P, P,
                                               Z, P]
+        C, S = ctypes.POINTER(CacheDescriptor), ctypes.c_int64
+        L.spec_kv_append.argtypes = [C, P, I, P, P, P, S, P, I, I, I, I, P]
+        L.spec_kv_read.argtypes = [C, P, I, P, P, P, I, I, I, P]
+        L.spec_attn_workspace_size.argtypes = [I, I, I, I, I, ctypes.POINTER(Z)]
+        L.spec_attn_tree.argtypes = [C, P, I, P, P, S, P, P, P, I, I, I, F, F, I, I, P, P, P, Z, P]
+        L.spec_attn_shared.argtypes = [C, P, I, P, I, P, P, S, P, P, P, I, I, I, F, F, I, I, P, P,
+                                       P, Z, P]
         L.spec_verify_status_string.argtypes = [I]
         L.spec_verify_status_string.restype = ctypes.c_char_p
         for name in EXPORTED[:-1]:
@@ -262,6 +289,43 @@ def spec_verify_tree_sample(target_ptr, draft_ptr, parents_ptr, node_tokens_ptr,
         target_ptr, draft_ptr, parents_ptr, node_tokens_ptr, uniforms_ptr, B, N, V, D,
         float(temperature), float(top_p), int(top_k), dtype, out_tokens_ptr, out_num_ptr,
         out_path_ptr, workspace_ptr, workspace_bytes, stream))
+
+
+def spec_kv_append(cache, table_ptr, table_width, starts_ptr, k_ptr, v_ptr, token_stride, rows_ptr,
+                   B, N, M, dtype, stream=0):
+    """`cache`: a CacheDescriptor, here and below."""
+    return _check(lib().spec_kv_append(cache, table_ptr, table_width, starts_ptr, k_ptr, v_ptr,
+                                       token_stride, rows_ptr, B, N, M, dtype, stream))
+
+
+def spec_kv_read(cache, table_ptr, table_width, starts_ptr, out_k_ptr, out_v_ptr, B, M, dtype,
+                 stream=0):
+    return _check(lib().spec_kv_read(cache, table_ptr, table_width, starts_ptr, out_k_ptr,
+                                     out_v_ptr, B, M, dtype, stream))
+
+
+def spec_attn_workspace_size(B, N, Hq, Hkv, D):
+    out = ctypes.c_size_t(0)
+    _check(lib().spec_attn_workspace_size(B, N, Hq, Hkv, D, ctypes.byref(out)))
+    return out.value
+
+
+def spec_attn_tree(cache, table_ptr, table_width, lens_ptr, q_ptr, q_stride, mask_ptr, pos_ptr,
+                   slopes_ptr, B, N, Hq, scale, cap, window, dtype, out_ptr, out_lse_ptr,
+                   workspace_ptr, workspace_bytes, stream=0):
+    return _check(lib().spec_attn_tree(
+        cache, table_ptr, table_width, lens_ptr, q_ptr, q_stride, mask_ptr, pos_ptr, slopes_ptr, B,
+        N, Hq, float(scale), float(cap), window, dtype, out_ptr, out_lse_ptr, workspace_ptr,
+        workspace_bytes, stream))
+
+
+def spec_attn_shared(cache, shared_table_ptr, shared_len, table_ptr, table_width, lens_ptr, q_ptr,
+                     q_stride, mask_ptr, pos_ptr, slopes_ptr, B, N, Hq, scale, cap, window, dtype,
+                     out_ptr, out_lse_ptr, workspace_ptr, workspace_bytes, stream=0):
+    return _check(lib().spec_attn_shared(
+        cache, shared_table_ptr, shared_len, table_ptr, table_width, lens_ptr, q_ptr, q_stride,
+        mask_ptr, pos_ptr, slopes_ptr, B, N, Hq, float(scale), float(cap), window, dtype, out_ptr,
+        out_lse_ptr, workspace_ptr, workspace_bytes, stream))
 
 
 def spec_verify_status_string(status):
@@ -475,3 +539,145 @@ def verify_tree_sample(target, draft, parents, node_tokens, uniforms, depth, tem
                             _ptr(out_t), _ptr(out_n), _ptr(out_p), _ptr(workspace),
                             workspace.numel(), _stream(stream))
     return out_t, out_n, out_p, workspace
+
+
+# ------------------------------------------- the target pass's cache and attention
+
+class KVCache(collections.namedtuple("KVCache", "k v k_exp v_exp")):
+    """A paged cache's tensors: k, v [num_pages, Hkv, page, D] bf16, or
+    float8_e4m3fn with int8 exponents k_exp, v_exp [num_pages, Hkv, page]
+    (else None)."""
+
+    def descriptor(self):
+        torch = _torch()
+        n, H, page, D = self.k.shape
+        e4m3 = self.k.dtype == torch.float8_e4m3fn
+        if not e4m3 and self.k.dtype != torch.bfloat16:
+            raise TypeError("a cache holds torch.bfloat16 or torch.float8_e4m3fn, got %s"
+                            % self.k.dtype)
+        for t, name in ((self.k, "cache.k"), (self.v, "cache.v")):
+            _need(t, name, self.k.dtype, (n, H, page, D))
+        if e4m3:
+            for t, name in ((self.k_exp, "cache.k_exp"), (self.v_exp, "cache.v_exp")):
+                _need(t, name, torch.int8, (n, H, page))
+        return CacheDescriptor(_ptr(self.k), _ptr(self.v), _ptr(self.k_exp) if e4m3 else None,
+                               _ptr(self.v_exp) if e4m3 else None, n, H, page, D,
+                               SPEC_E4M3 if e4m3 else SPEC_BF16)
+
+
+def new_cache(num_pages, Hkv, page, D, device, e4m3=False):
+    """An empty (zeroed) cache of num_pages pages."""
+    torch = _torch()
+    shape = (num_pages, Hkv, page, D)
+    if not e4m3:
+        k, v = (torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in "kv")
+        return KVCache(k, v, None, None)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            for _ in "kv")
+    ke, ve = (torch.zeros(shape[:3], dtype=torch.int8, device=device) for _ in "kv")
+    return KVCache(k, v, ke, ve)
+
+
+def _tokens(t, name, H, D, dtypes):
+    """[B, N, H, D] with packed tokens; returns their stride in elements.
+    Consecutive tokens may lie further apart (slices of a wider projection),
+    evenly over the whole batch."""
+    B, N = t.shape[:2]
+    if t.dtype not in dtypes or t.dim() != 4 or tuple(t.shape[2:]) != (H, D) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor [B, N, %d, %d] of %s, got %s %s"
+                         % (name, H, D, "/".join(map(str, dtypes)), t.dtype, tuple(t.shape)))
+    step = t.stride(1) if N > 1 else t.stride(0) if B > 1 else H * D
+    ok = t.stride(3) == 1 and (H == 1 or t.stride(2) == D)
+    if not t.numel() or (ok and (B < 2 or t.stride(0) == N * step)):
+        return step if t.numel() else 0
+    raise ValueError("%s: each token's heads must be contiguous and tokens evenly spaced, got "
+                     "strides %s" % (name, tuple(t.stride())))
+
+
+def kv_append(cache, page_table, starts, k, v, rows=None, stream=None):
+    """Tensor-level spec_kv_append: tokens k, v [B, N, Hkv, D] (fp32 or bf16)
+    to positions starts[b] + t of a KVCache; rows [B, M] int32 picks the
+    tokens (spec_verify_tree's out_path: the accepted nodes, -1 skipped)."""
+    torch = _torch()
+    c = cache.descriptor()
+    B, N = k.shape[:2]
+    kinds = (torch.float32, torch.bfloat16)
+    step = _tokens(k, "k", c.Hkv, c.D, kinds)
+    if _tokens(v, "v", c.Hkv, c.D, (k.dtype,)) != step or v.shape != k.shape:
+        raise ValueError("k and v must have one shape and token stride")
+    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
+    _need(starts, "starts", torch.int32, (B,))
+    M = N
+    if rows is not None:
+        M = rows.shape[1]
+        _need(rows, "rows", torch.int32, (B, M))
+    spec_kv_append(c, _ptr(page_table), page_table.shape[1], _ptr(starts), _ptr(k), _ptr(v), step,
+                   _ptr(rows), B, N, M, _dtype_code(k), _stream(stream))
+
+
+def kv_read(cache, page_table, starts, count, dtype=None, stream=None):
+    """Tensor-level spec_kv_read: (k, v) [B, count, Hkv, D] of the positions
+    from starts[b] on, in bf16 (or fp32)."""
+    torch = _torch()
+    c = cache.descriptor()
+    B = starts.shape[0]
+    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
+    _need(starts, "starts", torch.int32, (B,))
+    k, v = (torch.empty((B, count, c.Hkv, c.D), dtype=dtype or torch.bfloat16,
+                        device=starts.device) for _ in "kv")
+    spec_kv_read(c, _ptr(page_table), page_table.shape[1], _ptr(starts), _ptr(k), _ptr(v), B, count,
+                 _dtype_code(k), _stream(stream))
+    return k, v
+
+
+def _attn(call, q, cache, before, page_table, lens, mask, pos, slopes, scale, cap, window, out, lse,
+          workspace, stream):
+    torch = _torch()
+    c = cache.descriptor()
+    B, N, Hq = q.shape[:3]
+    step = _tokens(q, "q", Hq, c.D, (torch.bfloat16,))
+    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
+    _need(lens, "lens", torch.int32, (B,))
+    if mask is not None:
+        _need(mask, "mask", torch.uint8, (B, N, N))
+    if pos is not None:
+        _need(pos, "pos", torch.int32, (B, N))
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, (Hq,))
+    if out is None:
+        out = torch.empty((B, N, Hq, c.D), dtype=q.dtype, device=q.device)
+    _need(out, "out", q.dtype, (B, N, Hq, c.D))
+    if lse is True:
+        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, N, Hq))
+    if workspace is None:
+        workspace = new_workspace(spec_attn_workspace_size(B, N, Hq, c.Hkv, c.D), q.device)
+    call(c, *before, _ptr(page_table), page_table.shape[1], _ptr(lens), _ptr(q), step, _ptr(mask),
+         _ptr(pos), _ptr(slopes), B, N, Hq, c.D ** -0.5 if scale is None else scale, cap, window,
+         SPEC_BF16, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
+    return out if lse is None else (out, lse)
+
+
+def attn_tree(q, cache, page_table, lens, mask=None, pos=None, slopes=None, scale=None, cap=0.0,
+              window=0, out=None, lse=None, workspace=None, stream=None):
+    """Tensor-level spec_attn_tree: new tokens q [B, N, Hq, D] bf16 over a
+    KVCache; mask and pos as tree_mask returns them (None: a chain); scale
+    defaults to 1/sqrt(D).  Returns out [B, N, Hq, D], or (out, lse) with
+    lse=True or a tensor."""
+    return _attn(spec_attn_tree, q, cache, (), page_table, lens, mask, pos, slopes, scale, cap,
+                 window, out, lse, workspace, stream)
+
+
+def attn_shared(q, cache, shared_table, shared_len, page_table, lens, mask=None, pos=None,
+                slopes=None, scale=None, cap=0.0, window=0, out=None, lse=None, workspace=None,
+                stream=None):
+    """Tensor-level spec_attn_shared: attn_tree where every sequence's cache
+    continues the shared_len positions of the pages shared_table lists."""
+    torch = _torch()
+    _need(shared_table, "shared_table", torch.int32, (shared_table.numel(),))
+    if shared_table.numel() * cache.k.shape[2] < shared_len:
+        raise ValueError("shared_table holds %d pages, %d positions need more"
+                         % (shared_table.numel(), shared_len))
+    return _attn(spec_attn_shared, q, cache, (_ptr(shared_table), shared_len), page_table, lens,
+                 mask, pos, slopes, scale, cap, window, out, lse, workspace, stream)

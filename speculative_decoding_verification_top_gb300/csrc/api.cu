@@ -2,6 +2,7 @@
 // argument validation, workspace layout and kernel dispatch.  No compute.
 
 #include "common.cuh"
+#include "spec_attn.h"
 
 #define SPEC_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -533,6 +534,7 @@ SPEC_EXPORT const char *spec_verify_status_string(int status) {
     case SPEC_DATA_TREE_SHAPE:
         return "parents is not a rooted tree in topological order within depth D";
     case SPEC_DATA_PROB_RANGE: return "a gathered draft probability lies outside [0, 1]";
+    case SPEC_DATA_PAGE_RANGE: return "a cache length or page id is out of range";
     default: return "unknown status";
     }
 }
