@@ -50,6 +50,10 @@ enum { SPEC_E4M3 = 2 };
  * pages a sequence needs.  That sequence's outputs are NaN. */
 enum { SPEC_DATA_PAGE_RANGE = 1 << 7 };
 
+/* An internal wait of the attention kernel ran out (its waits are bounded):
+ * the call's outputs are undefined. */
+enum { SPEC_DATA_STALL = 1 << 8 };
+
 typedef struct spec_kv_cache {
     void *k, *v;            /* [num_pages, Hkv, page, D], 16-byte aligned     */
     int8_t *k_exp, *v_exp;  /* [num_pages, Hkv, page], 4-byte aligned

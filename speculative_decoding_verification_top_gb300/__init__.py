@@ -36,7 +36,8 @@ SOURCES = [os.path.join(CSRC, f)
            for f in ("api.cu", "rows.cu", "topp.cu", "final.cu", "noalloc.cu",
                      "accept.cu", "treemask.cu", "treesample.cu", "select.cu",
                      "kvcache.cu", "attn.cu", "attn_api.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh", "attn.cuh")]
+HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh", "attn.cuh",
+                                             "tensor.cuh")]
 INCLUDE = os.path.join(_ROOT, "include")
 HEADER = os.path.join(INCLUDE, "spec_verify.h")
 ATTN_HEADER = os.path.join(INCLUDE, "spec_attn.h")
@@ -52,6 +53,7 @@ SPEC_DATA_UNIFORM_RANGE = 1 << 4
 SPEC_DATA_TREE_SHAPE = 1 << 5
 SPEC_DATA_PROB_RANGE = 1 << 6
 SPEC_DATA_PAGE_RANGE = 1 << 7
+SPEC_DATA_STALL = 1 << 8
 SPEC_MAX_K = 31
 
 EXPORTED = (

@@ -535,6 +535,7 @@ SPEC_EXPORT const char *spec_verify_status_string(int status) {
         return "parents is not a rooted tree in topological order within depth D";
     case SPEC_DATA_PROB_RANGE: return "a gathered draft probability lies outside [0, 1]";
     case SPEC_DATA_PAGE_RANGE: return "a cache length or page id is out of range";
+    case SPEC_DATA_STALL: return "an internal wait ran out; outputs are undefined";
     default: return "unknown status";
     }
 }

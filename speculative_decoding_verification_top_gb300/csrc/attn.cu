@@ -1,121 +1,1129 @@
 // attn.cu -- attention of a target pass's new tokens to the paged cache.
 //
 // For one query row (token i, query head h) over the positions j it sees:
-//   s_j = scale q.k_j, capped and biased;  m = max s_j;
-//   l = sum 2^((s_j - m) log2 e);  out = sum 2^((s_j - m) log2 e) v_j / l.
-// One pass: m, l and the output's accumulator are kept as running values,
-// rescaled by 2^((m_old - m_new) log2 e) when the maximum grows.
+//   t_j = log2(e) * score_j;  m = max t_j;  l = sum 2^(t_j - m);
+//   out = sum 2^(t_j - m) v_j / l.
+// One pass over the cache.  m, l and the output's accumulator are running
+// values; two partial results (m, l, O) of the same row join as
+//   M = max m;  L = sum 2^(m - M) l;  out = sum 2^(m - M) O / L.
 //
-// attn_kernel   one warp per query row, 32 positions at a time: a lane takes
-//               a position's score, then the lanes take D / 32 output
-//               elements each.
+// attn_kernel   persistent, one CTA per SM.  A unit of work is one key/value
+//               head of one sequence (or of the shared prefix) and up to 256
+//               query rows: the N G rows (new token, query head of the group)
+//               that share the head's keys.  All units' tiles of 128
+//               positions, laid end to end, are cut into equal shares, one
+//               per CTA; a share's piece of a unit is a segment, and leaves
+//               one partial result per row.
+//                 warp 8      loads key and value tiles page by page (TMA)
+//                             into a ring of slots
+//                 warp 9      issues the products (tcgen05): S = Q K^T into
+//                             TMEM, then O += P V with P in TMEM
+//                 warps 0-3, 4-7   two softmax groups, a thread per row: S
+//                             from TMEM, 2^(t - m), P back into TMEM
+//                 warp 10     the e4m3 cache's exponents, as factors
+//               A unit of up to 128 rows alternates its tiles between the
+//               two groups, each with its own S and O (TMEM: 2 x 128 + 2 x D
+//               columns), so that one group's softmax runs under the other's
+//               products.  A larger unit gives each group 128 rows of its
+//               own and both work on every tile.
+// join_kernel   a programmatic dependent: joins each row's partial results.
+//
+// e4m3 cache: keys and values go to the tensor cores as the bytes they are.
+// The bf16 query, scaled per row by a power of two, splits exactly into two
+// e4m3 terms (4 + 4 significant bits; what falls under 2^-10 of the scaled
+// unit is at most 2^-18 of the row's maximum), and S = Q1 K^T + Q2 K^T at the
+// e4m3 rate costs what one bf16 product does.  The weights split into two
+// terms likewise (2^-8 relative at worst).  A key's exponent multiplies its
+// column of S; a value's exponent is added to t_j, so that the weight carries
+// it, and taken back in l.
 
 #include "attn.cuh"
+#include "tensor.cuh"
 
 namespace specv {
 namespace {
 
+constexpr int kTile = 128;        // positions a tile
+constexpr int kGroupRows = 128;   // query rows a softmax group
+constexpr int kAttnThreads = 352;
+constexpr int kMaxSlots = 16;
+constexpr int kScaleRing = 4;
+constexpr int kMaxGrid = 152;
+constexpr int kSmemMax = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kStalled = SPEC_DATA_STALL;
 
-template <int D, bool E4M3>
-__device__ __forceinline__ float element(const uint8_t *data, long long row, int d) {
-    if (E4M3) {
-        __nv_fp8_e4m3 x;
-        x.__x = data[row * D + d];
-        return static_cast<float>(x);
+// How the units are numbered and cut; the same arithmetic in both kernels.
+struct Plan {
+    int B, N, G, Hkv, width, page_shift;
+    int R, rt, ru;        // rows, 128-row tiles and units a (sequence, head)
+    int Ls;               // shared prefix
+    int sR, srt, sru, sT; // the same for the prefix (rows of all sequences), and its tiles
+    int sT0;              // first tile of the prefix (0: windows do not trim it)
+    int rc, src;          // rows a partial result holds (own, shared)
+    int grid;
+    const int32_t *lens, *pos;
+    int window;
+    long long *base;      // [B + 1] first cost of each sequence's units; the total
+    float4 *o, *so;       // [slots, 2, D / 4, rc] partial O
+    float2 *ml, *sml;     // [slots, 2, rc] partial (m, l)
+};
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// A sequence's tiles [t0, t1): those a row may see.
+struct Span {
+    int len, t0, t1;
+};
+
+__device__ __forceinline__ Span span_of(const Plan &p, int b) {
+    Span s;
+    s.len = p.lens[b];
+    if (s.len < 0 || s.len > (p.width << p.page_shift)) s.len = 0;  // the join fails it
+    s.t1 = (s.len + kTile - 1) / kTile;
+    s.t0 = 0;
+    if (p.window > 0) {
+        // pos_i - pos_j < window for some row: j >= min pos_i - window + 1 among the context;
+        // the new tokens themselves are kept whatever their positions say.
+        long long least = static_cast<long long>(p.Ls) + s.len - p.N;
+        if (p.pos) {
+            int m = INT_MAX;
+            for (int n = 0; n < p.N; ++n) m = min(m, p.pos[static_cast<long long>(b) * p.N + n]);
+            least = m;
+        }
+        long long j = least - p.window + 1 - p.Ls;
+        j = min(j, static_cast<long long>(s.len) - p.N);
+        if (j > 0) s.t0 = min(static_cast<int>(j / kTile), s.t1);
     }
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(data)[row * D + d]);
+    return s;
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const AttnArgs a) {
-    __shared__ float qs[kWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    if (row >= static_cast<long long>(a.B) * a.N * a.Hq) return;
-    const int hq = static_cast<int>(row % a.Hq);
-    const long long bn = row / a.Hq;
-    const int b = static_cast<int>(bn / a.N), n = static_cast<int>(bn % a.N), h = hq / a.G;
-    const __nv_bfloat16 *q = a.q + bn * a.q_stride + static_cast<long long>(hq) * D;
-    for (int d = lane; d < D; d += 32) qs[warp][d] = __bfloat162float(q[d]);
-    __syncwarp();
-    const int32_t *table = a.table + static_cast<long long>(b) * a.width;
-    const int most = a.width << a.c.page_shift;
-    const int len = a.lens[b];
-    bool bad = len < 0 || len > most;
-    const int own = bad ? 0 : len, Ls = a.shared_len, total = Ls + own;
-    const int first = own - a.N;  // own position of new token 0 (may be negative: padding)
-    const int pos_i = a.pos ? a.pos[bn] : Ls + first + n;
-    const float slope = a.slopes ? a.slopes[hq] : 0.0f;
-    float m = kNegInf, l = 0.0f, acc[D / 32] = {};
-    for (int j0 = 0; j0 < total; j0 += 32) {
-        const int j = j0 + lane;
-        bool seen = j < total;
-        long long at = -1;
-        float s = kNegInf;
-        if (seen) {
-            int slot = 0, page, pos_j = j;
-            if (j < Ls) {
-                page = page_of(a.c, a.shared_table, INT_MAX, j, &slot);
-            } else {
-                const int o = j - Ls, c = o - first;
-                page = page_of(a.c, table, a.width, o, &slot);
-                if (c >= 0) {  // a new token
-                    seen = a.mask ? a.mask[bn * a.N + c] != 0 : c <= n;
-                    if (a.pos) pos_j = a.pos[static_cast<long long>(b) * a.N + c];
+// One unit and this CTA's tiles [t0, t1) of it.
+struct Segment {
+    bool shared, dual;
+    int b, h, row0, rows;  // rows [row0, row0 + rows) of the unit's (sequence, head)
+    int t0, t1, len, slot;
+};
+
+// Walks a CTA's share [x, end) of the cost line.  A tile of a unit costs its
+// row tiles (1 or 2): the products' work.  Every warp walks it by itself.
+struct Walk {
+    long long ubase, x, end;
+    int b, h, u;          // next unit; b = -1: the shared prefix
+    Span s;
+    const Plan &p;
+
+    __device__ Walk(const Plan &plan, long long from, long long to, int b0, long long base0)
+        : ubase(0), x(from), end(to), b(b0), h(0), u(0), s(), p(plan) {
+        if (x >= end) {
+            ubase = end;
+            return;
+        }
+        const bool sh = b < 0;
+        if (!sh) s = span_of(p, b);
+        const int T = sh ? p.sT : s.t1 - s.t0, rt = sh ? p.srt : p.rt;
+        const long long in = x - base0, head = static_cast<long long>(T) * rt;
+        if (head == 0) return;
+        h = static_cast<int>(in / head);
+        u = static_cast<int>((in - h * head) / (2ll * T));
+        ubase = base0 + h * head + u * 2ll * T;
+    }
+
+    __device__ bool next(Segment *g) {
+        while (ubase < end && b < p.B) {
+            const bool sh = b < 0;
+            const int T = sh ? p.sT : s.t1 - s.t0;
+            if (T == 0) {  // a sequence without tiles
+                advance_sequence();
+                continue;
+            }
+            const int R = sh ? p.sR : p.R, ru = sh ? p.sru : p.ru;
+            g->shared = sh;
+            g->b = b;
+            g->h = h;
+            g->row0 = u * 2 * kGroupRows;
+            g->rows = min(R - g->row0, 2 * kGroupRows);
+            g->dual = g->rows > kGroupRows;
+            const int c = g->dual ? 2 : 1;
+            const int first = sh ? p.sT0 : s.t0;
+            g->t0 = x > ubase ? static_cast<int>((x - ubase + c - 1) / c) : 0;
+            g->t1 = static_cast<int>(min(static_cast<long long>(T), (end - ubase + c - 1) / c));
+            g->len = sh ? p.Ls : s.len;
+            g->slot = ((sh ? 0 : b) * p.Hkv + h) * ru + u + static_cast<int>(blockIdx.x);
+            const bool some = g->t0 < g->t1;
+            g->t0 += first;
+            g->t1 += first;
+            ubase += static_cast<long long>(T) * c;
+            if (++u == ru) {
+                u = 0;
+                if (++h == p.Hkv) {
+                    h = 0;
+                    if (sh) {
+                        b = 0;
+                        s = span_of(p, 0);
+                    } else {
+                        advance_sequence();
+                    }
                 }
             }
-            if (page < 0) bad = true;
-            seen = seen && page >= 0 &&
-                   (a.window == 0 || static_cast<long long>(pos_i) - pos_j < a.window);
-            if (seen) {
-                at = cache_row(a.c, page, h, slot);
-                float x = 0.0f;
-                for (int d = 0; d < D; ++d) x += qs[warp][d] * element<D, E4M3>(a.c.k, at, d);
-                if (E4M3) x *= exp2i(a.c.k_exp[at]);
-                x *= a.scale;
-                if (a.cap > 0.0f) x = a.cap * tanhf(x / a.cap);
-                s = (x - slope * static_cast<float>(pos_i - pos_j)) * kLog2e;
+            if (some) return true;
+        }
+        return false;
+    }
+
+    __device__ void advance_sequence() {
+        ++b;
+        if (b < p.B) s = span_of(p, b);
+    }
+};
+
+struct Barriers {
+    unsigned long long full[kMaxSlots], empty[kMaxSlots];
+    unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
+    unsigned long long q_full, o_full, s_full[2], p_full[2], drained;
+};
+
+struct Shared {
+    Barriers bar;
+    long long scan[kAttnThreads / 32 + 1];
+    long long total, from, to, base0;
+    int b0;
+    uint32_t tmem;
+    int dead;          // a wait ran out: everyone leaves
+    int fail[16];      // per segment (mod 16): a page id out of range
+    int odd[16];       // per segment (mod 16): a cleaned tile held values that are not finite
+};
+
+template <int D, bool E4M3>
+struct Shape {
+    static constexpr int kRow = E4M3 ? D : 128;              // bytes of a shared-memory matrix row
+    static constexpr int kHalves = E4M3 ? 1 : D / 64;        // 64-column blocks of a bf16 matrix
+    static constexpr int kMat = kTile * kRow;                // bytes of one block
+    static constexpr int kSlot = kMat * kHalves;             // a key or value tile
+    static constexpr int kQ = E4M3 ? 2 * kMat : kSlot;       // a group's query tile
+    static constexpr int kScale = E4M3 ? kScaleRing * 3 * kTile * 4 : 0;
+    static constexpr int kFixed = kScale + static_cast<int>((sizeof(Shared) + 1023) / 1024 * 1024);
+    static constexpr int slots(int q_tiles) {
+        const int n = (kSmemMax - 1024 - kFixed - q_tiles * kQ) / kSlot;
+        return n < kMaxSlots ? n : kMaxSlots;
+    }
+    static constexpr int bytes(int q_tiles) {
+        return 1024 + kFixed + q_tiles * kQ + slots(q_tiles) * kSlot;
+    }
+};
+
+struct KernelArgs {
+    AttnArgs a;
+    Plan p;
+    int q_tiles, slots;
+};
+
+// Whether row (own row r of sequence b, its token's position pos_i) sees own
+// position j; *pos_j gets the position's index.
+__device__ __forceinline__ bool sees(const AttnArgs &a, int b, int n, int pos_i, int first, int len,
+                                     int j, int *pos_j) {
+    *pos_j = a.shared_len + j;
+    if (j >= len) return false;
+    const int c = j - first;
+    if (c >= 0) {
+        const long long bn = static_cast<long long>(b) * a.N;
+        if (a.pos) *pos_j = a.pos[bn + c];
+        if (a.mask ? a.mask[(bn + n) * a.N + c] == 0 : c > n) return false;
+    }
+    return a.window == 0 || static_cast<long long>(pos_i) - *pos_j < a.window;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Query row -> the group's tile in shared memory.  e4m3: returns the row's
+// factor 2^e (see the top of the file).
+template <int D, bool E4M3>
+__device__ __forceinline__ float stage_query(const __nv_bfloat16 *q, uint8_t *tile, int row, bool neg) {
+    using S = Shape<D, E4M3>;
+    uint4 u[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+        u[i] = q ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0, 0, 0, 0);
+    const uint32_t flip = neg ? 0x80008000u : 0u;
+    if (!E4M3) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            uint4 w = u[i];
+            w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
+            *reinterpret_cast<uint4 *>(tile + (i / 8) * S::kMat + swizzled<S::kRow>(row, (i % 8) * 16)) = w;
+        }
+        return 1.0f;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            top = max(top, w[k] & 0x7fffu);
+            top = max(top, w[k] >> 16 & 0x7fffu);
+        }
+    }
+    // top: bf16 bits of max |q|.  e as in the cache: max |q| <= 448 * 2^e.
+    int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+    e = max(-120, min(120, e));
+    const float f = exp2i(-e);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 v = u[2 * i + k / 2];
+            const uint32_t a = (k & 1 ? v.z : v.x) ^ flip, b = (k & 1 ? v.w : v.y) ^ flip;
+            const float x0 = __uint_as_float(a << 16) * f, x1 = __uint_as_float(a & 0xffff0000u) * f;
+            const float x2 = __uint_as_float(b << 16) * f, x3 = __uint_as_float(b & 0xffff0000u) * f;
+            const uint32_t p = e4m3_pair(x0, x1), r = e4m3_pair(x2, x3);
+            const float2 y = e4m3_values(p), z = e4m3_values(r);
+            hi[k] = p | r << 16;
+            lo[k] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
+        }
+        const uint32_t o = swizzled<S::kRow>(row, i * 16);
+        *reinterpret_cast<uint4 *>(tile + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(tile + S::kMat + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    return exp2i(e);
+}
+
+// Row `row` of a value tile whose positions some rows do not see: zeros where
+// the position is not held (the slot has whatever was there), and zeros for
+// elements that are not finite, so that an unseen one does not reach a row
+// through 0 * inf.  Returns whether a held element was not finite.
+template <int D, bool E4M3>
+__device__ __forceinline__ bool clean_values(uint8_t *tile, int row, bool held) {
+    using S = Shape<D, E4M3>;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < D * (E4M3 ? 1 : 2) / 16; ++i) {
+        uint4 *at = reinterpret_cast<uint4 *>(tile + (i * 16 / S::kRow) * S::kMat +
+                                              swizzled<S::kRow>(row, i * 16 % S::kRow));
+        if (!held) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        uint4 u = *at;
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        bool here = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t keep;
+            if (E4M3) {
+                // 0x80 in each byte that is 0x7f or 0xff
+                const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                keep = ~((nan >> 7) * 0xffu);
+            } else {
+                keep = ((w[k] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                       ((w[k] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+            }
+            here |= keep != 0xffffffffu;
+            w[k] &= keep;
+        }
+        if (here) *at = make_uint4(w[0], w[1], w[2], w[3]);
+        odd |= here;
+    }
+    return odd;
+}
+
+template <int D, bool E4M3, bool EXTRA>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const __grid_constant__ KernelArgs ka, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
+    using S = Shape<D, E4M3>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    const AttnArgs &a = ka.a;
+    const Plan &p = ka.p;
+    uint8_t *qt = smem, *ring = qt + ka.q_tiles * S::kQ;
+    float *scales = reinterpret_cast<float *>(ring + ka.slots * S::kSlot);
+    Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(scales) + S::kScale);
+    Barriers &bar = sh.bar;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // The cost line: the prefix's units, then each sequence's.  Thread i sums
+    // a contiguous share of the sequences; a scan places them.
+    const int each = ceil_div(p.B, kAttnThreads);
+    const int bf = min(p.B, tid * each), bt = min(p.B, bf + each);
+    const long long per = static_cast<long long>(p.Hkv) * p.rt;
+    long long mine = 0;
+    for (int b = bf; b < bt; ++b) {
+        const Span s = span_of(p, b);
+        mine += (s.t1 - s.t0) * per;
+    }
+    long long incl = mine;
+    for (int o = 1; o < 32; o *= 2) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    if (tid == 0) {
+        for (int i = 0; i < ka.slots; ++i) {
+            bar_init(smem_addr(&bar.full[i]), 1);
+            bar_init(smem_addr(&bar.empty[i]), 1);
+        }
+        for (int i = 0; i < kScaleRing; ++i) {
+            bar_init(smem_addr(&bar.scale_full[i]), 1);
+            bar_init(smem_addr(&bar.scale_empty[i]), 8);
+        }
+        bar_init(smem_addr(&bar.q_full), 8);
+        bar_init(smem_addr(&bar.o_full), 1);
+        bar_init(smem_addr(&bar.drained), 1);
+        for (int w = 0; w < 2; ++w) {
+            bar_init(smem_addr(&bar.s_full[w]), 1);
+            bar_init(smem_addr(&bar.p_full[w]), 4);
+        }
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_proxy();
+    }
+    if (warp == 9) tmem_alloc(smem_addr(&sh.tmem), 512);
+    __syncthreads();
+    const long long prefix_cost = static_cast<long long>(p.Hkv) * p.srt * p.sT;
+    long long before = prefix_cost, total = prefix_cost;
+    for (int w = 0; w < kAttnThreads / 32; ++w) {
+        if (w < warp) before += sh.scan[w];
+        total += sh.scan[w];
+    }
+    before += incl - mine;
+    const long long from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
+    if (tid == 0) {
+        sh.b0 = -1;
+        sh.base0 = 0;
+    }
+    __syncthreads();
+    if (from >= prefix_cost && before <= from && from < before + mine) {
+        long long at = before;
+        for (int b = bf; b < bt; ++b) {
+            const Span s = span_of(p, b);
+            const long long c = (s.t1 - s.t0) * per;
+            if (from < at + c) {
+                sh.b0 = b;
+                sh.base0 = at;
+                break;
+            }
+            at += c;
+        }
+    }
+    if (blockIdx.x == 0) {
+        long long at = before;
+        for (int b = bf; b < bt; ++b) {
+            const Span s = span_of(p, b);
+            p.base[b] = at;
+            at += (s.t1 - s.t0) * per;
+        }
+        if (tid == 0) p.base[p.B] = total;
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    volatile int *dead = &sh.dead;
+    Walk walk(p, from, to, sh.b0, sh.base0);
+    Segment g;
+
+    if (warp == 8) {
+        // ---- loads: tiles in the order the products take them
+        uint32_t n = 0;  // slots filled
+        int seg = 0;
+        bool live = true;
+        while (live && walk.next(&g)) {
+            if (lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
+            __syncwarp();
+            const int32_t *table = g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
+            const int shift = a.c.page_shift, per_tile = kTile >> shift, n_tiles = g.t1 - g.t0;
+            // Alternating tiles: K0 K1 V0 K2 V1 ...; both groups on each tile: K0 V0 K1 V1 ...
+            int kt = 0, vt = 0;
+            for (int i = 0; i < 2 * n_tiles; ++i) {
+                const bool key = kt < n_tiles && (kt == vt || (!g.dual && kt == vt + 1));
+                const int t = g.t0 + (key ? kt++ : vt++);
+                const uint32_t slot = n % ka.slots, round = n / ka.slots;
+                ++n;
+                live = bar_wait(smem_addr(&bar.empty[slot]), (round & 1) ^ 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+                const int pages = min(per_tile, ((g.len - t * kTile) + (1 << shift) - 1) >> shift);
+                int id = -1;
+                if (lane < pages) {
+                    id = table[t * per_tile + lane];
+                    if (id < 0 || id >= a.c.num_pages) {
+                        id = -1;
+                        sh.fail[seg & 15] = 1;
+                        atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
+                    }
+                }
+                const int good = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                const uint32_t full = smem_addr(&bar.full[slot]);
+                if (lane == 0) bar_arrive_tx(full, static_cast<uint32_t>(good * (S::kSlot >> 7) << shift));
+                __syncwarp();
+                if (id >= 0) {
+                    const CUtensorMap *map = key ? &kmap : &vmap;
+                    const uint32_t dst = smem_addr(ring + slot * S::kSlot) + ((lane << shift) * S::kRow);
+#pragma unroll
+                    for (int x = 0; x < S::kHalves; ++x)
+                        tma_load(dst + x * S::kMat, map, full, x * 64, 0, id * a.c.Hkv + g.h);
+                }
+            }
+            ++seg;
+        }
+        if (!live) {  // the copies in flight land before the CTA's memory goes
+            for (uint32_t i = n > static_cast<uint32_t>(ka.slots) ? n - ka.slots : 0; i + 1 < n; ++i)
+                bar_drain(smem_addr(&bar.full[i % ka.slots]), (i / ka.slots) & 1);
+        }
+    } else if (warp == 9) {
+        // ---- products
+        if (lane == 0) {
+            constexpr uint32_t kQk = mma_desc(E4M3, kTile, false), kPv = mma_desc(E4M3, D, true);
+            uint32_t n = 0, segs = 0, pn[2] = {0, 0};
+            bool live = true;
+            const uint32_t q0 = smem_addr(qt), r0 = smem_addr(ring);
+            // S of group w from the key tile in `slot`
+            auto scores = [&](int w, bool dual, uint32_t slot) {
+                const uint32_t q = q0 + (dual && w ? S::kQ : 0), k = r0 + slot * S::kSlot;
+                const uint32_t d = tmem + w * kTile;
+                if (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < 2 * (D / 32); ++i) {
+                        const int half = i / (D / 32), j = i % (D / 32);
+                        mma_ss<true>(d, matrix_desc<S::kRow>(q + half * S::kMat + j * 32, 0),
+                                     matrix_desc<S::kRow>(k + j * 32, 0), kQk, i > 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t o = (i / 4) * S::kMat + (i % 4) * 32;
+                        mma_ss<false>(d, matrix_desc<S::kRow>(q + o, 0), matrix_desc<S::kRow>(k + o, 0), kQk, i > 0);
+                    }
+                }
+            };
+            // O += P V of group w with the value tile in `slot`
+            auto values = [&](int w, uint32_t slot, bool first) {
+                const uint32_t v = r0 + slot * S::kSlot;
+                const uint32_t d = tmem + 2 * kTile + w * D, pt = tmem + w * kTile;
+                if (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = i % 4;
+                        mma_ts<true>(d, pt + (i / 4) * 32 + j * 8,
+                                     matrix_desc<S::kRow>(v + j * 32 * S::kRow, S::kMat), kPv, !first || i > 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mma_ts<false>(d, pt + i * 8, matrix_desc<S::kRow>(v + i * 16 * S::kRow, S::kMat), kPv,
+                                      !first || i > 0);
+                }
+            };
+            auto slot_ready = [&](uint32_t i) {
+                return bar_wait(smem_addr(&bar.full[i % ka.slots]), (i / ka.slots) & 1, dead);
+            };
+            while (live && walk.next(&g)) {
+                const int T = g.t1 - g.t0;
+                live = bar_wait(smem_addr(&bar.q_full), segs & 1, dead);
+                fence_after_sync();
+                // scores of the first tile (of each group's first)
+                const int lead = g.dual ? 1 : min(2, T);
+                for (int t = 0; live && t < lead; ++t, ++n) {
+                    if (!(live = slot_ready(n))) break;
+                    for (int w = g.dual ? 0 : t; w <= (g.dual ? 1 : t); ++w) {
+                        scores(w, g.dual, n % ka.slots);
+                        if (w == (g.dual ? 1 : t)) mma_commit(smem_addr(&bar.empty[n % ka.slots]));
+                        mma_commit(smem_addr(&bar.s_full[w]));
+                    }
+                }
+                for (int t = 0; live && t < T; ++t) {
+                    const uint32_t vs = n++;
+                    const bool more = t + lead < T;
+                    const uint32_t ks = n;
+                    if (more) ++n;
+                    if (!(live = slot_ready(vs))) break;
+                    for (int w = g.dual ? 0 : t & 1; w <= (g.dual ? 1 : t & 1); ++w) {
+                        if (!(live = bar_wait(smem_addr(&bar.p_full[w]), pn[w]++ & 1, dead))) break;
+                        fence_after_sync();
+                        values(w, vs % ka.slots, g.dual ? t == 0 : t < 2);
+                        const bool last = !g.dual || w == 1;
+                        if (last) mma_commit(smem_addr(&bar.empty[vs % ka.slots]));
+                        if (more) {
+                            if (!(live = slot_ready(ks))) break;
+                            scores(w, g.dual, ks % ka.slots);
+                            if (last) mma_commit(smem_addr(&bar.empty[ks % ka.slots]));
+                            mma_commit(smem_addr(&bar.s_full[w]));
+                        }
+                    }
+                }
+                if (live) mma_commit(smem_addr(&bar.o_full));
+                ++segs;
+            }
+            if (!live) {  // products in flight end before TMEM is freed
+                mma_commit(smem_addr(&bar.drained));
+                bar_drain(smem_addr(&bar.drained), 0);
             }
         }
-        float top = s;
-        for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float mn = fmaxf(m, top);
-        if (mn == kNegInf) continue;
-        const float keep = ex2(m - mn), p = seen ? ex2(s - mn) : 0.0f;
-        m = mn;
-        l = l * keep + p;
-        for (int i = 0; i < D / 32; ++i) acc[i] *= keep;
-        for (int t = 0; t < 32; ++t) {
-            const long long r = __shfl_sync(0xffffffffu, at, t);
-            if (r < 0) continue;
-            float w = __shfl_sync(0xffffffffu, p, t);
-            if (E4M3) w *= exp2i(a.c.v_exp[r]);
-            for (int i = 0; i < D / 32; ++i) acc[i] += w * element<D, E4M3>(a.c.v, r, lane + 32 * i);
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- the e4m3 exponents as factors: 2^ek, ev, 2^-ev of every position
+        if (E4M3) {
+            uint32_t n = 0;
+            bool live = true;
+            while (live && walk.next(&g)) {
+                const int32_t *table = g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
+                for (int t = g.t0; t < g.t1; ++t, ++n) {
+                    const int j = t * kTile + lane * 4;
+                    int slot = 0;
+                    const int page = j < g.len ? page_of(a.c, table, INT_MAX, j, &slot) : -1;
+                    uint32_t ek = 0, ev = 0;
+                    if (page >= 0) {
+                        const long long row = cache_row(a.c, page, g.h, slot);
+                        ek = __ldg(reinterpret_cast<const uint32_t *>(a.c.k_exp + row));
+                        ev = __ldg(reinterpret_cast<const uint32_t *>(a.c.v_exp + row));
+                    }
+                    const uint32_t s = n % kScaleRing;
+                    live = bar_wait(smem_addr(&bar.scale_empty[s]), ((n / kScaleRing) & 1) ^ 1, dead);
+                    live = __all_sync(0xffffffffu, live);
+                    if (!live) break;
+                    float *f = scales + s * 3 * kTile + lane * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int x = max(-120, min(120, static_cast<int>(static_cast<int8_t>(ek >> 8 * i))));
+                        const int y = max(-120, min(120, static_cast<int>(static_cast<int8_t>(ev >> 8 * i))));
+                        f[i] = exp2i(x);
+                        f[kTile + i] = static_cast<float>(y);
+                        f[2 * kTile + i] = exp2i(-y);
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(smem_addr(&bar.scale_full[s]));
+                }
+            }
+        }
+    } else {
+        // ---- softmax groups
+        const int w = warp >> 2, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's TMEM lanes
+        const uint32_t st = tmem + lanes + w * kTile, ot = tmem + lanes + 2 * kTile + w * D;
+        // Growth of t over the reference maximum that is let stand: a weight
+        // stays under 2^8 (bf16), or 2^5 * 2^3.75 < 448 (e4m3, whose weights
+        // are scaled by 2^5 so that small ones keep their second term).
+        constexpr float kSlack = E4M3 ? 3.75f : 8.0f, kLift = E4M3 ? 5.0f : 0.0f;
+        const bool neg = a.scale < 0.0f;
+        const float mul = (a.cap > 0.0f ? fabsf(a.scale) / a.cap : fabsf(a.scale) * kLog2e);
+        const float capl = a.cap * kLog2e;
+        uint32_t segs = 0, sn = 0, n_ring = 0, n_scale = 0;
+        bool live = true;
+        while (live && walk.next(&g)) {
+            const int T = g.t1 - g.t0, row0 = g.row0 + (g.dual ? w * kGroupRows : 0);
+            const int rows = min(kGroupRows, g.rows - (g.dual ? w * kGroupRows : 0));
+            const bool has = row < rows, active = (warp & 3) * 32 < rows;
+            const int r = row0 + row, tok_in = has ? r / a.G : 0, head = g.h * a.G + (has ? r % a.G : 0);
+            const long long tok = g.shared ? tok_in : static_cast<long long>(g.b) * a.N + tok_in;
+            const int b = g.shared ? (has ? static_cast<int>(tok / a.N) : 0) : g.b;
+            const int n = has ? static_cast<int>(tok - static_cast<long long>(b) * a.N) : 0;
+            float qf = 1.0f;
+            if (g.dual || w == 0) {
+                const __nv_bfloat16 *q = has ? a.q + tok * a.q_stride + static_cast<long long>(head) * D : nullptr;
+                qf = stage_query<D, E4M3>(q, qt + (g.dual ? w : 0) * S::kQ, row, neg);
+            } else if (E4M3 && has) {
+                // the other group staged this row: its factor again
+                const __nv_bfloat16 *q = a.q + tok * a.q_stride + static_cast<long long>(head) * D;
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top = max(top, max(x[k] & 0x7fffu, x[k] >> 16 & 0x7fffu));
+                }
+                const int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+                qf = exp2i(max(-120, min(120, e)));
+            }
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
+            const int seq_len = g.shared ? (has ? a.lens[b] : 0) : g.len;
+            const int first = seq_len - a.N;
+            const int pos_i = !has ? 0 : a.pos ? a.pos[tok] : a.shared_len + first + n;
+            const float slope = EXTRA && a.slopes && has ? a.slopes[head] * kLog2e : 0.0f;
+            const float rs = mul * qf;
+            const int ctx = g.shared ? g.len : max(0, first);  // positions every row sees (no window)
+            // The unit's largest position index: every warp finds it from all the
+            // unit's rows, so that both groups treat a tile alike.
+            int far_most = INT_MIN;
+            if (a.window > 0) {
+                for (int i = lane; i < g.rows; i += 32) {
+                    const long long tk = (g.row0 + i) / a.G + (g.shared ? 0 : static_cast<long long>(g.b) * a.N);
+                    const int tb = static_cast<int>(tk / a.N);
+                    far_most = max(far_most, a.pos ? a.pos[tk] : a.shared_len + a.lens[tb] - a.N + static_cast<int>(tk % a.N));
+                }
+                far_most = __reduce_max_sync(0xffffffffu, far_most);
+            }
+            float m = kNegInf, l = 0.0f;
+            bool wrote = false;
+            for (int t = g.t0; t < g.t1; ++t) {
+                const int idx = t - g.t0;
+                if (!g.dual && (idx & 1) != w) continue;
+                const int j0 = t * kTile;
+                // Does every row see the whole tile?
+                bool whole = j0 + kTile <= ctx;
+                if (a.window > 0)
+                    whole = whole && static_cast<long long>(far_most) - (g.shared ? 0 : a.shared_len) - j0 < a.window;
+                live = bar_wait(smem_addr(&bar.s_full[w]), sn++ & 1, dead);
+                const float *fa = nullptr;
+                if (E4M3) {
+                    const uint32_t s = (n_scale + idx) % kScaleRing;
+                    live = live && bar_wait(smem_addr(&bar.scale_full[s]), ((n_scale + idx) / kScaleRing) & 1, dead);
+                    fa = scales + s * 3 * kTile;
+                }
+                if (!whole) {
+                    // the tile's values: slot index as the loads number them
+                    const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
+                    live = live && bar_wait(smem_addr(&bar.full[vi % ka.slots]), (vi / ka.slots) & 1, dead);
+                }
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+                fence_after_sync();
+                if (active) {
+                    float t_[kTile];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_load32(st + c * 32, t_ + c * 32);
+                    tmem_load_wait();
+                    float top = kNegInf;
+                    const float far0 = EXTRA ? static_cast<float>((g.shared ? 0 : a.shared_len) + j0 - pos_i) : 0.0f;
+                    uint32_t seen[4];
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            seen[c] = 0;
+                            for (int k = 0; k < 32; ++k) {
+                                const int j = j0 + c * 32 + k;
+                                int pj;
+                                const bool y = g.shared ? j < g.len && (a.window == 0 || static_cast<long long>(pos_i) - j < a.window)
+                                                        : sees(a, b, n, pos_i, first, g.len, j, &pj);
+                                seen[c] |= (y && has ? 1u : 0u) << k;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 4) {
+                        float4 ka4, kb4;
+                        if (E4M3) {
+                            ka4 = *reinterpret_cast<const float4 *>(fa + c);
+                            kb4 = *reinterpret_cast<const float4 *>(fa + kTile + c);
+                        }
+                        const float fk[4] = {ka4.x, ka4.y, ka4.z, ka4.w}, fb[4] = {kb4.x, kb4.y, kb4.z, kb4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float x = t_[c + k];
+                            if (E4M3) x *= fk[k];
+                            if (EXTRA && a.cap > 0.0f) {
+                                // cap tanh(x) log2 e, tanh(x) = 1 - 2 / (1 + e^2x)
+                                const float e = ex2(x * rs * (2.0f * kLog2e));
+                                x = capl - __fdividef(2.0f * capl, 1.0f + e);
+                            } else {
+                                x *= rs;
+                            }
+                            if (EXTRA) {
+                                float far = far0 + static_cast<float>(c + k);
+                                if (!whole && !g.shared && a.pos) {
+                                    const int node = j0 + c + k - first;
+                                    if (node >= 0 && node < a.N)
+                                        far = static_cast<float>(a.pos[static_cast<long long>(b) * a.N + node] - pos_i);
+                                }
+                                x = fmaf(slope, far, x);
+                            }
+                            if (E4M3) x += fb[k];
+                            if (!whole && !(seen[(c + k) / 32] >> ((c + k) % 32) & 1u)) x = kNegInf;
+                            t_[c + k] = x;
+                            top = fmaxf(top, x);
+                        }
+                    }
+                    // Grow the reference maximum where a row needs it.
+                    const bool grow = top > m + kSlack;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float mn = grow ? top : m;
+                        const float keep = m == mn ? 1.0f : ex2(m - mn);
+                        m = mn;
+                        l *= keep;
+                        if (wrote) {
+#pragma unroll
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                tmem_load32(ot + c, o);
+                                tmem_load_wait();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= keep;
+                                tmem_store32(ot + c, reinterpret_cast<const uint32_t *>(o));
+                            }
+                        }
+                    }
+                    const float ref = m == kNegInf ? 0.0f : m - kLift;
+                    float sum[4] = {};
+                    if (E4M3) {
+                        uint32_t hi[kTile / 4], lo[kTile / 4];
+#pragma unroll
+                        for (int c = 0; c < kTile; c += 4) {
+                            const float4 fc = *reinterpret_cast<const float4 *>(fa + 2 * kTile + c);
+                            const float x0 = ex2(t_[c] - ref), x1 = ex2(t_[c + 1] - ref);
+                            const float x2 = ex2(t_[c + 2] - ref), x3 = ex2(t_[c + 3] - ref);
+                            sum[0] = fmaf(x0, fc.x, sum[0]);
+                            sum[1] = fmaf(x1, fc.y, sum[1]);
+                            sum[2] = fmaf(x2, fc.z, sum[2]);
+                            sum[3] = fmaf(x3, fc.w, sum[3]);
+                            const uint32_t u = e4m3_pair(x0, x1), v = e4m3_pair(x2, x3);
+                            const float2 y = e4m3_values(u), z = e4m3_values(v);
+                            hi[c / 4] = u | v << 16;
+                            lo[c / 4] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
+                        }
+                        tmem_store32(st, hi);
+                        tmem_store32(st + 32, lo);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kTile; c += 64) {
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int k = 0; k < 64; k += 2) {
+                                const float x0 = ex2(t_[c + k] - ref), x1 = ex2(t_[c + k + 1] - ref);
+                                sum[k & 2] += x0;
+                                sum[(k & 2) + 1] += x1;
+                                pk[k / 2] = bf16_pair(x0, x1);
+                            }
+                            tmem_store32(st + c / 2, pk);
+                        }
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_store_wait();
+                }
+                wrote = true;
+                if (!whole) {
+                    const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
+                    if (clean_values<D, E4M3>(ring + vi % ka.slots * S::kSlot, row, j0 + row < g.len))
+                        sh.odd[segs & 15] = 1;
+                    fence_async_proxy();
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(smem_addr(&bar.p_full[w]));
+                    if (E4M3) bar_arrive(smem_addr(&bar.scale_empty[(n_scale + idx) % kScaleRing]), g.dual ? 1 : 2);
+                }
+            }
+            if (!live) break;
+            live = bar_wait(smem_addr(&bar.o_full), segs & 1, dead);
+            live = __all_sync(0xffffffffu, live);
+            if (!live) break;
+            fence_after_sync();
+            // ---- the partial result
+            const int rc = g.shared ? p.src : p.rc;
+            const long long part = static_cast<long long>(g.slot) * 2 + w;
+            float2 *ml = (g.shared ? p.sml : p.ml) + part * rc;
+            float4 *o = (g.shared ? p.so : p.o) + part * (D / 4) * rc;
+            const bool failed = reinterpret_cast<volatile int *>(sh.fail)[segs & 15] != 0;
+            const bool odd = reinterpret_cast<volatile int *>(sh.odd)[segs & 15] != 0;
+            if (has) ml[row] = make_float2(m == kNegInf ? kNegInf : m - kLift, failed ? NAN : l);
+            if (active && wrote) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float x[32];
+                    tmem_load32(ot + c, x);
+                    tmem_load_wait();
+                    if (odd && has) {
+                        // seen values that are not finite, left out of the products
+                        for (int t = g.t0; t < g.t1; ++t) {
+                            if (!g.dual && ((t - g.t0) & 1) != w) continue;
+                            for (int j = t * kTile; j < min(g.len, (t + 1) * kTile); ++j) {
+                                int pj, slot;
+                                if (g.shared ? a.window > 0 && static_cast<long long>(pos_i) - j >= a.window
+                                             : !sees(a, b, n, pos_i, first, g.len, j, &pj))
+                                    continue;
+                                const int32_t *table = g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
+                                const int page = page_of(a.c, table, INT_MAX, j, &slot);
+                                if (page < 0) continue;
+                                const long long at = cache_row(a.c, page, g.h, slot) * D + c;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    float v;
+                                    if (E4M3)
+                                        v = (a.c.v[at + k] & 0x7f) == 0x7f ? NAN : 0.0f;
+                                    else
+                                        v = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.c.v)[at + k]);
+                                    if (!isfinite(v)) x[k] += v;
+                                }
+                            }
+                        }
+                    }
+                    if (has) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            o[(c / 4 + k) * rc + row] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                    }
+                }
+            }
+            fence_before_sync();
+            ++segs;
+            n_ring += 2 * T;
+            n_scale += T;
+        }
+        if (!live && tid == 0) atomicOr(a.err, kStalled);
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 9) tmem_free(tmem, 512);
+}
+
+// ------------------------------------------------------------------ join
+
+// CTA whose share holds cost x: the largest c with total * c / grid <= x.
+__device__ __forceinline__ int owner(long long x, long long total, int grid) {
+    return static_cast<int>(((x + 1) * grid + total - 1) / total) - 1;
+}
+
+// A row's partial results of one unit: f(slot, half) for each written one.
+template <typename F>
+__device__ __forceinline__ void each_part(const Plan &p, long long total, long long ubase, int T,
+                                          int unit, int rows, int row, F f) {
+    const bool dual = rows > kGroupRows;
+    const int c = dual ? 2 : 1;
+    const long long uend = ubase + static_cast<long long>(T) * c;
+    const int lo = owner(ubase, total, p.grid), hi = owner(uend - 1, total, p.grid);
+    for (int i = lo; i <= hi; ++i) {
+        const long long from = total * i / p.grid, to = total * (i + 1) / p.grid;
+        const int t0 = from > ubase ? static_cast<int>((from - ubase + c - 1) / c) : 0;
+        const int t1 = static_cast<int>(min(static_cast<long long>(T), (to - ubase + c - 1) / c));
+        if (t0 >= t1) continue;
+        if (dual) {
+            f(unit + i, row / kGroupRows, row % kGroupRows);
+        } else {
+            f(unit + i, 0, row);
+            f(unit + i, 1, row);
         }
     }
-    for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-    bad = __any_sync(0xffffffffu, bad);
-    if (bad && lane == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
-    for (int i = 0; i < D / 32; ++i) {
-        const float o = bad ? NAN : l > 0.0f ? acc[i] / l : l == 0.0f ? 0.0f : NAN;
-        a.out[row * D + lane + 32 * i] = __float2bfloat16(o);
+}
+
+constexpr int kJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ KernelArgs ka) {
+    constexpr int kV = D / 16;  // float4 a thread: its warp's quarter of a row
+    const AttnArgs &a = ka.a;
+    const Plan &p = ka.p;
+    const int chunks = ceil_div(p.R, 32);
+    const int chunk = blockIdx.x % chunks, bh = blockIdx.x / chunks, b = bh / p.Hkv, h = bh % p.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = chunk * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (r >= p.R) return;
+    const long long total = p.base[p.B];
+    const int len = p.lens[b];
+    const bool bad = len < 0 || len > (p.width << p.page_shift);
+    const Span s = span_of(p, b);
+    float M = kNegInf, L = 0.0f;
+    float4 acc[kV] = {};
+    auto both = [&](auto f) {
+        if (p.sT > 0) {
+            const long long g = static_cast<long long>(b) * p.N * p.G + r;
+            const int u = static_cast<int>(g / (2 * kGroupRows)), rows = min(p.sR - u * 2 * kGroupRows, 2 * kGroupRows);
+            each_part(p, total, static_cast<long long>(h) * p.srt * p.sT + u * 2ll * p.sT, p.sT, h * p.sru + u, rows,
+                      static_cast<int>(g % (2 * kGroupRows)), [&](int slot, int half, int row) {
+                          const long long part = slot * 2ll + half;
+                          f(p.sml + part * p.src + row, p.so + part * (D / 4) * p.src + row, p.src);
+                      });
+        }
+        const int T = s.t1 - s.t0;
+        if (T > 0) {
+            const int u = r / (2 * kGroupRows), rows = min(p.R - u * 2 * kGroupRows, 2 * kGroupRows);
+            each_part(p, total, p.base[b] + static_cast<long long>(h) * p.rt * T + u * 2ll * T, T, bh * p.ru + u, rows,
+                      r % (2 * kGroupRows), [&](int slot, int half, int row) {
+                          const long long part = slot * 2ll + half;
+                          f(p.ml + part * p.rc + row, p.o + part * (D / 4) * p.rc + row, p.rc);
+                      });
+        }
+    };
+    both([&](const float2 *ml, const float4 *, int) { M = fmaxf(M, ml->x); });
+    both([&](const float2 *ml, const float4 *o, int rc) {
+        const float2 x = *ml;
+        if (isnan(x.y)) L = NAN;
+        if (x.x == kNegInf) return;
+        const float f = ex2(x.x - M);
+        L = fmaf(f, x.y, L);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+            const float4 y = o[(warp * kV + k) * rc];
+            acc[k].x = fmaf(f, y.x, acc[k].x);
+            acc[k].y = fmaf(f, y.y, acc[k].y);
+            acc[k].z = fmaf(f, y.z, acc[k].z);
+            acc[k].w = fmaf(f, y.w, acc[k].w);
+        }
+    });
+    if (bad) {
+        L = NAN;
+        if (lane == 0 && warp == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
     }
-    if (a.lse && lane == 0)
-        a.lse[row] = bad ? NAN : m == kNegInf && l == 0.0f ? kNegInf : (m + log2f(l)) / kLog2e;
+    const int tok = b * p.N + r / p.G, head = h * p.G + r % p.G;
+    const long long row = static_cast<long long>(tok) * a.Hq + head;
+    // Nothing seen: L = 0 and every accumulator 0.
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint4 *out = reinterpret_cast<uint4 *>(a.out + row * D + warp * kV * 4);
+#pragma unroll
+    for (int k = 0; k < kV; k += 2) {
+        uint4 w;
+        w.x = bf16_pair(acc[k].x * inv, acc[k].y * inv);
+        w.y = bf16_pair(acc[k].z * inv, acc[k].w * inv);
+        w.z = bf16_pair(acc[k + 1].x * inv, acc[k + 1].y * inv);
+        w.w = bf16_pair(acc[k + 1].z * inv, acc[k + 1].w * inv);
+        out[k / 2] = w;
+    }
+    if (a.lse && warp == 0) a.lse[row] = L == 0.0f ? kNegInf : (M + log2f(L)) / kLog2e;
+}
+
+// ------------------------------------------------------------------ host
+
+int round8(int n) { return (n + 7) / 8 * 8; }
+
+// Fills the plan's sizes and carves its arrays; returns the bytes needed.
+size_t carve_plan(Plan *p, int D, char *work) {
+    p->R = p->N * p->G;
+    p->rt = ceil_div(p->R, kGroupRows);
+    p->ru = ceil_div(p->R, 2 * kGroupRows);
+    p->sR = p->B * p->R;
+    p->srt = ceil_div(p->sR, kGroupRows);
+    p->sru = ceil_div(p->sR, 2 * kGroupRows);
+    p->rc = min(kGroupRows, round8(p->R));
+    p->src = min(kGroupRows, round8(p->sR));
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = (off + bytes + 255) / 256 * 256;
+        return work + at;
+    };
+    const size_t slots = static_cast<size_t>(p->B) * p->Hkv * p->ru + kMaxGrid;
+    const size_t sslots = static_cast<size_t>(p->Hkv) * p->sru + kMaxGrid;
+    p->base = reinterpret_cast<long long *>(take((p->B + 1) * sizeof(long long)));
+    p->ml = reinterpret_cast<float2 *>(take(slots * 2 * p->rc * sizeof(float2)));
+    p->o = reinterpret_cast<float4 *>(take(slots * 2 * p->rc * D * sizeof(float)));
+    p->sml = reinterpret_cast<float2 *>(take(sslots * 2 * p->src * sizeof(float2)));
+    p->so = reinterpret_cast<float4 *>(take(sslots * 2 * p->src * D * sizeof(float)));
+    return off;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// The cache as [num_pages * Hkv][page][D]; a box is one page's head, in
+// columns of one shared-memory row.
+bool make_map(CUtensorMap *map, void *data, const CacheView &c) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t esz = c.e4m3 ? 1 : 2, page = 1ull << c.page_shift, D = c.D;
+    const cuuint64_t dims[3] = {D, page, static_cast<cuuint64_t>(c.num_pages) * c.Hkv};
+    const cuuint64_t strides[2] = {D * esz, D * esz * page};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.e4m3 ? D : 64), static_cast<cuuint32_t>(page), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return fn(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, data, dims, strides,
+              box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              c.e4m3 && c.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E4M3, bool EXTRA>
+int launch_shape(KernelArgs &ka, cudaStream_t st) {
+    using S = Shape<D, E4M3>;
+    constexpr int kMaxDev = 64;
+    static int done[kMaxDev];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    auto kernel = attn_kernel<D, E4M3, EXTRA>;
+    if (!__atomic_load_n(&done[dev], __ATOMIC_RELAXED)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+            return SPEC_ERR_CUDA;
+        __atomic_store_n(&done[dev], 1, __ATOMIC_RELAXED);
+    }
+    CUtensorMap kmap, vmap;
+    if (!make_map(&kmap, ka.a.c.k, ka.a.c) || !make_map(&vmap, ka.a.c.v, ka.a.c)) return SPEC_ERR_CUDA;
+    Plan &p = ka.p;
+    p.grid = min(sms, kMaxGrid);
+    // One query tile a group where some unit has over 128 rows.
+    ka.q_tiles = p.R > kGroupRows || (p.sT > 0 && p.sR > kGroupRows) ? 2 : 1;
+    ka.slots = S::slots(ka.q_tiles);
+    kernel<<<p.grid, kAttnThreads, S::bytes(ka.q_tiles), st>>>(ka, kmap, vmap);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * ceil_div(p.R, 32)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, ka) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace
 
-size_t attn_work_bytes(int, int, int, int, int) { return 0; }
+size_t attn_work_bytes(int B, int N, int Hq, int Hkv, int D) {
+    Plan p = {};
+    p.B = B;
+    p.N = N;
+    p.G = Hq / Hkv;
+    p.Hkv = Hkv;
+    return carve_plan(&p, D, nullptr);
+}
 
 int launch_attn(const AttnArgs &a, cudaStream_t st) {
-    const long long rows = static_cast<long long>(a.B) * a.N * a.Hq;
-    const unsigned grid = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-    auto kernel = a.c.D == 128 ? (a.c.e4m3 ? attn_kernel<128, true> : attn_kernel<128, false>)
-                               : (a.c.e4m3 ? attn_kernel<64, true> : attn_kernel<64, false>);
-    kernel<<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    KernelArgs ka = {};
+    ka.a = a;
+    Plan &p = ka.p;
+    p.B = a.B;
+    p.N = a.N;
+    p.G = a.G;
+    p.Hkv = a.c.Hkv;
+    p.width = a.width;
+    p.page_shift = a.c.page_shift;
+    p.Ls = a.shared_len;
+    p.lens = a.lens;
+    p.pos = a.pos;
+    p.window = a.window;
+    carve_plan(&p, a.c.D, a.work);
+    p.sT = (a.shared_len + kTile - 1) / kTile;
+    const bool extra = a.cap > 0.0f || a.slopes, wide = a.c.D == 128;
+    if (a.c.e4m3)
+        return extra ? (wide ? launch_shape<128, true, true>(ka, st) : launch_shape<64, true, true>(ka, st))
+                     : (wide ? launch_shape<128, true, false>(ka, st) : launch_shape<64, true, false>(ka, st));
+    return extra ? (wide ? launch_shape<128, false, true>(ka, st) : launch_shape<64, false, true>(ka, st))
+                 : (wide ? launch_shape<128, false, false>(ka, st) : launch_shape<64, false, false>(ka, st));
 }
 
 }  // namespace specv
