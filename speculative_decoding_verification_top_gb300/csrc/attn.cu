@@ -61,12 +61,13 @@ struct Plan {
     int sR, srt, sru, sT; // the same for the prefix (rows of all sequences), and its tiles
     int sT0;              // first tile of the prefix (0: windows do not trim it)
     int rc, src;          // rows a partial result holds (own, shared)
+    int parts, sparts;    // partial results a slot: 2 where units pass 128 rows
     int grid;
     const int32_t *lens, *pos;
     int window;
     long long *base;      // [B + 1] first cost of each sequence's units; the total
-    float4 *o, *so;       // [slots, 2, D / 4, rc] partial O
-    float2 *ml, *sml;     // [slots, 2, rc] partial (m, l)
+    float4 *o, *so;       // [slots, parts, D / 4, rc] partial O
+    float2 *ml, *sml;     // [slots, parts, rc] partial (m, l)
 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -180,7 +181,7 @@ struct Walk {
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots];
     unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
-    unsigned long long q_full, o_full, s_full[2], p_full[2], drained;
+    unsigned long long q_full, o_full, s_full[2], p_full[2], fold, drained;
 };
 
 struct Shared {
@@ -188,6 +189,7 @@ struct Shared {
     long long scan[kAttnThreads / 32 + 1];
     long long total, from, to, base0;
     int b0;
+    float2 ml[8][32];  // per softmax warp and lane: (m, l), for the fold
     uint32_t tmem;
     int dead;          // a wait ran out: everyone leaves
     int fail[16];      // per segment (mod 16): a page id out of range
@@ -250,6 +252,26 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// The exponent e of a query row's e4m3 form: max |q| <= 448 * 2^e, from the
+// bf16 bits of max |q|.
+__device__ __forceinline__ int query_exponent(uint32_t top) {
+    const int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+    return max(-120, min(120, e));
+}
+
+template <int D>
+__device__ __forceinline__ float query_factor(const __nv_bfloat16 *q) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 u = q ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
+    }
+    return exp2i(query_exponent(top));
+}
+
 // Query row -> the group's tile in shared memory.  e4m3: returns the row's
 // factor 2^e (see the top of the file).
 template <int D, bool E4M3>
@@ -279,9 +301,7 @@ __device__ __forceinline__ float stage_query(const __nv_bfloat16 *q, uint8_t *ti
             top = max(top, w[k] >> 16 & 0x7fffu);
         }
     }
-    // top: bf16 bits of max |q|.  e as in the cache: max |q| <= 448 * 2^e.
-    int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-    e = max(-120, min(120, e));
+    const int e = query_exponent(top);
     const float f = exp2i(-e);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
@@ -343,6 +363,210 @@ __device__ __forceinline__ bool clean_values(uint8_t *tile, int row, bool held) 
     return odd;
 }
 
+// Growth of t over the reference maximum that is let stand: a weight stays
+// under 2^8 (bf16), or 2^5 * 2^3.75 < 448 (e4m3, whose weights are scaled by
+// 2^5 so that small ones keep their second term).
+constexpr float kSlackBf16 = 8.0f, kSlackE4M3 = 3.75f, kLiftE4M3 = 5.0f;
+
+// What a softmax thread holds of its row.
+struct Row {
+    int b, n, first, pos_i;  // sequence, new token, own position of token 0, position index
+    bool has;
+    float rs, slope;         // score factor (the log2 e and the query's own in it), slope * log2 e
+    float m, l;              // reference maximum and sum
+};
+
+// t of 32 columns from column `col` of a tile, from the raw products v in place.
+template <bool E4M3, bool EXTRA>
+__device__ __forceinline__ float scores32(const AttnArgs &a, const Segment &g, const Row &x, int j0, int col,
+                                          bool whole, const float *fa, float (&v)[32]) {
+    uint32_t seen = 0xffffffffu;
+    if (!whole) {
+        seen = 0;
+        for (int k = 0; k < 32; ++k) {
+            const int j = j0 + col + k;
+            int pj;
+            const bool y = g.shared ? j < g.len && (a.window == 0 || static_cast<long long>(x.pos_i) - j < a.window)
+                                    : sees(a, x.b, x.n, x.pos_i, x.first, g.len, j, &pj);
+            seen |= (y && x.has ? 1u : 0u) << k;
+        }
+    }
+    const float far0 =
+        EXTRA ? static_cast<float>((g.shared ? 0 : a.shared_len) + j0 + col - x.pos_i) : 0.0f;
+    const float capl = a.cap * kLog2e;
+    float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        float4 k4 = {}, b4 = {};
+        if (E4M3) {
+            k4 = *reinterpret_cast<const float4 *>(fa + col + c);
+            b4 = *reinterpret_cast<const float4 *>(fa + kTile + col + c);
+        }
+        const float fk[4] = {k4.x, k4.y, k4.z, k4.w}, fb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float y = v[c + k];
+            if (E4M3) y *= fk[k];
+            if (EXTRA && a.cap > 0.0f) {
+                // cap tanh(y) log2 e, tanh(y) = 1 - 2 / (1 + e^2y)
+                const float e = ex2(y * x.rs * (2.0f * kLog2e));
+                y = capl - __fdividef(2.0f * capl, 1.0f + e);
+            } else if (!E4M3 || EXTRA) {
+                y *= x.rs;
+            }
+            if (EXTRA) {
+                float far = far0 + static_cast<float>(c + k);
+                if (!whole && !g.shared && a.pos) {
+                    const int node = j0 + col + c + k - x.first;
+                    if (node >= 0 && node < a.N)
+                        far = static_cast<float>(a.pos[static_cast<long long>(x.b) * a.N + node] - x.pos_i);
+                }
+                y = fmaf(x.slope, far, y);
+                if (E4M3) y += fb[k];
+            } else if (E4M3) {
+                y = fmaf(y, x.rs, fb[k]);
+            }
+            if (!whole && !(seen >> (c + k) & 1u)) y = kNegInf;
+            v[c + k] = y;
+            top[k & 1] = fmaxf(top[k & 1], y);
+        }
+    }
+    return fmaxf(top[0], top[1]);
+}
+
+// Weights 2^(t - ref) of 32 columns into TMEM as the product's operand: 16
+// columns of bf16 pairs, or 8 of first and 8 of second e4m3 terms.
+template <bool E4M3>
+__device__ __forceinline__ float weights32(uint32_t dst, float ref, const float *fc, const float (&t)[32]) {
+    float sum[4] = {};
+    uint32_t pk[16];
+    if (E4M3) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(fc + c);
+            const float x0 = ex2(t[c] - ref), x1 = ex2(t[c + 1] - ref);
+            const float x2 = ex2(t[c + 2] - ref), x3 = ex2(t[c + 3] - ref);
+            sum[0] = fmaf(x0, f4.x, sum[0]);
+            sum[1] = fmaf(x1, f4.y, sum[1]);
+            sum[2] = fmaf(x2, f4.z, sum[2]);
+            sum[3] = fmaf(x3, f4.w, sum[3]);
+            const uint32_t u = e4m3_pair(x0, x1), v = e4m3_pair(x2, x3);
+            const float2 y = e4m3_values(u), z = e4m3_values(v);
+            pk[c / 4] = u | v << 16;
+            pk[8 + c / 4] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const float x0 = ex2(t[c] - ref), x1 = ex2(t[c + 1] - ref);
+            sum[c & 2] += x0;
+            sum[(c & 2) + 1] += x1;
+            pk[c / 2] = bf16_pair(x0, x1);
+        }
+    }
+    tmem_store16(dst, pk);
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Moves the row's reference maximum up to `top` where that is needed,
+// rescaling the sum and, if there is one, the accumulator in TMEM.
+template <int D, bool E4M3>
+__device__ __forceinline__ void grow(Row &x, float top, bool wrote, uint32_t ot) {
+    const bool up = top > x.m + (E4M3 ? kSlackE4M3 : kSlackBf16);
+    if (!__any_sync(0xffffffffu, up)) return;
+    const float keep = up ? ex2(x.m - top) : 1.0f;
+    if (up) x.m = top;
+    x.l *= keep;
+    if (!wrote) return;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_load32(ot + c, o);
+        tmem_load_wait();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= keep;
+        tmem_store32(ot + c, reinterpret_cast<const uint32_t *>(o));
+    }
+}
+
+// One tile of one row: this copy's NC chunks of 32 columns; the other
+// copies' columns get weight zero.
+template <int D, bool E4M3, bool EXTRA, int NC>
+__device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g, Row &x, int j0, bool whole,
+                                             bool wrote, int copy, uint32_t st, uint32_t ot, const float *fa) {
+    if constexpr (NC < 4) {
+        float t[NC][32], top = kNegInf;
+        const int c0 = copy * NC;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) tmem_load32(st + (c0 + c) * 32, t[c]);
+        tmem_load_wait();
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            top = fmaxf(top, scores32<E4M3, EXTRA>(a, g, x, j0, (c0 + c) * 32, whole, fa, t[c]));
+        grow<D, E4M3>(x, top, wrote, ot);
+        const float ref = x.m == kNegInf ? 0.0f : x.m - (E4M3 ? kLiftE4M3 : 0.0f);
+        const uint32_t zero[16] = {};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (c < c0 || c >= c0 + NC) tmem_store16(st + c * 16, zero);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            x.l += weights32<E4M3>(st + (c0 + c) * 16, ref, fa + 2 * kTile + (c0 + c) * 32, t[c]);
+    } else {
+        // Twice over the tile, so that 32 values are held at a time: t back
+        // into TMEM with the maximum, then the weights.
+        float top = kNegInf;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float t[32];
+            tmem_load32(st + c * 32, t);
+            tmem_load_wait();
+            top = fmaxf(top, scores32<E4M3, EXTRA>(a, g, x, j0, c * 32, whole, fa, t));
+            tmem_store32(st + c * 32, reinterpret_cast<const uint32_t *>(t));
+        }
+        grow<D, E4M3>(x, top, wrote, ot);
+        tmem_store_wait();
+        const float ref = x.m == kNegInf ? 0.0f : x.m - (E4M3 ? kLiftE4M3 : 0.0f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float t[32];
+            tmem_load32(st + c * 32, t);
+            tmem_load_wait();
+            x.l += weights32<E4M3>(st + c * 16, ref, fa + 2 * kTile + c * 32, t);
+        }
+    }
+    tmem_store_wait();
+}
+
+// Adds to `cols` output columns from `col` on, at dst[(k / 4) s4 + (k % 4) s1],
+// what the products left out: values that are not finite, of the positions
+// the row sees in its group's tiles.
+template <int D, bool E4M3>
+__device__ __noinline__ void add_odd_values(const AttnArgs &a, const Segment g, const Row x, int w, int col, int cols,
+                                            float *dst, int s4, int s1) {
+    const int32_t *table = g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
+    for (int t = g.t0; t < g.t1; ++t) {
+        if (!g.dual && ((t - g.t0) & 1) != w) continue;
+        for (int j = t * kTile; j < min(g.len, (t + 1) * kTile); ++j) {
+            int pj, slot;
+            if (g.shared ? a.window > 0 && static_cast<long long>(x.pos_i) - j >= a.window
+                         : !sees(a, x.b, x.n, x.pos_i, x.first, g.len, j, &pj))
+                continue;
+            const int page = page_of(a.c, table, INT_MAX, j, &slot);
+            if (page < 0) continue;
+            const long long at = cache_row(a.c, page, g.h, slot) * D + col;
+            for (int k = 0; k < cols; ++k) {
+                float y;
+                if (E4M3)
+                    y = (a.c.v[at + k] & 0x7f) == 0x7f ? NAN : 0.0f;
+                else
+                    y = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.c.v)[at + k]);
+                if (!isfinite(y)) dst[(k / 4) * s4 + (k % 4) * s1] += y;
+            }
+        }
+    }
+}
+
 template <int D, bool E4M3, bool EXTRA>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ KernelArgs ka, const __grid_constant__ CUtensorMap kmap,
@@ -386,6 +610,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         bar_init(smem_addr(&bar.q_full), 8);
         bar_init(smem_addr(&bar.o_full), 1);
+        bar_init(smem_addr(&bar.fold), 8);
         bar_init(smem_addr(&bar.drained), 1);
         for (int w = 0; w < 2; ++w) {
             bar_init(smem_addr(&bar.s_full[w]), 1);
@@ -522,7 +747,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int j = i % 4;
-                        mma_ts<true>(d, pt + (i / 4) * 32 + j * 8,
+                        mma_ts<true>(d, pt + j * 16 + (i / 4) * 8,
                                      matrix_desc<S::kRow>(v + j * 32 * S::kRow, S::kMat), kPv, !first || i > 0);
                     }
                 } else {
@@ -615,53 +840,54 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
     } else {
         // ---- softmax groups
-        const int w = warp >> 2, row = tid & 127;
-        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's TMEM lanes
+        const int w = warp >> 2, quad = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // this warp's TMEM lanes
         const uint32_t st = tmem + lanes + w * kTile, ot = tmem + lanes + 2 * kTile + w * D;
-        // Growth of t over the reference maximum that is let stand: a weight
-        // stays under 2^8 (bf16), or 2^5 * 2^3.75 < 448 (e4m3, whose weights
-        // are scaled by 2^5 so that small ones keep their second term).
-        constexpr float kSlack = E4M3 ? 3.75f : 8.0f, kLift = E4M3 ? 5.0f : 0.0f;
         const bool neg = a.scale < 0.0f;
         const float mul = (a.cap > 0.0f ? fabsf(a.scale) / a.cap : fabsf(a.scale) * kLog2e);
-        const float capl = a.cap * kLog2e;
-        uint32_t segs = 0, sn = 0, n_ring = 0, n_scale = 0;
+        uint32_t segs = 0, sn = 0, n_ring = 0, n_scale = 0, fn = 0;
         bool live = true;
+        // All eight softmax warps meet (bounded, unlike a hardware barrier).
+        auto meet = [&] {
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&bar.fold));
+            live = bar_wait(smem_addr(&bar.fold), fn++ & 1, dead);
+            live = __all_sync(0xffffffffu, live);
+            return live;
+        };
         while (live && walk.next(&g)) {
             const int T = g.t1 - g.t0, row0 = g.row0 + (g.dual ? w * kGroupRows : 0);
             const int rows = min(kGroupRows, g.rows - (g.dual ? w * kGroupRows : 0));
-            const bool has = row < rows, active = (warp & 3) * 32 < rows;
+            // Few rows are repeated over the 128 lanes, and each copy takes its
+            // share of a tile's columns.
+            const int copies = g.dual || rows > 64 ? 1 : rows > 32 ? 2 : 4, span = kGroupRows / copies;
+            const int copy = quad / (4 / copies), row = (quad * 32 + lane) & (span - 1);
+            const bool has = row < rows, active = (quad * 32 & (span - 1)) < rows;
             const int r = row0 + row, tok_in = has ? r / a.G : 0, head = g.h * a.G + (has ? r % a.G : 0);
             const long long tok = g.shared ? tok_in : static_cast<long long>(g.b) * a.N + tok_in;
             const int b = g.shared ? (has ? static_cast<int>(tok / a.N) : 0) : g.b;
             const int n = has ? static_cast<int>(tok - static_cast<long long>(b) * a.N) : 0;
+            const __nv_bfloat16 *q = has ? a.q + tok * a.q_stride + static_cast<long long>(head) * D : nullptr;
             float qf = 1.0f;
-            if (g.dual || w == 0) {
-                const __nv_bfloat16 *q = has ? a.q + tok * a.q_stride + static_cast<long long>(head) * D : nullptr;
-                qf = stage_query<D, E4M3>(q, qt + (g.dual ? w : 0) * S::kQ, row, neg);
-            } else if (E4M3 && has) {
-                // the other group staged this row: its factor again
-                const __nv_bfloat16 *q = a.q + tok * a.q_stride + static_cast<long long>(head) * D;
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(q) + i);
-                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top = max(top, max(x[k] & 0x7fffu, x[k] >> 16 & 0x7fffu));
-                }
-                const int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-                qf = exp2i(max(-120, min(120, e)));
-            }
+            if (g.dual || w == 0)
+                qf = stage_query<D, E4M3>(q, qt + (g.dual ? w : 0) * S::kQ, quad * 32 + lane, neg);
+            else if (E4M3)
+                qf = query_factor<D>(q);  // the other group stages this row
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
+            Row x;
+            x.b = b;
+            x.n = n;
             const int seq_len = g.shared ? (has ? a.lens[b] : 0) : g.len;
-            const int first = seq_len - a.N;
-            const int pos_i = !has ? 0 : a.pos ? a.pos[tok] : a.shared_len + first + n;
-            const float slope = EXTRA && a.slopes && has ? a.slopes[head] * kLog2e : 0.0f;
-            const float rs = mul * qf;
-            const int ctx = g.shared ? g.len : max(0, first);  // positions every row sees (no window)
+            x.first = seq_len - a.N;
+            x.pos_i = !has ? 0 : a.pos ? a.pos[tok] : a.shared_len + x.first + n;
+            x.has = has;
+            x.rs = mul * qf;
+            x.slope = EXTRA && a.slopes && has ? a.slopes[head] * kLog2e : 0.0f;
+            x.m = kNegInf;
+            x.l = 0.0f;
+            const int ctx = g.shared ? g.len : max(0, x.first);  // positions every row sees (no window)
             // The unit's largest position index: every warp finds it from all the
             // unit's rows, so that both groups treat a tile alike.
             int far_most = INT_MIN;
@@ -673,7 +899,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 far_most = __reduce_max_sync(0xffffffffu, far_most);
             }
-            float m = kNegInf, l = 0.0f;
             bool wrote = false;
             for (int t = g.t0; t < g.t1; ++t) {
                 const int idx = t - g.t0;
@@ -690,130 +915,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     live = live && bar_wait(smem_addr(&bar.scale_full[s]), ((n_scale + idx) / kScaleRing) & 1, dead);
                     fa = scales + s * 3 * kTile;
                 }
-                if (!whole) {
-                    // the tile's values: slot index as the loads number them
-                    const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
-                    live = live && bar_wait(smem_addr(&bar.full[vi % ka.slots]), (vi / ka.slots) & 1, dead);
-                }
+                // the tile's values: slot index as the loads number them
+                const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
+                if (!whole) live = live && bar_wait(smem_addr(&bar.full[vi % ka.slots]), (vi / ka.slots) & 1, dead);
                 live = __all_sync(0xffffffffu, live);
                 if (!live) break;
                 fence_after_sync();
                 if (active) {
-                    float t_[kTile];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_load32(st + c * 32, t_ + c * 32);
-                    tmem_load_wait();
-                    float top = kNegInf;
-                    const float far0 = EXTRA ? static_cast<float>((g.shared ? 0 : a.shared_len) + j0 - pos_i) : 0.0f;
-                    uint32_t seen[4];
-                    if (!whole) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            seen[c] = 0;
-                            for (int k = 0; k < 32; ++k) {
-                                const int j = j0 + c * 32 + k;
-                                int pj;
-                                const bool y = g.shared ? j < g.len && (a.window == 0 || static_cast<long long>(pos_i) - j < a.window)
-                                                        : sees(a, b, n, pos_i, first, g.len, j, &pj);
-                                seen[c] |= (y && has ? 1u : 0u) << k;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 4) {
-                        float4 ka4, kb4;
-                        if (E4M3) {
-                            ka4 = *reinterpret_cast<const float4 *>(fa + c);
-                            kb4 = *reinterpret_cast<const float4 *>(fa + kTile + c);
-                        }
-                        const float fk[4] = {ka4.x, ka4.y, ka4.z, ka4.w}, fb[4] = {kb4.x, kb4.y, kb4.z, kb4.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float x = t_[c + k];
-                            if (E4M3) x *= fk[k];
-                            if (EXTRA && a.cap > 0.0f) {
-                                // cap tanh(x) log2 e, tanh(x) = 1 - 2 / (1 + e^2x)
-                                const float e = ex2(x * rs * (2.0f * kLog2e));
-                                x = capl - __fdividef(2.0f * capl, 1.0f + e);
-                            } else {
-                                x *= rs;
-                            }
-                            if (EXTRA) {
-                                float far = far0 + static_cast<float>(c + k);
-                                if (!whole && !g.shared && a.pos) {
-                                    const int node = j0 + c + k - first;
-                                    if (node >= 0 && node < a.N)
-                                        far = static_cast<float>(a.pos[static_cast<long long>(b) * a.N + node] - pos_i);
-                                }
-                                x = fmaf(slope, far, x);
-                            }
-                            if (E4M3) x += fb[k];
-                            if (!whole && !(seen[(c + k) / 32] >> ((c + k) % 32) & 1u)) x = kNegInf;
-                            t_[c + k] = x;
-                            top = fmaxf(top, x);
-                        }
-                    }
-                    // Grow the reference maximum where a row needs it.
-                    const bool grow = top > m + kSlack;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float mn = grow ? top : m;
-                        const float keep = m == mn ? 1.0f : ex2(m - mn);
-                        m = mn;
-                        l *= keep;
-                        if (wrote) {
-#pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                tmem_load32(ot + c, o);
-                                tmem_load_wait();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= keep;
-                                tmem_store32(ot + c, reinterpret_cast<const uint32_t *>(o));
-                            }
-                        }
-                    }
-                    const float ref = m == kNegInf ? 0.0f : m - kLift;
-                    float sum[4] = {};
-                    if (E4M3) {
-                        uint32_t hi[kTile / 4], lo[kTile / 4];
-#pragma unroll
-                        for (int c = 0; c < kTile; c += 4) {
-                            const float4 fc = *reinterpret_cast<const float4 *>(fa + 2 * kTile + c);
-                            const float x0 = ex2(t_[c] - ref), x1 = ex2(t_[c + 1] - ref);
-                            const float x2 = ex2(t_[c + 2] - ref), x3 = ex2(t_[c + 3] - ref);
-                            sum[0] = fmaf(x0, fc.x, sum[0]);
-                            sum[1] = fmaf(x1, fc.y, sum[1]);
-                            sum[2] = fmaf(x2, fc.z, sum[2]);
-                            sum[3] = fmaf(x3, fc.w, sum[3]);
-                            const uint32_t u = e4m3_pair(x0, x1), v = e4m3_pair(x2, x3);
-                            const float2 y = e4m3_values(u), z = e4m3_values(v);
-                            hi[c / 4] = u | v << 16;
-                            lo[c / 4] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
-                        }
-                        tmem_store32(st, hi);
-                        tmem_store32(st + 32, lo);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kTile; c += 64) {
-                            uint32_t pk[32];
-#pragma unroll
-                            for (int k = 0; k < 64; k += 2) {
-                                const float x0 = ex2(t_[c + k] - ref), x1 = ex2(t_[c + k + 1] - ref);
-                                sum[k & 2] += x0;
-                                sum[(k & 2) + 1] += x1;
-                                pk[k / 2] = bf16_pair(x0, x1);
-                            }
-                            tmem_store32(st + c / 2, pk);
-                        }
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_store_wait();
+                    if (copies == 4)
+                        softmax_tile<D, E4M3, EXTRA, 1>(a, g, x, j0, whole, wrote, copy, st, ot, fa);
+                    else if (copies == 2)
+                        softmax_tile<D, E4M3, EXTRA, 2>(a, g, x, j0, whole, wrote, copy, st, ot, fa);
+                    else
+                        softmax_tile<D, E4M3, EXTRA, 4>(a, g, x, j0, whole, wrote, 0, st, ot, fa);
                 }
                 wrote = true;
                 if (!whole) {
-                    const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
-                    if (clean_values<D, E4M3>(ring + vi % ka.slots * S::kSlot, row, j0 + row < g.len))
-                        sh.odd[segs & 15] = 1;
+                    const int at = quad * 32 + lane;
+                    if (clean_values<D, E4M3>(ring + vi % ka.slots * S::kSlot, at, j0 + at < g.len)) sh.odd[segs & 15] = 1;
                     fence_async_proxy();
                 }
                 fence_before_sync();
@@ -828,50 +947,78 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
             fence_after_sync();
-            // ---- the partial result
+            // ---- the segment's partial result
             const int rc = g.shared ? p.src : p.rc;
-            const long long part = static_cast<long long>(g.slot) * 2 + w;
+            const long long part = static_cast<long long>(g.slot) * (g.shared ? p.sparts : p.parts) + (g.dual ? w : 0);
             float2 *ml = (g.shared ? p.sml : p.ml) + part * rc;
             float4 *o = (g.shared ? p.so : p.o) + part * (D / 4) * rc;
             const bool failed = reinterpret_cast<volatile int *>(sh.fail)[segs & 15] != 0;
             const bool odd = reinterpret_cast<volatile int *>(sh.odd)[segs & 15] != 0;
-            if (has) ml[row] = make_float2(m == kNegInf ? kNegInf : m - kLift, failed ? NAN : l);
-            if (active && wrote) {
+            const bool some = active && wrote;
+            const float lift = x.m == kNegInf ? kNegInf : x.m - (E4M3 ? kLiftE4M3 : 0.0f);
+            if (g.dual) {
+                if (has) ml[row] = make_float2(lift, failed ? NAN : x.l);
+                if (some) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float v[32];
+                        tmem_load32(ot + c, v);
+                        tmem_load_wait();
+                        if (has) {
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float x[32];
-                    tmem_load32(ot + c, x);
-                    tmem_load_wait();
-                    if (odd && has) {
-                        // seen values that are not finite, left out of the products
-                        for (int t = g.t0; t < g.t1; ++t) {
-                            if (!g.dual && ((t - g.t0) & 1) != w) continue;
-                            for (int j = t * kTile; j < min(g.len, (t + 1) * kTile); ++j) {
-                                int pj, slot;
-                                if (g.shared ? a.window > 0 && static_cast<long long>(pos_i) - j >= a.window
-                                             : !sees(a, b, n, pos_i, first, g.len, j, &pj))
-                                    continue;
-                                const int32_t *table = g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
-                                const int page = page_of(a.c, table, INT_MAX, j, &slot);
-                                if (page < 0) continue;
-                                const long long at = cache_row(a.c, page, g.h, slot) * D + c;
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    float v;
-                                    if (E4M3)
-                                        v = (a.c.v[at + k] & 0x7f) == 0x7f ? NAN : 0.0f;
-                                    else
-                                        v = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.c.v)[at + k]);
-                                    if (!isfinite(v)) x[k] += v;
-                                }
-                            }
+                            for (int k = 0; k < 8; ++k)
+                                o[(c / 4 + k) * rc + row] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                            if (odd)
+                                add_odd_values<D, E4M3>(a, g, x, w, c, 32, reinterpret_cast<float *>(o + (c / 4) * rc + row),
+                                                        4 * rc, 1);
                         }
                     }
-                    if (has) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            o[(c / 4 + k) * rc + row] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                }
+            } else {
+                // Fold the copies and the two groups into one: every warp scales its
+                // rows to the common maximum and hands them over through the query
+                // tile's memory (its products are done).
+                constexpr int kCols = S::kQ / (256 * 4) < 32 ? 16 : 32;
+                float *buf = reinterpret_cast<float *>(qt);
+                sh.ml[warp][lane] = make_float2(has && wrote ? lift : kNegInf, has && wrote ? x.l : 0.0f);
+                if (!meet()) break;
+                const int per = 4 / copies, in = quad % per;  // warps a copy, this one's place
+                float M = kNegInf, L = 0.0f;
+                for (int i = 0; i < 2 * copies; ++i)
+                    M = fmaxf(M, sh.ml[(i / copies) * 4 + (i % copies) * per + in][lane].x);
+                for (int i = 0; i < 2 * copies; ++i) {
+                    const float2 y = sh.ml[(i / copies) * 4 + (i % copies) * per + in][lane];
+                    L += (y.x == kNegInf ? 0.0f : ex2(y.x - M)) * y.y;
+                }
+                const float f = some && x.m != kNegInf ? ex2(lift - M) : 0.0f;
+                if (w == 0 && copy == 0 && has) ml[row] = make_float2(M, failed ? NAN : L);
+#pragma unroll 1
+                for (int c = 0; c < D; c += kCols) {
+                    float v[kCols];
+                    if (some) {
+                        if constexpr (kCols == 32)
+                            tmem_load32(ot + c, v);
+                        else
+                            tmem_load16(ot + c, v);
+                        tmem_load_wait();
                     }
+#pragma unroll
+                    for (int k = 0; k < kCols; ++k) buf[k * 256 + warp * 32 + lane] = f > 0.0f ? v[k] * f : 0.0f;
+                    if (odd && has && f > 0.0f)
+                        add_odd_values<D, E4M3>(a, g, x, w, c, kCols, buf + warp * 32 + lane, 1024, 256);
+                    if (!meet()) break;
+                    for (int i = tid; i < span * (kCols / 4); i += 256) {
+                        const int ri = i & (span - 1), c4 = i / span;
+                        if (ri >= rows) continue;
+                        float y[4] = {};
+                        for (int k = 0; k < 2 * copies; ++k) {
+                            const int from = ((k / copies) * 4 + (k % copies) * per + ri / 32) * 32 + ri % 32;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] += buf[(4 * c4 + e) * 256 + from];
+                        }
+                        o[(c / 4 + c4) * rc + ri] = make_float4(y[0], y[1], y[2], y[3]);
+                    }
+                    if (!meet()) break;
                 }
             }
             fence_before_sync();
@@ -911,7 +1058,6 @@ __device__ __forceinline__ void each_part(const Plan &p, long long total, long l
             f(unit + i, row / kGroupRows, row % kGroupRows);
         } else {
             f(unit + i, 0, row);
-            f(unit + i, 1, row);
         }
     }
 }
@@ -940,7 +1086,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             const int u = static_cast<int>(g / (2 * kGroupRows)), rows = min(p.sR - u * 2 * kGroupRows, 2 * kGroupRows);
             each_part(p, total, static_cast<long long>(h) * p.srt * p.sT + u * 2ll * p.sT, p.sT, h * p.sru + u, rows,
                       static_cast<int>(g % (2 * kGroupRows)), [&](int slot, int half, int row) {
-                          const long long part = slot * 2ll + half;
+                          const long long part = static_cast<long long>(slot) * p.sparts + half;
                           f(p.sml + part * p.src + row, p.so + part * (D / 4) * p.src + row, p.src);
                       });
         }
@@ -949,7 +1095,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             const int u = r / (2 * kGroupRows), rows = min(p.R - u * 2 * kGroupRows, 2 * kGroupRows);
             each_part(p, total, p.base[b] + static_cast<long long>(h) * p.rt * T + u * 2ll * T, T, bh * p.ru + u, rows,
                       r % (2 * kGroupRows), [&](int slot, int half, int row) {
-                          const long long part = slot * 2ll + half;
+                          const long long part = static_cast<long long>(slot) * p.parts + half;
                           f(p.ml + part * p.rc + row, p.o + part * (D / 4) * p.rc + row, p.rc);
                       });
         }
@@ -1005,6 +1151,8 @@ size_t carve_plan(Plan *p, int D, char *work) {
     p->sru = ceil_div(p->sR, 2 * kGroupRows);
     p->rc = min(kGroupRows, round8(p->R));
     p->src = min(kGroupRows, round8(p->sR));
+    p->parts = p->R > kGroupRows ? 2 : 1;
+    p->sparts = p->sR > kGroupRows ? 2 : 1;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -1014,10 +1162,10 @@ size_t carve_plan(Plan *p, int D, char *work) {
     const size_t slots = static_cast<size_t>(p->B) * p->Hkv * p->ru + kMaxGrid;
     const size_t sslots = static_cast<size_t>(p->Hkv) * p->sru + kMaxGrid;
     p->base = reinterpret_cast<long long *>(take((p->B + 1) * sizeof(long long)));
-    p->ml = reinterpret_cast<float2 *>(take(slots * 2 * p->rc * sizeof(float2)));
-    p->o = reinterpret_cast<float4 *>(take(slots * 2 * p->rc * D * sizeof(float)));
-    p->sml = reinterpret_cast<float2 *>(take(sslots * 2 * p->src * sizeof(float2)));
-    p->so = reinterpret_cast<float4 *>(take(sslots * 2 * p->src * D * sizeof(float)));
+    p->ml = reinterpret_cast<float2 *>(take(slots * p->parts * p->rc * sizeof(float2)));
+    p->o = reinterpret_cast<float4 *>(take(slots * p->parts * p->rc * D * sizeof(float)));
+    p->sml = reinterpret_cast<float2 *>(take(sslots * p->sparts * p->src * sizeof(float2)));
+    p->so = reinterpret_cast<float4 *>(take(sslots * p->sparts * p->src * D * sizeof(float)));
     return off;
 }
 

@@ -40,35 +40,31 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
-
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
+constexpr long long kWaitCycles = 1ll << 32;  // a wait gives up after about two seconds
 
 // Waits for the phase `parity`; false when the limit ran out here or, as
-// *dead tells, elsewhere in the CTA: the caller then leaves its loops.
+// *dead tells, elsewhere in the CTA: the caller then leaves its loops.  (The
+// SM's own clock: reading the global timer costs over a microsecond.)
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
-    if (bar_try(bar, parity)) return true;
-    const unsigned long long t0 = now_ns();
-    for (int i = 1;; ++i) {
-        if (bar_try(bar, parity)) return true;
-        if ((i & 31) == 0) {
-            if (*dead) return false;
-            if (now_ns() - t0 > kWaitNs) break;
+    long long t0 = 0;
+    for (uint32_t i = 0; !bar_try(bar, parity); ++i) {
+        if ((i & 63) != 63) continue;
+        if (*dead) return false;
+        const long long t = clock64();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitCycles) {
+            *dead = 1;
+            return false;
         }
     }
-    *dead = 1;
-    return false;
+    return true;
 }
 
 // The same without the flag: true if the phase completed in time.
 __device__ __forceinline__ bool bar_drain(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = now_ns();
+    const long long t0 = clock64();
     while (!bar_try(bar, parity))
-        if (now_ns() - t0 > kWaitNs) return false;
+        if (clock64() - t0 > kWaitCycles) return false;
     return true;
 }
 
@@ -177,6 +173,24 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t *r) {
         "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
