@@ -21,6 +21,7 @@
 //                 warps 0-3, 4-7   two softmax groups, a thread per row: S
 //                             from TMEM, 2^(t - m), P back into TMEM
 //                 warp 10     the e4m3 cache's exponents, as factors
+//                 warp 11     the query tiles (two, so mostly a segment ahead)
 //               A unit of up to 128 rows alternates its tiles between the
 //               two groups, each with its own S and O (TMEM: 2 x 128 + 2 x D
 //               columns), so that one group's softmax runs under the other's
@@ -45,11 +46,11 @@ namespace {
 
 constexpr int kTile = 128;        // positions a tile
 constexpr int kGroupRows = 128;   // query rows a softmax group
-constexpr int kAttnThreads = 352;
+constexpr int kAttnThreads = 384;
 constexpr int kMaxSlots = 16;
 constexpr int kScaleRing = 4;
 constexpr int kMaxGrid = 152;
-constexpr int kSmemMax = 232448;
+constexpr int kSmemMax = 232448;  // bytes a CTA may have
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kStalled = SPEC_DATA_STALL;
 
@@ -65,7 +66,7 @@ struct Plan {
     int grid;
     const int32_t *lens, *pos;
     int window;
-    long long *base;      // [B + 1] first cost of each sequence's units; the total
+    long long *base;      // [B + 2] first cost of each sequence's units; the total; a CTA's share
     float4 *o, *so;       // [slots, parts, D / 4, rc] partial O
     float2 *ml, *sml;     // [slots, parts, rc] partial (m, l)
 };
@@ -181,7 +182,7 @@ struct Walk {
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots];
     unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
-    unsigned long long q_full, o_full, s_full[2], p_full[2], fold, drained;
+    unsigned long long q_full[2], q_empty[2], o_full, s_full[2], p_full[2], fold, drained;
 };
 
 struct Shared {
@@ -203,21 +204,16 @@ struct Shape {
     static constexpr int kMat = kTile * kRow;                // bytes of one block
     static constexpr int kSlot = kMat * kHalves;             // a key or value tile
     static constexpr int kQ = E4M3 ? 2 * kMat : kSlot;       // a group's query tile
-    static constexpr int kScale = E4M3 ? kScaleRing * 3 * kTile * 4 : 0;
-    static constexpr int kFixed = kScale + static_cast<int>((sizeof(Shared) + 1023) / 1024 * 1024);
-    static constexpr int slots(int q_tiles) {
-        const int n = (kSmemMax - 1024 - kFixed - q_tiles * kQ) / kSlot;
-        return n < kMaxSlots ? n : kMaxSlots;
-    }
-    static constexpr int bytes(int q_tiles) {
-        return 1024 + kFixed + q_tiles * kQ + slots(q_tiles) * kSlot;
-    }
+    static constexpr int kScale = E4M3 ? (kScaleRing * 3 * kTile + 2 * kGroupRows) * 4 : 0;  // and query factors
+    static constexpr int kFixed = kScale + static_cast<int>((sizeof(Shared) + 127) / 128 * 128);
+    static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ) / kSlot;
+    static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
+    static constexpr int kBytes = kFixed + 2 * kQ + kSlots * kSlot;
 };
 
 struct KernelArgs {
     AttnArgs a;
     Plan p;
-    int q_tiles, slots;
 };
 
 // Whether row (own row r of sequence b, its token's position pos_i) sees own
@@ -252,30 +248,14 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// The exponent e of a query row's e4m3 form: max |q| <= 448 * 2^e, from the
-// bf16 bits of max |q|.
-__device__ __forceinline__ int query_exponent(uint32_t top) {
-    const int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-    return max(-120, min(120, e));
-}
+// Few query rows are repeated over a group's 128 lanes.
+__device__ __forceinline__ int copies_of(bool dual, int rows) { return dual || rows > 64 ? 1 : rows > 32 ? 2 : 4; }
 
-template <int D>
-__device__ __forceinline__ float query_factor(const __nv_bfloat16 *q) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        const uint4 u = q ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
-    }
-    return exp2i(query_exponent(top));
-}
-
-// Query row -> the group's tile in shared memory.  e4m3: returns the row's
-// factor 2^e (see the top of the file).
+// Query row -> rows row, row + span, ... of the group's tile in shared memory
+// (zeros without a query), and its factor 2^e (see the top of the file).
 template <int D, bool E4M3>
-__device__ __forceinline__ float stage_query(const __nv_bfloat16 *q, uint8_t *tile, int row, bool neg) {
+__device__ __forceinline__ void stage_query(const __nv_bfloat16 *q, uint8_t *tile, int row, int span, bool neg,
+                                            float *factor) {
     using S = Shape<D, E4M3>;
     uint4 u[D / 8];
 #pragma unroll
@@ -287,21 +267,21 @@ __device__ __forceinline__ float stage_query(const __nv_bfloat16 *q, uint8_t *ti
         for (int i = 0; i < D / 8; ++i) {
             uint4 w = u[i];
             w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
-            *reinterpret_cast<uint4 *>(tile + (i / 8) * S::kMat + swizzled<S::kRow>(row, (i % 8) * 16)) = w;
+            for (int r = row; r < kGroupRows; r += span)
+                *reinterpret_cast<uint4 *>(tile + (i / 8) * S::kMat + swizzled<S::kRow>(r, (i % 8) * 16)) = w;
         }
-        return 1.0f;
+        return;
     }
-    uint32_t top = 0;
+    uint32_t top = 0;  // bf16 bits of max |q|
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            top = max(top, w[k] & 0x7fffu);
-            top = max(top, w[k] >> 16 & 0x7fffu);
-        }
+        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
     }
-    const int e = query_exponent(top);
+    // e: max |q| <= 448 * 2^e
+    int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+    e = max(-120, min(120, e));
     const float f = exp2i(-e);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
@@ -317,11 +297,13 @@ __device__ __forceinline__ float stage_query(const __nv_bfloat16 *q, uint8_t *ti
             hi[k] = p | r << 16;
             lo[k] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
         }
-        const uint32_t o = swizzled<S::kRow>(row, i * 16);
-        *reinterpret_cast<uint4 *>(tile + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(tile + S::kMat + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int r = row; r < kGroupRows; r += span) {
+            const uint32_t o = swizzled<S::kRow>(r, i * 16);
+            *reinterpret_cast<uint4 *>(tile + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(tile + S::kMat + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
     }
-    return exp2i(e);
+    for (int r = row; r < kGroupRows; r += span) factor[r] = exp2i(e);
 }
 
 // Row `row` of a value tile whose positions some rows do not see: zeros where
@@ -370,7 +352,8 @@ constexpr float kSlackBf16 = 8.0f, kSlackE4M3 = 3.75f, kLiftE4M3 = 5.0f;
 
 // What a softmax thread holds of its row.
 struct Row {
-    int b, n, first, pos_i;  // sequence, new token, own position of token 0, position index
+    int b, n, tok;           // sequence, new token, token of the batch
+    int first, pos_i;        // own position of token 0, the token's position index
     bool has;
     float rs, slope;         // score factor (the log2 e and the query's own in it), slope * log2 e
     float m, l;              // reference maximum and sum
@@ -380,15 +363,29 @@ struct Row {
 template <bool E4M3, bool EXTRA>
 __device__ __forceinline__ float scores32(const AttnArgs &a, const Segment &g, const Row &x, int j0, int col,
                                           bool whole, const float *fa, float (&v)[32]) {
+    // Columns of positions some rows do not see: a row's set depends on its
+    // token alone, so the warp finds the sets of its tokens one by one, a
+    // lane a column.
     uint32_t seen = 0xffffffffu;
+    int pos_col = 0;  // position index of this lane's column
     if (!whole) {
+        const int lane = threadIdx.x & 31, j = j0 + col + lane, c = j - x.first;
+        const bool held = j < g.len, node = !g.shared && c >= 0;
+        pos_col = (g.shared ? 0 : a.shared_len) + j;
+        if (node && held && a.pos) pos_col = a.pos[static_cast<long long>(x.b) * a.N + c];
+        uint32_t todo = __ballot_sync(0xffffffffu, x.has);
         seen = 0;
-        for (int k = 0; k < 32; ++k) {
-            const int j = j0 + col + k;
-            int pj;
-            const bool y = g.shared ? j < g.len && (a.window == 0 || static_cast<long long>(x.pos_i) - j < a.window)
-                                    : sees(a, x.b, x.n, x.pos_i, x.first, g.len, j, &pj);
-            seen |= (y && x.has ? 1u : 0u) << k;
+        while (todo) {
+            const int from = __ffs(todo) - 1;
+            const int tok = __shfl_sync(0xffffffffu, x.tok, from), n = __shfl_sync(0xffffffffu, x.n, from);
+            const int pos_i = __shfl_sync(0xffffffffu, x.pos_i, from);
+            bool y = held;
+            if (node && held) y = a.mask ? a.mask[static_cast<long long>(tok) * a.N + c] != 0 : c <= n;
+            y = y && (a.window == 0 || static_cast<long long>(pos_i) - pos_col < a.window);
+            const uint32_t word = __ballot_sync(0xffffffffu, y);
+            const bool me = x.has && x.tok == tok;
+            if (me) seen = word;
+            todo &= ~__ballot_sync(0xffffffffu, me);
         }
     }
     const float far0 =
@@ -416,11 +413,7 @@ __device__ __forceinline__ float scores32(const AttnArgs &a, const Segment &g, c
             }
             if (EXTRA) {
                 float far = far0 + static_cast<float>(c + k);
-                if (!whole && !g.shared && a.pos) {
-                    const int node = j0 + col + c + k - x.first;
-                    if (node >= 0 && node < a.N)
-                        far = static_cast<float>(a.pos[static_cast<long long>(x.b) * a.N + node] - x.pos_i);
-                }
+                if (!whole && a.pos) far = static_cast<float>(__shfl_sync(0xffffffffu, pos_col, c + k) - x.pos_i);
                 y = fmaf(x.slope, far, y);
                 if (E4M3) y += fb[k];
             } else if (E4M3) {
@@ -538,15 +531,15 @@ __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g
     tmem_store_wait();
 }
 
-// Adds to `cols` output columns from `col` on, at dst[(k / 4) s4 + (k % 4) s1],
-// what the products left out: values that are not finite, of the positions
-// the row sees in its group's tiles.
+// Adds to `cols` output columns from `col` on, at dst[(k / 4) s4 + k % 4], what
+// the products left out: values that are not finite, of the positions the row
+// sees in the segment's cleaned tiles.  (In a tile that was not cleaned they
+// are in the sum already, and adding them again changes nothing.)
 template <int D, bool E4M3>
-__device__ __noinline__ void add_odd_values(const AttnArgs &a, const Segment g, const Row x, int w, int col, int cols,
-                                            float *dst, int s4, int s1) {
+__device__ __noinline__ void add_odd_values(const AttnArgs &a, const Segment g, const Row x, int col, int cols,
+                                            float *dst, int s4) {
     const int32_t *table = g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
     for (int t = g.t0; t < g.t1; ++t) {
-        if (!g.dual && ((t - g.t0) & 1) != w) continue;
         for (int j = t * kTile; j < min(g.len, (t + 1) * kTile); ++j) {
             int pj, slot;
             if (g.shared ? a.window > 0 && static_cast<long long>(x.pos_i) - j >= a.window
@@ -561,7 +554,7 @@ __device__ __noinline__ void add_odd_values(const AttnArgs &a, const Segment g, 
                     y = (a.c.v[at + k] & 0x7f) == 0x7f ? NAN : 0.0f;
                 else
                     y = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.c.v)[at + k]);
-                if (!isfinite(y)) dst[(k / 4) * s4 + (k % 4) * s1] += y;
+                if (!isfinite(y)) dst[(k / 4) * s4 + k % 4] += y;
             }
         }
     }
@@ -572,14 +565,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ KernelArgs ka, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
     using S = Shape<D, E4M3>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const AttnArgs &a = ka.a;
     const Plan &p = ka.p;
-    uint8_t *qt = smem, *ring = qt + ka.q_tiles * S::kQ;
-    float *scales = reinterpret_cast<float *>(ring + ka.slots * S::kSlot);
+    uint8_t *qt = smem, *ring = qt + 2 * S::kQ;
+    float *scales = reinterpret_cast<float *>(ring + S::kSlots * S::kSlot);
     Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(scales) + S::kScale);
     Barriers &bar = sh.bar;
+    float *q_factor = scales + kScaleRing * 3 * kTile;  // [2][kGroupRows], e4m3
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;");
 
@@ -600,7 +593,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (lane == 31) sh.scan[warp] = incl;
     if (tid == 0) {
-        for (int i = 0; i < ka.slots; ++i) {
+        for (int i = 0; i < S::kSlots; ++i) {
             bar_init(smem_addr(&bar.full[i]), 1);
             bar_init(smem_addr(&bar.empty[i]), 1);
         }
@@ -608,11 +601,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_init(smem_addr(&bar.scale_full[i]), 1);
             bar_init(smem_addr(&bar.scale_empty[i]), 8);
         }
-        bar_init(smem_addr(&bar.q_full), 8);
         bar_init(smem_addr(&bar.o_full), 1);
         bar_init(smem_addr(&bar.fold), 8);
         bar_init(smem_addr(&bar.drained), 1);
         for (int w = 0; w < 2; ++w) {
+            bar_init(smem_addr(&bar.q_full[w]), 1);
+            bar_init(smem_addr(&bar.q_empty[w]), 9);
             bar_init(smem_addr(&bar.s_full[w]), 1);
             bar_init(smem_addr(&bar.p_full[w]), 4);
         }
@@ -629,7 +623,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         total += sh.scan[w];
     }
     before += incl - mine;
-    const long long from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    const long long from = min(total, share * blockIdx.x), to = min(total, from + share);
     if (tid == 0) {
         sh.b0 = -1;
         sh.base0 = 0;
@@ -655,7 +650,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             p.base[b] = at;
             at += (s.t1 - s.t0) * per;
         }
-        if (tid == 0) p.base[p.B] = total;
+        if (tid == 0) {
+            p.base[p.B] = total;
+            p.base[p.B + 1] = share;
+        }
     }
     fence_before_sync();
     __syncthreads();
@@ -667,7 +665,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (warp == 8) {
         // ---- loads: tiles in the order the products take them
-        uint32_t n = 0;  // slots filled
+        uint32_t slot = 0, phase = 1, n = 0;
         int seg = 0;
         bool live = true;
         while (live && walk.next(&g)) {
@@ -680,11 +678,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int i = 0; i < 2 * n_tiles; ++i) {
                 const bool key = kt < n_tiles && (kt == vt || (!g.dual && kt == vt + 1));
                 const int t = g.t0 + (key ? kt++ : vt++);
-                const uint32_t slot = n % ka.slots, round = n / ka.slots;
-                ++n;
-                live = bar_wait(smem_addr(&bar.empty[slot]), (round & 1) ^ 1, dead);
-                live = __all_sync(0xffffffffu, live);
-                if (!live) break;
                 const int pages = min(per_tile, ((g.len - t * kTile) + (1 << shift) - 1) >> shift);
                 int id = -1;
                 if (lane < pages) {
@@ -696,6 +689,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
                 const int good = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                live = bar_wait(smem_addr(&bar.empty[slot]), phase, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
                 const uint32_t full = smem_addr(&bar.full[slot]);
                 if (lane == 0) bar_arrive_tx(full, static_cast<uint32_t>(good * (S::kSlot >> 7) << shift));
                 __syncwarp();
@@ -706,96 +702,119 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int x = 0; x < S::kHalves; ++x)
                         tma_load(dst + x * S::kMat, map, full, x * 64, 0, id * a.c.Hkv + g.h);
                 }
+                ++n;
+                if (++slot == static_cast<uint32_t>(S::kSlots)) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
             ++seg;
         }
         if (!live) {  // the copies in flight land before the CTA's memory goes
-            for (uint32_t i = n > static_cast<uint32_t>(ka.slots) ? n - ka.slots : 0; i + 1 < n; ++i)
-                bar_drain(smem_addr(&bar.full[i % ka.slots]), (i / ka.slots) & 1);
+            for (uint32_t i = n > static_cast<uint32_t>(S::kSlots) ? n - S::kSlots : 0; i < n; ++i)
+                bar_drain(smem_addr(&bar.full[i % S::kSlots]), (i / S::kSlots) & 1);
         }
     } else if (warp == 9) {
         // ---- products
         if (lane == 0) {
             constexpr uint32_t kQk = mma_desc(E4M3, kTile, false), kPv = mma_desc(E4M3, D, true);
-            uint32_t n = 0, segs = 0, pn[2] = {0, 0};
+            constexpr uint32_t kHi = kMatrixHi<S::kRow>;
+            uint32_t qn = 0, pn[2] = {0, 0};
+            uint32_t slot = 0, phase = 0;  // the ring, in the order it is filled
             bool live = true;
-            const uint32_t q0 = smem_addr(qt), r0 = smem_addr(ring);
-            // S of group w from the key tile in `slot`
-            auto scores = [&](int w, bool dual, uint32_t slot) {
-                const uint32_t q = q0 + (dual && w ? S::kQ : 0), k = r0 + slot * S::kSlot;
-                const uint32_t d = tmem + w * kTile;
+            const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(ring), 0);
+            const uint32_t v0 = matrix_lo(smem_addr(ring), S::kMat);
+            const uint32_t full0 = smem_addr(&bar.full[0]), empty0 = smem_addr(&bar.empty[0]);
+            const uint32_t s_full = smem_addr(&bar.s_full[0]), p_full = smem_addr(&bar.p_full[0]);
+            auto advance = [&] {
+                if (++slot == static_cast<uint32_t>(S::kSlots)) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            // S of group w from the query tile qi and the key tile in slot s
+            auto scores = [&](uint32_t w, uint32_t qi, uint32_t s) {
+                const uint32_t q = q0 + qi * (S::kQ >> 4), k = k0 + s * (S::kSlot >> 4), d = tmem + w * kTile;
                 if (E4M3) {
 #pragma unroll
                     for (int i = 0; i < 2 * (D / 32); ++i) {
-                        const int half = i / (D / 32), j = i % (D / 32);
-                        mma_ss<true>(d, matrix_desc<S::kRow>(q + half * S::kMat + j * 32, 0),
-                                     matrix_desc<S::kRow>(k + j * 32, 0), kQk, i > 0);
+                        const uint32_t half = i / (D / 32), j = i % (D / 32);
+                        mma_ss<true>(d, q + ((half * S::kMat + j * 32) >> 4), kHi, k + (j * 32 >> 4), kHi, kQk, i > 0);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t o = (i / 4) * S::kMat + (i % 4) * 32;
-                        mma_ss<false>(d, matrix_desc<S::kRow>(q + o, 0), matrix_desc<S::kRow>(k + o, 0), kQk, i > 0);
+                        const uint32_t o = ((i / 4) * S::kMat + (i % 4) * 32) >> 4;
+                        mma_ss<false>(d, q + o, kHi, k + o, kHi, kQk, i > 0);
                     }
                 }
             };
-            // O += P V of group w with the value tile in `slot`
-            auto values = [&](int w, uint32_t slot, bool first) {
-                const uint32_t v = r0 + slot * S::kSlot;
-                const uint32_t d = tmem + 2 * kTile + w * D, pt = tmem + w * kTile;
+            // O += P V of group w with the value tile in slot s
+            auto values = [&](uint32_t w, uint32_t s, bool first) {
+                const uint32_t v = v0 + s * (S::kSlot >> 4), d = tmem + 2 * kTile + w * D, pt = tmem + w * kTile;
                 if (E4M3) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int j = i % 4;
-                        mma_ts<true>(d, pt + j * 16 + (i / 4) * 8,
-                                     matrix_desc<S::kRow>(v + j * 32 * S::kRow, S::kMat), kPv, !first || i > 0);
+                        const uint32_t j = i % 4;
+                        mma_ts<true>(d, pt + j * 16 + (i / 4) * 8, v + (j * 32 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        mma_ts<false>(d, pt + i * 8, matrix_desc<S::kRow>(v + i * 16 * S::kRow, S::kMat), kPv,
-                                      !first || i > 0);
+                        mma_ts<false>(d, pt + i * 8, v + (i * 16 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
                 }
-            };
-            auto slot_ready = [&](uint32_t i) {
-                return bar_wait(smem_addr(&bar.full[i % ka.slots]), (i / ka.slots) & 1, dead);
             };
             while (live && walk.next(&g)) {
-                const int T = g.t1 - g.t0;
-                live = bar_wait(smem_addr(&bar.q_full), segs & 1, dead);
-                fence_after_sync();
-                // scores of the first tile (of each group's first)
-                const int lead = g.dual ? 1 : min(2, T);
-                for (int t = 0; live && t < lead; ++t, ++n) {
-                    if (!(live = slot_ready(n))) break;
-                    for (int w = g.dual ? 0 : t; w <= (g.dual ? 1 : t); ++w) {
-                        scores(w, g.dual, n % ka.slots);
-                        if (w == (g.dual ? 1 : t)) mma_commit(smem_addr(&bar.empty[n % ka.slots]));
-                        mma_commit(smem_addr(&bar.s_full[w]));
+                const int T = g.t1 - g.t0, lead = g.dual ? 1 : min(2, T);
+                uint32_t qi[2];  // the groups' query tiles
+                qi[0] = qi[1] = qn & 1;
+                live = bar_wait(smem_addr(&bar.q_full[qn & 1]), (qn >> 1) & 1, dead);
+                ++qn;
+                if (g.dual) {
+                    qi[1] = qn & 1;
+                    live = live && bar_wait(smem_addr(&bar.q_full[qn & 1]), (qn >> 1) & 1, dead);
+                    ++qn;
+                }
+                for (int t = 0; live && t < lead; ++t) {  // scores of each group's first tile
+                    if (!(live = bar_wait(full0 + 8 * slot, phase, dead))) break;
+                    fence_after_sync();
+                    if (g.dual) {
+                        scores(0, qi[0], slot);
+                        mma_commit(s_full);
+                        scores(1, qi[1], slot);
+                        mma_commit(s_full + 8);
+                    } else {
+                        scores(t, qi[0], slot);
+                        mma_commit(s_full + 8 * t);
                     }
+                    mma_commit(empty0 + 8 * slot);
+                    advance();
                 }
                 for (int t = 0; live && t < T; ++t) {
-                    const uint32_t vs = n++;
+                    const uint32_t vs = slot, vp = phase;
+                    advance();
                     const bool more = t + lead < T;
-                    const uint32_t ks = n;
-                    if (more) ++n;
-                    if (!(live = slot_ready(vs))) break;
-                    for (int w = g.dual ? 0 : t & 1; w <= (g.dual ? 1 : t & 1); ++w) {
-                        if (!(live = bar_wait(smem_addr(&bar.p_full[w]), pn[w]++ & 1, dead))) break;
+                    const uint32_t ks = slot, kp = phase;
+                    if (more) advance();
+                    if (!(live = bar_wait(full0 + 8 * vs, vp, dead))) break;
+                    const uint32_t w0 = g.dual ? 0 : t & 1, w1 = g.dual ? 1 : t & 1;
+                    for (uint32_t w = w0; w <= w1; ++w) {
+                        if (!(live = bar_wait(p_full + 8 * w, pn[w]++ & 1, dead))) break;
                         fence_after_sync();
-                        values(w, vs % ka.slots, g.dual ? t == 0 : t < 2);
-                        const bool last = !g.dual || w == 1;
-                        if (last) mma_commit(smem_addr(&bar.empty[vs % ka.slots]));
-                        if (more) {
-                            if (!(live = slot_ready(ks))) break;
-                            scores(w, g.dual, ks % ka.slots);
-                            if (last) mma_commit(smem_addr(&bar.empty[ks % ka.slots]));
-                            mma_commit(smem_addr(&bar.s_full[w]));
-                        }
+                        values(w, vs, g.dual ? t == 0 : t < 2);
+                        if (w == w1) mma_commit(empty0 + 8 * vs);
+                        if (!more) continue;
+                        if (!(live = bar_wait(full0 + 8 * ks, kp, dead))) break;
+                        scores(w, qi[w], ks);
+                        mma_commit(s_full + 8 * w);
+                        if (w == w1) mma_commit(empty0 + 8 * ks);
                     }
                 }
-                if (live) mma_commit(smem_addr(&bar.o_full));
-                ++segs;
+                if (live) {
+                    mma_commit(smem_addr(&bar.o_full));
+                    mma_commit(smem_addr(&bar.q_empty[qi[0]]));
+                    if (g.dual) mma_commit(smem_addr(&bar.q_empty[qi[1]]));
+                }
             }
             if (!live) {  // products in flight end before TMEM is freed
                 mma_commit(smem_addr(&bar.drained));
@@ -803,6 +822,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp == 11) {
+        // ---- query tiles, a segment ahead where the ring of two has room
+        uint32_t qn = 0;
+        bool live = true;
+        while (live && walk.next(&g)) {
+            for (int w = 0; live && w < (g.dual ? 2 : 1); ++w, ++qn) {
+                const int row0 = g.row0 + w * kGroupRows, rows = min(kGroupRows, g.rows - w * kGroupRows);
+                const int span = kGroupRows / copies_of(g.dual, rows);
+                live = bar_wait(smem_addr(&bar.q_empty[qn & 1]), ((qn >> 1) & 1) ^ 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+#pragma unroll 1
+                for (int row = lane; row < span; row += 32) {
+                    const __nv_bfloat16 *q = nullptr;
+                    if (row < rows) {
+                        const int r = row0 + row;
+                        const long long tok = (g.shared ? 0 : static_cast<long long>(g.b) * a.N) + r / a.G;
+                        q = a.q + tok * a.q_stride + static_cast<long long>(g.h * a.G + r % a.G) * D;
+                    }
+                    stage_query<D, E4M3>(q, qt + (qn & 1) * S::kQ, row, span, a.scale < 0.0f, q_factor + (qn & 1) * kGroupRows);
+                }
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.q_full[qn & 1]));
+            }
+        }
     } else if (warp == 10) {
         // ---- the e4m3 exponents as factors: 2^ek, ev, 2^-ev of every position
         if (E4M3) {
@@ -843,9 +888,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // this warp's TMEM lanes
         const uint32_t st = tmem + lanes + w * kTile, ot = tmem + lanes + 2 * kTile + w * D;
-        const bool neg = a.scale < 0.0f;
         const float mul = (a.cap > 0.0f ? fabsf(a.scale) / a.cap : fabsf(a.scale) * kLog2e);
-        uint32_t segs = 0, sn = 0, n_ring = 0, n_scale = 0, fn = 0;
+        uint32_t segs = 0, qn = 0, sn = 0, n_ring = 0, n_scale = 0, fn = 0;
         bool live = true;
         // All eight softmax warps meet (bounded, unlike a hardware barrier).
         auto meet = [&] {
@@ -860,30 +904,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int rows = min(kGroupRows, g.rows - (g.dual ? w * kGroupRows : 0));
             // Few rows are repeated over the 128 lanes, and each copy takes its
             // share of a tile's columns.
-            const int copies = g.dual || rows > 64 ? 1 : rows > 32 ? 2 : 4, span = kGroupRows / copies;
+            const int copies = copies_of(g.dual, rows), span = kGroupRows / copies;
             const int copy = quad / (4 / copies), row = (quad * 32 + lane) & (span - 1);
             const bool has = row < rows, active = (quad * 32 & (span - 1)) < rows;
             const int r = row0 + row, tok_in = has ? r / a.G : 0, head = g.h * a.G + (has ? r % a.G : 0);
             const long long tok = g.shared ? tok_in : static_cast<long long>(g.b) * a.N + tok_in;
             const int b = g.shared ? (has ? static_cast<int>(tok / a.N) : 0) : g.b;
             const int n = has ? static_cast<int>(tok - static_cast<long long>(b) * a.N) : 0;
-            const __nv_bfloat16 *q = has ? a.q + tok * a.q_stride + static_cast<long long>(head) * D : nullptr;
-            float qf = 1.0f;
-            if (g.dual || w == 0)
-                qf = stage_query<D, E4M3>(q, qt + (g.dual ? w : 0) * S::kQ, quad * 32 + lane, neg);
-            else if (E4M3)
-                qf = query_factor<D>(q);  // the other group stages this row
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
             Row x;
             x.b = b;
             x.n = n;
+            x.tok = static_cast<int>(tok);
             const int seq_len = g.shared ? (has ? a.lens[b] : 0) : g.len;
             x.first = seq_len - a.N;
             x.pos_i = !has ? 0 : a.pos ? a.pos[tok] : a.shared_len + x.first + n;
             x.has = has;
-            x.rs = mul * qf;
+            const uint32_t qi = (qn + (g.dual ? w : 0)) & 1, q_other = qi ^ 1;
+            if (E4M3) {
+                live = bar_wait(smem_addr(&bar.q_full[qi]), ((qn + (g.dual ? w : 0)) >> 1) & 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+            }
+            x.rs = mul * (E4M3 ? q_factor[qi * kGroupRows + quad * 32 + lane] : 1.0f);
             x.slope = EXTRA && a.slopes && has ? a.slopes[head] * kLog2e : 0.0f;
             x.m = kNegInf;
             x.l = 0.0f;
@@ -917,7 +959,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 // the tile's values: slot index as the loads number them
                 const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
-                if (!whole) live = live && bar_wait(smem_addr(&bar.full[vi % ka.slots]), (vi / ka.slots) & 1, dead);
+                if (!whole) live = live && bar_wait(smem_addr(&bar.full[vi % S::kSlots]), (vi / S::kSlots) & 1, dead);
                 live = __all_sync(0xffffffffu, live);
                 if (!live) break;
                 fence_after_sync();
@@ -932,7 +974,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 wrote = true;
                 if (!whole) {
                     const int at = quad * 32 + lane;
-                    if (clean_values<D, E4M3>(ring + vi % ka.slots * S::kSlot, at, j0 + at < g.len)) sh.odd[segs & 15] = 1;
+                    if (clean_values<D, E4M3>(ring + vi % S::kSlots * S::kSlot, at, j0 + at < g.len)) sh.odd[segs & 15] = 1;
                     fence_async_proxy();
                 }
                 fence_before_sync();
@@ -969,17 +1011,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             for (int k = 0; k < 8; ++k)
                                 o[(c / 4 + k) * rc + row] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                             if (odd)
-                                add_odd_values<D, E4M3>(a, g, x, w, c, 32, reinterpret_cast<float *>(o + (c / 4) * rc + row),
-                                                        4 * rc, 1);
+                                add_odd_values<D, E4M3>(a, g, x, c, 32, reinterpret_cast<float *>(o + (c / 4) * rc + row), 4 * rc);
                         }
                     }
                 }
             } else {
-                // Fold the copies and the two groups into one: every warp scales its
-                // rows to the common maximum and hands them over through the query
-                // tile's memory (its products are done).
-                constexpr int kCols = S::kQ / (256 * 4) < 32 ? 16 : 32;
-                float *buf = reinterpret_cast<float *>(qt);
+                // Fold the copies and the two groups into one.  The groups' accumulators
+                // of a row lie in one lane: each group joins both for half of the
+                // columns; the copies meet in the query tile's memory (its products
+                // are done).
+                constexpr int kCols = S::kQ >= 32768 ? 32 : 16;
+                float4 *buf = reinterpret_cast<float4 *>(qt + qi * S::kQ) + w * (kCols / 4) * kGroupRows;
                 sh.ml[warp][lane] = make_float2(has && wrote ? lift : kNegInf, has && wrote ? x.l : 0.0f);
                 if (!meet()) break;
                 const int per = 4 / copies, in = quad % per;  // warps a copy, this one's place
@@ -990,37 +1032,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const float2 y = sh.ml[(i / copies) * 4 + (i % copies) * per + in][lane];
                     L += (y.x == kNegInf ? 0.0f : ex2(y.x - M)) * y.y;
                 }
-                const float f = some && x.m != kNegInf ? ex2(lift - M) : 0.0f;
+                // this lane's two accumulators and their factors
+                const float m0 = sh.ml[quad][lane].x, m1 = sh.ml[4 + quad][lane].x;
+                const float f0 = m0 == kNegInf ? 0.0f : ex2(m0 - M), f1 = m1 == kNegInf ? 0.0f : ex2(m1 - M);
                 if (w == 0 && copy == 0 && has) ml[row] = make_float2(M, failed ? NAN : L);
+                const uint32_t o0 = tmem + lanes + 2 * kTile, o1 = o0 + D;
 #pragma unroll 1
-                for (int c = 0; c < D; c += kCols) {
-                    float v[kCols];
-                    if (some) {
-                        if constexpr (kCols == 32)
-                            tmem_load32(ot + c, v);
-                        else
-                            tmem_load16(ot + c, v);
-                        tmem_load_wait();
+                for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += kCols) {
+                    float v[kCols], u[kCols];
+                    if constexpr (kCols == 32) {
+                        tmem_load32(o0 + c, v);
+                        tmem_load32(o1 + c, u);
+                    } else {
+                        tmem_load16(o0 + c, v);
+                        tmem_load16(o1 + c, u);
+                    }
+                    tmem_load_wait();
+#pragma unroll
+                    for (int k = 0; k < kCols; ++k)  // an accumulator that was not written may hold anything
+                        v[k] = (f0 > 0.0f ? v[k] * f0 : 0.0f) + (f1 > 0.0f ? u[k] * f1 : 0.0f);
+                    if (copies == 1) {
+                        if (!has) continue;
+#pragma unroll
+                        for (int k = 0; k < kCols / 4; ++k)
+                            o[(c / 4 + k) * rc + row] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        if (odd)
+                            add_odd_values<D, E4M3>(a, g, x, c, kCols, reinterpret_cast<float *>(o + (c / 4) * rc + row), 4 * rc);
+                        continue;
                     }
 #pragma unroll
-                    for (int k = 0; k < kCols; ++k) buf[k * 256 + warp * 32 + lane] = f > 0.0f ? v[k] * f : 0.0f;
-                    if (odd && has && f > 0.0f)
-                        add_odd_values<D, E4M3>(a, g, x, w, c, kCols, buf + warp * 32 + lane, 1024, 256);
+                    for (int k = 0; k < kCols / 4; ++k)
+                        buf[k * kGroupRows + quad * 32 + lane] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                     if (!meet()) break;
-                    for (int i = tid; i < span * (kCols / 4); i += 256) {
-                        const int ri = i & (span - 1), c4 = i / span;
+                    for (int i = quad * 32 + lane; i < span * (kCols / 4); i += kGroupRows) {
+                        const int ri = i & (span - 1), k = i / span;
                         if (ri >= rows) continue;
-                        float y[4] = {};
-                        for (int k = 0; k < 2 * copies; ++k) {
-                            const int from = ((k / copies) * 4 + (k % copies) * per + ri / 32) * 32 + ri % 32;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e] += buf[(4 * c4 + e) * 256 + from];
+                        float4 y = buf[k * kGroupRows + ri];
+                        for (int e = 1; e < copies; ++e) {
+                            const float4 z = buf[k * kGroupRows + e * span + ri];
+                            y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
                         }
-                        o[(c / 4 + c4) * rc + ri] = make_float4(y[0], y[1], y[2], y[3]);
+                        o[(c / 4 + k) * rc + ri] = y;
+                    }
+                    if (odd) {
+                        __threadfence_block();
+                        if (!meet()) break;
+                        if (has && copy == 0)
+                            add_odd_values<D, E4M3>(a, g, x, c, kCols, reinterpret_cast<float *>(o + (c / 4) * rc + row), 4 * rc);
                     }
                     if (!meet()) break;
                 }
+                if (!live) break;
             }
+            if (lane == 0) {
+                bar_arrive(smem_addr(&bar.q_empty[qi]));
+                if (g.dual) bar_arrive(smem_addr(&bar.q_empty[q_other]));
+            }
+            qn += g.dual ? 2 : 1;
             fence_before_sync();
             ++segs;
             n_ring += 2 * T;
@@ -1036,37 +1104,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 // ------------------------------------------------------------------ join
 
-// CTA whose share holds cost x: the largest c with total * c / grid <= x.
-__device__ __forceinline__ int owner(long long x, long long total, int grid) {
-    return static_cast<int>(((x + 1) * grid + total - 1) / total) - 1;
-}
+// A row's partial results of one unit, kBatch at a time: f(slots, half, row,
+// count) with a slot of -1 where a share holds no whole tile of the unit.
+constexpr int kBatchParts = 4;
 
-// A row's partial results of one unit: f(slot, half) for each written one.
 template <typename F>
-__device__ __forceinline__ void each_part(const Plan &p, long long total, long long ubase, int T,
-                                          int unit, int rows, int row, F f) {
+__device__ __forceinline__ void each_part(long long share, long long ubase, int T, int unit, int rows, int row, F f) {
     const bool dual = rows > kGroupRows;
     const int c = dual ? 2 : 1;
     const long long uend = ubase + static_cast<long long>(T) * c;
-    const int lo = owner(ubase, total, p.grid), hi = owner(uend - 1, total, p.grid);
-    for (int i = lo; i <= hi; ++i) {
-        const long long from = total * i / p.grid, to = total * (i + 1) / p.grid;
-        const int t0 = from > ubase ? static_cast<int>((from - ubase + c - 1) / c) : 0;
-        const int t1 = static_cast<int>(min(static_cast<long long>(T), (to - ubase + c - 1) / c));
-        if (t0 >= t1) continue;
-        if (dual) {
-            f(unit + i, row / kGroupRows, row % kGroupRows);
-        } else {
-            f(unit + i, 0, row);
+    int lo, hi;
+    if (uend < INT_MAX) {
+        lo = static_cast<int>(ubase) / static_cast<int>(share);
+        hi = static_cast<int>(uend - 1) / static_cast<int>(share);
+    } else {
+        lo = static_cast<int>(ubase / share);
+        hi = static_cast<int>((uend - 1) / share);
+    }
+    for (int i = lo; i <= hi; i += kBatchParts) {
+        int slots[kBatchParts];
+#pragma unroll
+        for (int k = 0; k < kBatchParts; ++k) {
+            const long long from = (i + k) * share, to = from + share;
+            const long long t0 = from > ubase ? (from - ubase + c - 1) / c : 0;
+            const long long t1 = min(static_cast<long long>(T), (to - ubase + c - 1) / c);
+            slots[k] = i + k <= hi && t0 < t1 ? unit + i + k : -1;
         }
+        f(slots, dual ? row / kGroupRows : 0, dual ? row % kGroupRows : row);
     }
 }
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ KernelArgs ka) {
-    constexpr int kV = D / 16;  // float4 a thread: its warp's quarter of a row
+    constexpr int kV = D / 32;  // float4 a thread: its warp's eighth of a row
     const AttnArgs &a = ka.a;
     const Plan &p = ka.p;
     const int chunks = ceil_div(p.R, 32);
@@ -1074,48 +1146,61 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = chunk * 32 + lane;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (r >= p.R) return;
-    const long long total = p.base[p.B];
+    const long long share = p.base[p.B + 1];
     const int len = p.lens[b];
     const bool bad = len < 0 || len > (p.width << p.page_shift);
     const Span s = span_of(p, b);
     float M = kNegInf, L = 0.0f;
     float4 acc[kV] = {};
-    auto both = [&](auto f) {
-        if (p.sT > 0) {
-            const long long g = static_cast<long long>(b) * p.N * p.G + r;
-            const int u = static_cast<int>(g / (2 * kGroupRows)), rows = min(p.sR - u * 2 * kGroupRows, 2 * kGroupRows);
-            each_part(p, total, static_cast<long long>(h) * p.srt * p.sT + u * 2ll * p.sT, p.sT, h * p.sru + u, rows,
-                      static_cast<int>(g % (2 * kGroupRows)), [&](int slot, int half, int row) {
-                          const long long part = static_cast<long long>(slot) * p.sparts + half;
-                          f(p.sml + part * p.src + row, p.so + part * (D / 4) * p.src + row, p.src);
-                      });
+    auto add = [&](const float2 *ml, const float4 *o, int parts, int rc, const int *slots, int half, int row) {
+        float2 x[kBatchParts];
+        float4 y[kBatchParts][kV];
+#pragma unroll
+        for (int i = 0; i < kBatchParts; ++i) {
+            const long long part = static_cast<long long>(max(slots[i], 0)) * parts + half;
+            x[i] = slots[i] >= 0 ? ml[part * rc + row] : make_float2(kNegInf, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kV; ++k)
+                y[i][k] = slots[i] >= 0 ? o[(part * (D / 4) + warp * kV + k) * rc + row] : float4{};
         }
-        const int T = s.t1 - s.t0;
-        if (T > 0) {
-            const int u = r / (2 * kGroupRows), rows = min(p.R - u * 2 * kGroupRows, 2 * kGroupRows);
-            each_part(p, total, p.base[b] + static_cast<long long>(h) * p.rt * T + u * 2ll * T, T, bh * p.ru + u, rows,
-                      r % (2 * kGroupRows), [&](int slot, int half, int row) {
-                          const long long part = static_cast<long long>(slot) * p.parts + half;
-                          f(p.ml + part * p.rc + row, p.o + part * (D / 4) * p.rc + row, p.rc);
-                      });
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kBatchParts; ++i) {
+            top = fmaxf(top, x[i].x);
+            if (isnan(x[i].y)) L = NAN;
+        }
+        if (top == kNegInf) return;
+        const float keep = ex2(M - top);
+        M = top;
+        L *= keep;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[k].x *= keep, acc[k].y *= keep, acc[k].z *= keep, acc[k].w *= keep;
+#pragma unroll
+        for (int i = 0; i < kBatchParts; ++i) {
+            if (x[i].x == kNegInf) continue;  // nothing seen: its accumulator was not written
+            const float f = ex2(x[i].x - top);
+            L = fmaf(f, x[i].y, L);
+#pragma unroll
+            for (int k = 0; k < kV; ++k) {
+                acc[k].x = fmaf(f, y[i][k].x, acc[k].x);
+                acc[k].y = fmaf(f, y[i][k].y, acc[k].y);
+                acc[k].z = fmaf(f, y[i][k].z, acc[k].z);
+                acc[k].w = fmaf(f, y[i][k].w, acc[k].w);
+            }
         }
     };
-    both([&](const float2 *ml, const float4 *, int) { M = fmaxf(M, ml->x); });
-    both([&](const float2 *ml, const float4 *o, int rc) {
-        const float2 x = *ml;
-        if (isnan(x.y)) L = NAN;
-        if (x.x == kNegInf) return;
-        const float f = ex2(x.x - M);
-        L = fmaf(f, x.y, L);
-#pragma unroll
-        for (int k = 0; k < kV; ++k) {
-            const float4 y = o[(warp * kV + k) * rc];
-            acc[k].x = fmaf(f, y.x, acc[k].x);
-            acc[k].y = fmaf(f, y.y, acc[k].y);
-            acc[k].z = fmaf(f, y.z, acc[k].z);
-            acc[k].w = fmaf(f, y.w, acc[k].w);
-        }
-    });
+    if (p.sT > 0) {
+        const int g = b * p.R + r, u = g / (2 * kGroupRows), rows = min(p.sR - u * 2 * kGroupRows, 2 * kGroupRows);
+        each_part(share, static_cast<long long>(h) * p.srt * p.sT + u * 2ll * p.sT, p.sT, h * p.sru + u, rows,
+                  g % (2 * kGroupRows),
+                  [&](const int *slots, int half, int row) { add(p.sml, p.so, p.sparts, p.src, slots, half, row); });
+    }
+    if (s.t1 > s.t0) {
+        const int T = s.t1 - s.t0, u = r / (2 * kGroupRows), rows = min(p.R - u * 2 * kGroupRows, 2 * kGroupRows);
+        each_part(share, p.base[b] + static_cast<long long>(h) * p.rt * T + u * 2ll * T, T, bh * p.ru + u, rows,
+                  r % (2 * kGroupRows),
+                  [&](const int *slots, int half, int row) { add(p.ml, p.o, p.parts, p.rc, slots, half, row); });
+    }
     if (bad) {
         L = NAN;
         if (lane == 0 && warp == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
@@ -1124,16 +1209,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const long long row = static_cast<long long>(tok) * a.Hq + head;
     // Nothing seen: L = 0 and every accumulator 0.
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint4 *out = reinterpret_cast<uint4 *>(a.out + row * D + warp * kV * 4);
+    __nv_bfloat16 *out = a.out + row * D + warp * kV * 4;
 #pragma unroll
-    for (int k = 0; k < kV; k += 2) {
-        uint4 w;
-        w.x = bf16_pair(acc[k].x * inv, acc[k].y * inv);
-        w.y = bf16_pair(acc[k].z * inv, acc[k].w * inv);
-        w.z = bf16_pair(acc[k + 1].x * inv, acc[k + 1].y * inv);
-        w.w = bf16_pair(acc[k + 1].z * inv, acc[k + 1].w * inv);
-        out[k / 2] = w;
-    }
+    for (int k = 0; k < kV; ++k)
+        reinterpret_cast<uint2 *>(out)[k] = make_uint2(bf16_pair(acc[k].x * inv, acc[k].y * inv),
+                                                       bf16_pair(acc[k].z * inv, acc[k].w * inv));
     if (a.lse && warp == 0) a.lse[row] = L == 0.0f ? kNegInf : (M + log2f(L)) / kLog2e;
 }
 
@@ -1161,7 +1241,7 @@ size_t carve_plan(Plan *p, int D, char *work) {
     };
     const size_t slots = static_cast<size_t>(p->B) * p->Hkv * p->ru + kMaxGrid;
     const size_t sslots = static_cast<size_t>(p->Hkv) * p->sru + kMaxGrid;
-    p->base = reinterpret_cast<long long *>(take((p->B + 1) * sizeof(long long)));
+    p->base = reinterpret_cast<long long *>(take((p->B + 2) * sizeof(long long)));
     p->ml = reinterpret_cast<float2 *>(take(slots * p->parts * p->rc * sizeof(float2)));
     p->o = reinterpret_cast<float4 *>(take(slots * p->parts * p->rc * D * sizeof(float)));
     p->sml = reinterpret_cast<float2 *>(take(sslots * p->sparts * p->src * sizeof(float2)));
@@ -1222,10 +1302,7 @@ int launch_shape(KernelArgs &ka, cudaStream_t st) {
     if (!make_map(&kmap, ka.a.c.k, ka.a.c) || !make_map(&vmap, ka.a.c.v, ka.a.c)) return SPEC_ERR_CUDA;
     Plan &p = ka.p;
     p.grid = min(sms, kMaxGrid);
-    // One query tile a group where some unit has over 128 rows.
-    ka.q_tiles = p.R > kGroupRows || (p.sT > 0 && p.sR > kGroupRows) ? 2 : 1;
-    ka.slots = S::slots(ka.q_tiles);
-    kernel<<<p.grid, kAttnThreads, S::bytes(ka.q_tiles), st>>>(ka, kmap, vmap);
+    kernel<<<p.grid, kAttnThreads, S::kBytes, st>>>(ka, kmap, vmap);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * ceil_div(p.R, 32)));

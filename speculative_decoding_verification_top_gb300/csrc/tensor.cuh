@@ -113,37 +113,37 @@ __device__ __forceinline__ void fence_after_sync() {
 }
 
 // D[tmem] (+)= A B with A and B in shared memory, or A in TMEM.  F8: both
-// operands e4m3, 32 deep; else both bf16, 16 deep.
+// operands e4m3, 32 deep; else both bf16, 16 deep.  A matrix descriptor comes
+// as its low word (which moves along the matrix) and its high word.
 template <bool F8>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                       uint32_t idesc, bool add) {
     if (F8)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-            : "memory");
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-            : "memory");
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
 }
 
 template <bool F8>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool add) {
     if (F8)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-            : "memory");
+            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-            : "memory");
+            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
 }
 
 // 32 consecutive TMEM columns of this thread's lane (a warp reads its own 32
@@ -203,16 +203,13 @@ __device__ __forceinline__ void tmem_store_wait() {
 }
 
 // Shared-memory matrix descriptor of rows of `kRow` bytes (128 or 64), each
-// swizzled over its whole width, eight rows to a pattern.  `lead`: bytes
-// between 64-element column blocks where the matrix is wider than a row (the
-// values' second half); unused otherwise.
+// swizzled over its whole width, eight rows to a pattern: the low word holds
+// the address and `lead`, the bytes between 64-element column blocks where the
+// matrix is wider than a row (the values' second half; unused otherwise).
+__device__ __forceinline__ uint32_t matrix_lo(uint32_t addr, uint32_t lead) { return addr >> 4 | (lead >> 4) << 16; }
+
 template <int kRow>
-__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead) {
-    constexpr uint64_t kSwizzle = kRow == 128 ? 2 : 4;
-    return static_cast<uint64_t>((addr >> 4) & 0x3fff) |
-           static_cast<uint64_t>((lead >> 4) & 0x3fff) << 16 |
-           static_cast<uint64_t>((8 * kRow) >> 4) << 32 | 1ull << 46 | kSwizzle << 61;
-}
+constexpr uint32_t kMatrixHi = static_cast<uint32_t>((8 * kRow) >> 4) | 1u << 14 | (kRow == 128 ? 2u : 4u) << 29;
 
 // Byte offset of (row, byte) in such a matrix: 16-byte units are permuted
 // within a row by the row's place in its pattern of 1024 (512) bytes.
