@@ -35,9 +35,9 @@ CSRC = os.path.join(_PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("api.cu", "rows.cu", "topp.cu", "final.cu", "noalloc.cu",
                      "accept.cu", "treemask.cu", "treesample.cu", "select.cu",
-                     "kvcache.cu", "attn.cu", "attn_api.cu")]
+                     "kvcache.cu", "attn.cu", "attn_few.cu", "attn_wide.cu", "attn_api.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh", "attn.cuh",
-                                             "tensor.cuh")]
+                                             "attn_plan.cuh", "tensor.cuh")]
 INCLUDE = os.path.join(_ROOT, "include")
 HEADER = os.path.join(INCLUDE, "spec_verify.h")
 ATTN_HEADER = os.path.join(INCLUDE, "spec_attn.h")

@@ -1,0 +1,655 @@
+// attn_few.cu -- attention of units with few query rows: a chain of drafts, a
+// single token, and whatever else has at most 64 rows (new tokens x query
+// heads of a group) per key/value head.
+//
+// attn_few_kernel   persistent, one CTA per SM; its share of the tiles (see
+//                   attn.cu) segment by segment.  Memory-bound: a tile's keys
+//                   and values are read once and used for few rows.
+// The products are taken transposed, so that the 128 positions of a tile fill
+// the tensor core's 128 rows and the query rows are its columns (NR = 32 or
+// 64): S^T = K Q^T, O^T += V^T P^T.  That makes a product cost a quarter of
+// what 128 padded query rows would, gives a softmax thread a position and NR
+// scores, and leaves room in TMEM for two S ahead per group.
+//   warps 0-3, 4-7   two softmax groups, a thread per position, on alternate
+//                    tiles, each with its own (m, l, O)
+//   warps 8, 10      load key and value tiles page by page (TMA) into a ring
+//                    each
+//   warp 9           issues the products (tcgen05); scores run up to two tiles
+//                    ahead of the values
+//   warp 11          the query tile, and what belongs to its rows, of the next
+//                    segment
+// The reference maximum of a row is common to a group's 128 threads; a vote per
+// tile (one hardware barrier) says whether any score outgrew it, which after
+// the first tile of a segment is rare, so maxima are reduced only then.  l is
+// kept per thread and summed once a segment.
+
+#include "attn_plan.cuh"
+
+namespace specv {
+namespace {
+
+constexpr int kGroupBarrier = 1;  // hardware barrier of softmax group 0; + 1 for group 1
+constexpr float kNone = -FLT_MAX; // reference of a row that has seen nothing: below any score
+
+struct Barriers {
+    unsigned long long k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
+    unsigned long long q_full[2], q_empty[2];
+    unsigned long long s_full[2][2], s_empty[2][2], p_full[2][2], p_empty[2][2], drained;
+};
+
+template <int NR>
+struct alignas(16) Rows {  // what belongs to the query rows of a segment
+    float rs[NR];       // score factor (the log2 e and the query's own in it)
+    float slope[NR];    // slope * log2 e
+    float at[NR];       // position index less the segment's origin
+    int pos[NR];        // position index
+};
+
+template <int NR>
+struct Shared {
+    Barriers bar;
+    Start start;
+    Rows<NR> rows[2];
+    alignas(16) float ref[2][NR];  // per group: reference maximum less the lift; +inf for no row
+    alignas(16) float keep[2][NR]; // per group: factor of the last growth
+    float red[2][4][NR];   // per group and warp
+    float factor[2][NR];   // e4m3: the query rows' own factors
+    uint32_t tmem;
+    int dead;              // a wait ran out: everyone leaves
+    int fail[16];          // per segment (mod 16): a page id out of range
+    int odd[16];           // per segment (mod 16): a cleaned tile held values that are not finite
+};
+
+template <int D, bool E4M3, int NR>
+struct Layout : Shape<D, E4M3> {
+    using S = Shape<D, E4M3>;
+    static constexpr int kQBlock = NR * S::kRow;                     // a block of the query tile
+    static constexpr int kQ = kQBlock * (E4M3 ? 2 : S::kHalves);
+    static constexpr int kPRow = E4M3 ? NR : 2 * NR;                 // bytes of a row of weights
+    static constexpr int kPMat = kTile * kPRow;
+    static constexpr int kP = kPMat * (E4M3 ? 2 : 1);                // one buffer of weights
+    static constexpr int kFixed = static_cast<int>((sizeof(Shared<NR>) + 127) / 128 * 128);
+    static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ - 4 * kP) / S::kSlot;
+    static constexpr int kSlots = kRoom < 2 * kMaxSlots ? kRoom : 2 * kMaxSlots;
+    static constexpr int kK = kSlots / 2, kV = kSlots - kK;          // slots of keys, of values
+    static constexpr int kBytes = kFixed + 2 * kQ + 4 * kP + kSlots * S::kSlot;
+    static constexpr uint32_t kColumns = NR == 32 ? 256 : 512;       // TMEM: 4 S and 2 O of NR columns
+};
+
+// Folds v[0..NR) over a warp's lanes with f: lane i ends up with column(s) i
+// (NR = 32), or 2 i and 2 i + 1 (NR = 64).
+template <int NR, typename F>
+__device__ __forceinline__ void fold_columns(const float (&v)[NR], float (&out)[NR / 32], F f) {
+    const int lane = threadIdx.x & 31;
+    float x[NR / 2];
+    const bool up = lane & 16;
+#pragma unroll
+    for (int k = 0; k < NR / 2; ++k) {
+        const float mine = up ? v[k + NR / 2] : v[k], other = up ? v[k] : v[k + NR / 2];
+        x[k] = f(mine, __shfl_xor_sync(0xffffffffu, other, 16));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o /= 2) {
+        const int n = NR / 2 * o / 16;  // columns after this step
+        const bool hi = lane & o;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float mine = hi ? x[k + n] : x[k], other = hi ? x[k] : x[k + n];
+            x[k] = f(mine, __shfl_xor_sync(0xffffffffu, other, o));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NR / 32; ++k) out[k] = x[k];
+}
+
+// The rows (bits) that see this thread's position, in a tile that some rows do
+// not see whole.  Rows of a token see alike: four tokens at a time, their mask
+// bytes in flight together.
+template <int NR>
+__device__ __forceinline__ unsigned long long seen_rows(const AttnArgs &a, const Segment &g, const Rows<NR> &rows, int j,
+                                                        int pos_j) {
+    constexpr int kAtOnce = 4;
+    const int c = j - (g.len - a.N), tokens = g.rows / a.G;
+    const bool held = j < g.len, node = !g.shared && held && c >= 0;
+    const unsigned long long per = a.G >= 64 ? ~0ull : (1ull << a.G) - 1;
+    unsigned long long seen = 0;
+    for (int n0 = 0; n0 < tokens; n0 += kAtOnce) {
+        uint8_t m[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int n = min(n0 + k, tokens - 1);
+            m[k] = !node ? 1 : a.mask ? a.mask[(static_cast<long long>(g.b) * a.N + n) * a.N + c] : c <= n;
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int n = min(n0 + k, tokens - 1);
+            const bool y = held && m[k] != 0 &&
+                           (a.window == 0 || static_cast<long long>(rows.pos[n * a.G]) - pos_j < a.window);
+            if (y && n0 + k < tokens) seen |= per << (n * a.G);
+        }
+    }
+    return seen;
+}
+
+// Adds to the unit's rows of output column d what the products left out:
+// values that are not finite, of the positions each row sees in the segment's
+// tiles.  (In a tile that was not cleaned they are in the sum already, and
+// adding them again changes nothing.)
+template <int D, bool E4M3, int NR>
+__device__ __noinline__ void add_odd_values(const AttnArgs &a, const Segment g, const Rows<NR> &rows, int d, float *o) {
+    for (int j = g.t0 * kTile; j < min(g.len, g.t1 * kTile); ++j) {
+        int slot;
+        const int page = page_of(a.c, pages_of(a, g), INT_MAX, j, &slot);
+        if (page < 0) continue;
+        const float y = odd_value<E4M3>(a.c, cache_row(a.c, page, g.h, slot) * D + d);
+        if (isfinite(y)) continue;
+        const int c = j - (g.len - a.N);
+        const int pos_j = !g.shared && c >= 0 && a.pos ? a.pos[static_cast<long long>(g.b) * a.N + c]
+                                                       : (g.shared ? 0 : a.shared_len) + j;
+        const unsigned long long seen = seen_rows<NR>(a, g, rows, j, pos_j);
+        for (int i = 0; i < g.rows; ++i)
+            if (seen >> i & 1) o[static_cast<long long>(i) * D] += y;
+    }
+}
+
+template <int D, bool E4M3, bool EXTRA, int NR>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_few_kernel(const __grid_constant__ KernelArgs ka, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap) {
+    using S = Layout<D, E4M3, NR>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const AttnArgs &a = ka.a;
+    const Plan &p = ka.p;
+    uint8_t *k_ring = smem, *v_ring = k_ring + S::kK * S::kSlot, *pt = v_ring + S::kV * S::kSlot, *qt = pt + 4 * S::kP;
+    Shared<NR> &sh = *reinterpret_cast<Shared<NR> *>(qt + 2 * S::kQ);
+    Barriers &bar = sh.bar;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    if (tid == 0) {
+        for (int i = 0; i < kMaxSlots; ++i) {
+            bar_init(smem_addr(&bar.k_full[i]), 1);
+            bar_init(smem_addr(&bar.k_empty[i]), 1);
+            bar_init(smem_addr(&bar.v_full[i]), 1);
+            bar_init(smem_addr(&bar.v_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_addr(&bar.q_full[i]), 1);
+            bar_init(smem_addr(&bar.q_empty[i]), 9);  // the products, and eight softmax warps
+            for (int w = 0; w < 2; ++w) {
+                bar_init(smem_addr(&bar.s_full[w][i]), 1);
+                bar_init(smem_addr(&bar.s_empty[w][i]), 4);
+                bar_init(smem_addr(&bar.p_full[w][i]), 4);
+                bar_init(smem_addr(&bar.p_empty[w][i]), 1);
+            }
+        }
+        bar_init(smem_addr(&bar.drained), 1);
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_proxy();
+    }
+    if (warp == 9) tmem_alloc(smem_addr(&sh.tmem), S::kColumns);
+    long long from, to;
+    find_share(p, sh.start, &from, &to);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    volatile int *dead = &sh.dead;
+    Walk walk(p, from, to, sh.start.b0, sh.start.base0);
+    Segment g;
+    const float mul = a.cap > 0.0f ? fabsf(a.scale) / a.cap : fabsf(a.scale) * kLog2e;
+
+    // A segment's query tile and rows into half i of the ring of two.
+    auto stage = [&](int i, int me, int threads) {
+        stage_queries<D, E4M3>(a, g, 0, g.rows, NR, qt + i * S::kQ, sh.factor[i], me, threads);
+    };
+    auto stage_rows = [&](int i, int me, int threads) {
+        const int origin = (g.shared ? 0 : a.shared_len) + g.len;
+        for (int r = me; r < NR; r += threads) {
+            const bool has = r < g.rows;
+            const int tok = (g.shared ? 0 : g.b * a.N) + (has ? r / a.G : 0), b = tok / a.N;
+            const int pos = !has ? 0 : a.pos ? a.pos[tok] : a.shared_len + (g.shared ? a.lens[b] : g.len) - a.N + tok % a.N;
+            sh.rows[i].rs[r] = mul * (E4M3 ? sh.factor[i][r] : 1.0f);
+            sh.rows[i].slope[r] = EXTRA && a.slopes && has ? a.slopes[g.h * a.G + r % a.G] * kLog2e : 0.0f;
+            sh.rows[i].at[r] = static_cast<float>(pos - origin);
+            sh.rows[i].pos[r] = pos;
+        }
+    };
+    {
+        // The first segment's: everyone takes a share.
+        Walk ahead = walk;
+        const bool some = ahead.next(&g);
+        if (some) stage(0, tid, kAttnThreads);
+        fence_async_proxy();
+        __syncthreads();
+        if (some) stage_rows(0, tid, kAttnThreads);
+        __syncthreads();
+    }
+
+    if (warp == 8 || warp == 10) {
+        // ---- loads: keys, values
+        const bool key = warp == 8;
+        bool live = true;
+        int seg = 0;
+        auto run = [&](auto &load, uint8_t *ring, unsigned long long *full, unsigned long long *empty) {
+            while (live && walk.next(&g)) {
+                if (key && lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
+                __syncwarp();
+                for (int t = g.t0; live && t < g.t1; ++t)
+                    live = load.tile(a, g, pages_of(a, g), t, key ? &kmap : &vmap, smem_addr(ring), full, empty, dead,
+                                     &sh.fail[seg & 15], key);
+                ++seg;
+            }
+            if (!live) load.drain(full);
+        };
+        if (key) {
+            Loader<D, E4M3, S::kK> load;
+            run(load, k_ring, bar.k_full, bar.k_empty);
+        } else {
+            Loader<D, E4M3, S::kV> load;
+            run(load, v_ring, bar.v_full, bar.v_empty);
+        }
+    } else if (warp == 9) {
+        // ---- products
+        if (elect_one()) {
+            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kPv = mma_desc(E4M3, NR, true, true);
+            constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>;
+            // Values narrower than 128 columns: the second block is the first again,
+            // and its rows of O are not read.
+            constexpr uint32_t kLead = D == 128 && !E4M3 ? S::kMat : 0;
+            const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(k_ring), 0);
+            const uint32_t v0 = matrix_lo(smem_addr(v_ring), kLead), p0 = matrix_lo(smem_addr(pt), 0);
+            const uint32_t k_full = smem_addr(&bar.k_full[0]), k_empty = smem_addr(&bar.k_empty[0]);
+            const uint32_t v_full = smem_addr(&bar.v_full[0]), v_empty = smem_addr(&bar.v_empty[0]);
+            const uint32_t s_full = smem_addr(&bar.s_full[0][0]), s_empty = smem_addr(&bar.s_empty[0][0]);
+            const uint32_t p_full = smem_addr(&bar.p_full[0][0]), p_empty = smem_addr(&bar.p_empty[0][0]);
+            // Two walks over the same tiles: the scores', and the values' behind it.
+            Walk ahead = walk;
+            Segment s;
+            uint32_t is = 0, iv = 0, seg_s = 0, seg_v = 0, ks = 0, kp = 0, vs = 0, vp = 0;
+            bool more_s = ahead.next(&s), more_v = walk.next(&g), live = true;
+            int ts = s.t0, tv = g.t0;
+            while (live && more_v) {
+                // At most two tiles and one segment ahead: the query ring holds two.
+                if (more_s && is <= iv + 2 && seg_s <= seg_v + 1) {
+                    const uint32_t w = is & 1, cnt = is >> 1, buf = w * 2 + (cnt & 1), qi = seg_s & 1;
+                    if (ts == s.t0) live = bar_wait(smem_addr(&bar.q_full[qi]), (seg_s >> 1) & 1, dead);
+                    live = live && bar_wait(k_full + 8 * ks, kp, dead) &&
+                           bar_wait(s_empty + 8 * buf, ((cnt >> 1) & 1) ^ 1, dead);
+                    if (!live) break;
+                    fence_after_sync();
+                    const uint32_t k = k0 + ks * (S::kSlot >> 4), q = q0 + qi * (S::kQ >> 4), d = tmem + buf * NR;
+                    if (E4M3) {
+#pragma unroll
+                        for (int i = 0; i < 2 * (D / 32); ++i) {
+                            const uint32_t term = i / (D / 32), j = i % (D / 32);
+                            mma_ss<true>(d, k + (j * 32 >> 4), kHi, q + ((term * S::kQBlock + j * 32) >> 4), kHi, kQk, i > 0);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+                            mma_ss<false>(d, k + (((i / 4) * S::kMat + (i % 4) * 32) >> 4), kHi,
+                                          q + (((i / 4) * S::kQBlock + (i % 4) * 32) >> 4), kHi, kQk, i > 0);
+                    }
+                    mma_commit(s_full + 8 * buf);
+                    mma_commit(k_empty + 8 * ks);
+                    if (++ks == S::kK) {
+                        ks = 0;
+                        kp ^= 1;
+                    }
+                    ++is;
+                    if (++ts == s.t1) {
+                        mma_commit(smem_addr(&bar.q_empty[qi]));
+                        more_s = ahead.next(&s);
+                        ts = s.t0;
+                        ++seg_s;
+                    }
+                } else {
+                    const uint32_t w = iv & 1, cnt = iv >> 1, buf = w * 2 + (cnt & 1);
+                    live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * buf, (cnt >> 1) & 1, dead);
+                    if (!live) break;
+                    fence_after_sync();
+                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + buf * (S::kP >> 4), d = tmem + (4 + w) * NR;
+                    const bool first = tv - g.t0 < 2;  // the group's first tile of the segment
+                    if (E4M3) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t j = i % 4;
+                            mma_ss<true>(d, v + (j * 32 * S::kRow >> 4), kHi,
+                                         pb + (((i / 4) * S::kPMat + j * 32 * S::kPRow) >> 4), kPHi, kPv, i > 0 || !first);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mma_ss<false>(d, v + (i * 16 * S::kRow >> 4), kHi, pb + (i * 16 * S::kPRow >> 4), kPHi, kPv,
+                                          i > 0 || !first);
+                    }
+                    mma_commit(p_empty + 8 * buf);
+                    mma_commit(v_empty + 8 * vs);
+                    if (++vs == S::kV) {
+                        vs = 0;
+                        vp ^= 1;
+                    }
+                    ++iv;
+                    if (++tv == g.t1) {
+                        more_v = walk.next(&g);
+                        tv = g.t0;
+                        ++seg_v;
+                    }
+                }
+            }
+            if (!live) {  // products in flight end before TMEM is freed
+                mma_commit(smem_addr(&bar.drained));
+                bar_drain(smem_addr(&bar.drained), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 11) {
+        // ---- query tiles, a segment ahead (the first segment's is there)
+        bool live = true;
+        for (uint32_t seg = 0; live && walk.next(&g); ++seg) {
+            if (seg > 0) {
+                live = bar_wait(smem_addr(&bar.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+                stage(seg & 1, lane, 32);
+                __syncwarp();
+                stage_rows(seg & 1, lane, 32);
+                fence_async_proxy();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&bar.q_full[seg & 1]));
+        }
+    } else {
+        // ---- softmax groups
+        const int w = warp >> 2, quad = warp & 3, row = tid & 127;  // row: the thread's position in a tile
+        const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // this warp's TMEM lanes
+        const uint32_t ot = tmem + lanes + (4 + w) * NR;
+        constexpr float kSlack = E4M3 ? kSlackE4M3 : kSlackBf16, kLift = E4M3 ? kLiftE4M3 : 0.0f;
+        const float capl = a.cap * kLog2e;
+        float *ref = sh.ref[w], *keep = sh.keep[w];
+        auto vote = [&](bool x) {
+            __syncwarp();
+            return any_of(kGroupBarrier + w, 128, x);
+        };
+        uint32_t seg = 0, tile = 0, cnt = 0;  // segments, tiles of the CTA, tiles of this group
+        bool live = true;
+        while (live && walk.next(&g)) {
+            const Units &u = g.shared ? p.shared : p.own;
+            const long long part = static_cast<long long>(g.slot) * 2 + w;
+            float2 *ml = u.ml + part * u.rc;
+            const uint32_t half = seg & 1;
+            const Rows<NR> &rows = sh.rows[half];
+            bool ok = bar_wait(smem_addr(&bar.q_full[half]), (seg >> 1) & 1, dead);
+            const int n_rows = g.rows, first_tile = g.t0 + ((tile ^ w) & 1);  // this group's first
+            const int origin = (g.shared ? 0 : a.shared_len) + g.len;
+            const int last_pos = a.window > 0 ? last_position(a, g) : 0;
+            const int32_t *table = pages_of(a, g);
+            float l[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) l[i] = 0.0f;
+            if (row < NR) ref[row] = row < n_rows ? kNone : INFINITY;
+            // exponents of this thread's position in tile t
+            auto exponents = [&](int t, int *ek, int *ev) {
+                const int j = t * kTile + row;
+                int slot = 0;
+                const int page = t < g.t1 && j < g.len ? page_of(a.c, table, INT_MAX, j, &slot) : -1;
+                const long long at = cache_row(a.c, max(page, 0), g.h, slot);
+                *ek = page < 0 ? 0 : a.c.k_exp[at];
+                *ev = page < 0 ? 0 : a.c.v_exp[at];
+            };
+            int ek = 0, ev = 0;
+            if (E4M3) exponents(first_tile, &ek, &ev);
+            vote(false);  // the reference is set
+            for (int t = first_tile; t < g.t1; t += 2, ++cnt) {
+                const int j0 = t * kTile, j = j0 + row;
+                const uint32_t buf = cnt & 1, phase = (cnt >> 1) & 1;
+                int ek_next = 0, ev_next = 0;
+                if (E4M3) exponents(t + 2, &ek_next, &ev_next);
+                const bool whole = sees_whole(a, g, j0, last_pos);
+                // Position index of this thread's position, and the rows that see it.
+                int pos_j = (g.shared ? 0 : a.shared_len) + j;
+                unsigned long long seen = ~0ull;
+                const uint32_t vi = tile + (t - g.t0);
+                if (!whole) {
+                    const int c = j - (g.len - a.N);
+                    if (!g.shared && c >= 0 && j < g.len && a.pos) pos_j = a.pos[static_cast<long long>(g.b) * a.N + c];
+                    seen = seen_rows<NR>(a, g, rows, j, pos_j);
+                    ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
+                }
+                ok = ok && bar_wait(smem_addr(&bar.s_full[w][buf]), phase, dead);
+                fence_after_sync();
+                __syncwarp();
+                float s[NR];
+#pragma unroll
+                for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + (w * 2 + buf) * NR + c, s + c);
+                tmem_load_wait();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.s_empty[w][buf]));
+                const float fk = E4M3 ? exp2i(max(-120, min(120, ek))) : 1.0f;
+                const float fb = E4M3 ? static_cast<float>(max(-120, min(120, ev))) : 0.0f;
+                const float fl = E4M3 ? exp2i(-max(-120, min(120, ev))) : 1.0f;
+                const float at = static_cast<float>(pos_j - origin);
+                float over = kNegInf;
+#pragma unroll
+                for (int c = 0; c < NR; c += 4) {
+                    if (c >= n_rows) break;
+                    const float4 r4 = *reinterpret_cast<const float4 *>(&rows.rs[c]);
+                    const float4 m4 = *reinterpret_cast<const float4 *>(&ref[c]);
+                    const float4 s4 = EXTRA ? *reinterpret_cast<const float4 *>(&rows.slope[c]) : float4{};
+                    const float4 a4 = EXTRA ? *reinterpret_cast<const float4 *>(&rows.at[c]) : float4{};
+                    const float rs[4] = {r4.x, r4.y, r4.z, r4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w};
+                    const float sl[4] = {s4.x, s4.y, s4.z, s4.w}, ra[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float y = s[c + k];
+                        if (E4M3) y *= fk;
+                        if (EXTRA) {
+                            y = a.cap > 0.0f ? capped(y * rs[k], capl) : y * rs[k];
+                            y = fmaf(sl[k], at - ra[k], y);
+                            if (E4M3) y += fb;
+                        } else {
+                            y = E4M3 ? fmaf(y, rs[k], fb) : y * rs[k];
+                        }
+                        if (!whole && !(seen >> (c + k) & 1)) y = kNegInf;
+                        s[c + k] = y;
+                        over = fmaxf(over, y - m[k]);
+                    }
+                }
+                const bool grown = vote(!ok || over > kSlack + kLift);
+                if (grown) {
+                    if (vote(!ok)) {
+                        live = false;
+                        break;
+                    }
+                    // Some row outgrew its reference: reduce the maxima, rescale.
+#pragma unroll
+                    for (int c = 0; c < NR; c += 4)
+                        if (c >= n_rows)
+                            for (int k = 0; k < 4; ++k) s[c + k] = kNegInf;
+                    float top[NR / 32];
+                    fold_columns<NR>(s, top, [](float x, float y) { return fmaxf(x, y); });
+#pragma unroll
+                    for (int k = 0; k < NR / 32; ++k) sh.red[w][quad][lane * (NR / 32) + k] = top[k];
+                    vote(false);
+                    if (row < NR) {
+                        const float m0 = ref[row];
+                        const float m1 = fmaxf(fmaxf(sh.red[w][0][row], sh.red[w][1][row]),
+                                               fmaxf(sh.red[w][2][row], sh.red[w][3][row])) - kLift;
+                        const bool up = m1 > m0 && (m0 == kNone || m1 - m0 > kSlack);
+                        keep[row] = !up ? 1.0f : m0 == kNone ? 0.0f : ex2(m0 - m1);
+                        if (up) ref[row] = m1;
+                    }
+                    vote(false);
+                    const bool wrote = t >= g.t0 + 2;
+                    if (wrote) {  // the products so far have to be in
+                        ok = bar_wait(smem_addr(&bar.p_empty[w][(cnt - 1) & 1]), ((cnt - 1) >> 1) & 1, dead);
+                        ok = __all_sync(0xffffffffu, ok);
+                        fence_after_sync();
+                    }
+#pragma unroll
+                    for (int c = 0; c < NR; c += 32) {
+                        if (wrote) {
+                            float o[32];
+                            tmem_load32(ot + c, o);
+                            tmem_load_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] *= keep[c + k];
+                            tmem_store32(ot + c, reinterpret_cast<const uint32_t *>(o));
+                            tmem_store_wait();
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) l[c + k] *= keep[c + k];
+                    }
+                }
+                // Weights, and their place as the product's operand: a row per position.
+                ok = ok && bar_wait(smem_addr(&bar.p_empty[w][buf]), phase ^ 1, dead);
+                uint8_t *pb = pt + (w * 2 + buf) * S::kP;
+                if (E4M3) {
+#pragma unroll
+                    for (int c = 0; c < NR; c += 16) {
+                        if (c >= n_rows) break;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 m4 = *reinterpret_cast<const float4 *>(&ref[c + 4 * k]);
+                            float *x = s + c + 4 * k;
+                            const float x0 = ex2(x[0] - m4.x), x1 = ex2(x[1] - m4.y), x2 = ex2(x[2] - m4.z),
+                                        x3 = ex2(x[3] - m4.w);
+                            float *y = l + c + 4 * k;
+                            y[0] = fmaf(x0, fl, y[0]), y[1] = fmaf(x1, fl, y[1]);
+                            y[2] = fmaf(x2, fl, y[2]), y[3] = fmaf(x3, fl, y[3]);
+                            const uint32_t e = e4m3_pair(x0, x1), f = e4m3_pair(x2, x3);
+                            const float2 ex = e4m3_values(e), fx = e4m3_values(f);
+                            hi[k] = e | f << 16;
+                            lo[k] = e4m3_pair(x0 - ex.x, x1 - ex.y) | e4m3_pair(x2 - fx.x, x3 - fx.y) << 16;
+                        }
+                        const uint32_t o = swizzled<S::kPRow>(row, c);
+                        *reinterpret_cast<uint4 *>(pb + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(pb + S::kPMat + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NR; c += 8) {
+                        if (c >= n_rows) break;
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int k = 0; k < 8; k += 4) {
+                            const float4 m4 = *reinterpret_cast<const float4 *>(&ref[c + k]);
+                            float *x = s + c + k, *y = l + c + k;
+                            const float x0 = ex2(x[0] - m4.x), x1 = ex2(x[1] - m4.y), x2 = ex2(x[2] - m4.z),
+                                        x3 = ex2(x[3] - m4.w);
+                            y[0] += x0, y[1] += x1, y[2] += x2, y[3] += x3;
+                            pk[k / 2] = bf16_pair(x0, x1);
+                            pk[k / 2 + 1] = bf16_pair(x2, x3);
+                        }
+                        *reinterpret_cast<uint4 *>(pb + swizzled<S::kPRow>(row, 2 * c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                }
+                if (!whole && clean_values<D, E4M3>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[seg & 15] = 1;
+                fence_async_proxy();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.p_full[w][buf]));
+                ek = ek_next;
+                ev = ev_next;
+            }
+            if (!live) break;
+            // ---- the group's partial result of the segment
+            const bool wrote = first_tile < g.t1;
+            if (wrote) {
+                ok = ok && bar_wait(smem_addr(&bar.p_empty[w][(cnt - 1) & 1]), ((cnt - 1) >> 1) & 1, dead);
+                fence_after_sync();
+                __syncwarp();
+                float sum[NR / 32];
+                fold_columns<NR>(l, sum, [](float x, float y) { return x + y; });
+#pragma unroll
+                for (int k = 0; k < NR / 32; ++k) sh.red[w][quad][lane * (NR / 32) + k] = sum[k];
+            }
+            if (vote(!ok)) {
+                live = false;
+                break;
+            }
+            const bool failed = reinterpret_cast<volatile int *>(sh.fail)[seg & 15] != 0;
+            const bool odd = reinterpret_cast<volatile int *>(sh.odd)[seg & 15] != 0;
+            if (row < n_rows) {
+                const float m = ref[row];
+                const float sum = !wrote ? 0.0f : (sh.red[w][0][row] + sh.red[w][1][row]) + (sh.red[w][2][row] + sh.red[w][3][row]);
+                ml[row] = make_float2(m == kNone ? kNegInf : m, failed ? NAN : sum);
+            }
+            if (wrote && row < D) {
+                float *o = u.o + part * u.rc * D + row;
+#pragma unroll
+                for (int c = 0; c < NR; c += 32) {
+                    if (c >= n_rows) break;
+                    float v[32];
+                    tmem_load32(ot + c, v);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c + k < n_rows) o[static_cast<long long>(c + k) * D] = v[k];
+                }
+                if (odd) add_odd_values<D, E4M3, NR>(a, g, rows, row, o);
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&bar.q_empty[half]));
+            ++seg;
+            tile += g.t1 - g.t0;
+        }
+        if (!live && row == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 9) tmem_free(tmem, S::kColumns);
+    // Launched beside the prefix's kernel: this grid ends after that one.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <int D, bool E4M3, bool EXTRA, int NR>
+int launch_shape(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,
+                 cudaStream_t st) {
+    static int done[64];
+    auto kernel = attn_few_kernel<D, E4M3, EXTRA, NR>;
+    if (!allow_smem(kernel, Layout<D, E4M3, NR>::kBytes, done)) return SPEC_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = Layout<D, E4M3, NR>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, ka, kmap, vmap) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+template <int D, bool E4M3, bool EXTRA>
+int launch_rows(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,
+                cudaStream_t st) {
+    const int rows = ka.p.do_shared ? ka.p.shared.rows : ka.p.own.rows;
+    return rows <= 32 ? launch_shape<D, E4M3, EXTRA, 32>(ka, grid, kmap, vmap, dependent, st)
+                      : launch_shape<D, E4M3, EXTRA, 64>(ka, grid, kmap, vmap, dependent, st);
+}
+
+}  // namespace
+
+int launch_few(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,
+               cudaStream_t st) {
+    const bool extra = ka.a.cap > 0.0f || ka.a.slopes, wide = ka.a.c.D == 128;
+    if (ka.a.c.e4m3)
+        return extra ? (wide ? launch_rows<128, true, true>(ka, grid, kmap, vmap, dependent, st)
+                             : launch_rows<64, true, true>(ka, grid, kmap, vmap, dependent, st))
+                     : (wide ? launch_rows<128, true, false>(ka, grid, kmap, vmap, dependent, st)
+                             : launch_rows<64, true, false>(ka, grid, kmap, vmap, dependent, st));
+    return extra ? (wide ? launch_rows<128, false, true>(ka, grid, kmap, vmap, dependent, st)
+                         : launch_rows<64, false, true>(ka, grid, kmap, vmap, dependent, st))
+                 : (wide ? launch_rows<128, false, false>(ka, grid, kmap, vmap, dependent, st)
+                         : launch_rows<64, false, false>(ka, grid, kmap, vmap, dependent, st));
+}
+
+}  // namespace specv

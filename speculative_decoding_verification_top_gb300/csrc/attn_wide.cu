@@ -1,0 +1,647 @@
+// attn_wide.cu -- attention of units with many query rows: a candidate tree's
+// nodes, or a whole batch over its shared prefix.
+//
+// attn_wide_kernel   persistent, one CTA per SM; its share of the tiles (see
+//                    attn.cu) segment by segment.
+//   warps 0-3, 4-7   two softmax groups, a thread per query row: S from TMEM,
+//                    2^(t - m), P back into TMEM over S
+//   warp 8           loads key and value tiles page by page (TMA)
+//   warp 9           issues the products (tcgen05, M = 128 rows): S = Q K^T,
+//                    then O += P V with P in TMEM
+//   warp 10          the e4m3 cache's exponents, as factors
+//   warp 11          the query tiles of the next segment
+// A unit of over 128 rows gives each group 128 rows of its own and both work
+// on every tile; a smaller one alternates its tiles between the groups, so
+// that one group's softmax runs under the other's products.  TMEM: two S of
+// 128 columns and two O of D.
+//
+// e4m3 cache: S = Q1 K^T + Q2 K^T with the query's two e4m3 terms, at the
+// e4m3 rate, costs what one bf16 product does; the weights likewise (two
+// terms, 2^-8 relative at worst).  A key's exponent multiplies its column of
+// S; a value's is added to t, so that the weight carries it, and taken back
+// in l.
+
+#include "attn_plan.cuh"
+
+namespace specv {
+namespace {
+
+constexpr int kScaleRing = 4;
+
+struct Barriers {
+    unsigned long long full[kMaxSlots], empty[kMaxSlots];
+    unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
+    unsigned long long q_full[2], q_empty[2], o_full[2], s_full[2], p_full[2], drained;
+};
+
+struct Shared {
+    Barriers bar;
+    Start start;
+    uint32_t tmem;
+    int dead;      // a wait ran out: everyone leaves
+    int fail[16];  // per segment (mod 16): a page id out of range
+    int odd[16];   // per segment (mod 16): a cleaned tile held values that are not finite
+};
+
+template <int D, bool E4M3>
+struct Layout : Shape<D, E4M3> {
+    using S = Shape<D, E4M3>;
+    static constexpr int kQ = E4M3 ? 2 * S::kMat : S::kSlot;  // a group's query tile
+    // factors of the positions, and of the query rows
+    static constexpr int kScale = E4M3 ? (kScaleRing * 3 * kTile + 2 * kGroupRows) * 4 : 0;
+    static constexpr int kFixed = kScale + static_cast<int>((sizeof(Shared) + 127) / 128 * 128);
+    static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ) / S::kSlot;
+    static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
+    static constexpr int kBytes = kFixed + 2 * kQ + kSlots * S::kSlot;
+};
+
+// What a softmax thread holds of its row.
+struct Row {
+    int b, n, tok;           // sequence, new token, token of the batch
+    int first, pos_i;        // own position of token 0, the token's position index
+    bool has;
+    float rs, slope;         // score factor (the log2 e and the query's own in it), slope * log2 e
+    float m, l;              // reference maximum and sum
+};
+
+// In a tile of positions that some rows do not see: the columns of each 32
+// that this row sees, and the position index of this lane's column in each.  A
+// row's set depends on its token alone, so the warp, a lane a column, finds
+// the sets of its tokens (consecutive ones) four at a time, all their mask
+// bytes in flight together.
+__device__ __noinline__ void seen_columns(const AttnArgs &a, const Segment g, const Row x, int j0, uint32_t (&seen)[4],
+                                          int (&pos_col)[4]) {
+    constexpr int kAtOnce = 4;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rows = __ballot_sync(0xffffffffu, x.has);
+    const int lo = __shfl_sync(0xffffffffu, x.tok, 0), hi = __shfl_sync(0xffffffffu, x.tok, 31 - __clz(rows));
+    bool held[4], node[4];
+    int c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i * 32 + lane;
+        c[i] = j - x.first;
+        held[i] = j < g.len;
+        node[i] = !g.shared && c[i] >= 0 && held[i];
+        pos_col[i] = (g.shared ? 0 : a.shared_len) + j;
+        if (node[i] && a.pos) pos_col[i] = a.pos[static_cast<long long>(x.b) * a.N + c[i]];
+        seen[i] = 0;
+    }
+    for (int tok = lo; tok <= hi; tok += kAtOnce) {
+        uint8_t m[kAtOnce][4];
+        int n[kAtOnce], pos_i[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int tk = min(tok + k, hi);
+            const uint32_t who = __ballot_sync(0xffffffffu, x.has && x.tok == tk);
+            n[k] = __shfl_sync(0xffffffffu, x.n, __ffs(who) - 1);
+            pos_i[k] = __shfl_sync(0xffffffffu, x.pos_i, __ffs(who) - 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m[k][i] = !node[i] ? 1 : a.mask ? a.mask[static_cast<long long>(tk) * a.N + c[i]] : c[i] <= n[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool y = held[i] && m[k][i] != 0 &&
+                               (a.window == 0 || static_cast<long long>(pos_i[k]) - pos_col[i] < a.window);
+                const uint32_t word = __ballot_sync(0xffffffffu, y);
+                if (x.has && x.tok == tok + k) seen[i] = word;
+            }
+    }
+}
+
+// t of 32 columns from column `col` of a tile, from the raw products v in
+// place; returns their maximum.
+template <bool E4M3, bool EXTRA>
+__device__ __forceinline__ float scores32(const AttnArgs &a, const Segment &g, const Row &x, int j0, int col, bool whole,
+                                          uint32_t seen, int pos_col, const float *fa, float (&v)[32]) {
+    // The bias of a whole tile: slope * (position index - pos_i), linear in the column.
+    const float base = EXTRA ? x.slope * static_cast<float>((g.shared ? 0 : a.shared_len) + j0 + col - x.pos_i) : 0.0f;
+    const float capl = a.cap * kLog2e;
+    float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        float4 k4 = {}, b4 = {};
+        if (E4M3) {
+            k4 = *reinterpret_cast<const float4 *>(fa + col + c);
+            b4 = *reinterpret_cast<const float4 *>(fa + kTile + col + c);
+        }
+        const float fk[4] = {k4.x, k4.y, k4.z, k4.w}, fb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float y = v[c + k];
+            if (E4M3) y *= fk[k];
+            if (EXTRA) {
+                y = a.cap > 0.0f ? capped(y * x.rs, capl) : y * x.rs;
+                if (!whole && a.pos)
+                    y = fmaf(x.slope, static_cast<float>(__shfl_sync(0xffffffffu, pos_col, c + k) - x.pos_i), y);
+                else
+                    y += fmaf(x.slope, static_cast<float>(c + k), base);
+                if (E4M3) y += fb[k];
+            } else {
+                y = E4M3 ? fmaf(y, x.rs, fb[k]) : y * x.rs;
+            }
+            if (!whole && !(seen >> (c + k) & 1u)) y = kNegInf;
+            v[c + k] = y;
+            top[k & 1] = fmaxf(top[k & 1], y);
+        }
+    }
+    return fmaxf(top[0], top[1]);
+}
+
+// Weights 2^(t mul - ref) of 32 columns into TMEM as the product's operand: 16
+// columns of bf16 pairs, or 8 of first and 8 of second e4m3 terms.  Returns
+// their sum, in e4m3 without the values' exponents (fc: 2^-ev).
+template <bool E4M3>
+__device__ __forceinline__ float weights32(uint32_t dst, float mul, float ref, const float *fc, const float (&t)[32]) {
+    float sum[4] = {};
+    uint32_t pk[16];
+    if (E4M3) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(fc + c);
+            const float x0 = ex2(t[c] - ref), x1 = ex2(t[c + 1] - ref);
+            const float x2 = ex2(t[c + 2] - ref), x3 = ex2(t[c + 3] - ref);
+            sum[0] = fmaf(x0, f4.x, sum[0]);
+            sum[1] = fmaf(x1, f4.y, sum[1]);
+            sum[2] = fmaf(x2, f4.z, sum[2]);
+            sum[3] = fmaf(x3, f4.w, sum[3]);
+            const uint32_t u = e4m3_pair(x0, x1), v = e4m3_pair(x2, x3);
+            const float2 y = e4m3_values(u), z = e4m3_values(v);
+            pk[c / 4] = u | v << 16;
+            pk[8 + c / 4] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const float x0 = ex2(fmaf(t[c], mul, -ref)), x1 = ex2(fmaf(t[c + 1], mul, -ref));
+            sum[c & 2] += x0;
+            sum[(c & 2) + 1] += x1;
+            pk[c / 2] = bf16_pair(x0, x1);
+        }
+    }
+    tmem_store16(dst, pk);
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Moves the row's reference maximum up to `top` where that is needed,
+// rescaling the sum and, if there is one, the accumulator in TMEM.
+template <int D, bool E4M3>
+__device__ __forceinline__ void grow(Row &x, float top, bool wrote, uint32_t ot) {
+    const bool up = top > x.m + (E4M3 ? kSlackE4M3 : kSlackBf16);
+    if (!__any_sync(0xffffffffu, up)) return;
+    const float keep = up ? ex2(x.m - top) : 1.0f;
+    if (up) x.m = top;
+    x.l *= keep;
+    if (!wrote) return;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_load32(ot + c, o);
+        tmem_load_wait();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= keep;
+        tmem_store32(ot + c, reinterpret_cast<const uint32_t *>(o));
+    }
+}
+
+// One tile of one row, twice over it, so that 32 values are worked on (and 32
+// on their way) at a time: the maximum, with t back into TMEM where it is more
+// than a multiple of the product; then the weights.
+template <int D, bool E4M3, bool EXTRA>
+__device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g, Row &x, int j0, bool whole, bool wrote,
+                                             uint32_t st, uint32_t ot, const float *fa) {
+    float top = kNegInf, mul = 1.0f, t[2][32];
+    if (!E4M3 && !EXTRA && whole) {
+        tmem_load32(st, t[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            tmem_load_wait();
+            if (c < 3) tmem_load32(st + (c + 1) * 32, t[(c + 1) & 1]);
+            float u[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+            for (int k = 0; k < 32; ++k) u[k & 3] = fmaxf(u[k & 3], t[c & 1][k]);
+            top = fmaxf(top, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
+        }
+        top *= x.rs;  // rs >= 0
+        mul = x.rs;
+    } else {
+        uint32_t seen[4] = {};
+        int pos_col[4] = {};
+        if (!whole) seen_columns(a, g, x, j0, seen, pos_col);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            tmem_load32(st + c * 32, t[0]);
+            tmem_load_wait();
+            top = fmaxf(top, scores32<E4M3, EXTRA>(a, g, x, j0, c * 32, whole, seen[c], pos_col[c], fa, t[0]));
+            tmem_store32(st + c * 32, reinterpret_cast<const uint32_t *>(t[0]));
+        }
+    }
+    grow<D, E4M3>(x, top, wrote, ot);
+    const float ref = x.m == kNegInf ? 0.0f : x.m - (E4M3 ? kLiftE4M3 : 0.0f);
+    tmem_store_wait();
+    tmem_load32(st, t[0]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tmem_load_wait();
+        if (c < 3) tmem_load32(st + (c + 1) * 32, t[(c + 1) & 1]);
+        x.l += weights32<E4M3>(st + c * 16, mul, ref, fa + 2 * kTile + c * 32, t[c & 1]);
+    }
+    tmem_store_wait();
+}
+
+// Adds to the 32 output columns from `col` on what the products left out:
+// values that are not finite, of the positions the row sees in the segment's
+// cleaned tiles.  (In a tile that was not cleaned they are in the sum already,
+// and adding them again changes nothing.)
+template <int D, bool E4M3>
+__device__ __noinline__ void add_odd_values(const AttnArgs &a, const Segment g, const Row x, int col, float *dst) {
+    for (int t = g.t0; t < g.t1; ++t) {
+        for (int j = t * kTile; j < min(g.len, (t + 1) * kTile); ++j) {
+            int pj, slot;
+            if (g.shared ? a.window > 0 && static_cast<long long>(x.pos_i) - j >= a.window
+                         : !sees(a, x.b, x.n, x.pos_i, x.first, g.len, j, &pj))
+                continue;
+            const int page = page_of(a.c, pages_of(a, g), INT_MAX, j, &slot);
+            if (page < 0) continue;
+            const long long at = cache_row(a.c, page, g.h, slot) * D + col;
+            for (int k = 0; k < 32; ++k) {
+                const float y = odd_value<E4M3>(a.c, at + k);
+                if (!isfinite(y)) dst[k] += y;
+            }
+        }
+    }
+}
+
+template <int D, bool E4M3, bool EXTRA>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_wide_kernel(const __grid_constant__ KernelArgs ka, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+    using S = Layout<D, E4M3>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const AttnArgs &a = ka.a;
+    const Plan &p = ka.p;
+    uint8_t *qt = smem, *ring = qt + 2 * S::kQ;
+    float *scales = reinterpret_cast<float *>(ring + S::kSlots * S::kSlot);
+    float *q_factor = scales + kScaleRing * 3 * kTile;  // [2][kGroupRows], e4m3
+    Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(scales) + S::kScale);
+    Barriers &bar = sh.bar;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    if (tid == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            bar_init(smem_addr(&bar.full[i]), 1);
+            bar_init(smem_addr(&bar.empty[i]), 1);
+        }
+        for (int i = 0; i < kScaleRing; ++i) {
+            bar_init(smem_addr(&bar.scale_full[i]), 1);
+            bar_init(smem_addr(&bar.scale_empty[i]), 8);
+        }
+        for (int w = 0; w < 2; ++w) {
+            bar_init(smem_addr(&bar.q_full[w]), 1);
+            bar_init(smem_addr(&bar.q_empty[w]), 9);  // the products, and eight softmax warps
+            bar_init(smem_addr(&bar.o_full[w]), 1);
+            bar_init(smem_addr(&bar.s_full[w]), 1);
+            bar_init(smem_addr(&bar.p_full[w]), 4);
+        }
+        bar_init(smem_addr(&bar.drained), 1);
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_proxy();
+    }
+    if (warp == 9) tmem_alloc(smem_addr(&sh.tmem), 512);
+    long long from, to;
+    find_share(p, sh.start, &from, &to);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    volatile int *dead = &sh.dead;
+    Walk walk(p, from, to, sh.start.b0, sh.start.base0);
+    Segment g;
+    {
+        // The first segment's query tiles: everyone takes a share.
+        Walk ahead = walk;
+        if (ahead.next(&g))
+            for (int w = 0; w < (g.dual ? 2 : 1); ++w)
+                stage_queries<D, E4M3>(a, g, g.row0 + w * kGroupRows, min(kGroupRows, g.rows - w * kGroupRows), kGroupRows,
+                                       qt + w * S::kQ, q_factor + w * kGroupRows, tid, kAttnThreads);
+        fence_async_proxy();
+        __syncthreads();
+    }
+
+    if (warp == 8) {
+        // ---- loads.  Alternating tiles: K0 K1 V0 K2 V1 ...; both groups on each
+        // tile: K0 V0 K1 V1 ...
+        Loader<D, E4M3, S::kSlots> load;
+        int seg = 0;
+        bool live = true;
+        while (live && walk.next(&g)) {
+            if (lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
+            __syncwarp();
+            const int n = g.t1 - g.t0;
+            int kt = 0, vt = 0;
+            for (int i = 0; live && i < 2 * n; ++i) {
+                const bool key = kt < n && (kt == vt || (!g.dual && kt == vt + 1));
+                live = load.tile(a, g, pages_of(a, g), g.t0 + (key ? kt++ : vt++), key ? &kmap : &vmap, smem_addr(ring),
+                                 bar.full, bar.empty, dead, &sh.fail[seg & 15]);
+            }
+            ++seg;
+        }
+        if (!live) load.drain(bar.full);
+    } else if (warp == 9) {
+        // ---- products
+        if (elect_one()) {
+            constexpr uint32_t kQk = mma_desc(E4M3, kTile, false, false), kPv = mma_desc(E4M3, D, false, true);
+            constexpr uint32_t kHi = kMatrixHi<S::kRow>;
+            uint32_t segs = 0, qn = 0, pn[2] = {0, 0};
+            uint32_t slot = 0, phase = 0;  // the ring, in the order it is filled
+            bool live = true;
+            const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(ring), 0);
+            const uint32_t v0 = matrix_lo(smem_addr(ring), S::kMat);
+            const uint32_t full0 = smem_addr(&bar.full[0]), empty0 = smem_addr(&bar.empty[0]);
+            const uint32_t s_full = smem_addr(&bar.s_full[0]), p_full = smem_addr(&bar.p_full[0]);
+            auto advance = [&] {
+                if (++slot == S::kSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            // S of group w from the query tile qi and the key tile in slot s
+            auto scores = [&](uint32_t w, uint32_t qi, uint32_t s) {
+                const uint32_t q = q0 + qi * (S::kQ >> 4), k = k0 + s * (S::kSlot >> 4), d = tmem + w * kTile;
+                if (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < 2 * (D / 32); ++i) {
+                        const uint32_t half = i / (D / 32), j = i % (D / 32);
+                        mma_ss<true>(d, q + ((half * S::kMat + j * 32) >> 4), kHi, k + (j * 32 >> 4), kHi, kQk, i > 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t o = ((i / 4) * S::kMat + (i % 4) * 32) >> 4;
+                        mma_ss<false>(d, q + o, kHi, k + o, kHi, kQk, i > 0);
+                    }
+                }
+            };
+            // O += P V of group w with the value tile in slot s
+            auto values = [&](uint32_t w, uint32_t s, bool first) {
+                const uint32_t v = v0 + s * (S::kSlot >> 4), d = tmem + 2 * kTile + w * D, pt = tmem + w * kTile;
+                if (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t j = i % 4;
+                        mma_ts<true>(d, pt + j * 16 + (i / 4) * 8, v + (j * 32 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mma_ts<false>(d, pt + i * 8, v + (i * 16 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
+                }
+            };
+            while (live && walk.next(&g)) {
+                const int T = g.t1 - g.t0, lead = g.dual ? 1 : min(2, T);
+                uint32_t qi[2];  // the groups' query tiles
+                qi[0] = qi[1] = qn & 1;
+                live = bar_wait(smem_addr(&bar.q_full[qn & 1]), (qn >> 1) & 1, dead);
+                ++qn;
+                if (g.dual) {
+                    qi[1] = qn & 1;
+                    live = live && bar_wait(smem_addr(&bar.q_full[qn & 1]), (qn >> 1) & 1, dead);
+                    ++qn;
+                }
+                for (int t = 0; live && t < lead; ++t) {  // scores of each group's first tile
+                    if (!(live = bar_wait(full0 + 8 * slot, phase, dead))) break;
+                    fence_after_sync();
+                    if (g.dual) {
+                        scores(0, qi[0], slot);
+                        mma_commit(s_full);
+                        scores(1, qi[1], slot);
+                        mma_commit(s_full + 8);
+                    } else {
+                        scores(t, qi[0], slot);
+                        mma_commit(s_full + 8 * t);
+                    }
+                    mma_commit(empty0 + 8 * slot);
+                    advance();
+                }
+                for (int t = 0; live && t < T; ++t) {
+                    const uint32_t vs = slot, vp = phase;
+                    advance();
+                    const bool more = t + lead < T;
+                    const uint32_t ks = slot, kp = phase;
+                    if (more) advance();
+                    if (!(live = bar_wait(full0 + 8 * vs, vp, dead))) break;
+                    const uint32_t w0 = g.dual ? 0 : t & 1, w1 = g.dual ? 1 : t & 1;
+                    for (uint32_t w = w0; w <= w1; ++w) {
+                        if (!(live = bar_wait(p_full + 8 * w, pn[w]++ & 1, dead))) break;
+                        fence_after_sync();
+                        values(w, vs, g.dual ? t == 0 : t < 2);
+                        if (w == w1) mma_commit(empty0 + 8 * vs);
+                        if (!more) continue;
+                        if (!(live = bar_wait(full0 + 8 * ks, kp, dead))) break;
+                        scores(w, qi[w], ks);
+                        mma_commit(s_full + 8 * w);
+                        if (w == w1) mma_commit(empty0 + 8 * ks);
+                    }
+                }
+                if (live) {
+                    mma_commit(smem_addr(&bar.o_full[segs++ & 1]));
+                    mma_commit(smem_addr(&bar.q_empty[qi[0]]));
+                    if (g.dual) mma_commit(smem_addr(&bar.q_empty[qi[1]]));
+                }
+            }
+            if (!live) {  // products in flight end before TMEM is freed
+                mma_commit(smem_addr(&bar.drained));
+                bar_drain(smem_addr(&bar.drained), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- the e4m3 exponents as factors: 2^ek, ev, 2^-ev of every position
+        if (E4M3) {
+            uint32_t n = 0;
+            bool live = true;
+            while (live && walk.next(&g)) {
+                for (int t = g.t0; t < g.t1; ++t, ++n) {
+                    const int j = t * kTile + lane * 4;
+                    int slot = 0;
+                    const int page = j < g.len ? page_of(a.c, pages_of(a, g), INT_MAX, j, &slot) : -1;
+                    uint32_t ek = 0, ev = 0;
+                    if (page >= 0) {
+                        const long long row = cache_row(a.c, page, g.h, slot);
+                        ek = __ldg(reinterpret_cast<const uint32_t *>(a.c.k_exp + row));
+                        ev = __ldg(reinterpret_cast<const uint32_t *>(a.c.v_exp + row));
+                    }
+                    const uint32_t s = n % kScaleRing;
+                    live = bar_wait(smem_addr(&bar.scale_empty[s]), ((n / kScaleRing) & 1) ^ 1, dead);
+                    live = __all_sync(0xffffffffu, live);
+                    if (!live) break;
+                    float *f = scales + s * 3 * kTile + lane * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int x = exponent_of(ek, i), y = exponent_of(ev, i);
+                        f[i] = exp2i(x);
+                        f[kTile + i] = static_cast<float>(y);
+                        f[2 * kTile + i] = exp2i(-y);
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(smem_addr(&bar.scale_full[s]));
+                }
+            }
+        }
+    } else if (warp == 11) {
+        // ---- query tiles, a segment ahead where the ring of two has room (the
+        // first segment's are there)
+        uint32_t qn = 0;
+        bool live = true;
+        for (bool first = true; live && walk.next(&g); first = false) {
+            for (int w = 0; live && w < (g.dual ? 2 : 1); ++w, ++qn) {
+                if (!first) {
+                    live = bar_wait(smem_addr(&bar.q_empty[qn & 1]), ((qn >> 1) & 1) ^ 1, dead);
+                    live = __all_sync(0xffffffffu, live);
+                    if (!live) break;
+                    stage_queries<D, E4M3>(a, g, g.row0 + w * kGroupRows, min(kGroupRows, g.rows - w * kGroupRows),
+                                           kGroupRows, qt + (qn & 1) * S::kQ, q_factor + (qn & 1) * kGroupRows, lane, 32);
+                    fence_async_proxy();
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.q_full[qn & 1]));
+            }
+        }
+    } else if (warp < 8) {
+        // ---- softmax groups
+        const int w = warp >> 2, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's TMEM lanes
+        const uint32_t st = tmem + lanes + w * kTile, ot = tmem + lanes + 2 * kTile + w * D;
+        const float mul = (a.cap > 0.0f ? fabsf(a.scale) / a.cap : fabsf(a.scale) * kLog2e);
+        uint32_t segs = 0, qn = 0, sn = 0, n_ring = 0, n_scale = 0;
+        bool live = true;
+        while (live && walk.next(&g)) {
+            const int T = g.t1 - g.t0, row0 = g.row0 + (g.dual ? w * kGroupRows : 0);
+            const int rows = min(kGroupRows, g.rows - (g.dual ? w * kGroupRows : 0));
+            const bool has = row < rows, active = (row & ~31) < rows;
+            const int r = row0 + row, tok_in = has ? r / a.G : 0, head = g.h * a.G + (has ? r % a.G : 0);
+            Row x;
+            x.tok = g.shared ? tok_in : g.b * a.N + tok_in;
+            x.b = g.shared ? (has ? x.tok / a.N : 0) : g.b;
+            x.n = has ? x.tok - x.b * a.N : 0;
+            x.first = (g.shared ? (has ? a.lens[x.b] : 0) : g.len) - a.N;
+            x.pos_i = !has ? 0 : a.pos ? a.pos[x.tok] : a.shared_len + x.first + x.n;
+            x.has = has;
+            x.rs = mul;
+            if (E4M3) {
+                const uint32_t qi = qn + (g.dual ? w : 0);
+                live = bar_wait(smem_addr(&bar.q_full[qi & 1]), (qi >> 1) & 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+                x.rs *= q_factor[(qi & 1) * kGroupRows + row];
+            }
+            x.slope = EXTRA && a.slopes && has ? a.slopes[head] * kLog2e : 0.0f;
+            x.m = kNegInf;
+            x.l = 0.0f;
+            const int last_pos = a.window > 0 ? last_position(a, g) : 0;
+            bool wrote = false;
+            for (int t = g.t0; t < g.t1; ++t) {
+                const int idx = t - g.t0;
+                if (!g.dual && (idx & 1) != w) continue;
+                const int j0 = t * kTile;
+                const bool whole = sees_whole(a, g, j0, last_pos);
+                live = bar_wait(smem_addr(&bar.s_full[w]), sn++ & 1, dead);
+                const float *fa = nullptr;
+                if (E4M3) {
+                    const uint32_t s = (n_scale + idx) % kScaleRing;
+                    live = live && bar_wait(smem_addr(&bar.scale_full[s]), ((n_scale + idx) / kScaleRing) & 1, dead);
+                    fa = scales + s * 3 * kTile;
+                }
+                // the tile's values: slot index as the loads number them
+                const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
+                if (!whole) live = live && bar_wait(smem_addr(&bar.full[vi % S::kSlots]), (vi / S::kSlots) & 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+                fence_after_sync();
+                if (active) softmax_tile<D, E4M3, EXTRA>(a, g, x, j0, whole, wrote, st, ot, fa);
+                wrote = true;
+                if (!whole) {
+                    if (clean_values<D, E4M3>(ring + vi % S::kSlots * S::kSlot, row, j0 + row < g.len)) sh.odd[segs & 15] = 1;
+                    fence_async_proxy();
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(smem_addr(&bar.p_full[w]));
+                    if (E4M3) bar_arrive(smem_addr(&bar.scale_empty[(n_scale + idx) % kScaleRing]), g.dual ? 1 : 2);
+                }
+            }
+            if (!live) break;
+            live = bar_wait(smem_addr(&bar.o_full[segs & 1]), (segs >> 1) & 1, dead);
+            live = __all_sync(0xffffffffu, live);
+            if (!live) break;
+            fence_after_sync();
+            // ---- the group's partial result of the segment
+            const Units &k = g.shared ? p.shared : p.own;
+            const long long at = (static_cast<long long>(g.slot) * 2 + w) * k.rc + row;
+            const bool failed = reinterpret_cast<volatile int *>(sh.fail)[segs & 15] != 0;
+            const bool odd = reinterpret_cast<volatile int *>(sh.odd)[segs & 15] != 0;
+            if (has)
+                k.ml[at] = make_float2(x.m == kNegInf ? kNegInf : x.m - (E4M3 ? kLiftE4M3 : 0.0f), failed ? NAN : x.l);
+            if (active && wrote) {
+                float *o = k.o + at * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    tmem_load32(ot + c, v);
+                    tmem_load_wait();
+                    if (has) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(o + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        if (odd) add_odd_values<D, E4M3>(a, g, x, c, o + c);
+                    }
+                    __syncwarp();
+                }
+            }
+            fence_before_sync();
+            __syncwarp();
+            for (int i = 0; i < (g.dual ? 2 : 1); ++i, ++qn)
+                if (lane == 0) bar_arrive(smem_addr(&bar.q_empty[qn & 1]));
+            ++segs;
+            n_ring += 2 * T;
+            n_scale += T;
+        }
+        if (!live && tid == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 9) tmem_free(tmem, 512);
+}
+
+template <int D, bool E4M3, bool EXTRA>
+int launch_shape(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+    static int done[64];
+    auto kernel = attn_wide_kernel<D, E4M3, EXTRA>;
+    if (!allow_smem(kernel, Layout<D, E4M3>::kBytes, done)) return SPEC_ERR_CUDA;
+    kernel<<<grid, kAttnThreads, Layout<D, E4M3>::kBytes, st>>>(ka, kmap, vmap);
+    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_wide(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+    const bool extra = ka.a.cap > 0.0f || ka.a.slopes, wide = ka.a.c.D == 128;
+    if (ka.a.c.e4m3)
+        return extra ? (wide ? launch_shape<128, true, true>(ka, grid, kmap, vmap, st)
+                             : launch_shape<64, true, true>(ka, grid, kmap, vmap, st))
+                     : (wide ? launch_shape<128, true, false>(ka, grid, kmap, vmap, st)
+                             : launch_shape<64, true, false>(ka, grid, kmap, vmap, st));
+    return extra ? (wide ? launch_shape<128, false, true>(ka, grid, kmap, vmap, st)
+                         : launch_shape<64, false, true>(ka, grid, kmap, vmap, st))
+                 : (wide ? launch_shape<128, false, false>(ka, grid, kmap, vmap, st)
+                         : launch_shape<64, false, false>(ka, grid, kmap, vmap, st));
+}
+
+}  // namespace specv

@@ -68,6 +68,30 @@ __device__ __forceinline__ bool bar_drain(uint32_t bar, uint32_t parity) {
     return true;
 }
 
+// True in one lane of a converged warp.  Code under it counts as one thread's
+// to the compiler, which then keeps descriptors in uniform registers: under
+// `lane == 0` a product took over 100 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// `threads` threads, whole warps, meet at hardware barrier `id`; whether any of
+// them came with x.
+__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(x ? 1u : 0u), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+
 // Generic-proxy writes to shared memory, made visible to TMA and the tensor cores.
 __device__ __forceinline__ void fence_async_proxy() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -202,27 +226,30 @@ __device__ __forceinline__ void tmem_store_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory matrix descriptor of rows of `kRow` bytes (128 or 64), each
+// Shared-memory matrix descriptor of rows of `kRow` bytes (128, 64 or 32), each
 // swizzled over its whole width, eight rows to a pattern: the low word holds
-// the address and `lead`, the bytes between 64-element column blocks where the
-// matrix is wider than a row (the values' second half; unused otherwise).
+// the address and `lead`, the bytes between column blocks of kRow bytes where
+// the matrix's columns are taken along memory and there is more than one.
 __device__ __forceinline__ uint32_t matrix_lo(uint32_t addr, uint32_t lead) { return addr >> 4 | (lead >> 4) << 16; }
 
 template <int kRow>
-constexpr uint32_t kMatrixHi = static_cast<uint32_t>((8 * kRow) >> 4) | 1u << 14 | (kRow == 128 ? 2u : 4u) << 29;
+constexpr uint32_t kMatrixHi = static_cast<uint32_t>((8 * kRow) >> 4) | 1u << 14 |
+                               (kRow == 128 ? 2u : kRow == 64 ? 4u : 6u) << 29;
 
 // Byte offset of (row, byte) in such a matrix: 16-byte units are permuted
-// within a row by the row's place in its pattern of 1024 (512) bytes.
+// within a row by the row's place in its pattern of eight rows.
 template <int kRow>
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t byte) {
+    static_assert(kRow == 128 || kRow == 64 || kRow == 32, "swizzled rows");
     const uint32_t o = row * kRow + byte;
-    return kRow == 128 ? o ^ ((o >> 7 & 7u) << 4) : o ^ ((o >> 7 & 3u) << 4);
+    return o ^ ((o >> 7 & (kRow / 16 - 1)) << 4);
 }
 
-// Instruction descriptor: fp32 accumulators, M = 128, N columns, both operands
-// of one type (bf16, or e4m3), B transposed (its N runs along memory) or not.
-__host__ __device__ constexpr uint32_t mma_desc(bool f8, int n, bool b_along_n) {
-    return 1u << 4 | (f8 ? 0u : 1u << 7 | 1u << 10) | (b_along_n ? 1u << 16 : 0u) |
+// Instruction descriptor: fp32 accumulators, M = 128, N = n columns, both
+// operands of one type (bf16, or e4m3); a_along / b_along: the operand's M or N
+// runs along memory (else its K does).
+__host__ __device__ constexpr uint32_t mma_desc(bool f8, int n, bool a_along, bool b_along) {
+    return 1u << 4 | (f8 ? 0u : 1u << 7 | 1u << 10) | (a_along ? 1u << 15 : 0u) | (b_along ? 1u << 16 : 0u) |
            static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
