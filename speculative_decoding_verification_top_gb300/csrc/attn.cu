@@ -22,37 +22,27 @@
 namespace specv {
 namespace {
 
-// A row's partial results of one unit, kBatch at a time: f(slots, row) with a
-// slot of -1 where a share holds no whole tile of the unit.
-constexpr int kBatch = 4;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 4;                                      // rows a warp
+constexpr int kBlockRows = kJoinRows * kJoinThreads / 32;
 
-template <typename F>
-__device__ __forceinline__ void each_slot(long long share, long long ubase, int T, bool dual, int unit, F f) {
-    const int c = dual ? 2 : 1;
+// The shares that hold tiles of a unit [ubase, ubase + T c) of the cost line:
+// f(first slot, number of shares).  A share may hold less than one whole tile
+// of a unit of two row tiles (c = 2) at its ends: its slot is then not written.
+__device__ __forceinline__ void shares_of(long long share, long long ubase, int T, int c, int *lo, int *hi) {
     const long long uend = ubase + static_cast<long long>(T) * c;
-    int lo, hi;
     if (uend < INT_MAX) {
-        lo = static_cast<int>(ubase) / static_cast<int>(share);
-        hi = static_cast<int>(uend - 1) / static_cast<int>(share);
+        *lo = static_cast<int>(ubase) / static_cast<int>(share);
+        *hi = static_cast<int>(uend - 1) / static_cast<int>(share);
     } else {
-        lo = static_cast<int>(ubase / share);
-        hi = static_cast<int>((uend - 1) / share);
-    }
-    for (int i = lo; i <= hi; i += kBatch) {
-        int slots[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const long long from = (i + k) * share, to = from + share;
-            const long long t0 = from > ubase ? (from - ubase + c - 1) / c : 0;
-            const long long t1 = min(static_cast<long long>(T), (to - ubase + c - 1) / c);
-            slots[k] = i + k <= hi && t0 < t1 ? unit + i + k : -1;
-        }
-        f(slots);
+        *lo = static_cast<int>(ubase / share);
+        *hi = static_cast<int>((uend - 1) / share);
     }
 }
 
-constexpr int kJoinThreads = 256;
-
+// A block joins kBlockRows rows of one (sequence, key/value head), a warp
+// kJoinRows of them together, so that their loads are in flight at once: bound
+// by the latency of the chain lens, line, (m, l), O otherwise.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ KernelArgs ka) {
     constexpr int kV = D / 32;  // elements a lane: a warp holds a row
@@ -62,79 +52,111 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const AttnArgs &a = ka.a;
     const Plan &p = ka.p;
     const int lane = threadIdx.x & 31;
-    const long long at = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    if (at >= static_cast<long long>(p.B) * p.N * a.Hq) return;
-    const int head = static_cast<int>(at % a.Hq), tok = static_cast<int>(at / a.Hq);
-    const int b = tok / p.N, h = head / p.G, r = (tok - b * p.N) * p.G + head % p.G;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int len = p.lens[b];
+    const int chunks = ceil_div(p.own.rows, kBlockRows);
+    const int bh = blockIdx.x / chunks, b = bh / p.Hkv, h = bh - b * p.Hkv;
+    const int r0 = (blockIdx.x - bh * chunks) * kBlockRows + (threadIdx.x >> 5) * kJoinRows;
+    if (r0 >= p.own.rows) return;
+    const int n = min(kJoinRows, p.own.rows - r0);
+    const int len = p.lens[b];  // an input: there before the grids this one follows
     const bool bad = len < 0 || len > (p.width << p.page_shift);
     const Tiles s = tiles_of(p, b);
-    float M = kNegInf, L = 0.0f;
-    Vec acc = {};
-    auto add = [&](const Units &u, int slot0, int slot1, int slot2, int slot3, bool dual, int row) {
-        // Two groups' results a slot: both of this row, or each of its own 128 rows.
-        const int slots[kBatch] = {slot0, slot1, slot2, slot3};
-        float2 x[kBatch][2];
-        Vec y[kBatch][2];
+    float M[kJoinRows], L[kJoinRows];
+    Vec acc[kJoinRows] = {};
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < kJoinRows; ++i) {
+        M[i] = kNegInf;
+        L[i] = 0.0f;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Adds the rows' results of one slot: two groups, both of these rows, or each
+    // of its own 128 rows.
+    auto add = [&](const Units &u, int slot, const int (&row)[kJoinRows], const bool (&dual)[kJoinRows],
+                   const bool (&here)[kJoinRows]) {
+        float2 x[kJoinRows][2];
+        Vec y[kJoinRows][2];
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const bool here = slots[i] >= 0 && (!dual || w == row / kGroupRows);
-                const long long k = (max(slots[i], 0) * 2ll + w) * u.rc + (dual ? row % kGroupRows : row);
-                x[i][w] = here ? u.ml[k] : make_float2(kNegInf, 0.0f);
-                y[i][w] = here ? *reinterpret_cast<const Vec *>(u.o + k * D + lane * kV) : Vec{};
+                const bool some = here[i] && (!dual[i] || w == row[i] / kGroupRows);
+                const long long k = (slot * 2ll + w) * u.rc + (dual[i] ? row[i] % kGroupRows : row[i]);
+                x[i][w] = some ? u.ml[k] : make_float2(kNegInf, 0.0f);
+                y[i][w] = some ? *reinterpret_cast<const Vec *>(u.o + k * D + lane * kV) : Vec{};
             }
-        float top = M;
 #pragma unroll
-        for (int i = 0; i < 2 * kBatch; ++i) {
-            top = fmaxf(top, x[i / 2][i % 2].x);
-            if (isnan(x[i / 2][i % 2].y)) L = NAN;
-        }
-        if (top == kNegInf) return;
-        const float keep = ex2(M - top);
-        M = top;
-        L *= keep;
+        for (int i = 0; i < kJoinRows; ++i) {
+            const float top = fmaxf(M[i], fmaxf(x[i][0].x, x[i][1].x));
+            if (isnan(x[i][0].y) || isnan(x[i][1].y)) L[i] = NAN;
+            if (top == kNegInf) continue;
+            const float keep = ex2(M[i] - top);
+            M[i] = top;
+            L[i] *= keep;
 #pragma unroll
-        for (int k = 0; k < kV; ++k) acc.x[k] *= keep;
+            for (int k = 0; k < kV; ++k) acc[i].x[k] *= keep;
 #pragma unroll
-        for (int i = 0; i < 2 * kBatch; ++i) {
-            const float2 ml = x[i / 2][i % 2];
-            if (ml.x == kNegInf) continue;  // nothing seen: its accumulator was not written
-            const float f = ex2(ml.x - top);
-            L = fmaf(f, ml.y, L);
+            for (int w = 0; w < 2; ++w) {
+                if (x[i][w].x == kNegInf) continue;  // nothing seen: its accumulator was not written
+                const float f = ex2(x[i][w].x - top);
+                L[i] = fmaf(f, x[i][w].y, L[i]);
 #pragma unroll
-            for (int k = 0; k < kV; ++k) acc.x[k] = fmaf(f, y[i / 2][i % 2].x[k], acc.x[k]);
+                for (int k = 0; k < kV; ++k) acc[i].x[k] = fmaf(f, y[i][w].x[k], acc[i].x[k]);
+            }
         }
     };
-    if (p.sT > 0) {
-        const int g = b * p.own.rows + r, u = g / (2 * kGroupRows), row = g % (2 * kGroupRows);
-        const bool dual = p.shared.rows - u * 2 * kGroupRows > kGroupRows;
-        each_slot(p.share[1], static_cast<long long>(h) * p.shared.row_tiles * p.sT + u * 2ll * p.sT, p.sT, dual,
-                  h * p.shared.units + u,
-                  [&](const int *k) { add(p.shared, k[0], k[1], k[2], k[3], dual, row); });
+    // The units of `u` that hold rows first.. (of a unit line that starts at
+    // line, units of T tiles): they may straddle two units.
+    auto join = [&](const Units &u, long long share, long long line, int T, int slot0, int first) {
+        int row[kJoinRows], unit[kJoinRows];
+        bool dual[kJoinRows];
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i) {
+            unit[i] = (first + min(i, n - 1)) / (2 * kGroupRows);
+            row[i] = (first + min(i, n - 1)) % (2 * kGroupRows);
+            dual[i] = u.rows - unit[i] * 2 * kGroupRows > kGroupRows;
+        }
+        for (int k = unit[0]; k <= unit[kJoinRows - 1]; ++k) {
+            const int c = u.rows - k * 2 * kGroupRows > kGroupRows ? 2 : 1;
+            const long long ubase = line + k * 2ll * T;
+            int lo, hi;
+            shares_of(share, ubase, T, c, &lo, &hi);
+#pragma unroll 2
+            for (int i = lo; i <= hi; ++i) {
+                bool written = true;
+                if (c == 2) {
+                    const long long from = i * share, to = from + share;
+                    const long long t0 = from > ubase ? (from - ubase + 1) / 2 : 0;
+                    written = t0 < min(static_cast<long long>(T), (to - ubase + 1) / 2);
+                }
+                bool here[kJoinRows];
+#pragma unroll
+                for (int q = 0; q < kJoinRows; ++q) here[q] = written && unit[q] == k;
+                add(u, slot0 + k + i, row, dual, here);
+            }
+        }
+    };
+    if (p.sT > 0)
+        join(p.shared, p.share[1], static_cast<long long>(h) * p.shared.row_tiles * p.sT, p.sT, h * p.shared.units,
+             b * p.own.rows + r0);
+    if (s.t1 > s.t0)
+        join(p.own, p.share[0], p.base[b] + static_cast<long long>(h) * p.own.row_tiles * (s.t1 - s.t0), s.t1 - s.t0,
+             bh * p.own.units, r0);
+    if (bad && lane == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+        if (i >= n) break;
+        const int r = r0 + i;
+        const long long at = static_cast<long long>(b * p.N + r / p.G) * a.Hq + h * p.G + r % p.G;
+        if (bad) L[i] = NAN;
+        // Nothing seen: L = 0 and every accumulator 0.
+        const float inv = L[i] == 0.0f ? 0.0f : 1.0f / L[i];
+        uint32_t *out = reinterpret_cast<uint32_t *>(a.out + at * D) + lane * (kV / 2);
+        if constexpr (kV == 4)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(bf16_pair(acc[i].x[0] * inv, acc[i].x[1] * inv),
+                                                         bf16_pair(acc[i].x[2] * inv, acc[i].x[3] * inv));
+        else
+            *out = bf16_pair(acc[i].x[0] * inv, acc[i].x[1] * inv);
+        if (a.lse && lane == 0) a.lse[at] = L[i] == 0.0f ? kNegInf : (M[i] + log2f(L[i])) / kLog2e;
     }
-    if (s.t1 > s.t0) {
-        const int T = s.t1 - s.t0, u = r / (2 * kGroupRows), row = r % (2 * kGroupRows);
-        const bool dual = p.own.rows - u * 2 * kGroupRows > kGroupRows;
-        each_slot(p.share[0], p.base[b] + static_cast<long long>(h) * p.own.row_tiles * T + u * 2ll * T, T, dual,
-                  (b * p.Hkv + h) * p.own.units + u,
-                  [&](const int *k) { add(p.own, k[0], k[1], k[2], k[3], dual, row); });
-    }
-    if (bad) {
-        L = NAN;
-        if (lane == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
-    }
-    // Nothing seen: L = 0 and every accumulator 0.
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint32_t *out = reinterpret_cast<uint32_t *>(a.out + at * D) + lane * (kV / 2);
-    if constexpr (kV == 4)
-        *reinterpret_cast<uint2 *>(out) =
-            make_uint2(bf16_pair(acc.x[0] * inv, acc.x[1] * inv), bf16_pair(acc.x[2] * inv, acc.x[3] * inv));
-    else
-        *out = bf16_pair(acc.x[0] * inv, acc.x[1] * inv);
-    if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? kNegInf : (M + log2f(L)) / kLog2e;
 }
 
 // ------------------------------------------------------------------ host
@@ -199,9 +221,8 @@ bool make_map(CUtensorMap *map, void *data, const CacheView &c) {
 
 template <int D>
 int launch_join(const KernelArgs &ka, cudaStream_t st) {
-    const long long rows = static_cast<long long>(ka.p.B) * ka.p.N * ka.a.Hq;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    cfg.gridDim = dim3(static_cast<unsigned>(ka.p.B * ka.p.Hkv * ceil_div(ka.p.own.rows, kBlockRows)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr;

@@ -65,15 +65,19 @@ struct Layout : Shape<D, E4M3> {
     using S = Shape<D, E4M3>;
     static constexpr int kQBlock = NR * S::kRow;                     // a block of the query tile
     static constexpr int kQ = kQBlock * (E4M3 ? 2 : S::kHalves);
-    static constexpr int kPRow = E4M3 ? NR : 2 * NR;                 // bytes of a row of weights
+    static constexpr int kPRow = E4M3 && NR == 64 ? NR : 2 * NR;     // bytes of a row of weights
     static constexpr int kPMat = kTile * kPRow;
-    static constexpr int kP = kPMat * (E4M3 ? 2 : 1);                // one buffer of weights
+    static constexpr int kP = kPMat * (E4M3 && NR == 64 ? 2 : 1);    // one buffer of weights
     static constexpr int kFixed = static_cast<int>((sizeof(Shared<NR>) + 127) / 128 * 128);
     static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ - 4 * kP) / S::kSlot;
     static constexpr int kSlots = kRoom < 2 * kMaxSlots ? kRoom : 2 * kMaxSlots;
     static constexpr int kK = kSlots / 2, kV = kSlots - kK;          // slots of keys, of values
     static constexpr int kBytes = kFixed + 2 * kQ + 4 * kP + kSlots * S::kSlot;
-    static constexpr uint32_t kColumns = NR == 32 ? 256 : 512;       // TMEM: 4 S and 2 O of NR columns
+    // e4m3 with 32 rows: the two terms of the queries, and of the weights, side by
+    // side as 64 columns (half the products; the halves are added on reading).
+    static constexpr bool kPair = E4M3 && NR == 32;
+    static constexpr int kN = kPair ? 2 * NR : NR;                   // columns of a product
+    static constexpr uint32_t kColumns = kN == 32 ? 256 : 512;       // TMEM: 4 S and 2 O of kN columns
 };
 
 // Folds v[0..NR) over a warp's lanes with f: lane i ends up with column(s) i
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else if (warp == 9) {
         // ---- products
         if (elect_one()) {
-            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kPv = mma_desc(E4M3, NR, true, true);
+            constexpr uint32_t kQk = mma_desc(E4M3, S::kN, false, false), kPv = mma_desc(E4M3, S::kN, true, true);
             constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>;
             // Values narrower than 128 columns: the second block is the first again,
             // and its rows of O are not read.
@@ -279,10 +283,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                            bar_wait(s_empty + 8 * buf, ((cnt >> 1) & 1) ^ 1, dead);
                     if (!live) break;
                     fence_after_sync();
-                    const uint32_t k = k0 + ks * (S::kSlot >> 4), q = q0 + qi * (S::kQ >> 4), d = tmem + buf * NR;
+                    const uint32_t k = k0 + ks * (S::kSlot >> 4), q = q0 + qi * (S::kQ >> 4), d = tmem + buf * S::kN;
                     if (E4M3) {
 #pragma unroll
-                        for (int i = 0; i < 2 * (D / 32); ++i) {
+                        for (int i = 0; i < (S::kPair ? 1 : 2) * (D / 32); ++i) {
                             const uint32_t term = i / (D / 32), j = i % (D / 32);
                             mma_ss<true>(d, k + (j * 32 >> 4), kHi, q + ((term * S::kQBlock + j * 32) >> 4), kHi, kQk, i > 0);
                         }
@@ -310,11 +314,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * buf, (cnt >> 1) & 1, dead);
                     if (!live) break;
                     fence_after_sync();
-                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + buf * (S::kP >> 4), d = tmem + (4 + w) * NR;
+                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + buf * (S::kP >> 4), d = tmem + (4 + w) * S::kN;
                     const bool first = tv - g.t0 < 2;  // the group's first tile of the segment
                     if (E4M3) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < (S::kPair ? 4 : 8); ++i) {
                             const uint32_t j = i % 4;
                             mma_ss<true>(d, v + (j * 32 * S::kRow >> 4), kHi,
                                          pb + (((i / 4) * S::kPMat + j * 32 * S::kPRow) >> 4), kPHi, kPv, i > 0 || !first);
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ---- softmax groups
         const int w = warp >> 2, quad = warp & 3, row = tid & 127;  // row: the thread's position in a tile
         const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // this warp's TMEM lanes
-        const uint32_t ot = tmem + lanes + (4 + w) * NR;
+        const uint32_t ot = tmem + lanes + (4 + w) * S::kN;
         constexpr float kSlack = E4M3 ? kSlackE4M3 : kSlackBf16, kLift = E4M3 ? kLiftE4M3 : 0.0f;
         const float capl = a.cap * kLog2e;
         float *ref = sh.ref[w], *keep = sh.keep[w];
@@ -423,7 +427,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
                 float s[NR];
 #pragma unroll
-                for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + (w * 2 + buf) * NR + c, s + c);
+                for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + (w * 2 + buf) * S::kN + c, s + c);
+                float s2[S::kPair ? 32 : 1];
+                if constexpr (S::kPair) tmem_load32(tmem + lanes + (w * 2 + buf) * S::kN + 32, s2);
                 tmem_load_wait();
                 fence_before_sync();
                 __syncwarp();
@@ -445,6 +451,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         float y = s[c + k];
+                        if constexpr (S::kPair) y += s2[c + k];
                         if (E4M3) y *= fk;
                         if (EXTRA) {
                             y = a.cap > 0.0f ? capped(y * rs[k], capl) : y * rs[k];
@@ -492,13 +499,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                     for (int c = 0; c < NR; c += 32) {
                         if (wrote) {
-                            float o[32];
-                            tmem_load32(ot + c, o);
-                            tmem_load_wait();
+#pragma unroll 1
+                            for (int e = 0; e < (S::kPair ? 2 : 1); ++e) {
+                                float o[32];
+                                tmem_load32(ot + e * 32 + c, o);
+                                tmem_load_wait();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= keep[c + k];
-                            tmem_store32(ot + c, reinterpret_cast<const uint32_t *>(o));
-                            tmem_store_wait();
+                                for (int k = 0; k < 32; ++k) o[k] *= keep[c + k];
+                                tmem_store32(ot + e * 32 + c, reinterpret_cast<const uint32_t *>(o));
+                                tmem_store_wait();
+                            }
                         }
 #pragma unroll
                         for (int k = 0; k < 32; ++k) l[c + k] *= keep[c + k];
@@ -528,7 +538,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                         const uint32_t o = swizzled<S::kPRow>(row, c);
                         *reinterpret_cast<uint4 *>(pb + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(pb + S::kPMat + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4 *>(S::kPair ? pb + swizzled<S::kPRow>(row, 32 + c) : pb + S::kPMat + o) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 } else {
 #pragma unroll
@@ -586,7 +597,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (c >= n_rows) break;
                     float v[32];
                     tmem_load32(ot + c, v);
-                    tmem_load_wait();
+                    if constexpr (S::kPair) {
+                        float v2[32];
+                        tmem_load32(ot + 32, v2);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] += v2[k];
+                    } else {
+                        tmem_load_wait();
+                    }
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (c + k < n_rows) o[static_cast<long long>(c + k) * D] = v[k];

@@ -68,48 +68,57 @@ struct Row {
 // that this row sees, and the position index of this lane's column in each.  A
 // row's set depends on its token alone, so the warp, a lane a column, finds
 // the sets of its tokens (consecutive ones) four at a time, all their mask
-// bytes in flight together.
-__device__ __noinline__ void seen_columns(const AttnArgs &a, const Segment g, const Row x, int j0, uint32_t (&seen)[4],
-                                          int (&pos_col)[4]) {
+// bytes in flight together.  (Out of line, with its arguments by value: inlined
+// it would cost the main loop registers.)
+struct Seen {
+    uint32_t rows[4];
+    int pos[4];
+};
+
+__device__ __noinline__ Seen seen_columns(const uint8_t *mask, const int32_t *pos, int N, int window, int pos0, bool shared,
+                                          int len, int first, bool has, int tok, int b_tok, int pos_i, int j0) {
     constexpr int kAtOnce = 4;
     const int lane = threadIdx.x & 31;
-    const uint32_t rows = __ballot_sync(0xffffffffu, x.has);
-    const int lo = __shfl_sync(0xffffffffu, x.tok, 0), hi = __shfl_sync(0xffffffffu, x.tok, 31 - __clz(rows));
+    const uint32_t rows = __ballot_sync(0xffffffffu, has);
+    const int lo = __shfl_sync(0xffffffffu, tok, 0), hi = __shfl_sync(0xffffffffu, tok, 31 - __clz(rows));
+    Seen s;
     bool held[4], node[4];
     int c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int j = j0 + i * 32 + lane;
-        c[i] = j - x.first;
-        held[i] = j < g.len;
-        node[i] = !g.shared && c[i] >= 0 && held[i];
-        pos_col[i] = (g.shared ? 0 : a.shared_len) + j;
-        if (node[i] && a.pos) pos_col[i] = a.pos[static_cast<long long>(x.b) * a.N + c[i]];
-        seen[i] = 0;
+        c[i] = j - first;
+        held[i] = j < len;
+        node[i] = !shared && c[i] >= 0 && held[i];
+        s.pos[i] = pos0 + j;
+        if (node[i] && pos) s.pos[i] = pos[b_tok + c[i]];
+        s.rows[i] = 0;
     }
-    for (int tok = lo; tok <= hi; tok += kAtOnce) {
-        uint8_t m[kAtOnce][4];
-        int n[kAtOnce], pos_i[kAtOnce];
+    const uint8_t *row = mask ? mask + static_cast<long long>(lo) * N : nullptr;
+    for (int t = lo; t <= hi; t += kAtOnce) {
+        uint32_t m[kAtOnce][4];
+        int who[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const int tk = min(tok + k, hi);
-            const uint32_t who = __ballot_sync(0xffffffffu, x.has && x.tok == tk);
-            n[k] = __shfl_sync(0xffffffffu, x.n, __ffs(who) - 1);
-            pos_i[k] = __shfl_sync(0xffffffffu, x.pos_i, __ffs(who) - 1);
+            who[k] = __ffs(__ballot_sync(0xffffffffu, has && tok == min(t + k, hi))) - 1;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                m[k][i] = !node[i] ? 1 : a.mask ? a.mask[static_cast<long long>(tk) * a.N + c[i]] : c[i] <= n[k];
+                m[k][i] = !node[i] ? 1u : mask ? row[c[i]] : static_cast<uint32_t>(c[i] <= min(t + k, hi) - b_tok);
+            if (mask && t + k < hi) row += N;
         }
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
+        for (int k = 0; k < kAtOnce; ++k) {
+            const long long at = __shfl_sync(0xffffffffu, pos_i, who[k]);
+            const bool me = has && tok == t + k;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool y = held[i] && m[k][i] != 0 &&
-                               (a.window == 0 || static_cast<long long>(pos_i[k]) - pos_col[i] < a.window);
+                const bool y = held[i] && m[k][i] != 0 && (window == 0 || at - s.pos[i] < window);
                 const uint32_t word = __ballot_sync(0xffffffffu, y);
-                if (x.has && x.tok == tok + k) seen[i] = word;
+                if (me) s.rows[i] = word;
             }
+        }
     }
+    return s;
 }
 
 // t of 32 columns from column `col` of a tile, from the raw products v in
@@ -228,14 +237,15 @@ __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g
         top *= x.rs;  // rs >= 0
         mul = x.rs;
     } else {
-        uint32_t seen[4] = {};
-        int pos_col[4] = {};
-        if (!whole) seen_columns(a, g, x, j0, seen, pos_col);
+        Seen seen = {};
+        if (!whole)
+            seen = seen_columns(a.mask, a.pos, a.N, a.window, g.shared ? 0 : a.shared_len, g.shared, g.len, x.first, x.has,
+                                x.tok, x.b * a.N, x.pos_i, j0);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             tmem_load32(st + c * 32, t[0]);
             tmem_load_wait();
-            top = fmaxf(top, scores32<E4M3, EXTRA>(a, g, x, j0, c * 32, whole, seen[c], pos_col[c], fa, t[0]));
+            top = fmaxf(top, scores32<E4M3, EXTRA>(a, g, x, j0, c * 32, whole, seen.rows[c], seen.pos[c], fa, t[0]));
             tmem_store32(st + c * 32, reinterpret_cast<const uint32_t *>(t[0]));
         }
     }
@@ -589,20 +599,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (has)
                 k.ml[at] = make_float2(x.m == kNegInf ? kNegInf : x.m - (E4M3 ? kLiftE4M3 : 0.0f), failed ? NAN : x.l);
             if (active && wrote) {
-                float *o = k.o + at * D;
+                // Rows go out through this warp's part of the query tile's memory (its
+                // products are done), so that a store instruction covers whole lines.
+                constexpr int kCols = S::kQ >= 32768 ? 32 : 16, kQuads = kCols / 4;
+                float4 *buf = reinterpret_cast<float4 *>(qt + ((qn + (g.dual ? w : 0)) & 1) * S::kQ) +
+                              (g.dual ? warp & 3 : warp) * 32 * kQuads;
+                float *o = k.o + (at - lane) * D;  // the warp's first row
+                const int n = min(32, rows - (row & ~31));
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float v[32];
-                    tmem_load32(ot + c, v);
+                for (int c = 0; c < D; c += kCols) {
+                    float v[kCols];
+                    if constexpr (kCols == 32)
+                        tmem_load32(ot + c, v);
+                    else
+                        tmem_load16(ot + c, v);
                     tmem_load_wait();
-                    if (has) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(o + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                        if (odd) add_odd_values<D, E4M3>(a, g, x, c, o + c);
+                    for (int i = 0; i < kQuads; ++i)
+                        buf[lane * kQuads + (i ^ (lane & (kQuads - 1)))] =
+                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = lane; i < 32 * kQuads; i += 32) {
+                        const int r = i / kQuads, q = i % kQuads;
+                        if (r < n)
+                            *reinterpret_cast<float4 *>(o + static_cast<long long>(r) * D + c + 4 * q) =
+                                buf[r * kQuads + (q ^ (r & (kQuads - 1)))];
                     }
                     __syncwarp();
                 }
+                if (odd && has)
+                    for (int c = 0; c < D; c += 32) add_odd_values<D, E4M3>(a, g, x, c, k.o + at * D + c);
+                __syncwarp();
             }
             fence_before_sync();
             __syncwarp();
