@@ -23,8 +23,7 @@ namespace specv {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 4;                                      // rows a warp
-constexpr int kBlockRows = kJoinRows * kJoinThreads / 32;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
 // The shares that hold tiles of a unit [ubase, ubase + T c) of the cost line:
 // f(first slot, number of shares).  A share may hold less than one whole tile
@@ -40,21 +39,25 @@ __device__ __forceinline__ void shares_of(long long share, long long ubase, int 
     }
 }
 
-// A block joins kBlockRows rows of one (sequence, key/value head), a warp
-// kJoinRows of them together, so that their loads are in flight at once: bound
-// by the latency of the chain lens, line, (m, l), O otherwise.
-template <int D>
+// Joins the rows of one (sequence, key/value head).  SPLIT: a block takes one
+// row, its warps the shares in turn, for units cut into many shares (a long
+// cache of few sequences).  Else a warp takes four rows together, so that their
+// loads are in flight at once: it is bound by the latency of the chain lens,
+// line, (m, l) and O.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ KernelArgs ka) {
+    constexpr int kJoinRows = SPLIT ? 1 : 4;                              // rows a warp
+    constexpr int kBlockRows = SPLIT ? 1 : kJoinRows * kJoinWarps;
     constexpr int kV = D / 32;  // elements a lane: a warp holds a row
     struct alignas(4 * kV) Vec {
         float x[kV];
     };
     const AttnArgs &a = ka.a;
     const Plan &p = ka.p;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunks = ceil_div(p.own.rows, kBlockRows);
     const int bh = blockIdx.x / chunks, b = bh / p.Hkv, h = bh - b * p.Hkv;
-    const int r0 = (blockIdx.x - bh * chunks) * kBlockRows + (threadIdx.x >> 5) * kJoinRows;
+    const int r0 = (blockIdx.x - bh * chunks) * kBlockRows + (SPLIT ? 0 : warp * kJoinRows);
     if (r0 >= p.own.rows) return;
     const int n = min(kJoinRows, p.own.rows - r0);
     const int len = p.lens[b];  // an input: there before the grids this one follows
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             int lo, hi;
             shares_of(share, ubase, T, c, &lo, &hi);
 #pragma unroll 2
-            for (int i = lo; i <= hi; ++i) {
+            for (int i = lo + (SPLIT ? warp : 0); i <= hi; i += SPLIT ? kJoinWarps : 1) {
                 bool written = true;
                 if (c == 2) {
                     const long long from = i * share, to = from + share;
@@ -140,6 +143,24 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     if (s.t1 > s.t0)
         join(p.own, p.share[0], p.base[b] + static_cast<long long>(h) * p.own.row_tiles * (s.t1 - s.t0), s.t1 - s.t0,
              bh * p.own.units, r0);
+    if constexpr (SPLIT) {
+        __shared__ float2 ml[kJoinWarps];
+        __shared__ Vec part[kJoinWarps][32];
+        if (lane == 0) ml[warp] = make_float2(M[0], L[0]);
+        part[warp][lane] = acc[0];
+        __syncthreads();
+        if (warp > 0) return;
+        for (int w = 0; w < kJoinWarps; ++w) M[0] = fmaxf(M[0], ml[w].x);
+        L[0] = 0.0f;
+        acc[0] = Vec{};
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float2 x = ml[w];
+            const float f = x.x == kNegInf ? 0.0f : ex2(x.x - M[0]);
+            L[0] = isnan(x.y) ? NAN : fmaf(f, x.y, L[0]);
+#pragma unroll
+            for (int k = 0; k < kV; ++k) acc[0].x[k] = fmaf(f, part[w][lane].x[k], acc[0].x[k]);
+        }
+    }
     if (bad && lane == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
 #pragma unroll
     for (int i = 0; i < kJoinRows; ++i) {
@@ -220,9 +241,14 @@ bool make_map(CUtensorMap *map, void *data, const CacheView &c) {
 }
 
 template <int D>
-int launch_join(const KernelArgs &ka, cudaStream_t st) {
+int launch_join(const KernelArgs &ka, int grid, cudaStream_t st) {
+    // Units that reach over four shares or more: 12 us with SPLIT against 25 for
+    // one sequence over 131077 positions; without, 23 us against 57 for 16
+    // sequences of 85 nodes (two to three shares a unit).
+    const Plan &p = ka.p;
+    const bool split = 4ll * p.B * p.Hkv * p.own.units <= grid && p.sT == 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ka.p.B * ka.p.Hkv * ceil_div(ka.p.own.rows, kBlockRows)));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * ceil_div(p.own.rows, split ? 1 : 4 * kJoinWarps)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr;
@@ -230,7 +256,9 @@ int launch_join(const KernelArgs &ka, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, ka) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, split ? attn_join_kernel<D, true> : attn_join_kernel<D, false>, ka) == cudaSuccess
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
 }
 
 }  // namespace
@@ -280,7 +308,7 @@ int launch_attn(const AttnArgs &a, cudaStream_t st) {
         rc = launch_few(ka, grid, kmap, vmap, true, st);
         if (rc != SPEC_OK) return rc;
     }
-    return a.c.D == 128 ? launch_join<128>(ka, st) : launch_join<64>(ka, st);
+    return a.c.D == 128 ? launch_join<128>(ka, grid, st) : launch_join<64>(ka, grid, st);
 }
 
 }  // namespace specv

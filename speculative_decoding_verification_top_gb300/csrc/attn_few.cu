@@ -17,7 +17,7 @@
 //   warp 9           issues the products (tcgen05); scores run up to two tiles
 //                    ahead of the values
 //   warp 11          the query tile, and what belongs to its rows, of the next
-//                    segment
+//                    segment; tells the softmax groups which it is
 // The reference maximum of a row is common to a group's 128 threads; a vote per
 // tile (one hardware barrier) says whether any score outgrew it, which after
 // the first tile of a segment is rare, so maxima are reduced only then.  l is
@@ -50,6 +50,7 @@ struct Shared {
     Barriers bar;
     Start start;
     Rows<NR> rows[2];
+    Segment seg[2];        // the segment of each query tile; rows = 0: no more
     alignas(16) float ref[2][NR];  // per group: reference maximum less the lift; +inf for no row
     alignas(16) float keep[2][NR]; // per group: factor of the last growth
     float red[2][4][NR];   // per group and warp
@@ -65,19 +66,15 @@ struct Layout : Shape<D, E4M3> {
     using S = Shape<D, E4M3>;
     static constexpr int kQBlock = NR * S::kRow;                     // a block of the query tile
     static constexpr int kQ = kQBlock * (E4M3 ? 2 : S::kHalves);
-    static constexpr int kPRow = E4M3 && NR == 64 ? NR : 2 * NR;     // bytes of a row of weights
+    static constexpr int kPRow = E4M3 ? NR : 2 * NR;                 // bytes of a row of weights
     static constexpr int kPMat = kTile * kPRow;
-    static constexpr int kP = kPMat * (E4M3 && NR == 64 ? 2 : 1);    // one buffer of weights
+    static constexpr int kP = kPMat * (E4M3 ? 2 : 1);                // one buffer of weights
     static constexpr int kFixed = static_cast<int>((sizeof(Shared<NR>) + 127) / 128 * 128);
     static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ - 4 * kP) / S::kSlot;
     static constexpr int kSlots = kRoom < 2 * kMaxSlots ? kRoom : 2 * kMaxSlots;
     static constexpr int kK = kSlots / 2, kV = kSlots - kK;          // slots of keys, of values
     static constexpr int kBytes = kFixed + 2 * kQ + 4 * kP + kSlots * S::kSlot;
-    // e4m3 with 32 rows: the two terms of the queries, and of the weights, side by
-    // side as 64 columns (half the products; the halves are added on reading).
-    static constexpr bool kPair = E4M3 && NR == 32;
-    static constexpr int kN = kPair ? 2 * NR : NR;                   // columns of a product
-    static constexpr uint32_t kColumns = kN == 32 ? 256 : 512;       // TMEM: 4 S and 2 O of kN columns
+    static constexpr uint32_t kColumns = NR == 32 ? 256 : 512;       // TMEM: 4 S and 2 O of NR columns
 };
 
 // Folds v[0..NR) over a warp's lanes with f: lane i ends up with column(s) i
@@ -224,10 +221,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // The first segment's: everyone takes a share.
         Walk ahead = walk;
         const bool some = ahead.next(&g);
+        if (!some) g.rows = 0;
         if (some) stage(0, tid, kAttnThreads);
         fence_async_proxy();
-        __syncthreads();
+        if (E4M3) __syncthreads();  // the rows' factors
         if (some) stage_rows(0, tid, kAttnThreads);
+        if (tid == 0) sh.seg[0] = g;
         __syncthreads();
     }
 
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else if (warp == 9) {
         // ---- products
         if (elect_one()) {
-            constexpr uint32_t kQk = mma_desc(E4M3, S::kN, false, false), kPv = mma_desc(E4M3, S::kN, true, true);
+            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kPv = mma_desc(E4M3, NR, true, true);
             constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>;
             // Values narrower than 128 columns: the second block is the first again,
             // and its rows of O are not read.
@@ -283,10 +282,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                            bar_wait(s_empty + 8 * buf, ((cnt >> 1) & 1) ^ 1, dead);
                     if (!live) break;
                     fence_after_sync();
-                    const uint32_t k = k0 + ks * (S::kSlot >> 4), q = q0 + qi * (S::kQ >> 4), d = tmem + buf * S::kN;
+                    const uint32_t k = k0 + ks * (S::kSlot >> 4), q = q0 + qi * (S::kQ >> 4), d = tmem + buf * NR;
                     if (E4M3) {
 #pragma unroll
-                        for (int i = 0; i < (S::kPair ? 1 : 2) * (D / 32); ++i) {
+                        for (int i = 0; i < 2 * (D / 32); ++i) {
                             const uint32_t term = i / (D / 32), j = i % (D / 32);
                             mma_ss<true>(d, k + (j * 32 >> 4), kHi, q + ((term * S::kQBlock + j * 32) >> 4), kHi, kQk, i > 0);
                         }
@@ -314,11 +313,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * buf, (cnt >> 1) & 1, dead);
                     if (!live) break;
                     fence_after_sync();
-                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + buf * (S::kP >> 4), d = tmem + (4 + w) * S::kN;
+                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + buf * (S::kP >> 4), d = tmem + (4 + w) * NR;
                     const bool first = tv - g.t0 < 2;  // the group's first tile of the segment
                     if (E4M3) {
 #pragma unroll
-                        for (int i = 0; i < (S::kPair ? 4 : 8); ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             const uint32_t j = i % 4;
                             mma_ss<true>(d, v + (j * 32 * S::kRow >> 4), kHi,
                                          pb + (((i / 4) * S::kPMat + j * 32 * S::kPRow) >> 4), kPHi, kPv, i > 0 || !first);
@@ -351,15 +350,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
     } else if (warp == 11) {
         // ---- query tiles, a segment ahead (the first segment's is there)
-        bool live = true;
-        for (uint32_t seg = 0; live && walk.next(&g); ++seg) {
+        bool live = true, more = true;
+        for (uint32_t seg = 0; live && more; ++seg) {
+            more = walk.next(&g);
             if (seg > 0) {
                 live = bar_wait(smem_addr(&bar.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1, dead);
                 live = __all_sync(0xffffffffu, live);
                 if (!live) break;
-                stage(seg & 1, lane, 32);
-                __syncwarp();
-                stage_rows(seg & 1, lane, 32);
+                if (more) {
+                    stage(seg & 1, lane, 32);
+                    __syncwarp();
+                    stage_rows(seg & 1, lane, 32);
+                } else {
+                    g.rows = 0;
+                }
+                if (lane == 0) sh.seg[seg & 1] = g;
                 fence_async_proxy();
             }
             __syncwarp();
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ---- softmax groups
         const int w = warp >> 2, quad = warp & 3, row = tid & 127;  // row: the thread's position in a tile
         const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // this warp's TMEM lanes
-        const uint32_t ot = tmem + lanes + (4 + w) * S::kN;
+        const uint32_t ot = tmem + lanes + (4 + w) * NR;
         constexpr float kSlack = E4M3 ? kSlackE4M3 : kSlackBf16, kLift = E4M3 ? kLiftE4M3 : 0.0f;
         const float capl = a.cap * kLog2e;
         float *ref = sh.ref[w], *keep = sh.keep[w];
@@ -379,13 +384,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         uint32_t seg = 0, tile = 0, cnt = 0;  // segments, tiles of the CTA, tiles of this group
         bool live = true;
-        while (live && walk.next(&g)) {
+        while (live) {
+            const uint32_t half = seg & 1;
+            bool ok = bar_wait(smem_addr(&bar.q_full[half]), (seg >> 1) & 1, dead);
+            if (vote(!ok)) {
+                live = false;
+                break;
+            }
+            g = sh.seg[half];
+            if (g.rows == 0) break;
             const Units &u = g.shared ? p.shared : p.own;
             const long long part = static_cast<long long>(g.slot) * 2 + w;
             float2 *ml = u.ml + part * u.rc;
-            const uint32_t half = seg & 1;
             const Rows<NR> &rows = sh.rows[half];
-            bool ok = bar_wait(smem_addr(&bar.q_full[half]), (seg >> 1) & 1, dead);
             const int n_rows = g.rows, first_tile = g.t0 + ((tile ^ w) & 1);  // this group's first
             const int origin = (g.shared ? 0 : a.shared_len) + g.len;
             const int last_pos = a.window > 0 ? last_position(a, g) : 0;
@@ -427,9 +438,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
                 float s[NR];
 #pragma unroll
-                for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + (w * 2 + buf) * S::kN + c, s + c);
-                float s2[S::kPair ? 32 : 1];
-                if constexpr (S::kPair) tmem_load32(tmem + lanes + (w * 2 + buf) * S::kN + 32, s2);
+                for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + (w * 2 + buf) * NR + c, s + c);
                 tmem_load_wait();
                 fence_before_sync();
                 __syncwarp();
@@ -438,32 +447,58 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const float fb = E4M3 ? static_cast<float>(max(-120, min(120, ev))) : 0.0f;
                 const float fl = E4M3 ? exp2i(-max(-120, min(120, ev))) : 1.0f;
                 const float at = static_cast<float>(pos_j - origin);
+                const bool cap = EXTRA && a.cap > 0.0f;
+                const F2 fk2 = pair_of(fk, fk), fb2 = pair_of(fb, fb), rs2 = pair_of(mul, mul), at2 = pair_of(at, at);
+                const F2 minus = pair_of(-1.0f, -1.0f);
                 float over = kNegInf;
 #pragma unroll
-                for (int c = 0; c < NR; c += 4) {
-                    if (c >= n_rows) break;
-                    const float4 r4 = *reinterpret_cast<const float4 *>(&rows.rs[c]);
-                    const float4 m4 = *reinterpret_cast<const float4 *>(&ref[c]);
-                    const float4 s4 = EXTRA ? *reinterpret_cast<const float4 *>(&rows.slope[c]) : float4{};
-                    const float4 a4 = EXTRA ? *reinterpret_cast<const float4 *>(&rows.at[c]) : float4{};
-                    const float rs[4] = {r4.x, r4.y, r4.z, r4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w};
-                    const float sl[4] = {s4.x, s4.y, s4.z, s4.w}, ra[4] = {a4.x, a4.y, a4.z, a4.w};
+                for (int c0 = 0; c0 < NR; c0 += 16) {
+                    if (c0 >= n_rows) break;
+                    if (cap) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float y = s[c + k];
-                        if constexpr (S::kPair) y += s2[c + k];
-                        if (E4M3) y *= fk;
-                        if (EXTRA) {
-                            y = a.cap > 0.0f ? capped(y * rs[k], capl) : y * rs[k];
-                            y = fmaf(sl[k], at - ra[k], y);
-                            if (E4M3) y += fb;
-                        } else {
-                            y = E4M3 ? fmaf(y, rs[k], fb) : y * rs[k];
-                        }
-                        if (!whole && !(seen >> (c + k) & 1)) y = kNegInf;
-                        s[c + k] = y;
-                        over = fmaxf(over, y - m[k]);
+                        for (int c = c0; c < c0 + 16; ++c)
+                            s[c] = capped(E4M3 ? s[c] * fk * rows.rs[c] : s[c] * mul, capl);
                     }
+                    float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+                    for (int c = c0; c < c0 + 16; c += 4) {
+                        F2 y[2] = {pair_of(s[c], s[c + 1]), pair_of(s[c + 2], s[c + 3])};
+                        const ulonglong2 m4 = *reinterpret_cast<const ulonglong2 *>(&ref[c]);
+                        const F2 m[2] = {{m4.x}, {m4.y}};
+                        if (!cap) {
+                            if (E4M3) {
+                                const ulonglong2 r4 = *reinterpret_cast<const ulonglong2 *>(&rows.rs[c]);
+                                y[0] = mul2(mul2(y[0], fk2), F2{r4.x});
+                                y[1] = mul2(mul2(y[1], fk2), F2{r4.y});
+                            } else {
+                                y[0] = mul2(y[0], rs2);
+                                y[1] = mul2(y[1], rs2);
+                            }
+                        }
+                        if (EXTRA) {
+                            const ulonglong2 s4 = *reinterpret_cast<const ulonglong2 *>(&rows.slope[c]);
+                            const ulonglong2 a4 = *reinterpret_cast<const ulonglong2 *>(&rows.at[c]);
+                            y[0] = fma2(F2{s4.x}, fma2(F2{a4.x}, minus, at2), y[0]);
+                            y[1] = fma2(F2{s4.y}, fma2(F2{a4.y}, minus, at2), y[1]);
+                        }
+                        if (E4M3) {
+                            y[0] = add2(y[0], fb2);
+                            y[1] = add2(y[1], fb2);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float2 t2 = parts_of(y[k]);
+                            if (!whole) {
+                                if (!(seen >> (c + 2 * k) & 1)) t2.x = kNegInf;
+                                if (!(seen >> (c + 2 * k + 1) & 1)) t2.y = kNegInf;
+                            }
+                            s[c + 2 * k] = t2.x;
+                            s[c + 2 * k + 1] = t2.y;
+                            const float2 d = parts_of(fma2(m[k], minus, pair_of(t2.x, t2.y)));
+                            top[k] = max3(top[k], d.x, d.y);
+                        }
+                    }
+                    over = max3(over, top[0], top[1]);
                 }
                 const bool grown = vote(!ok || over > kSlack + kLift);
                 if (grown) {
@@ -473,9 +508,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     // Some row outgrew its reference: reduce the maxima, rescale.
 #pragma unroll
-                    for (int c = 0; c < NR; c += 4)
+                    for (int c = 0; c < NR; c += 16)
                         if (c >= n_rows)
-                            for (int k = 0; k < 4; ++k) s[c + k] = kNegInf;
+                            for (int k = 0; k < 16; ++k) s[c + k] = kNegInf;
                     float top[NR / 32];
                     fold_columns<NR>(s, top, [](float x, float y) { return fmaxf(x, y); });
 #pragma unroll
@@ -499,16 +534,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                     for (int c = 0; c < NR; c += 32) {
                         if (wrote) {
-#pragma unroll 1
-                            for (int e = 0; e < (S::kPair ? 2 : 1); ++e) {
-                                float o[32];
-                                tmem_load32(ot + e * 32 + c, o);
-                                tmem_load_wait();
+                            float o[32];
+                            tmem_load32(ot + c, o);
+                            tmem_load_wait();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= keep[c + k];
-                                tmem_store32(ot + e * 32 + c, reinterpret_cast<const uint32_t *>(o));
-                                tmem_store_wait();
-                            }
+                            for (int k = 0; k < 32; ++k) o[k] *= keep[c + k];
+                            tmem_store32(ot + c, reinterpret_cast<const uint32_t *>(o));
+                            tmem_store_wait();
                         }
 #pragma unroll
                         for (int k = 0; k < 32; ++k) l[c + k] *= keep[c + k];
@@ -517,47 +549,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 // Weights, and their place as the product's operand: a row per position.
                 ok = ok && bar_wait(smem_addr(&bar.p_empty[w][buf]), phase ^ 1, dead);
                 uint8_t *pb = pt + (w * 2 + buf) * S::kP;
-                if (E4M3) {
 #pragma unroll
-                    for (int c = 0; c < NR; c += 16) {
-                        if (c >= n_rows) break;
-                        uint32_t hi[4], lo[4];
+                for (int c0 = 0; c0 < NR; c0 += 16) {
+                    if (c0 >= n_rows) break;
+                    uint32_t pk[8];  // bf16 pairs, or four words of first and four of second terms
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 m4 = *reinterpret_cast<const float4 *>(&ref[c + 4 * k]);
-                            float *x = s + c + 4 * k;
-                            const float x0 = ex2(x[0] - m4.x), x1 = ex2(x[1] - m4.y), x2 = ex2(x[2] - m4.z),
-                                        x3 = ex2(x[3] - m4.w);
-                            float *y = l + c + 4 * k;
-                            y[0] = fmaf(x0, fl, y[0]), y[1] = fmaf(x1, fl, y[1]);
-                            y[2] = fmaf(x2, fl, y[2]), y[3] = fmaf(x3, fl, y[3]);
-                            const uint32_t e = e4m3_pair(x0, x1), f = e4m3_pair(x2, x3);
-                            const float2 ex = e4m3_values(e), fx = e4m3_values(f);
-                            hi[k] = e | f << 16;
-                            lo[k] = e4m3_pair(x0 - ex.x, x1 - ex.y) | e4m3_pair(x2 - fx.x, x3 - fx.y) << 16;
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = c0 + 4 * k;
+                        const ulonglong2 m4 = *reinterpret_cast<const ulonglong2 *>(&ref[c]);
+                        const float2 u = parts_of(fma2(F2{m4.x}, minus, pair_of(s[c], s[c + 1])));
+                        const float2 v = parts_of(fma2(F2{m4.y}, minus, pair_of(s[c + 2], s[c + 3])));
+                        const float x0 = ex2(u.x), x1 = ex2(u.y), x2 = ex2(v.x), x3 = ex2(v.y);
+                        if (E4M3) {
+                            l[c] = fmaf(x0, fl, l[c]), l[c + 1] = fmaf(x1, fl, l[c + 1]);
+                            l[c + 2] = fmaf(x2, fl, l[c + 2]), l[c + 3] = fmaf(x3, fl, l[c + 3]);
+                            uint32_t h0, l0, h1, l1;
+                            e4m3_terms(x0, x1, &h0, &l0);
+                            e4m3_terms(x2, x3, &h1, &l1);
+                            pk[k] = h0 | h1 << 16;
+                            pk[4 + k] = l0 | l1 << 16;
+                        } else {
+                            l[c] += x0, l[c + 1] += x1, l[c + 2] += x2, l[c + 3] += x3;
+                            pk[2 * k] = bf16_pair(x0, x1);
+                            pk[2 * k + 1] = bf16_pair(x2, x3);
                         }
-                        const uint32_t o = swizzled<S::kPRow>(row, c);
-                        *reinterpret_cast<uint4 *>(pb + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(S::kPair ? pb + swizzled<S::kPRow>(row, 32 + c) : pb + S::kPMat + o) =
-                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < NR; c += 8) {
-                        if (c >= n_rows) break;
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            const float4 m4 = *reinterpret_cast<const float4 *>(&ref[c + k]);
-                            float *x = s + c + k, *y = l + c + k;
-                            const float x0 = ex2(x[0] - m4.x), x1 = ex2(x[1] - m4.y), x2 = ex2(x[2] - m4.z),
-                                        x3 = ex2(x[3] - m4.w);
-                            y[0] += x0, y[1] += x1, y[2] += x2, y[3] += x3;
-                            pk[k / 2] = bf16_pair(x0, x1);
-                            pk[k / 2 + 1] = bf16_pair(x2, x3);
-                        }
-                        *reinterpret_cast<uint4 *>(pb + swizzled<S::kPRow>(row, 2 * c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    }
+                    const uint32_t o = swizzled<S::kPRow>(row, E4M3 ? c0 : 2 * c0);
+                    const uint32_t o2 = E4M3 ? o + S::kPMat : swizzled<S::kPRow>(row, 2 * c0 + 16);
+                    *reinterpret_cast<uint4 *>(pb + o) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    *reinterpret_cast<uint4 *>(pb + o2) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }
                 if (!whole && clean_values<D, E4M3>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[seg & 15] = 1;
                 fence_async_proxy();
@@ -597,15 +617,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (c >= n_rows) break;
                     float v[32];
                     tmem_load32(ot + c, v);
-                    if constexpr (S::kPair) {
-                        float v2[32];
-                        tmem_load32(ot + 32, v2);
-                        tmem_load_wait();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] += v2[k];
-                    } else {
-                        tmem_load_wait();
-                    }
+                    tmem_load_wait();
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (c + k < n_rows) o[static_cast<long long>(c + k) * D] = v[k];

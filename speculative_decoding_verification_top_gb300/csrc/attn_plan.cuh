@@ -285,6 +285,61 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// Two fp32 operations an instruction (sm_100 and later).
+struct F2 {
+    unsigned long long v;
+};
+
+__device__ __forceinline__ F2 pair_of(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float2 parts_of(F2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two weights as two e4m3 terms each: x = hi + lo up to 2^-8 of x.  The
+// remainder is taken in fp16, which holds x to 2^-11 (x is at most 2^9).
+__device__ __forceinline__ void e4m3_terms(float x0, float x1, uint32_t *hi, uint32_t *lo) {
+    const __half2 x = __floats2half2_rn(x0, x1);
+    uint16_t h, l;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(h));
+    const __half2 d = __hsub2(x, *reinterpret_cast<const __half2 *>(&y));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t *>(&d)));
+    *hi = h;
+    *lo = l;
+}
+
 // cap tanh(y) log2 e with capl = cap log2 e; tanh(y) = 1 - 2 / (1 + e^2y).
 __device__ __forceinline__ float capped(float y, float capl) {
     return capl - __fdividef(2.0f * capl, 1.0f + ex2(y * (2.0f * kLog2e)));
@@ -301,51 +356,62 @@ template <int D, bool E4M3>
 __device__ __forceinline__ void stage_queries(const AttnArgs &a, const Segment &g, int row0, int rows, int tile_rows,
                                               uint8_t *tile, float *factor, int me, int threads) {
     constexpr int kRow = Shape<D, E4M3>::kRow, kParts = D / 16;
-    const int block = tile_rows * kRow;
+    constexpr int kAtOnce = 4;  // rows a thread has in flight
+    const int block = tile_rows * kRow, step = threads / kParts;
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const int part = me % kParts;
-    for (int row = me / kParts; row < tile_rows; row += threads / kParts) {
-        uint4 u[2] = {};
-        if (row < rows) {
-            const int r = row0 + row;
-            const long long tok = (g.shared ? 0 : static_cast<long long>(g.b) * a.N) + r / a.G;
+    for (int first = me / kParts; first < tile_rows; first += kAtOnce * step) {
+        uint4 u[kAtOnce][2] = {};
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int row = first + i * step;
+            if (row >= min(rows, tile_rows)) continue;
+            const int r = row0 + row, n = r / a.G;
+            const long long tok = (g.shared ? 0 : static_cast<long long>(g.b) * a.N) + n;
             const uint4 *q = reinterpret_cast<const uint4 *>(
-                a.q + tok * a.q_stride + static_cast<long long>(g.h * a.G + r % a.G) * D + part * 16);
-            u[0] = __ldg(q);
-            u[1] = __ldg(q + 1);
+                a.q + tok * a.q_stride + static_cast<long long>(g.h * a.G + r - n * a.G) * D + part * 16);
+            u[i][0] = __ldg(q);
+            u[i][1] = __ldg(q + 1);
         }
-        uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] ^= flip;
-        if (!E4M3) {
-            uint8_t *at = tile + (part / 4) * block;
-            *reinterpret_cast<uint4 *>(at + swizzled<kRow>(row, part % 4 * 32)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4 *>(at + swizzled<kRow>(row, part % 4 * 32 + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
-            continue;
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int row = first + i * step;
+            if (row >= tile_rows) break;  // whole warps alike
+            uint32_t w[8] = {u[i][0].x, u[i][0].y, u[i][0].z, u[i][0].w, u[i][1].x, u[i][1].y, u[i][1].z, u[i][1].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] ^= flip;
+            if (!E4M3) {
+                uint8_t *at = tile + (part / 4) * block;
+                *reinterpret_cast<uint4 *>(at + swizzled<kRow>(row, part % 4 * 32)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(at + swizzled<kRow>(row, part % 4 * 32 + 16)) =
+                    make_uint4(w[4], w[5], w[6], w[7]);
+                continue;
+            }
+            uint32_t top = 0;  // bf16 bits of max |q|
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
+#pragma unroll
+            for (int s = kParts / 2; s > 0; s /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+            // e: max |q| <= 448 * 2^e
+            int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+            e = max(-120, min(120, e));
+            const float f = exp2i(-e);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float x0 = __uint_as_float(w[2 * k] << 16) * f, x1 = __uint_as_float(w[2 * k] & 0xffff0000u) * f;
+                const float x2 = __uint_as_float(w[2 * k + 1] << 16) * f,
+                            x3 = __uint_as_float(w[2 * k + 1] & 0xffff0000u) * f;
+                const uint32_t p = e4m3_pair(x0, x1), r = e4m3_pair(x2, x3);
+                const float2 y = e4m3_values(p), z = e4m3_values(r);
+                hi[k] = p | r << 16;
+                lo[k] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
+            }
+            const uint32_t o = swizzled<kRow>(row, part * 16);
+            *reinterpret_cast<uint4 *>(tile + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(tile + block + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (part == 0) factor[row] = exp2i(e);
         }
-        uint32_t top = 0;  // bf16 bits of max |q|
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
-#pragma unroll
-        for (int s = kParts / 2; s > 0; s /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-        // e: max |q| <= 448 * 2^e
-        int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-        e = max(-120, min(120, e));
-        const float f = exp2i(-e);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float x0 = __uint_as_float(w[2 * k] << 16) * f, x1 = __uint_as_float(w[2 * k] & 0xffff0000u) * f;
-            const float x2 = __uint_as_float(w[2 * k + 1] << 16) * f, x3 = __uint_as_float(w[2 * k + 1] & 0xffff0000u) * f;
-            const uint32_t p = e4m3_pair(x0, x1), r = e4m3_pair(x2, x3);
-            const float2 y = e4m3_values(p), z = e4m3_values(r);
-            hi[k] = p | r << 16;
-            lo[k] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
-        }
-        const uint32_t o = swizzled<kRow>(row, part * 16);
-        *reinterpret_cast<uint4 *>(tile + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(tile + block + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (part == 0) factor[row] = exp2i(e);
     }
 }
 

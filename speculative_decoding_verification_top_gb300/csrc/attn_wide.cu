@@ -9,7 +9,7 @@
 //   warp 9           issues the products (tcgen05, M = 128 rows): S = Q K^T,
 //                    then O += P V with P in TMEM
 //   warp 10          the e4m3 cache's exponents, as factors
-//   warp 11          the query tiles of the next segment
+//   (the softmax groups stage the query tiles of their next segment)
 // A unit of over 128 rows gives each group 128 rows of its own and both work
 // on every tile; a smaller one alternates its tiles between the groups, so
 // that one group's softmax runs under the other's products.  TMEM: two S of
@@ -31,7 +31,7 @@ constexpr int kScaleRing = 4;
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots];
     unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
-    unsigned long long q_full[2], q_empty[2], o_full[2], s_full[2], p_full[2], drained;
+    unsigned long long q_full, left, o_full[2], s_full[2], p_full[2], drained;
 };
 
 struct Shared {
@@ -122,77 +122,84 @@ __device__ __noinline__ Seen seen_columns(const uint8_t *mask, const int32_t *po
 }
 
 // t of 32 columns from column `col` of a tile, from the raw products v in
-// place; returns their maximum.
-template <bool E4M3, bool EXTRA>
-__device__ __forceinline__ float scores32(const AttnArgs &a, const Segment &g, const Row &x, int j0, int col, bool whole,
-                                          uint32_t seen, int pos_col, const float *fa, float (&v)[32]) {
-    // The bias of a whole tile: slope * (position index - pos_i), linear in the column.
-    const float base = EXTRA ? x.slope * static_cast<float>((g.shared ? 0 : a.shared_len) + j0 + col - x.pos_i) : 0.0f;
+// place; returns their maximum.  WHOLE: the row sees them all, and without a cap
+// t is linear in the product and the column.
+template <bool E4M3, bool EXTRA, bool WHOLE>
+__device__ __forceinline__ float scores32(const AttnArgs &a, const Row &x, float base, int col, uint32_t seen, int pos_col,
+                                          const float *fa, float (&v)[32]) {
     const float capl = a.cap * kLog2e;
     float top[2] = {kNegInf, kNegInf};
+    if constexpr (WHOLE) {
+        const F2 rs = pair_of(x.rs, x.rs), slope = pair_of(x.slope, x.slope), base2 = pair_of(base, base);
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-        float4 k4 = {}, b4 = {};
-        if (E4M3) {
-            k4 = *reinterpret_cast<const float4 *>(fa + col + c);
-            b4 = *reinterpret_cast<const float4 *>(fa + kTile + col + c);
-        }
-        const float fk[4] = {k4.x, k4.y, k4.z, k4.w}, fb[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float y = v[c + k];
-            if (E4M3) y *= fk[k];
-            if (EXTRA) {
-                y = a.cap > 0.0f ? capped(y * x.rs, capl) : y * x.rs;
-                if (!whole && a.pos)
-                    y = fmaf(x.slope, static_cast<float>(__shfl_sync(0xffffffffu, pos_col, c + k) - x.pos_i), y);
-                else
-                    y += fmaf(x.slope, static_cast<float>(c + k), base);
-                if (E4M3) y += fb[k];
+        for (int c = 0; c < 32; c += 2) {
+            F2 y = pair_of(v[c], v[c + 1]);
+            F2 b;
+            if (E4M3) {
+                y = mul2(y, *reinterpret_cast<const F2 *>(fa + col + c));
+                b = *reinterpret_cast<const F2 *>(fa + kTile + col + c);
+                if (EXTRA) b = add2(b, fma2(slope, pair_of(col + c, col + c + 1), base2));
             } else {
-                y = E4M3 ? fmaf(y, x.rs, fb[k]) : y * x.rs;
+                b = EXTRA ? fma2(slope, pair_of(col + c, col + c + 1), base2) : pair_of(0.0f, 0.0f);
             }
-            if (!whole && !(seen >> (c + k) & 1u)) y = kNegInf;
-            v[c + k] = y;
-            top[k & 1] = fmaxf(top[k & 1], y);
+            const float2 t = parts_of(fma2(y, rs, b));
+            v[c] = t.x;
+            v[c + 1] = t.y;
+            top[c / 2 & 1] = max3(top[c / 2 & 1], t.x, t.y);
         }
+        return fmaxf(top[0], top[1]);
+    }
+    const bool cap = EXTRA && a.cap > 0.0f, by_pos = EXTRA && a.pos != nullptr;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        float y = v[c];
+        if (E4M3) y *= fa[col + c];
+        y *= x.rs;
+        if (EXTRA) {
+            if (cap) y = capped(y, capl);
+            if (by_pos)
+                y = fmaf(x.slope, static_cast<float>(__shfl_sync(0xffffffffu, pos_col, c) - x.pos_i), y);
+            else
+                y += fmaf(x.slope, static_cast<float>(col + c), base);
+        }
+        if (E4M3) y += fa[kTile + col + c];
+        if (!(seen >> c & 1u)) y = kNegInf;
+        v[c] = y;
+        top[c & 1] = fmaxf(top[c & 1], y);
     }
     return fmaxf(top[0], top[1]);
 }
 
-// Weights 2^(t mul - ref) of 32 columns into TMEM as the product's operand: 16
-// columns of bf16 pairs, or 8 of first and 8 of second e4m3 terms.  Returns
-// their sum, in e4m3 without the values' exponents (fc: 2^-ev).
+// Weights 2^t of 32 columns, t already less the reference, into TMEM as the
+// product's operand: 16 columns of bf16 pairs, or 8 of first and 8 of second
+// e4m3 terms.  Returns their sum, in e4m3 without the values' exponents (fc:
+// 2^-ev).
 template <bool E4M3>
-__device__ __forceinline__ float weights32(uint32_t dst, float mul, float ref, const float *fc, const float (&t)[32]) {
-    float sum[4] = {};
+__device__ __forceinline__ float weights32(uint32_t dst, const float *fc, const F2 (&t)[16]) {
+    F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
     uint32_t pk[16];
-    if (E4M3) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-            const float4 f4 = *reinterpret_cast<const float4 *>(fc + c);
-            const float x0 = ex2(t[c] - ref), x1 = ex2(t[c + 1] - ref);
-            const float x2 = ex2(t[c + 2] - ref), x3 = ex2(t[c + 3] - ref);
-            sum[0] = fmaf(x0, f4.x, sum[0]);
-            sum[1] = fmaf(x1, f4.y, sum[1]);
-            sum[2] = fmaf(x2, f4.z, sum[2]);
-            sum[3] = fmaf(x3, f4.w, sum[3]);
-            const uint32_t u = e4m3_pair(x0, x1), v = e4m3_pair(x2, x3);
-            const float2 y = e4m3_values(u), z = e4m3_values(v);
-            pk[c / 4] = u | v << 16;
-            pk[8 + c / 4] = e4m3_pair(x0 - y.x, x1 - y.y) | e4m3_pair(x2 - z.x, x3 - z.y) << 16;
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const float x0 = ex2(fmaf(t[c], mul, -ref)), x1 = ex2(fmaf(t[c + 1], mul, -ref));
-            sum[c & 2] += x0;
-            sum[(c & 2) + 1] += x1;
-            pk[c / 2] = bf16_pair(x0, x1);
+    for (int c = 0; c < 16; c += 2) {
+        const float2 u = parts_of(t[c]), v = parts_of(t[c + 1]);
+        const float x0 = ex2(u.x), x1 = ex2(u.y), x2 = ex2(v.x), x3 = ex2(v.y);
+        if (E4M3) {
+            sum[0] = fma2(pair_of(x0, x1), *reinterpret_cast<const F2 *>(fc + 2 * c), sum[0]);
+            sum[1] = fma2(pair_of(x2, x3), *reinterpret_cast<const F2 *>(fc + 2 * c + 2), sum[1]);
+            uint32_t h0, l0, h1, l1;
+            e4m3_terms(x0, x1, &h0, &l0);
+            e4m3_terms(x2, x3, &h1, &l1);
+            pk[c / 2] = h0 | h1 << 16;
+            pk[8 + c / 2] = l0 | l1 << 16;
+        } else {
+            sum[0] = add2(sum[0], pair_of(x0, x1));
+            sum[1] = add2(sum[1], pair_of(x2, x3));
+            pk[c] = bf16_pair(x0, x1);
+            pk[c + 1] = bf16_pair(x2, x3);
         }
     }
     tmem_store16(dst, pk);
-    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    const float2 s = parts_of(add2(sum[0], sum[1]));
+    return s.x + s.y;
 }
 
 // Moves the row's reference maximum up to `top` where that is needed,
@@ -217,47 +224,76 @@ __device__ __forceinline__ void grow(Row &x, float top, bool wrote, uint32_t ot)
 }
 
 // One tile of one row, twice over it, so that 32 values are worked on (and 32
-// on their way) at a time: the maximum, with t back into TMEM where it is more
-// than a multiple of the product; then the weights.
+// on their way) at a time: the maximum, with t back into TMEM where it is not
+// cheap to take again; then the weights.
 template <int D, bool E4M3, bool EXTRA>
 __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g, Row &x, int j0, bool whole, bool wrote,
                                              uint32_t st, uint32_t ot, const float *fa) {
-    float top = kNegInf, mul = 1.0f, t[2][32];
-    if (!E4M3 && !EXTRA && whole) {
+    const bool linear = whole && (!EXTRA || a.cap == 0.0f);
+    // The bias: slope * (position index - pos_i), in a whole tile linear in the column.
+    const float base = EXTRA ? x.slope * static_cast<float>((g.shared ? 0 : a.shared_len) + j0 - x.pos_i) : 0.0f;
+    float top = kNegInf, t[2][32];
+    if (linear) {
         tmem_load32(st, t[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             tmem_load_wait();
             if (c < 3) tmem_load32(st + (c + 1) * 32, t[(c + 1) & 1]);
-            float u[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            float(&v)[32] = t[c & 1];
+            if constexpr (!E4M3 && !EXTRA) {
+                float u[2] = {kNegInf, kNegInf};
 #pragma unroll
-            for (int k = 0; k < 32; ++k) u[k & 3] = fmaxf(u[k & 3], t[c & 1][k]);
-            top = fmaxf(top, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
+                for (int k = 0; k < 32; k += 4) {
+                    u[0] = max3(u[0], v[k], v[k + 1]);
+                    u[1] = max3(u[1], v[k + 2], v[k + 3]);
+                }
+                top = max3(top, u[0], u[1]);
+            } else {
+                top = fmaxf(top, scores32<E4M3, EXTRA, true>(a, x, base, c * 32, 0, 0, fa, v));
+                if (E4M3) tmem_store32(st + c * 32, reinterpret_cast<const uint32_t *>(v));
+            }
         }
-        top *= x.rs;  // rs >= 0
-        mul = x.rs;
+        if (!E4M3 && !EXTRA) top *= x.rs;  // rs >= 0
     } else {
-        Seen seen = {};
+        Seen seen = {{~0u, ~0u, ~0u, ~0u}, {}};
         if (!whole)
             seen = seen_columns(a.mask, a.pos, a.N, a.window, g.shared ? 0 : a.shared_len, g.shared, g.len, x.first, x.has,
                                 x.tok, x.b * a.N, x.pos_i, j0);
-#pragma unroll
+        else
+            for (int c = 0; c < 4; ++c) seen.pos[c] = (g.shared ? 0 : a.shared_len) + j0 + c * 32 + (threadIdx.x & 31);
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             tmem_load32(st + c * 32, t[0]);
             tmem_load_wait();
-            top = fmaxf(top, scores32<E4M3, EXTRA>(a, g, x, j0, c * 32, whole, seen.rows[c], seen.pos[c], fa, t[0]));
+            const uint32_t s = c == 0 ? seen.rows[0] : c == 1 ? seen.rows[1] : c == 2 ? seen.rows[2] : seen.rows[3];
+            const int p = c == 0 ? seen.pos[0] : c == 1 ? seen.pos[1] : c == 2 ? seen.pos[2] : seen.pos[3];
+            top = fmaxf(top, scores32<E4M3, EXTRA, false>(a, x, base, c * 32, s, p, fa, t[0]));
             tmem_store32(st + c * 32, reinterpret_cast<const uint32_t *>(t[0]));
         }
     }
     grow<D, E4M3>(x, top, wrote, ot);
     const float ref = x.m == kNegInf ? 0.0f : x.m - (E4M3 ? kLiftE4M3 : 0.0f);
+    const bool stored = E4M3 || !linear;
+    const float mul = stored ? 1.0f : x.rs, slope = stored ? 0.0f : x.slope, add = (stored ? 0.0f : base) - ref;
+    const F2 mul_2 = pair_of(mul, mul), slope_2 = pair_of(slope, slope), add_2 = pair_of(add, add);
     tmem_store_wait();
     tmem_load32(st, t[0]);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         tmem_load_wait();
         if (c < 3) tmem_load32(st + (c + 1) * 32, t[(c + 1) & 1]);
-        x.l += weights32<E4M3>(st + c * 16, mul, ref, fa + 2 * kTile + c * 32, t[c & 1]);
+        F2 y[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const F2 v = pair_of(t[c & 1][2 * k], t[c & 1][2 * k + 1]);
+            if (E4M3)
+                y[k] = add2(v, add_2);
+            else if (EXTRA)
+                y[k] = fma2(v, mul_2, fma2(slope_2, pair_of(c * 32 + 2 * k, c * 32 + 2 * k + 1), add_2));
+            else
+                y[k] = fma2(v, mul_2, add_2);
+        }
+        x.l += weights32<E4M3>(st + c * 16, fa + 2 * kTile + c * 32, y);
     }
     tmem_store_wait();
 }
@@ -311,12 +347,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_init(smem_addr(&bar.scale_empty[i]), 8);
         }
         for (int w = 0; w < 2; ++w) {
-            bar_init(smem_addr(&bar.q_full[w]), 1);
-            bar_init(smem_addr(&bar.q_empty[w]), 9);  // the products, and eight softmax warps
             bar_init(smem_addr(&bar.o_full[w]), 1);
             bar_init(smem_addr(&bar.s_full[w]), 1);
             bar_init(smem_addr(&bar.p_full[w]), 4);
         }
+        bar_init(smem_addr(&bar.q_full), 8);
+        bar_init(smem_addr(&bar.left), 8);
         bar_init(smem_addr(&bar.drained), 1);
         sh.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -367,7 +403,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (elect_one()) {
             constexpr uint32_t kQk = mma_desc(E4M3, kTile, false, false), kPv = mma_desc(E4M3, D, false, true);
             constexpr uint32_t kHi = kMatrixHi<S::kRow>;
-            uint32_t segs = 0, qn = 0, pn[2] = {0, 0};
+            uint32_t segs = 0, pn[2] = {0, 0};
             uint32_t slot = 0, phase = 0;  // the ring, in the order it is filled
             bool live = true;
             const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(ring), 0);
@@ -414,25 +450,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             while (live && walk.next(&g)) {
                 const int T = g.t1 - g.t0, lead = g.dual ? 1 : min(2, T);
-                uint32_t qi[2];  // the groups' query tiles
-                qi[0] = qi[1] = qn & 1;
-                live = bar_wait(smem_addr(&bar.q_full[qn & 1]), (qn >> 1) & 1, dead);
-                ++qn;
-                if (g.dual) {
-                    qi[1] = qn & 1;
-                    live = live && bar_wait(smem_addr(&bar.q_full[qn & 1]), (qn >> 1) & 1, dead);
-                    ++qn;
-                }
+                live = bar_wait(smem_addr(&bar.q_full), segs & 1, dead);
                 for (int t = 0; live && t < lead; ++t) {  // scores of each group's first tile
                     if (!(live = bar_wait(full0 + 8 * slot, phase, dead))) break;
                     fence_after_sync();
                     if (g.dual) {
-                        scores(0, qi[0], slot);
+                        scores(0, 0, slot);
                         mma_commit(s_full);
-                        scores(1, qi[1], slot);
+                        scores(1, 1, slot);
                         mma_commit(s_full + 8);
                     } else {
-                        scores(t, qi[0], slot);
+                        scores(t, 0, slot);
                         mma_commit(s_full + 8 * t);
                     }
                     mma_commit(empty0 + 8 * slot);
@@ -453,15 +481,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (w == w1) mma_commit(empty0 + 8 * vs);
                         if (!more) continue;
                         if (!(live = bar_wait(full0 + 8 * ks, kp, dead))) break;
-                        scores(w, qi[w], ks);
+                        scores(w, g.dual ? w : 0, ks);
                         mma_commit(s_full + 8 * w);
                         if (w == w1) mma_commit(empty0 + 8 * ks);
                     }
                 }
                 if (live) {
                     mma_commit(smem_addr(&bar.o_full[segs++ & 1]));
-                    mma_commit(smem_addr(&bar.q_empty[qi[0]]));
-                    if (g.dual) mma_commit(smem_addr(&bar.q_empty[qi[1]]));
                 }
             }
             if (!live) {  // products in flight end before TMEM is freed
@@ -503,34 +529,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
         }
-    } else if (warp == 11) {
-        // ---- query tiles, a segment ahead where the ring of two has room (the
-        // first segment's are there)
-        uint32_t qn = 0;
-        bool live = true;
-        for (bool first = true; live && walk.next(&g); first = false) {
-            for (int w = 0; live && w < (g.dual ? 2 : 1); ++w, ++qn) {
-                if (!first) {
-                    live = bar_wait(smem_addr(&bar.q_empty[qn & 1]), ((qn >> 1) & 1) ^ 1, dead);
-                    live = __all_sync(0xffffffffu, live);
-                    if (!live) break;
-                    stage_queries<D, E4M3>(a, g, g.row0 + w * kGroupRows, min(kGroupRows, g.rows - w * kGroupRows),
-                                           kGroupRows, qt + (qn & 1) * S::kQ, q_factor + (qn & 1) * kGroupRows, lane, 32);
-                    fence_async_proxy();
-                }
-                __syncwarp();
-                if (lane == 0) bar_arrive(smem_addr(&bar.q_full[qn & 1]));
-            }
-        }
     } else if (warp < 8) {
         // ---- softmax groups
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's TMEM lanes
         const uint32_t st = tmem + lanes + w * kTile, ot = tmem + lanes + 2 * kTile + w * D;
         const float mul = (a.cap > 0.0f ? fabsf(a.scale) / a.cap : fabsf(a.scale) * kLog2e);
-        uint32_t segs = 0, qn = 0, sn = 0, n_ring = 0, n_scale = 0;
-        bool live = true;
-        while (live && walk.next(&g)) {
+        uint32_t segs = 0, sn = 0, n_ring = 0, n_scale = 0;
+        bool live = true, more = walk.next(&g);
+        if (more && lane == 0) bar_arrive(smem_addr(&bar.q_full));  // the first segment's queries are there
+        while (live && more) {
             const int T = g.t1 - g.t0, row0 = g.row0 + (g.dual ? w * kGroupRows : 0);
             const int rows = min(kGroupRows, g.rows - (g.dual ? w * kGroupRows : 0));
             const bool has = row < rows, active = (row & ~31) < rows;
@@ -544,11 +552,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             x.has = has;
             x.rs = mul;
             if (E4M3) {
-                const uint32_t qi = qn + (g.dual ? w : 0);
-                live = bar_wait(smem_addr(&bar.q_full[qi & 1]), (qi >> 1) & 1, dead);
+                live = bar_wait(smem_addr(&bar.q_full), segs & 1, dead);
                 live = __all_sync(0xffffffffu, live);
                 if (!live) break;
-                x.rs *= q_factor[(qi & 1) * kGroupRows + row];
+                x.rs *= q_factor[(g.dual ? w : 0) * kGroupRows + row];
             }
             x.slope = EXTRA && a.slopes && has ? a.slopes[head] * kLog2e : 0.0f;
             x.m = kNegInf;
@@ -587,6 +594,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             if (!live) break;
+            Segment next;  // found while the last products run
+            more = walk.next(&next);
             live = bar_wait(smem_addr(&bar.o_full[segs & 1]), (segs >> 1) & 1, dead);
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 // Rows go out through this warp's part of the query tile's memory (its
                 // products are done), so that a store instruction covers whole lines.
                 constexpr int kCols = S::kQ >= 32768 ? 32 : 16, kQuads = kCols / 4;
-                float4 *buf = reinterpret_cast<float4 *>(qt + ((qn + (g.dual ? w : 0)) & 1) * S::kQ) +
+                float4 *buf = reinterpret_cast<float4 *>(qt + (g.dual ? w : 0) * S::kQ) +
                               (g.dual ? warp & 3 : warp) * 32 * kQuads;
                 float *o = k.o + (at - lane) * D;  // the warp's first row
                 const int n = min(32, rows - (row & ~31));
@@ -633,12 +642,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
             }
             fence_before_sync();
+            // ---- the next segment's query tiles, once all have left this one's
             __syncwarp();
-            for (int i = 0; i < (g.dual ? 2 : 1); ++i, ++qn)
-                if (lane == 0) bar_arrive(smem_addr(&bar.q_empty[qn & 1]));
+            if (lane == 0) bar_arrive(smem_addr(&bar.left));
+            if (more) {
+                live = bar_wait(smem_addr(&bar.left), segs & 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+                if (next.dual) {
+                    stage_queries<D, E4M3>(a, next, next.row0 + w * kGroupRows,
+                                           min(kGroupRows, next.rows - w * kGroupRows), kGroupRows, qt + w * S::kQ,
+                                           q_factor + w * kGroupRows, row, 128);
+                } else {
+                    stage_queries<D, E4M3>(a, next, next.row0, next.rows, kGroupRows, qt, q_factor, tid, 256);
+                }
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
+            }
             ++segs;
             n_ring += 2 * T;
             n_scale += T;
+            g = next;
         }
         if (!live && tid == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
     }
