@@ -25,17 +25,14 @@ namespace {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-// The shares that hold tiles of a unit [ubase, ubase + T c) of the cost line:
-// f(first slot, number of shares).  A share may hold less than one whole tile
-// of a unit of two row tiles (c = 2) at its ends: its slot is then not written.
-__device__ __forceinline__ void shares_of(long long share, long long ubase, int T, int c, int *lo, int *hi) {
-    const long long uend = ubase + static_cast<long long>(T) * c;
-    if (uend < INT_MAX) {
+// The shares that a unit of `cost` from ubase on touches.
+__device__ __forceinline__ void shares_of(long long share, long long ubase, long long cost, int *lo, int *hi) {
+    if (ubase + cost < INT_MAX) {
         *lo = static_cast<int>(ubase) / static_cast<int>(share);
-        *hi = static_cast<int>(uend - 1) / static_cast<int>(share);
+        *hi = static_cast<int>(ubase + cost - 1) / static_cast<int>(share);
     } else {
         *lo = static_cast<int>(ubase / share);
-        *hi = static_cast<int>((uend - 1) / share);
+        *hi = static_cast<int>((ubase + cost - 1) / share);
     }
 }
 
@@ -119,17 +116,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         }
         for (int k = unit[0]; k <= unit[kJoinRows - 1]; ++k) {
             const int c = u.rows - k * 2 * kGroupRows > kGroupRows ? 2 : 1;
-            const long long ubase = line + k * 2ll * T;
+            const long long ubase = line + k * 2ll * (T + u.start);
             int lo, hi;
-            shares_of(share, ubase, T, c, &lo, &hi);
+            shares_of(share, ubase, static_cast<long long>(T + u.start) * c, &lo, &hi);
 #pragma unroll 2
             for (int i = lo + (SPLIT ? warp : 0); i <= hi; i += SPLIT ? kJoinWarps : 1) {
-                bool written = true;
-                if (c == 2) {
-                    const long long from = i * share, to = from + share;
-                    const long long t0 = from > ubase ? (from - ubase + 1) / 2 : 0;
-                    written = t0 < min(static_cast<long long>(T), (to - ubase + 1) / 2);
-                }
+                int t0, t1;  // a share that holds no whole tile of the unit wrote nothing
+                tiles_in(i * share, i * share + share, ubase, T, u.start, c, &t0, &t1);
+                const bool written = t0 < t1;
                 bool here[kJoinRows];
 #pragma unroll
                 for (int q = 0; q < kJoinRows; ++q) here[q] = written && unit[q] == k;
@@ -138,10 +132,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         }
     };
     if (p.sT > 0)
-        join(p.shared, p.share[1], static_cast<long long>(h) * p.shared.row_tiles * p.sT, p.sT, h * p.shared.units,
+        join(p.shared, p.share[1], static_cast<long long>(h) * p.shared.row_tiles * (p.sT + p.shared.start), p.sT, h * p.shared.units,
              b * p.own.rows + r0);
     if (s.t1 > s.t0)
-        join(p.own, p.share[0], p.base[b] + static_cast<long long>(h) * p.own.row_tiles * (s.t1 - s.t0), s.t1 - s.t0,
+        join(p.own, p.share[0], p.base[b] + static_cast<long long>(h) * p.own.row_tiles * (s.t1 - s.t0 + p.own.start), s.t1 - s.t0,
              bh * p.own.units, r0);
     if constexpr (SPLIT) {
         __shared__ float2 ml[kJoinWarps];
@@ -182,6 +176,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 
 // ------------------------------------------------------------------ host
 
+// What beginning a unit costs, in tiles: staging its queries, a first tile that
+// waits for them, the partial result.
+constexpr int kStartFew = 3, kStartWide = 8;
+
 // Fills the plan's sizes and carves its arrays; returns the bytes needed.
 size_t carve_plan(Plan *p, int D, char *work) {
     size_t off = 0;
@@ -196,6 +194,7 @@ size_t carve_plan(Plan *p, int D, char *work) {
         u->units = ceil_div(rows, 2 * kGroupRows);
         u->rc = min(kGroupRows, (rows + 7) / 8 * 8);
         u->few = rows <= kFewRows;
+        u->start = u->few ? kStartFew : kStartWide;
         const size_t parts = (static_cast<size_t>(heads) * u->units + kMaxGrid) * 2 * u->rc;
         u->ml = reinterpret_cast<float2 *>(take(parts * sizeof(float2)));
         u->o = reinterpret_cast<float *>(take(parts * D * sizeof(float)));

@@ -12,12 +12,13 @@
 // scores, and leaves room in TMEM for two S ahead per group.
 //   warps 0-3, 4-7   two softmax groups, a thread per position, on alternate
 //                    tiles, each with its own (m, l, O)
-//   warps 8, 10      load key and value tiles page by page (TMA) into a ring
-//                    each
-//   warp 9           issues the products (tcgen05); scores run up to two tiles
-//                    ahead of the values
-//   warp 11          the query tile, and what belongs to its rows, of the next
-//                    segment; tells the softmax groups which it is
+//   warps 8, 11      load key and value tiles page by page (TMA) into a ring
+//                    each; warp 11 also stages the next segment's query tile and
+//                    what belongs to its rows
+//   warps 9, 10      issue the products (tcgen05): scores, values.  The scores run
+//                    up to two tiles a group ahead.  (One thread for both spent
+//                    over 1000 cycles a tile on its waits and bookkeeping beside
+//                    the products, where a tile's bytes take 1400 to arrive.)
 // The reference maximum of a row is common to a group's 128 threads; a vote per
 // tile (one hardware barrier) says whether any score outgrew it, which after
 // the first tile of a segment is rare, so maxima are reduced only then.  l is
@@ -34,7 +35,7 @@ constexpr float kNone = -FLT_MAX; // reference of a row that has seen nothing: b
 struct Barriers {
     unsigned long long k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
     unsigned long long q_full[2], q_empty[2];
-    unsigned long long s_full[2][2], s_empty[2][2], p_full[2][2], p_empty[2][2], drained;
+    unsigned long long s_full[2][2], s_empty[2][2], p_full[2][2], p_empty[2][2], drained[2];
 };
 
 template <int NR>
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_init(smem_addr(&bar.v_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
+            bar_init(smem_addr(&bar.drained[i]), 1);
             bar_init(smem_addr(&bar.q_full[i]), 1);
             bar_init(smem_addr(&bar.q_empty[i]), 9);  // the products, and eight softmax warps
             for (int w = 0; w < 2; ++w) {
@@ -184,7 +186,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 bar_init(smem_addr(&bar.p_empty[w][i]), 1);
             }
         }
-        bar_init(smem_addr(&bar.drained), 1);
         sh.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_proxy();
@@ -230,59 +231,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncthreads();
     }
 
-    if (warp == 8 || warp == 10) {
-        // ---- loads: keys, values
-        const bool key = warp == 8;
+    if (warp == 8) {
+        // ---- key loads
+        Loader<D, E4M3, S::kK> load;
+        PageIds ids;
         bool live = true;
-        int seg = 0;
-        auto run = [&](auto &load, uint8_t *ring, unsigned long long *full, unsigned long long *empty) {
-            while (live && walk.next(&g)) {
-                if (key && lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
-                __syncwarp();
-                for (int t = g.t0; live && t < g.t1; ++t)
-                    live = load.tile(a, g, pages_of(a, g), t, key ? &kmap : &vmap, smem_addr(ring), full, empty, dead,
-                                     &sh.fail[seg & 15], key);
-                ++seg;
-            }
-            if (!live) load.drain(full);
-        };
-        if (key) {
-            Loader<D, E4M3, S::kK> load;
-            run(load, k_ring, bar.k_full, bar.k_empty);
-        } else {
-            Loader<D, E4M3, S::kV> load;
-            run(load, v_ring, bar.v_full, bar.v_empty);
+        for (uint32_t seg = 0; live && walk.next(&g); ++seg) {
+            if (lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
+            __syncwarp();
+            ids.begin(a, g);
+            for (int t = g.t0; live && t < g.t1; ++t)
+                live = load.tile(a, g, ids, t, &kmap, smem_addr(k_ring), bar.k_full, bar.k_empty, dead, &sh.fail[seg & 15]);
         }
+        if (!live) load.drain(bar.k_full);
     } else if (warp == 9) {
-        // ---- products
+        // ---- scores
         if (elect_one()) {
-            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kPv = mma_desc(E4M3, NR, true, true);
-            constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>;
-            // Values narrower than 128 columns: the second block is the first again,
-            // and its rows of O are not read.
-            constexpr uint32_t kLead = D == 128 && !E4M3 ? S::kMat : 0;
+            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kHi = kMatrixHi<S::kRow>;
             const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(k_ring), 0);
-            const uint32_t v0 = matrix_lo(smem_addr(v_ring), kLead), p0 = matrix_lo(smem_addr(pt), 0);
             const uint32_t k_full = smem_addr(&bar.k_full[0]), k_empty = smem_addr(&bar.k_empty[0]);
-            const uint32_t v_full = smem_addr(&bar.v_full[0]), v_empty = smem_addr(&bar.v_empty[0]);
             const uint32_t s_full = smem_addr(&bar.s_full[0][0]), s_empty = smem_addr(&bar.s_empty[0][0]);
-            const uint32_t p_full = smem_addr(&bar.p_full[0][0]), p_empty = smem_addr(&bar.p_empty[0][0]);
-            // Two walks over the same tiles: the scores', and the values' behind it.
-            Walk ahead = walk;
-            Segment s;
-            uint32_t is = 0, iv = 0, seg_s = 0, seg_v = 0, ks = 0, kp = 0, vs = 0, vp = 0;
-            bool more_s = ahead.next(&s), more_v = walk.next(&g), live = true;
-            int ts = s.t0, tv = g.t0;
-            while (live && more_v) {
-                // At most two tiles and one segment ahead: the query ring holds two.
-                if (more_s && is <= iv + 2 && seg_s <= seg_v + 1) {
-                    const uint32_t w = is & 1, cnt = is >> 1, buf = w * 2 + (cnt & 1), qi = seg_s & 1;
-                    if (ts == s.t0) live = bar_wait(smem_addr(&bar.q_full[qi]), (seg_s >> 1) & 1, dead);
-                    live = live && bar_wait(k_full + 8 * ks, kp, dead) &&
-                           bar_wait(s_empty + 8 * buf, ((cnt >> 1) & 1) ^ 1, dead);
+            const uint32_t q_full = smem_addr(&bar.q_full[0]), q_empty = smem_addr(&bar.q_empty[0]);
+            uint32_t n = 0, seg = 0, ks = 0, kp = 0;
+            bool live = true;
+            while (live && walk.next(&g)) {
+                const uint32_t qi = seg & 1, q = q0 + qi * (S::kQ >> 4);
+                live = bar_wait(q_full + 8 * qi, (seg >> 1) & 1, dead);
+                for (int t = g.t0; live && t < g.t1; ++t, ++n) {
+                    // buffers in turn: group 0's first, group 1's first, then the second ones
+                    const uint32_t buf = (n & 1) * 2 + ((n >> 1) & 1);
+                    live = bar_wait(k_full + 8 * ks, kp, dead) && bar_wait(s_empty + 8 * buf, ((n >> 2) & 1) ^ 1, dead);
                     if (!live) break;
                     fence_after_sync();
-                    const uint32_t k = k0 + ks * (S::kSlot >> 4), q = q0 + qi * (S::kQ >> 4), d = tmem + buf * NR;
+                    const uint32_t k = k0 + ks * (S::kSlot >> 4), d = tmem + buf * NR;
                     if (E4M3) {
 #pragma unroll
                         for (int i = 0; i < 2 * (D / 32); ++i) {
@@ -301,20 +282,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         ks = 0;
                         kp ^= 1;
                     }
-                    ++is;
-                    if (++ts == s.t1) {
-                        mma_commit(smem_addr(&bar.q_empty[qi]));
-                        more_s = ahead.next(&s);
-                        ts = s.t0;
-                        ++seg_s;
-                    }
-                } else {
-                    const uint32_t w = iv & 1, cnt = iv >> 1, buf = w * 2 + (cnt & 1);
-                    live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * buf, (cnt >> 1) & 1, dead);
+                }
+                if (live) mma_commit(q_empty + 8 * qi);
+                ++seg;
+            }
+            if (!live) {  // products in flight end before TMEM is freed
+                mma_commit(smem_addr(&bar.drained[0]));
+                bar_drain(smem_addr(&bar.drained[0]), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- values
+        if (elect_one()) {
+            constexpr uint32_t kPv = mma_desc(E4M3, NR, true, true);
+            constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>;
+            // Values narrower than 128 columns: the second block is the first again,
+            // and its rows of O are not read.
+            constexpr uint32_t kLead = D == 128 && !E4M3 ? S::kMat : 0;
+            const uint32_t v0 = matrix_lo(smem_addr(v_ring), kLead), p0 = matrix_lo(smem_addr(pt), 0);
+            const uint32_t v_full = smem_addr(&bar.v_full[0]), v_empty = smem_addr(&bar.v_empty[0]);
+            const uint32_t p_full = smem_addr(&bar.p_full[0][0]), p_empty = smem_addr(&bar.p_empty[0][0]);
+            uint32_t n = 0, vs = 0, vp = 0;
+            bool live = true;
+            while (live && walk.next(&g)) {
+                for (int t = g.t0; live && t < g.t1; ++t, ++n) {
+                    const uint32_t w = n & 1, buf = w * 2 + ((n >> 1) & 1);
+                    live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * buf, (n >> 2) & 1, dead);
                     if (!live) break;
                     fence_after_sync();
                     const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + buf * (S::kP >> 4), d = tmem + (4 + w) * NR;
-                    const bool first = tv - g.t0 < 2;  // the group's first tile of the segment
+                    const bool first = t - g.t0 < 2;  // the group's first tile of the segment
                     if (E4M3) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -334,42 +332,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         vs = 0;
                         vp ^= 1;
                     }
-                    ++iv;
-                    if (++tv == g.t1) {
-                        more_v = walk.next(&g);
-                        tv = g.t0;
-                        ++seg_v;
-                    }
                 }
             }
-            if (!live) {  // products in flight end before TMEM is freed
-                mma_commit(smem_addr(&bar.drained));
-                bar_drain(smem_addr(&bar.drained), 0);
+            if (!live) {
+                mma_commit(smem_addr(&bar.drained[1]));
+                bar_drain(smem_addr(&bar.drained[1]), 0);
             }
         }
         __syncwarp();
     } else if (warp == 11) {
-        // ---- query tiles, a segment ahead (the first segment's is there)
-        bool live = true, more = true;
-        for (uint32_t seg = 0; live && more; ++seg) {
+        // ---- value loads; after a segment's, the query tile of the next (the
+        // first segment's is there)
+        Loader<D, E4M3, S::kV> load;
+        PageIds ids;
+        bool live = true, more = walk.next(&g);
+        if (lane == 0) bar_arrive(smem_addr(&bar.q_full[0]));
+        for (uint32_t seg = 1; live && more; ++seg) {
+            ids.begin(a, g);
+            for (int t = g.t0; live && t < g.t1; ++t)
+                live = load.tile(a, g, ids, t, &vmap, smem_addr(v_ring), bar.v_full, bar.v_empty, dead, nullptr);
             more = walk.next(&g);
-            if (seg > 0) {
-                live = bar_wait(smem_addr(&bar.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1, dead);
-                live = __all_sync(0xffffffffu, live);
-                if (!live) break;
-                if (more) {
-                    stage(seg & 1, lane, 32);
-                    __syncwarp();
-                    stage_rows(seg & 1, lane, 32);
-                } else {
-                    g.rows = 0;
-                }
-                if (lane == 0) sh.seg[seg & 1] = g;
-                fence_async_proxy();
+            live = live && bar_wait(smem_addr(&bar.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1, dead);
+            live = __all_sync(0xffffffffu, live);
+            if (!live) break;
+            if (more) {
+                stage(seg & 1, lane, 32);
+                __syncwarp();
+                stage_rows(seg & 1, lane, 32);
+            } else {
+                g.rows = 0;
             }
+            if (lane == 0) sh.seg[seg & 1] = g;
+            fence_async_proxy();
             __syncwarp();
             if (lane == 0) bar_arrive(smem_addr(&bar.q_full[seg & 1]));
         }
+        if (!live) load.drain(bar.v_full);
     } else {
         // ---- softmax groups
         const int w = warp >> 2, quad = warp & 3, row = tid & 127;  // row: the thread's position in a tile
@@ -603,8 +601,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 live = false;
                 break;
             }
-            const bool failed = reinterpret_cast<volatile int *>(sh.fail)[seg & 15] != 0;
-            const bool odd = reinterpret_cast<volatile int *>(sh.odd)[seg & 15] != 0;
+            // (A group without a tile of the segment has not waited for its loads: it
+            // leaves the flags to the other.)
+            const bool failed = wrote && reinterpret_cast<volatile int *>(sh.fail)[seg & 15] != 0;
+            const bool odd = wrote && reinterpret_cast<volatile int *>(sh.odd)[seg & 15] != 0;
             if (row < n_rows) {
                 const float m = ref[row];
                 const float sum = !wrote ? 0.0f : (sh.red[w][0][row] + sh.red[w][1][row]) + (sh.red[w][2][row] + sh.red[w][3][row]);

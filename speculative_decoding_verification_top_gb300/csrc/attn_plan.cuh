@@ -27,6 +27,7 @@ struct Units {
     int rows;             // query rows a (sequence, head); of all sequences for the prefix
     int row_tiles, units; // 128-row tiles and units (256 rows) of those
     int rc, few;          // rows a partial result holds; handled by the few-row kernel
+    int start;            // what beginning a unit costs, in tiles
     float *o;             // [slots, 2, rc, D] partial O
     float2 *ml;           // [slots, 2, rc] partial (m, l)
 };
@@ -77,6 +78,15 @@ __device__ __forceinline__ Tiles tiles_of(const Plan &p, int b) {
     return s;
 }
 
+// A unit's place on the cost line: `start` tiles' worth for beginning it, then
+// its tiles, each of c row tiles.  The share [from, to) of the line holds the
+// tiles [*t0, *t1) of the unit at ubase, possibly none.
+__device__ __forceinline__ void tiles_in(long long from, long long to, long long ubase, int T, int start, int c, int *t0,
+                                         int *t1) {
+    *t0 = from > ubase ? max(0, static_cast<int>((from - ubase + c - 1) / c) - start) : 0;
+    *t1 = max(0, static_cast<int>(min(static_cast<long long>(T), (to - ubase + c - 1) / c - start)));
+}
+
 // One unit and this CTA's tiles [t0, t1) of it.
 struct Segment {
     bool shared, dual;
@@ -85,7 +95,8 @@ struct Segment {
 };
 
 // Walks a CTA's share [x, end) of the cost line.  A tile of a unit costs its
-// row tiles (1 or 2): the products' work.  Every warp walks it by itself.
+// row tiles (1 or 2), the products' work; so does the unit's start, `start`
+// times.  Every warp walks it by itself.
 struct Walk {
     long long ubase, x, end;
     int b, h, u;          // next unit; b = -1: the shared prefix
@@ -100,9 +111,9 @@ struct Walk {
         }
         const bool sh = b < 0;
         if (!sh) s = tiles_of(p, b);
-        const int T = sh ? p.sT : s.t1 - s.t0, rt = sh ? p.shared.row_tiles : p.own.row_tiles;
-        const long long in = x - base0, head = static_cast<long long>(T) * rt;
-        if (head == 0) return;
+        const Units &k = sh ? p.shared : p.own;
+        const int T = (sh ? p.sT : s.t1 - s.t0) + k.start;
+        const long long in = x - base0, head = static_cast<long long>(T) * k.row_tiles;
         if (in < INT_MAX && head < INT_MAX) {
             h = static_cast<int>(in) / static_cast<int>(head);
             u = (static_cast<int>(in) - h * static_cast<int>(head)) / (2 * T);
@@ -130,14 +141,13 @@ struct Walk {
             g->dual = g->rows > kGroupRows;
             const int c = g->dual ? 2 : 1;
             const int first = sh ? 0 : s.t0;
-            g->t0 = x > ubase ? static_cast<int>((x - ubase + c - 1) / c) : 0;
-            g->t1 = static_cast<int>(min(static_cast<long long>(T), (end - ubase + c - 1) / c));
+            tiles_in(x, end, ubase, T, k.start, c, &g->t0, &g->t1);
             g->len = sh ? p.Ls : s.len;
             g->slot = ((sh ? 0 : b) * p.Hkv + h) * k.units + u + static_cast<int>(blockIdx.x);
             const bool some = g->t0 < g->t1;
             g->t0 += first;
             g->t1 += first;
-            ubase += static_cast<long long>(T) * c;
+            ubase += static_cast<long long>(T + k.start) * c;
             if (++u == k.units) {
                 u = 0;
                 if (++h == p.Hkv) {
@@ -161,6 +171,11 @@ struct Walk {
     }
 };
 
+// Cost of a sequence's unit a row tile; nothing without tiles.
+__device__ __forceinline__ int cost_of(const Units &u, const Tiles &s) {
+    return s.t1 > s.t0 ? s.t1 - s.t0 + u.start : 0;
+}
+
 // The start of a CTA's share, found by all its threads together.
 struct Start {
     long long scan[kAttnThreads / 32];
@@ -180,7 +195,7 @@ __device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *
     long long mine = 0;
     for (int b = bf; b < bt; ++b) {
         const Tiles s = tiles_of(p, b);
-        mine += (s.t1 - s.t0) * per;
+        mine += cost_of(p.own, s) * per;
     }
     long long incl = mine;
     for (int o = 1; o < 32; o *= 2) {
@@ -193,7 +208,7 @@ __device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *
         sh.base0 = 0;
     }
     __syncthreads();
-    const long long prefix = p.do_shared ? static_cast<long long>(p.Hkv) * p.shared.row_tiles * p.sT : 0;
+    const long long prefix = p.do_shared ? static_cast<long long>(p.Hkv) * p.shared.row_tiles * (p.sT + p.shared.start) : 0;
     long long before = prefix, total = prefix;
     for (int w = 0; w < kAttnThreads / 32; ++w) {
         if (w < warp) before += sh.scan[w];
@@ -211,7 +226,7 @@ __device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *
         long long at = before;
         for (int b = bf; b < bt; ++b) {
             const Tiles s = tiles_of(p, b);
-            const long long c = (s.t1 - s.t0) * per;
+            const long long c = cost_of(p.own, s) * per;
             if (here && x >= at && x < at + c) {
                 sh.b0 = b;
                 sh.base0 = at;
@@ -466,7 +481,38 @@ __device__ __forceinline__ int exponent_of(uint32_t four, int i) {
     return max(-120, min(120, static_cast<int>(static_cast<int8_t>(four >> 8 * i))));
 }
 
-// The loads of one CTA: a ring of slots, filled by one warp in the order the
+__device__ __forceinline__ const int32_t *pages_of(const AttnArgs &a, const Segment &g) {
+    return g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
+}
+
+// A warp's view of the page tables for one run of tiles in order: ids are read
+// 32 at a time, a lane each, with 32 more on their way, so that a tile waits
+// for a table entry once a segment.
+struct PageIds {
+    int block, ids, ids_next;
+
+    __device__ int entries(const AttnArgs &a, const Segment &g, int first) const {
+        const int i = first + (threadIdx.x & 31), shift = a.c.page_shift;
+        return i < (g.len + (1 << shift) - 1) >> shift ? pages_of(a, g)[i] : -1;
+    }
+
+    __device__ void begin(const AttnArgs &a, const Segment &g) {
+        block = (g.t0 * (kTile >> a.c.page_shift)) >> 5;
+        ids = entries(a, g, block * 32);
+        ids_next = entries(a, g, block * 32 + 32);
+    }
+
+    // Makes the block of page `first` (a tile's first: its pages lie in one
+    // block) the one held.
+    __device__ void turn(const AttnArgs &a, const Segment &g, int first) {
+        if (first >> 5 == block) return;
+        block = first >> 5;
+        ids = ids_next;
+        ids_next = entries(a, g, block * 32 + 32);
+    }
+};
+
+// The loads of one CTA into a ring of slots, by one warp, in the order the
 // products take the tiles.
 template <int D, bool E4M3, int kSlots>
 struct Loader {
@@ -476,19 +522,18 @@ struct Loader {
     // Tile t of segment g (keys or values) into the next slot.  False when a
     // wait ran out.  *fail is set where a page id is out of range (that page's
     // rows keep what the slot had; the segment's results are failed).
-    __device__ bool tile(const AttnArgs &a, const Segment &g, const int32_t *table, int t, const CUtensorMap *map,
-                         uint32_t ring, unsigned long long *full_bar, unsigned long long *empty_bar, volatile int *dead,
-                         int *fail, bool report = true) {
-        const int lane = threadIdx.x & 31, shift = a.c.page_shift, per_tile = kTile >> shift;
-        const int pages = min(per_tile, ((g.len - t * kTile) + (1 << shift) - 1) >> shift);
-        int id = -1;
-        if (lane < pages) {
-            id = table[t * per_tile + lane];
-            if (id < 0 || id >= a.c.num_pages) {
-                id = -1;
-                if (report) *fail = 1;
-                atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
-            }
+    __device__ bool tile(const AttnArgs &a, const Segment &g, PageIds &from, int t, const CUtensorMap *map, uint32_t ring,
+                         unsigned long long *full_bar, unsigned long long *empty_bar, volatile int *dead, int *fail) {
+        const int lane = threadIdx.x & 31, shift = a.c.page_shift, first = t * (kTile >> shift);
+        const int pages = min(kTile >> shift, ((g.len - t * kTile) + (1 << shift) - 1) >> shift);
+        from.turn(a, g, first);
+        int id = __shfl_sync(0xffffffffu, from.ids, (first + lane) & 31);
+        if (lane >= pages) {
+            id = -1;
+        } else if (id < 0 || id >= a.c.num_pages) {
+            id = -1;
+            if (fail) *fail = 1;
+            atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
         }
         const int good = __popc(__ballot_sync(0xffffffffu, id >= 0));
         const bool live = bar_wait(smem_addr(empty_bar + slot), phase, dead);
@@ -516,10 +561,6 @@ struct Loader {
             bar_drain(smem_addr(full_bar + i % kSlots), (i / kSlots) & 1);
     }
 };
-
-__device__ __forceinline__ const int32_t *pages_of(const AttnArgs &a, const Segment &g) {
-    return g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
-}
 
 int launch_wide(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
 int launch_few(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,

@@ -383,16 +383,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ---- loads.  Alternating tiles: K0 K1 V0 K2 V1 ...; both groups on each
         // tile: K0 V0 K1 V1 ...
         Loader<D, E4M3, S::kSlots> load;
+        PageIds key_ids, value_ids;
         int seg = 0;
         bool live = true;
         while (live && walk.next(&g)) {
             if (lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
             __syncwarp();
+            key_ids.begin(a, g);
+            value_ids = key_ids;
             const int n = g.t1 - g.t0;
             int kt = 0, vt = 0;
             for (int i = 0; live && i < 2 * n; ++i) {
                 const bool key = kt < n && (kt == vt || (!g.dual && kt == vt + 1));
-                live = load.tile(a, g, pages_of(a, g), g.t0 + (key ? kt++ : vt++), key ? &kmap : &vmap, smem_addr(ring),
+                live = load.tile(a, g, key ? key_ids : value_ids, g.t0 + (key ? kt++ : vt++), key ? &kmap : &vmap, smem_addr(ring),
                                  bar.full, bar.empty, dead, &sh.fail[seg & 15]);
             }
             ++seg;
