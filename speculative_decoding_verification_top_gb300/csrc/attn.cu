@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 
 // What beginning a unit costs, in tiles: staging its queries, a first tile that
 // waits for them, the partial result.
-constexpr int kStartFew = 3, kStartWide = 8;
+constexpr int kStartFew = 5, kStartWide = 16;
 
 // Fills the plan's sizes and carves its arrays; returns the bytes needed.
 size_t carve_plan(Plan *p, int D, char *work) {

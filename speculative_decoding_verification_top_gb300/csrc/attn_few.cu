@@ -30,6 +30,7 @@ namespace specv {
 namespace {
 
 constexpr int kGroupBarrier = 1;  // hardware barrier of softmax group 0; + 1 for group 1
+constexpr int kFirstBarrier = 3;  // of both
 constexpr float kNone = -FLT_MAX; // reference of a row that has seen nothing: below any score
 
 struct Barriers {
@@ -218,19 +219,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sh.rows[i].pos[r] = pos;
         }
     };
-    {
-        // The first segment's: everyone takes a share.
-        Walk ahead = walk;
-        const bool some = ahead.next(&g);
-        if (!some) g.rows = 0;
-        if (some) stage(0, tid, kAttnThreads);
-        fence_async_proxy();
-        if (E4M3) __syncthreads();  // the rows' factors
-        if (some) stage_rows(0, tid, kAttnThreads);
-        if (tid == 0) sh.seg[0] = g;
-        __syncthreads();
-    }
-
     if (warp == 8) {
         // ---- key loads
         Loader<D, E4M3, S::kK> load;
@@ -342,11 +330,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
     } else if (warp == 11) {
         // ---- value loads; after a segment's, the query tile of the next (the
-        // first segment's is there)
+        // softmax groups stage the first)
         Loader<D, E4M3, S::kV> load;
         PageIds ids;
         bool live = true, more = walk.next(&g);
-        if (lane == 0) bar_arrive(smem_addr(&bar.q_full[0]));
         for (uint32_t seg = 1; live && more; ++seg) {
             ids.begin(a, g);
             for (int t = g.t0; live && t < g.t1; ++t)
@@ -382,15 +369,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         uint32_t seg = 0, tile = 0, cnt = 0;  // segments, tiles of the CTA, tiles of this group
         bool live = true;
-        while (live) {
+        // Exponents of this thread's position in tile t of segment s.
+        auto exponents = [&](const Segment &s, int t, int *ek, int *ev) {
+            const int j = t * kTile + row;
+            int slot = 0;
+            const int page = t < s.t1 && j < s.len ? page_of(a.c, pages_of(a, s), INT_MAX, j, &slot) : -1;
+            const long long at = cache_row(a.c, max(page, 0), s.h, slot);
+            *ek = page < 0 ? 0 : a.c.k_exp[at];
+            *ev = page < 0 ? 0 : a.c.v_exp[at];
+        };
+        // The first segment's query tile: all eight warps, while the loads start.
+        if (!walk.next(&g)) g.rows = 0;
+        if (g.rows) stage(0, tid, 256);
+        __syncwarp();
+        if (E4M3) any_of(kFirstBarrier, 256, false);  // the rows' factors
+        if (g.rows) stage_rows(0, tid, 256);
+        if (tid == 0) sh.seg[0] = g;
+        fence_async_proxy();
+        __syncwarp();
+        any_of(kFirstBarrier, 256, false);
+        if (tid == 0) bar_arrive(smem_addr(&bar.q_full[0]));
+        bool ok = true;
+        int ek = 0, ev = 0;
+        if (E4M3 && g.rows) exponents(g, g.t0 + w, &ek, &ev);
+        while (g.rows) {
             const uint32_t half = seg & 1;
-            bool ok = bar_wait(smem_addr(&bar.q_full[half]), (seg >> 1) & 1, dead);
-            if (vote(!ok)) {
-                live = false;
-                break;
-            }
-            g = sh.seg[half];
-            if (g.rows == 0) break;
             const Units &u = g.shared ? p.shared : p.own;
             const long long part = static_cast<long long>(g.slot) * 2 + w;
             float2 *ml = u.ml + part * u.rc;
@@ -398,28 +401,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int n_rows = g.rows, first_tile = g.t0 + ((tile ^ w) & 1);  // this group's first
             const int origin = (g.shared ? 0 : a.shared_len) + g.len;
             const int last_pos = a.window > 0 ? last_position(a, g) : 0;
-            const int32_t *table = pages_of(a, g);
             float l[NR];
 #pragma unroll
             for (int i = 0; i < NR; ++i) l[i] = 0.0f;
             if (row < NR) ref[row] = row < n_rows ? kNone : INFINITY;
-            // exponents of this thread's position in tile t
-            auto exponents = [&](int t, int *ek, int *ev) {
-                const int j = t * kTile + row;
-                int slot = 0;
-                const int page = t < g.t1 && j < g.len ? page_of(a.c, table, INT_MAX, j, &slot) : -1;
-                const long long at = cache_row(a.c, max(page, 0), g.h, slot);
-                *ek = page < 0 ? 0 : a.c.k_exp[at];
-                *ev = page < 0 ? 0 : a.c.v_exp[at];
-            };
-            int ek = 0, ev = 0;
-            if (E4M3) exponents(first_tile, &ek, &ev);
-            vote(false);  // the reference is set
+            if (vote(!ok)) {  // the reference is set
+                live = false;
+                break;
+            }
             for (int t = first_tile; t < g.t1; t += 2, ++cnt) {
                 const int j0 = t * kTile, j = j0 + row;
                 const uint32_t buf = cnt & 1, phase = (cnt >> 1) & 1;
                 int ek_next = 0, ev_next = 0;
-                if (E4M3) exponents(t + 2, &ek_next, &ev_next);
+                if (E4M3) exponents(g, t + 2, &ek_next, &ev_next);
                 const bool whole = sees_whole(a, g, j0, last_pos);
                 // Position index of this thread's position, and the rows that see it.
                 int pos_j = (g.shared ? 0 : a.shared_len) + j;
@@ -588,6 +582,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!live) break;
             // ---- the group's partial result of the segment
             const bool wrote = first_tile < g.t1;
+            // What comes next, and its first exponents, while the last product runs.
+            ok = ok && bar_wait(smem_addr(&bar.q_full[half ^ 1]), ((seg + 1) >> 1) & 1, dead);
+            const Segment next = sh.seg[half ^ 1];
+            if (E4M3 && ok && next.rows) exponents(next, next.t0 + ((tile + (g.t1 - g.t0) ^ w) & 1), &ek, &ev);
             if (wrote) {
                 ok = ok && bar_wait(smem_addr(&bar.p_empty[w][(cnt - 1) & 1]), ((cnt - 1) >> 1) & 1, dead);
                 fence_after_sync();
@@ -629,6 +627,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (lane == 0) bar_arrive(smem_addr(&bar.q_empty[half]));
             ++seg;
             tile += g.t1 - g.t0;
+            g = next;
         }
         if (!live && row == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
     }
