@@ -12,13 +12,13 @@
 // scores, and leaves room in TMEM for two S ahead per group.
 //   warps 0-3, 4-7   two softmax groups, a thread per position, on alternate
 //                    tiles, each with its own (m, l, O)
-//   warps 8, 11      load key and value tiles page by page (TMA) into a ring
-//                    each; warp 11 also stages the next segment's query tile and
-//                    what belongs to its rows
-//   warps 9, 10      issue the products (tcgen05): scores, values.  The scores run
-//                    up to two tiles a group ahead.  (One thread for both spent
-//                    over 1000 cycles a tile on its waits and bookkeeping beside
-//                    the products, where a tile's bytes take 1400 to arrive.)
+//   warps 8, 10      load key and value tiles page by page (TMA) into a ring each
+//   warp 9           issues the products (tcgen05); scores run up to two tiles
+//                    ahead of the values.  (Scores and values issued by two warps
+//                    took 70 us where this takes 62, one sequence of 131077 e4m3
+//                    positions.)
+//   warp 11          the query tile, and what belongs to its rows, of the next
+//                    segment; tells the softmax groups which it is
 // The reference maximum of a row is common to a group's 128 threads; a vote per
 // tile (one hardware barrier) says whether any score outgrew it, which after
 // the first tile of a segment is rare, so maxima are reduced only then.  l is
@@ -29,14 +29,17 @@
 namespace specv {
 namespace {
 
+// Key slots: at most as many as there are score buffers, so that a slot is free
+// when the buffer of the tile kMaxKeys before is full.
+constexpr int kMaxKeys = 4;
 constexpr int kGroupBarrier = 1;  // hardware barrier of softmax group 0; + 1 for group 1
 constexpr int kFirstBarrier = 3;  // of both
 constexpr float kNone = -FLT_MAX; // reference of a row that has seen nothing: below any score
 
 struct Barriers {
-    unsigned long long k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
+    unsigned long long k_full[kMaxKeys], v_full[kMaxSlots], v_empty[kMaxSlots];
     unsigned long long q_full[2], q_empty[2];
-    unsigned long long s_full[2][2], s_empty[2][2], p_full[2][2], p_empty[2][2], drained[2];
+    unsigned long long s_full[4], p_full[4], drained;
 };
 
 template <int NR>
@@ -73,8 +76,8 @@ struct Layout : Shape<D, E4M3> {
     static constexpr int kP = kPMat * (E4M3 ? 2 : 1);                // one buffer of weights
     static constexpr int kFixed = static_cast<int>((sizeof(Shared<NR>) + 127) / 128 * 128);
     static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ - 4 * kP) / S::kSlot;
-    static constexpr int kSlots = kRoom < 2 * kMaxSlots ? kRoom : 2 * kMaxSlots;
-    static constexpr int kK = kSlots / 2, kV = kSlots - kK;          // slots of keys, of values
+    static constexpr int kSlots = kRoom < 2 * kMaxKeys + 4 ? kRoom : 2 * kMaxKeys + 4;
+    static constexpr int kK = kSlots / 2 < kMaxKeys ? kSlots / 2 : kMaxKeys, kV = kSlots - kK;  // of keys, of values
     static constexpr int kBytes = kFixed + 2 * kQ + 4 * kP + kSlots * S::kSlot;
     static constexpr uint32_t kColumns = NR == 32 ? 256 : 512;       // TMEM: 4 S and 2 O of NR columns
 };
@@ -170,23 +173,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");
 
     if (tid == 0) {
-        for (int i = 0; i < kMaxSlots; ++i) {
-            bar_init(smem_addr(&bar.k_full[i]), 1);
-            bar_init(smem_addr(&bar.k_empty[i]), 1);
+        for (int i = 0; i < S::kK; ++i) bar_init(smem_addr(&bar.k_full[i]), 1);
+        for (int i = 0; i < S::kV; ++i) {
             bar_init(smem_addr(&bar.v_full[i]), 1);
             bar_init(smem_addr(&bar.v_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            bar_init(smem_addr(&bar.drained[i]), 1);
             bar_init(smem_addr(&bar.q_full[i]), 1);
             bar_init(smem_addr(&bar.q_empty[i]), 9);  // the products, and eight softmax warps
-            for (int w = 0; w < 2; ++w) {
-                bar_init(smem_addr(&bar.s_full[w][i]), 1);
-                bar_init(smem_addr(&bar.s_empty[w][i]), 4);
-                bar_init(smem_addr(&bar.p_full[w][i]), 4);
-                bar_init(smem_addr(&bar.p_empty[w][i]), 1);
-            }
         }
+        for (int i = 0; i < 4; ++i) {
+            bar_init(smem_addr(&bar.s_full[i]), 1);
+            bar_init(smem_addr(&bar.p_full[i]), 4);
+        }
+        bar_init(smem_addr(&bar.drained), 1);
         sh.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_proxy();
@@ -228,118 +228,129 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
             __syncwarp();
             ids.begin(a, g);
-            for (int t = g.t0; live && t < g.t1; ++t)
-                live = load.tile(a, g, ids, t, &kmap, smem_addr(k_ring), bar.k_full, bar.k_empty, dead, &sh.fail[seg & 15]);
+            for (int t = g.t0; live && t < g.t1; ++t) {
+                // The slot's last tile n: its scores are in buffer n % 4.
+                const int n = static_cast<int>(load.n) - S::kK;
+                if (n >= 0) live = bar_wait(smem_addr(&bar.s_full[n & 3]), (n >> 2) & 1, dead);
+                live = __all_sync(0xffffffffu, live) &&
+                       load.tile(a, g, ids, t, &kmap, smem_addr(k_ring), bar.k_full, 0, dead, &sh.fail[seg & 15]);
+            }
         }
         if (!live) load.drain(bar.k_full);
-    } else if (warp == 9) {
-        // ---- scores
-        if (elect_one()) {
-            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kHi = kMatrixHi<S::kRow>;
-            const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(k_ring), 0);
-            const uint32_t k_full = smem_addr(&bar.k_full[0]), k_empty = smem_addr(&bar.k_empty[0]);
-            const uint32_t s_full = smem_addr(&bar.s_full[0][0]), s_empty = smem_addr(&bar.s_empty[0][0]);
-            const uint32_t q_full = smem_addr(&bar.q_full[0]), q_empty = smem_addr(&bar.q_empty[0]);
-            uint32_t n = 0, seg = 0, ks = 0, kp = 0;
-            bool live = true;
-            while (live && walk.next(&g)) {
-                const uint32_t qi = seg & 1, q = q0 + qi * (S::kQ >> 4);
-                live = bar_wait(q_full + 8 * qi, (seg >> 1) & 1, dead);
-                for (int t = g.t0; live && t < g.t1; ++t, ++n) {
-                    // buffers in turn: group 0's first, group 1's first, then the second ones
-                    const uint32_t buf = (n & 1) * 2 + ((n >> 1) & 1);
-                    live = bar_wait(k_full + 8 * ks, kp, dead) && bar_wait(s_empty + 8 * buf, ((n >> 2) & 1) ^ 1, dead);
-                    if (!live) break;
-                    fence_after_sync();
-                    const uint32_t k = k0 + ks * (S::kSlot >> 4), d = tmem + buf * NR;
-                    if (E4M3) {
-#pragma unroll
-                        for (int i = 0; i < 2 * (D / 32); ++i) {
-                            const uint32_t term = i / (D / 32), j = i % (D / 32);
-                            mma_ss<true>(d, k + (j * 32 >> 4), kHi, q + ((term * S::kQBlock + j * 32) >> 4), kHi, kQk, i > 0);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
-                            mma_ss<false>(d, k + (((i / 4) * S::kMat + (i % 4) * 32) >> 4), kHi,
-                                          q + (((i / 4) * S::kQBlock + (i % 4) * 32) >> 4), kHi, kQk, i > 0);
-                    }
-                    mma_commit(s_full + 8 * buf);
-                    mma_commit(k_empty + 8 * ks);
-                    if (++ks == S::kK) {
-                        ks = 0;
-                        kp ^= 1;
-                    }
-                }
-                if (live) mma_commit(q_empty + 8 * qi);
-                ++seg;
-            }
-            if (!live) {  // products in flight end before TMEM is freed
-                mma_commit(smem_addr(&bar.drained[0]));
-                bar_drain(smem_addr(&bar.drained[0]), 0);
-            }
-        }
-        __syncwarp();
     } else if (warp == 10) {
-        // ---- values
+        // ---- value loads
+        Loader<D, E4M3, S::kV> load;
+        PageIds ids;
+        bool live = true;
+        while (live && walk.next(&g)) {
+            ids.begin(a, g);
+            for (int t = g.t0; live && t < g.t1; ++t)
+                live = load.tile(a, g, ids, t, &vmap, smem_addr(v_ring), bar.v_full, smem_addr(&bar.v_empty[load.slot]), dead,
+                                 nullptr);
+        }
+        if (!live) load.drain(bar.v_full);
+    } else if (warp == 9) {
+        // ---- products
         if (elect_one()) {
-            constexpr uint32_t kPv = mma_desc(E4M3, NR, true, true);
+            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kPv = mma_desc(E4M3, NR, true, true);
             constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>;
             // Values narrower than 128 columns: the second block is the first again,
             // and its rows of O are not read.
             constexpr uint32_t kLead = D == 128 && !E4M3 ? S::kMat : 0;
+            const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(k_ring), 0);
             const uint32_t v0 = matrix_lo(smem_addr(v_ring), kLead), p0 = matrix_lo(smem_addr(pt), 0);
-            const uint32_t v_full = smem_addr(&bar.v_full[0]), v_empty = smem_addr(&bar.v_empty[0]);
-            const uint32_t p_full = smem_addr(&bar.p_full[0][0]), p_empty = smem_addr(&bar.p_empty[0][0]);
-            uint32_t n = 0, vs = 0, vp = 0;
-            bool live = true;
+            const uint32_t k_full = smem_addr(&bar.k_full[0]), v_full = smem_addr(&bar.v_full[0]);
+            const uint32_t v_empty = smem_addr(&bar.v_empty[0]), q_full = smem_addr(&bar.q_full[0]);
+            const uint32_t s_full = smem_addr(&bar.s_full[0]), p_full = smem_addr(&bar.p_full[0]);
+            // Two walks over the same tiles: the scores', and the values' behind it.
+            Walk ahead = walk;
+            Segment s;
+            uint32_t is = 0, iv = 0, seg_s = 0, seg_v = 0, ks = 0, kp = 0, vs = 0, vp = 0, q = q0;
+            bool more_s = ahead.next(&s), live = true, begin = true;
+            int left_s = s.t1 - s.t0;
             while (live && walk.next(&g)) {
-                for (int t = g.t0; live && t < g.t1; ++t, ++n) {
-                    const uint32_t w = n & 1, buf = w * 2 + ((n >> 1) & 1);
-                    live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * buf, (n >> 2) & 1, dead);
-                    if (!live) break;
+                int left_v = g.t1 - g.t0;
+                uint32_t first = 2;  // tiles to come that are their group's first of the segment
+                while (live && left_v > 0) {
+                    // At most two tiles ahead, and one segment: the query ring holds two.  A
+                    // score buffer is free then: its last tile's weights have been waited for.
+                    if (more_s && is <= iv + 2 && seg_s <= seg_v + 1) {
+                        if (begin) {
+                            live = bar_wait(q_full + 8 * (seg_s & 1), (seg_s >> 1) & 1, dead);
+                            q = q0 + (seg_s & 1) * (S::kQ >> 4);
+                            begin = false;
+                        }
+                        live = live && bar_wait(k_full + 8 * ks, kp, dead);
+                        fence_after_sync();
+                        const uint32_t k = k0 + ks * (S::kSlot >> 4), d = tmem + (is & 3) * NR;
+                        if (E4M3) {
+#pragma unroll
+                            for (int i = 0; i < 2 * (D / 32); ++i) {
+                                const uint32_t term = i / (D / 32), j = i % (D / 32);
+                                mma_ss<true>(d, k + (j * 32 >> 4), kHi, q + ((term * S::kQBlock + j * 32) >> 4), kHi, kQk,
+                                             i > 0);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+                                mma_ss<false>(d, k + (((i / 4) * S::kMat + (i % 4) * 32) >> 4), kHi,
+                                              q + (((i / 4) * S::kQBlock + (i % 4) * 32) >> 4), kHi, kQk, i > 0);
+                        }
+                        mma_commit(s_full + 8 * (is & 3));
+                        if (++ks == S::kK) {
+                            ks = 0;
+                            kp ^= 1;
+                        }
+                        ++is;
+                        if (--left_s == 0) {
+                            mma_commit(smem_addr(&bar.q_empty[seg_s & 1]));
+                            more_s = ahead.next(&s);
+                            left_s = s.t1 - s.t0;
+                            ++seg_s;
+                            begin = true;
+                        }
+                        continue;
+                    }
+                    live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * (iv & 3), (iv >> 2) & 1, dead);
                     fence_after_sync();
-                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + buf * (S::kP >> 4), d = tmem + (4 + w) * NR;
-                    const bool first = t - g.t0 < 2;  // the group's first tile of the segment
+                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + (iv & 3) * (S::kP >> 4);
+                    const uint32_t d = tmem + (4 + (iv & 1)) * NR;
                     if (E4M3) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint32_t j = i % 4;
                             mma_ss<true>(d, v + (j * 32 * S::kRow >> 4), kHi,
-                                         pb + (((i / 4) * S::kPMat + j * 32 * S::kPRow) >> 4), kPHi, kPv, i > 0 || !first);
+                                         pb + (((i / 4) * S::kPMat + j * 32 * S::kPRow) >> 4), kPHi, kPv, i > 0 || first == 0);
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             mma_ss<false>(d, v + (i * 16 * S::kRow >> 4), kHi, pb + (i * 16 * S::kPRow >> 4), kPHi, kPv,
-                                          i > 0 || !first);
+                                          i > 0 || first == 0);
                     }
-                    mma_commit(p_empty + 8 * buf);
                     mma_commit(v_empty + 8 * vs);
                     if (++vs == S::kV) {
                         vs = 0;
                         vp ^= 1;
                     }
+                    ++iv;
+                    first -= first > 0;
+                    --left_v;
                 }
+                ++seg_v;
             }
-            if (!live) {
-                mma_commit(smem_addr(&bar.drained[1]));
-                bar_drain(smem_addr(&bar.drained[1]), 0);
+            if (!live) {  // products in flight end before TMEM is freed
+                mma_commit(smem_addr(&bar.drained));
+                bar_drain(smem_addr(&bar.drained), 0);
             }
         }
         __syncwarp();
     } else if (warp == 11) {
-        // ---- value loads; after a segment's, the query tile of the next (the
-        // softmax groups stage the first)
-        Loader<D, E4M3, S::kV> load;
-        PageIds ids;
+        // ---- query tiles, a segment ahead (the softmax groups stage the first)
         bool live = true, more = walk.next(&g);
         for (uint32_t seg = 1; live && more; ++seg) {
-            ids.begin(a, g);
-            for (int t = g.t0; live && t < g.t1; ++t)
-                live = load.tile(a, g, ids, t, &vmap, smem_addr(v_ring), bar.v_full, bar.v_empty, dead, nullptr);
             more = walk.next(&g);
-            live = live && bar_wait(smem_addr(&bar.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1, dead);
+            live = bar_wait(smem_addr(&bar.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1, dead);
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
             if (more) {
@@ -354,7 +365,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(smem_addr(&bar.q_full[seg & 1]));
         }
-        if (!live) load.drain(bar.v_full);
     } else {
         // ---- softmax groups
         const int w = warp >> 2, quad = warp & 3, row = tid & 127;  // row: the thread's position in a tile
@@ -411,7 +421,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             for (int t = first_tile; t < g.t1; t += 2, ++cnt) {
                 const int j0 = t * kTile, j = j0 + row;
-                const uint32_t buf = cnt & 1, phase = (cnt >> 1) & 1;
+                const uint32_t buf = w + 2 * (cnt & 1), phase = (cnt >> 1) & 1;
                 int ek_next = 0, ev_next = 0;
                 if (E4M3) exponents(g, t + 2, &ek_next, &ev_next);
                 const bool whole = sees_whole(a, g, j0, last_pos);
@@ -425,16 +435,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     seen = seen_rows<NR>(a, g, rows, j, pos_j);
                     ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
                 }
-                ok = ok && bar_wait(smem_addr(&bar.s_full[w][buf]), phase, dead);
+                ok = ok && bar_wait(smem_addr(&bar.s_full[buf]), phase, dead);
                 fence_after_sync();
                 __syncwarp();
                 float s[NR];
 #pragma unroll
-                for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + (w * 2 + buf) * NR + c, s + c);
+                for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + buf * NR + c, s + c);
                 tmem_load_wait();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) bar_arrive(smem_addr(&bar.s_empty[w][buf]));
                 const float fk = E4M3 ? exp2i(max(-120, min(120, ek))) : 1.0f;
                 const float fb = E4M3 ? static_cast<float>(max(-120, min(120, ev))) : 0.0f;
                 const float fl = E4M3 ? exp2i(-max(-120, min(120, ev))) : 1.0f;
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     vote(false);
                     const bool wrote = t >= g.t0 + 2;
                     if (wrote) {  // the products so far have to be in
-                        ok = bar_wait(smem_addr(&bar.p_empty[w][(cnt - 1) & 1]), ((cnt - 1) >> 1) & 1, dead);
+                        ok = bar_wait(smem_addr(&bar.v_empty[(vi - 2) % S::kV]), ((vi - 2) / S::kV) & 1, dead);
                         ok = __all_sync(0xffffffffu, ok);
                         fence_after_sync();
                     }
@@ -539,8 +546,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
                 // Weights, and their place as the product's operand: a row per position.
-                ok = ok && bar_wait(smem_addr(&bar.p_empty[w][buf]), phase ^ 1, dead);
-                uint8_t *pb = pt + (w * 2 + buf) * S::kP;
+                // (Their buffer is free: these scores came after the product that read it.)
+                uint8_t *pb = pt + buf * S::kP;
 #pragma unroll
                 for (int c0 = 0; c0 < NR; c0 += 16) {
                     if (c0 >= n_rows) break;
@@ -575,7 +582,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 fence_async_proxy();
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) bar_arrive(smem_addr(&bar.p_full[w][buf]));
+                if (lane == 0) bar_arrive(smem_addr(&bar.p_full[buf]));
                 ek = ek_next;
                 ev = ev_next;
             }
@@ -587,7 +594,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const Segment next = sh.seg[half ^ 1];
             if (E4M3 && ok && next.rows) exponents(next, next.t0 + ((tile + (g.t1 - g.t0) ^ w) & 1), &ek, &ev);
             if (wrote) {
-                ok = ok && bar_wait(smem_addr(&bar.p_empty[w][(cnt - 1) & 1]), ((cnt - 1) >> 1) & 1, dead);
+                const uint32_t vi = tile + ((g.t1 - 1 - first_tile) & ~1) + (first_tile - g.t0);  // the group's last tile
+                ok = ok && bar_wait(smem_addr(&bar.v_empty[vi % S::kV]), (vi / S::kV) & 1, dead);
                 fence_after_sync();
                 __syncwarp();
                 float sum[NR / 32];

@@ -519,11 +519,12 @@ struct Loader {
     using S = Shape<D, E4M3>;
     uint32_t slot = 0, phase = 1, n = 0;
 
-    // Tile t of segment g (keys or values) into the next slot.  False when a
+    // Tile t of segment g (keys or values) into the next slot, once `empty` (if
+    // given) has completed its last use: in the ring's own phase.  False when a
     // wait ran out.  *fail is set where a page id is out of range (that page's
     // rows keep what the slot had; the segment's results are failed).
     __device__ bool tile(const AttnArgs &a, const Segment &g, PageIds &from, int t, const CUtensorMap *map, uint32_t ring,
-                         unsigned long long *full_bar, unsigned long long *empty_bar, volatile int *dead, int *fail) {
+                         unsigned long long *full_bar, uint32_t empty, volatile int *dead, int *fail) {
         const int lane = threadIdx.x & 31, shift = a.c.page_shift, first = t * (kTile >> shift);
         const int pages = min(kTile >> shift, ((g.len - t * kTile) + (1 << shift) - 1) >> shift);
         from.turn(a, g, first);
@@ -536,7 +537,7 @@ struct Loader {
             atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
         }
         const int good = __popc(__ballot_sync(0xffffffffu, id >= 0));
-        const bool live = bar_wait(smem_addr(empty_bar + slot), phase, dead);
+        const bool live = empty == 0 || bar_wait(empty, phase, dead);
         if (!__all_sync(0xffffffffu, live)) return false;
         const uint32_t full = smem_addr(full_bar + slot);
         if (lane == 0) bar_arrive_tx(full, static_cast<uint32_t>(good * (S::kSlot >> 7) << shift));

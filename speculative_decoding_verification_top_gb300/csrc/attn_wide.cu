@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int i = 0; live && i < 2 * n; ++i) {
                 const bool key = kt < n && (kt == vt || (!g.dual && kt == vt + 1));
                 live = load.tile(a, g, key ? key_ids : value_ids, g.t0 + (key ? kt++ : vt++), key ? &kmap : &vmap, smem_addr(ring),
-                                 bar.full, bar.empty, dead, &sh.fail[seg & 15]);
+                                 bar.full, smem_addr(&bar.empty[load.slot]), dead, &sh.fail[seg & 15]);
             }
             ++seg;
         }

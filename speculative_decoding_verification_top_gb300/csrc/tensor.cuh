@@ -40,32 +40,36 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-constexpr long long kWaitCycles = 1ll << 32;  // a wait gives up after about two seconds
+constexpr uint32_t kTries = 1u << 21;  // a wait gives up after this many (each may suspend): seconds
 
-// Waits for the phase `parity`; false when the limit ran out here or, as
-// *dead tells, elsewhere in the CTA: the caller then leaves its loops.  (The
-// SM's own clock: reading the global timer costs over a microsecond.)
+// Waits for the phase `parity`; false when the tries ran out: *dead is set and
+// the caller leaves its loops (others then run out of theirs).  The loop is one
+// asm statement: the thread that issues the products is bound by its own
+// instructions, and this is most of what it does.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
-    long long t0 = 0;
-    for (uint32_t i = 0; !bar_try(bar, parity); ++i) {
-        if ((i & 63) != 63) continue;
-        if (*dead) return false;
-        const long long t = clock64();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > kWaitCycles) {
-            *dead = 1;
-            return false;
-        }
-    }
-    return true;
+    uint32_t tries;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mov.u32 %0, 0;\n"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 %0, %0, 1;\n\t"
+        "setp.lt.u32 p, %0, %3;\n\t"
+        "@p bra AGAIN;\n"
+        "DONE:\n\t}"
+        : "=&r"(tries)
+        : "r"(bar), "r"(parity), "n"(kTries)
+        : "memory");
+    if (tries < kTries) return true;
+    *dead = 1;
+    return false;
 }
 
-// The same without the flag: true if the phase completed in time.
-__device__ __forceinline__ bool bar_drain(uint32_t bar, uint32_t parity) {
-    const long long t0 = clock64();
-    while (!bar_try(bar, parity))
-        if (clock64() - t0 > kWaitCycles) return false;
-    return true;
+// The same without the flag.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kTries && !bar_try(bar, parity); ++i) {
+    }
 }
 
 // True in one lane of a converged warp.  Code under it counts as one thread's
