@@ -361,8 +361,7 @@ def _stream(stream):
 
 
 def _need(t, name, dtype, shape):
-    torch = _torch()
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != dtype or t.shape != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
         raise ValueError("%s must be a contiguous CUDA %s tensor of shape %s, got %s %s"
                          % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
@@ -548,23 +547,24 @@ def verify_tree_sample(target, draft, parents, node_tokens, uniforms, depth, tem
 class KVCache(collections.namedtuple("KVCache", "k v k_exp v_exp")):
     """A paged cache's tensors: k, v [num_pages, Hkv, page, D] bf16, or
     float8_e4m3fn with int8 exponents k_exp, v_exp [num_pages, Hkv, page]
-    (else None)."""
+    (else None).  Checked once, here; the calls pass its C descriptor."""
 
-    def descriptor(self):
+    def __new__(cls, k, v, k_exp=None, v_exp=None):
         torch = _torch()
-        n, H, page, D = self.k.shape
-        e4m3 = self.k.dtype == torch.float8_e4m3fn
-        if not e4m3 and self.k.dtype != torch.bfloat16:
-            raise TypeError("a cache holds torch.bfloat16 or torch.float8_e4m3fn, got %s"
-                            % self.k.dtype)
-        for t, name in ((self.k, "cache.k"), (self.v, "cache.v")):
-            _need(t, name, self.k.dtype, (n, H, page, D))
+        self = super().__new__(cls, k, v, k_exp, v_exp)
+        n, H, page, D = k.shape
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if not e4m3 and k.dtype != torch.bfloat16:
+            raise TypeError("a cache holds torch.bfloat16 or torch.float8_e4m3fn, got %s" % k.dtype)
+        for t, name in ((k, "cache.k"), (v, "cache.v")):
+            _need(t, name, k.dtype, (n, H, page, D))
         if e4m3:
-            for t, name in ((self.k_exp, "cache.k_exp"), (self.v_exp, "cache.v_exp")):
+            for t, name in ((k_exp, "cache.k_exp"), (v_exp, "cache.v_exp")):
                 _need(t, name, torch.int8, (n, H, page))
-        return CacheDescriptor(_ptr(self.k), _ptr(self.v), _ptr(self.k_exp) if e4m3 else None,
-                               _ptr(self.v_exp) if e4m3 else None, n, H, page, D,
-                               SPEC_E4M3 if e4m3 else SPEC_BF16)
+        self.descriptor = CacheDescriptor(
+            _ptr(k), _ptr(v), _ptr(k_exp) if e4m3 else None, _ptr(v_exp) if e4m3 else None, n, H,
+            page, D, SPEC_E4M3 if e4m3 else SPEC_BF16)
+        return self
 
 
 def new_cache(num_pages, Hkv, page, D, device, e4m3=False):
@@ -584,16 +584,18 @@ def _tokens(t, name, H, D, dtypes):
     """[B, N, H, D] with packed tokens; returns their stride in elements.
     Consecutive tokens may lie further apart (slices of a wider projection),
     evenly over the whole batch."""
-    B, N = t.shape[:2]
-    if t.dtype not in dtypes or t.dim() != 4 or tuple(t.shape[2:]) != (H, D) or not t.is_cuda:
+    if t.dtype not in dtypes or t.dim() != 4 or t.shape[2:] != (H, D) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor [B, N, %d, %d] of %s, got %s %s"
                          % (name, H, D, "/".join(map(str, dtypes)), t.dtype, tuple(t.shape)))
-    step = t.stride(1) if N > 1 else t.stride(0) if B > 1 else H * D
-    ok = t.stride(3) == 1 and (H == 1 or t.stride(2) == D)
-    if not t.numel() or (ok and (B < 2 or t.stride(0) == N * step)):
-        return step if t.numel() else 0
+    if t.is_contiguous():
+        return H * D
+    B, N = t.shape[:2]
+    s = t.stride()
+    step = s[1] if N > 1 else s[0] if B > 1 else H * D
+    if s[3] == 1 and (H == 1 or s[2] == D) and (B < 2 or s[0] == N * step):
+        return step
     raise ValueError("%s: each token's heads must be contiguous and tokens evenly spaced, got "
-                     "strides %s" % (name, tuple(t.stride())))
+                     "strides %s" % (name, s))
 
 
 def kv_append(cache, page_table, starts, k, v, rows=None, stream=None):
@@ -601,10 +603,9 @@ def kv_append(cache, page_table, starts, k, v, rows=None, stream=None):
     to positions starts[b] + t of a KVCache; rows [B, M] int32 picks the
     tokens (spec_verify_tree's out_path: the accepted nodes, -1 skipped)."""
     torch = _torch()
-    c = cache.descriptor()
+    c = cache.descriptor
     B, N = k.shape[:2]
-    kinds = (torch.float32, torch.bfloat16)
-    step = _tokens(k, "k", c.Hkv, c.D, kinds)
+    step = _tokens(k, "k", c.Hkv, c.D, (torch.bfloat16, torch.float32))
     if _tokens(v, "v", c.Hkv, c.D, (k.dtype,)) != step or v.shape != k.shape:
         raise ValueError("k and v must have one shape and token stride")
     _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
@@ -621,7 +622,7 @@ def kv_read(cache, page_table, starts, count, dtype=None, stream=None):
     """Tensor-level spec_kv_read: (k, v) [B, count, Hkv, D] of the positions
     from starts[b] on, in bf16 (or fp32)."""
     torch = _torch()
-    c = cache.descriptor()
+    c = cache.descriptor
     B = starts.shape[0]
     _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
     _need(starts, "starts", torch.int32, (B,))
@@ -635,7 +636,7 @@ def kv_read(cache, page_table, starts, count, dtype=None, stream=None):
 def _attn(call, q, cache, before, page_table, lens, mask, pos, slopes, scale, cap, window, out, lse,
           workspace, stream):
     torch = _torch()
-    c = cache.descriptor()
+    c = cache.descriptor
     B, N, Hq = q.shape[:3]
     step = _tokens(q, "q", Hq, c.D, (torch.bfloat16,))
     _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))

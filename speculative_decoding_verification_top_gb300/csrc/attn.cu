@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         M[i] = kNegInf;
         L[i] = 0.0f;
     }
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // Adds the rows' results of one slot: two groups, both of these rows, or each
     // of its own 128 rows.
@@ -246,21 +247,24 @@ int launch_join(const KernelArgs &ka, int grid, cudaStream_t st) {
     // sequences of 85 nodes (two to three shares a unit).
     const Plan &p = ka.p;
     const bool split = 4ll * p.B * p.Hkv * p.own.units <= grid && p.sT == 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * ceil_div(p.own.rows, split ? 1 : 4 * kJoinWarps)));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split ? attn_join_kernel<D, true> : attn_join_kernel<D, false>, ka) == cudaSuccess
+    const dim3 blocks(static_cast<unsigned>(p.B * p.Hkv * ceil_div(p.own.rows, split ? 1 : 4 * kJoinWarps)));
+    return launch_early(split ? attn_join_kernel<D, true> : attn_join_kernel<D, false>, blocks, dim3(kJoinThreads), 0, st, ka)
                ? SPEC_OK
                : SPEC_ERR_CUDA;
 }
 
 }  // namespace
+
+// The current device's multiprocessors, asked for once a device.
+static int multiprocessors() {
+    static int known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if ((n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
+    return n;
+}
 
 size_t attn_work_bytes(int B, int N, int Hq, int Hkv, int D) {
     Plan p = {};
@@ -288,23 +292,21 @@ int launch_attn(const AttnArgs &a, cudaStream_t st) {
     p.window = a.window;
     carve_plan(&p, a.c.D, a.work);
     CUtensorMap kmap, vmap;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        !make_map(&kmap, a.c.k, a.c) || !make_map(&vmap, a.c.v, a.c))
-        return SPEC_ERR_CUDA;
+    const int sms = multiprocessors();
+    if (sms <= 0 || !make_map(&kmap, a.c.k, a.c) || !make_map(&vmap, a.c.v, a.c)) return SPEC_ERR_CUDA;
     const int grid = min(sms, kMaxGrid);
     // One launch where both kinds of units (or the only one) go to one kernel;
     // else the prefix's wide one and, beside its tail, the sequences' few-row one.
     p.do_shared = p.sT > 0;
     p.do_own = !p.do_shared || p.shared.few == p.own.few;
     const bool few = p.do_shared ? p.shared.few : p.own.few;
-    int rc = few ? launch_few(ka, grid, kmap, vmap, false, st) : launch_wide(ka, grid, kmap, vmap, st);
+    int rc = few ? launch_few(ka, grid, kmap, vmap, st) : launch_wide(ka, grid, kmap, vmap, st);
     if (rc != SPEC_OK) return rc;
     if (!p.do_own) {
         p.do_shared = 0;
         p.do_own = 1;
-        rc = launch_few(ka, grid, kmap, vmap, true, st);
+        ka.beside = 1;
+        rc = launch_few(ka, grid, kmap, vmap, st);
         if (rc != SPEC_OK) return rc;
     }
     return a.c.D == 128 ? launch_join<128>(ka, grid, st) : launch_join<64>(ka, grid, st);

@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Shared<NR> &sh = *reinterpret_cast<Shared<NR> *>(qt + 2 * S::kQ);
     Barriers &bar = sh.bar;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;");
 
     if (tid == 0) {
         for (int i = 0; i < S::kK; ++i) bar_init(smem_addr(&bar.k_full[i]), 1);
@@ -192,6 +191,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         fence_async_proxy();
     }
     if (warp == 9) tmem_alloc(smem_addr(&sh.tmem), S::kColumns);
+    // Up to here this may run beside the kernel before it.  (Beside the prefix's
+    // kernel all of it may: that one has waited for what came before the call.)
+    if (!ka.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     long long from, to;
     find_share(p, sh.start, &from, &to);
     fence_before_sync();
@@ -644,50 +647,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     fence_after_sync();
     if (warp == 9) tmem_free(tmem, S::kColumns);
     // Launched beside the prefix's kernel: this grid ends after that one.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (ka.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, bool E4M3, bool EXTRA, int NR>
-int launch_shape(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,
+int launch_shape(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap,
                  cudaStream_t st) {
     static int done[64];
     auto kernel = attn_few_kernel<D, E4M3, EXTRA, NR>;
     if (!allow_smem(kernel, Layout<D, E4M3, NR>::kBytes, done)) return SPEC_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kAttnThreads);
-    cfg.dynamicSmemBytes = Layout<D, E4M3, NR>::kBytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = dependent ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, ka, kmap, vmap) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_early(kernel, dim3(grid), dim3(kAttnThreads), Layout<D, E4M3, NR>::kBytes, st, ka, kmap, vmap)
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
 }
 
 template <int D, bool E4M3, bool EXTRA>
-int launch_rows(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,
+int launch_rows(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap,
                 cudaStream_t st) {
     const int rows = ka.p.do_shared ? ka.p.shared.rows : ka.p.own.rows;
-    return rows <= 32 ? launch_shape<D, E4M3, EXTRA, 32>(ka, grid, kmap, vmap, dependent, st)
-                      : launch_shape<D, E4M3, EXTRA, 64>(ka, grid, kmap, vmap, dependent, st);
+    return rows <= 32 ? launch_shape<D, E4M3, EXTRA, 32>(ka, grid, kmap, vmap, st)
+                      : launch_shape<D, E4M3, EXTRA, 64>(ka, grid, kmap, vmap, st);
 }
 
 }  // namespace
 
-int launch_few(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,
-               cudaStream_t st) {
+int launch_few(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
     const bool extra = ka.a.cap > 0.0f || ka.a.slopes, wide = ka.a.c.D == 128;
     if (ka.a.c.e4m3)
-        return extra ? (wide ? launch_rows<128, true, true>(ka, grid, kmap, vmap, dependent, st)
-                             : launch_rows<64, true, true>(ka, grid, kmap, vmap, dependent, st))
-                     : (wide ? launch_rows<128, true, false>(ka, grid, kmap, vmap, dependent, st)
-                             : launch_rows<64, true, false>(ka, grid, kmap, vmap, dependent, st));
-    return extra ? (wide ? launch_rows<128, false, true>(ka, grid, kmap, vmap, dependent, st)
-                         : launch_rows<64, false, true>(ka, grid, kmap, vmap, dependent, st))
-                 : (wide ? launch_rows<128, false, false>(ka, grid, kmap, vmap, dependent, st)
-                         : launch_rows<64, false, false>(ka, grid, kmap, vmap, dependent, st));
+        return extra ? (wide ? launch_rows<128, true, true>(ka, grid, kmap, vmap, st)
+                             : launch_rows<64, true, true>(ka, grid, kmap, vmap, st))
+                     : (wide ? launch_rows<128, true, false>(ka, grid, kmap, vmap, st)
+                             : launch_rows<64, true, false>(ka, grid, kmap, vmap, st));
+    return extra ? (wide ? launch_rows<128, false, true>(ka, grid, kmap, vmap, st)
+                         : launch_rows<64, false, true>(ka, grid, kmap, vmap, st))
+                 : (wide ? launch_rows<128, false, false>(ka, grid, kmap, vmap, st)
+                         : launch_rows<64, false, false>(ka, grid, kmap, vmap, st));
 }
 
 }  // namespace specv

@@ -47,6 +47,7 @@ struct Plan {
 struct KernelArgs {
     AttnArgs a;
     Plan p;
+    int beside;  // launched beside the tail of this call's other kernel
 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -564,11 +565,27 @@ struct Loader {
 };
 
 int launch_wide(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
-int launch_few(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, bool dependent,
-               cudaStream_t st);
+int launch_few(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
 
-// The device's multiprocessors, and the kernel's shared-memory limit raised
-// (once per kernel and device: `done` is the kernel's own).
+// A launch that may start before the kernel ahead of it in the stream has ended
+// (each kernel here waits for that itself before it touches memory).
+template <typename... Params, typename... Args>
+bool launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+// Raises the kernel's shared-memory limit, once per kernel and device (`done`
+// is the kernel's own).
 template <typename Kernel>
 bool allow_smem(Kernel kernel, int bytes, int (&done)[64]) {
     int dev = 0;

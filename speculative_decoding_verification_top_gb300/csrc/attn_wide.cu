@@ -335,7 +335,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(scales) + S::kScale);
     Barriers &bar = sh.bar;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;");
 
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
@@ -359,6 +358,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         fence_async_proxy();
     }
     if (warp == 9) tmem_alloc(smem_addr(&sh.tmem), 512);
+    // Up to here this may run beside the kernel before it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     long long from, to;
     find_share(p, sh.start, &from, &to);
     fence_before_sync();
@@ -681,8 +683,9 @@ int launch_shape(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtens
     static int done[64];
     auto kernel = attn_wide_kernel<D, E4M3, EXTRA>;
     if (!allow_smem(kernel, Layout<D, E4M3>::kBytes, done)) return SPEC_ERR_CUDA;
-    kernel<<<grid, kAttnThreads, Layout<D, E4M3>::kBytes, st>>>(ka, kmap, vmap);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_early(kernel, dim3(grid), dim3(kAttnThreads), Layout<D, E4M3>::kBytes, st, ka, kmap, vmap)
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
 }
 
 }  // namespace
