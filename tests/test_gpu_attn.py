@@ -151,6 +151,12 @@ SHAPES = [  # lens, N, Hq, Hkv, D, page
     ([400, 257], 5, 12, 12, 64, 128),
     ([390, 100], 40, 8, 1, 128, 16),   # 320 rows a key/value head
     ([200, 333], 130, 4, 2, 64, 32),   # more new tokens than a tile
+    ([600, 70, 129, 12], 12, 8, 2, 128, 64),   # 48 rows a key/value head
+    ([300, 31, 256], 16, 4, 1, 64, 16),        # 64 rows
+    ([500, 27, 260], 25, 12, 4, 128, 32),      # 75 rows
+    ([260, 131], 32, 8, 2, 64, 128),           # 128 rows
+    ([129, 400], 43, 12, 4, 128, 64),          # 129 rows: a unit of two row tiles
+    ([3, 1, 2] * 100, 1, 2, 1, 64, 16),        # many short sequences
 ]
 
 
@@ -185,6 +191,23 @@ def test_shared(Ls, lens, N, Hq, H, D, page, tree, e4m3):
     p = Problem(3, lens, N, Hq, H, D, page, e4m3, shared=Ls, tree=tree)
     p.check()
     p.check(cap=8.0, window=100, slopes=0.5 ** np.arange(Hq))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("N,Hq,H", [(10, 4, 1), (25, 4, 1), (60, 8, 2)])
+def test_windows_over_groups_of_rows(N, Hq, H, e4m3):
+    """Windows that cut tiles and leave some out, by cache position and by
+    tree position, for 40, 100 and 240 rows a head."""
+    for tree in (False, True):
+        p = Problem(20, [700, 200, 61], N, Hq, H, 64, 32, e4m3, tree=tree)
+        for window in (1, 64, 150):
+            p.check(window=window)
+    p = Problem(21, [300, 77], N, Hq, H, 128, 64, e4m3, shared=400)
+    p.check(window=350)
+
+
+def test_a_tree_of_many_nodes():
+    Problem(22, [1400, 900], 700, 2, 1, 64, 64, False, tree=True).check(only=[1])
 
 
 def test_shared_equals_the_same_cache_held_apart():
