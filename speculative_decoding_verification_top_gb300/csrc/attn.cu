@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             dual[i] = u.rows - unit[i] * 2 * kGroupRows > kGroupRows;
         }
         for (int k = unit[0]; k <= unit[kJoinRows - 1]; ++k) {
-            const int c = u.rows - k * 2 * kGroupRows > kGroupRows ? 2 : 1;
-            const long long ubase = line + k * 2ll * (T + u.start);
+            const int c = k + 1 == u.units ? u.last : u.cost;
+            const long long ubase = line + static_cast<long long>(k) * u.cost * (T + u.start);
             int lo, hi;
             shares_of(share, ubase, static_cast<long long>(T + u.start) * c, &lo, &hi);
 #pragma unroll 2
@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         }
     };
     if (p.sT > 0)
-        join(p.shared, p.share[1], static_cast<long long>(h) * p.shared.row_tiles * (p.sT + p.shared.start), p.sT, h * p.shared.units,
+        join(p.shared, p.share[1], static_cast<long long>(h) * p.shared.head * (p.sT + p.shared.start), p.sT, h * p.shared.units,
              b * p.own.rows + r0);
     if (s.t1 > s.t0)
-        join(p.own, p.share[0], p.base[b] + static_cast<long long>(h) * p.own.row_tiles * (s.t1 - s.t0 + p.own.start), s.t1 - s.t0,
+        join(p.own, p.share[0], p.base[b] + static_cast<long long>(h) * p.own.head * (s.t1 - s.t0 + p.own.start), s.t1 - s.t0,
              bh * p.own.units, r0);
     if constexpr (SPLIT) {
         __shared__ float2 ml[kJoinWarps];
@@ -178,30 +178,44 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 // ------------------------------------------------------------------ host
 
 // What beginning a unit costs, in tiles: staging its queries, a first tile that
-// waits for them, the partial result.
-constexpr int kStartFew = 5, kStartWide = 16;
+// waits for them, masked tiles, the partial result.  Few rows: 3 to 12 are
+// within 2 %.  Many rows (16 trees of 85 nodes under a prefix of 8190 / 16 trees
+// over caches of up to 7001): 5 takes 251 / 213 us, 8 224 / 212, 11 231 / 216.
+// A prefix has one masked tile at most: 3 takes 218 us for 64 chains of 6 under
+// 16001, 8 226.
+constexpr int kStartFew = 5, kStartWide = 8, kStartPrefix = 3;
+
+// A tile's cost in a unit of two row tiles and of one.  In bf16 one row tile is
+// held up by its loads (64 KB a tile) and by one chain of softmax and products
+// a group, and takes 0.9 of what two take: 4 to 3 gives 212 and 224 us on the
+// trees above, 2 to 1 217 and 240.  In e4m3 the softmax is what takes the time:
+// 2 to 1 gives 258 us on the trees over their own caches, 4 to 3 264.
+constexpr int kDualBf16 = 4, kSingleBf16 = 3, kDualE4M3 = 2, kSingleE4M3 = 1;
 
 // Fills the plan's sizes and carves its arrays; returns the bytes needed.
-size_t carve_plan(Plan *p, int D, char *work) {
+size_t carve_plan(Plan *p, int D, bool e4m3, char *work) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off = (off + bytes + 255) / 256 * 256;
         return work + at;
     };
-    auto kind = [&](Units *u, int rows, int heads) {
+    auto kind = [&](Units *u, int rows, int heads, bool own) {
         u->rows = rows;
-        u->row_tiles = ceil_div(rows, kGroupRows);
         u->units = ceil_div(rows, 2 * kGroupRows);
         u->rc = min(kGroupRows, (rows + 7) / 8 * 8);
         u->few = rows <= kFewRows;
-        u->start = u->few ? kStartFew : kStartWide;
+        u->cost = e4m3 ? kDualE4M3 : kDualBf16;
+        const bool dual = rows - (u->units - 1) * 2 * kGroupRows > kGroupRows;
+        u->last = u->few ? 1 : dual ? u->cost : e4m3 ? kSingleE4M3 : kSingleBf16;
+        u->head = (u->units - 1) * u->cost + u->last;
+        u->start = u->few ? kStartFew : own ? kStartWide : kStartPrefix;
         const size_t parts = (static_cast<size_t>(heads) * u->units + kMaxGrid) * 2 * u->rc;
         u->ml = reinterpret_cast<float2 *>(take(parts * sizeof(float2)));
         u->o = reinterpret_cast<float *>(take(parts * D * sizeof(float)));
     };
-    kind(&p->own, p->N * p->G, p->B * p->Hkv);
-    kind(&p->shared, p->B * p->N * p->G, p->Hkv);
+    kind(&p->own, p->N * p->G, p->B * p->Hkv, true);
+    kind(&p->shared, p->B * p->N * p->G, p->Hkv, false);
     p->base = reinterpret_cast<long long *>(take(p->B * sizeof(long long)));
     p->share = reinterpret_cast<long long *>(take(2 * sizeof(long long)));
     return off;
@@ -272,7 +286,7 @@ size_t attn_work_bytes(int B, int N, int Hq, int Hkv, int D) {
     p.N = N;
     p.G = Hq / Hkv;
     p.Hkv = Hkv;
-    return carve_plan(&p, D, nullptr);
+    return carve_plan(&p, D, false, nullptr);
 }
 
 int launch_attn(const AttnArgs &a, cudaStream_t st) {
@@ -290,7 +304,7 @@ int launch_attn(const AttnArgs &a, cudaStream_t st) {
     p.lens = a.lens;
     p.pos = a.pos;
     p.window = a.window;
-    carve_plan(&p, a.c.D, a.work);
+    carve_plan(&p, a.c.D, a.c.e4m3, a.work);
     CUtensorMap kmap, vmap;
     const int sms = multiprocessors();
     if (sms <= 0 || !make_map(&kmap, a.c.k, a.c) || !make_map(&vmap, a.c.v, a.c)) return SPEC_ERR_CUDA;

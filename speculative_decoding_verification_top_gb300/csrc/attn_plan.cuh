@@ -25,7 +25,8 @@ constexpr float kSlackBf16 = 8.0f, kSlackE4M3 = 3.75f, kLiftE4M3 = 5.0f;
 // The units of one kind (the prefix's, or the sequences' own).
 struct Units {
     int rows;             // query rows a (sequence, head); of all sequences for the prefix
-    int row_tiles, units; // 128-row tiles and units (256 rows) of those
+    int units;            // of 256 rows, the last of fewer
+    int cost, last, head; // a tile's cost in a unit of over 128 rows, in the last unit, in all units
     int rc, few;          // rows a partial result holds; handled by the few-row kernel
     int start;            // what beginning a unit costs, in tiles
     float *o;             // [slots, 2, rc, D] partial O
@@ -80,7 +81,7 @@ __device__ __forceinline__ Tiles tiles_of(const Plan &p, int b) {
 }
 
 // A unit's place on the cost line: `start` tiles' worth for beginning it, then
-// its tiles, each of c row tiles.  The share [from, to) of the line holds the
+// its tiles, each at cost c.  The share [from, to) of the line holds the
 // tiles [*t0, *t1) of the unit at ubase, possibly none.
 __device__ __forceinline__ void tiles_in(long long from, long long to, long long ubase, int T, int start, int c, int *t0,
                                          int *t1) {
@@ -95,9 +96,9 @@ struct Segment {
     int t0, t1, len, slot;
 };
 
-// Walks a CTA's share [x, end) of the cost line.  A tile of a unit costs its
-// row tiles (1 or 2), the products' work; so does the unit's start, `start`
-// times.  Every warp walks it by itself.
+// Walks a CTA's share [x, end) of the cost line.  A tile of a unit has
+// a cost by its row tiles (1 or 2); so does the unit's start, `start` times.
+// Every warp walks it by itself.
 struct Walk {
     long long ubase, x, end;
     int b, h, u;          // next unit; b = -1: the shared prefix
@@ -114,15 +115,15 @@ struct Walk {
         if (!sh) s = tiles_of(p, b);
         const Units &k = sh ? p.shared : p.own;
         const int T = (sh ? p.sT : s.t1 - s.t0) + k.start;
-        const long long in = x - base0, head = static_cast<long long>(T) * k.row_tiles;
+        const long long in = x - base0, head = static_cast<long long>(T) * k.head;
         if (in < INT_MAX && head < INT_MAX) {
             h = static_cast<int>(in) / static_cast<int>(head);
-            u = (static_cast<int>(in) - h * static_cast<int>(head)) / (2 * T);
+            u = (static_cast<int>(in) - h * static_cast<int>(head)) / (k.cost * T);
         } else {
             h = static_cast<int>(in / head);
-            u = static_cast<int>((in - h * head) / (2ll * T));
+            u = static_cast<int>((in - h * head) / (static_cast<long long>(k.cost) * T));
         }
-        ubase = base0 + h * head + u * 2ll * T;
+        ubase = base0 + h * head + static_cast<long long>(u) * k.cost * T;
     }
 
     __device__ bool next(Segment *g) {
@@ -140,7 +141,7 @@ struct Walk {
             g->row0 = u * 2 * kGroupRows;
             g->rows = min(k.rows - g->row0, 2 * kGroupRows);
             g->dual = g->rows > kGroupRows;
-            const int c = g->dual ? 2 : 1;
+            const int c = u + 1 == k.units ? k.last : k.cost;
             const int first = sh ? 0 : s.t0;
             tiles_in(x, end, ubase, T, k.start, c, &g->t0, &g->t1);
             g->len = sh ? p.Ls : s.len;
@@ -172,7 +173,7 @@ struct Walk {
     }
 };
 
-// Cost of a sequence's unit a row tile; nothing without tiles.
+// Tiles a sequence's unit counts for; nothing without tiles.
 __device__ __forceinline__ int cost_of(const Units &u, const Tiles &s) {
     return s.t1 > s.t0 ? s.t1 - s.t0 + u.start : 0;
 }
@@ -192,7 +193,7 @@ __device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = p.do_own ? ceil_div(p.B, kAttnThreads) : 0;
     const int bf = min(p.B, tid * each), bt = min(p.B, bf + each);
-    const long long per = static_cast<long long>(p.Hkv) * p.own.row_tiles;
+    const long long per = static_cast<long long>(p.Hkv) * p.own.head;
     long long mine = 0;
     for (int b = bf; b < bt; ++b) {
         const Tiles s = tiles_of(p, b);
@@ -209,7 +210,7 @@ __device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *
         sh.base0 = 0;
     }
     __syncthreads();
-    const long long prefix = p.do_shared ? static_cast<long long>(p.Hkv) * p.shared.row_tiles * (p.sT + p.shared.start) : 0;
+    const long long prefix = p.do_shared ? static_cast<long long>(p.Hkv) * p.shared.head * (p.sT + p.shared.start) : 0;
     long long before = prefix, total = prefix;
     for (int w = 0; w < kAttnThreads / 32; ++w) {
         if (w < warp) before += sh.scan[w];

@@ -65,59 +65,83 @@ struct Row {
 };
 
 // In a tile of positions that some rows do not see: the columns of each 32
-// that this row sees, and the position index of this lane's column in each.  A
-// row's set depends on its token alone, so the warp, a lane a column, finds
-// the sets of its tokens (consecutive ones) four at a time, all their mask
-// bytes in flight together.  (Out of line, with its arguments by value: inlined
-// it would cost the main loop registers.)
+// that this row sees, and the position index of this lane's column in each.
 struct Seen {
     uint32_t rows[4];
     int pos[4];
 };
 
+// The first n of 32 bits, n clamped to 0..32.
+__device__ __forceinline__ uint32_t first_bits(int n) {
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+// Loads that are not taken leave `otherwise`; no branch, so that many are in
+// flight together.
+__device__ __forceinline__ uint32_t byte_if(bool on, const uint8_t *at, uint32_t otherwise) {
+    uint32_t r;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t@p ld.global.u8 %0, [%1];\n\t}"
+        : "=&r"(r)
+        : "l"(at), "r"(static_cast<uint32_t>(on)), "r"(otherwise));
+    return r;
+}
+
+// A row's set depends on its token alone, so the warp, a lane a column, finds
+// the sets of its tokens (consecutive ones, from lo) four at a time, all their
+// mask bytes in flight together (3 thousand cycles for 8 tokens of 85 columns,
+where loads under branches took 13); without a mask it is arithmetic.  (Out of
+// line, with its arguments by value: inlined it would cost the main loop
+// registers.)
 __device__ __noinline__ Seen seen_columns(const uint8_t *mask, const int32_t *pos, int N, int window, int pos0, bool shared,
                                           int len, int first, bool has, int tok, int b_tok, int pos_i, int j0) {
     constexpr int kAtOnce = 4;
     const int lane = threadIdx.x & 31;
-    const uint32_t rows = __ballot_sync(0xffffffffu, has);
-    const int lo = __shfl_sync(0xffffffffu, tok, 0), hi = __shfl_sync(0xffffffffu, tok, 31 - __clz(rows));
     Seen s;
-    bool held[4], node[4];
-    int c[4];
+    bool node[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int j = j0 + i * 32 + lane;
-        c[i] = j - first;
-        held[i] = j < len;
-        node[i] = !shared && c[i] >= 0 && held[i];
+        node[i] = !shared && j >= first && j < len;
         s.pos[i] = pos0 + j;
-        if (node[i] && pos) s.pos[i] = pos[b_tok + c[i]];
-        s.rows[i] = 0;
+        if (node[i] && pos) s.pos[i] = pos[b_tok + j - first];
+        s.rows[i] = first_bits(len - (j0 + i * 32));
     }
-    const uint8_t *row = mask ? mask + static_cast<long long>(lo) * N : nullptr;
-    for (int t = lo; t <= hi; t += kAtOnce) {
-        uint32_t m[kAtOnce][4];
-        int who[kAtOnce];
+    if (!shared && mask) {
+        const uint32_t rows = __ballot_sync(0xffffffffu, has);
+        const int lo = __shfl_sync(0xffffffffu, tok, 0), hi = __shfl_sync(0xffffffffu, tok, 31 - __clz(rows));
+        const uint8_t *at = mask + static_cast<long long>(lo) * N + (j0 + lane - first);
+        for (int t = lo; t <= hi; t += kAtOnce) {
+            uint32_t m[kAtOnce][4];
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            who[k] = __ffs(__ballot_sync(0xffffffffu, has && tok == min(t + k, hi))) - 1;
+            for (int k = 0; k < kAtOnce; ++k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                m[k][i] = !node[i] ? 1u : mask ? row[c[i]] : static_cast<uint32_t>(c[i] <= min(t + k, hi) - b_tok);
-            if (mask && t + k < hi) row += N;
-        }
+                for (int i = 0; i < 4; ++i) m[k][i] = byte_if(node[i] && t + k <= hi, at + i * 32, 1u);
+                at += N;
+            }
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const long long at = __shfl_sync(0xffffffffu, pos_i, who[k]);
-            const bool me = has && tok == t + k;
+            for (int k = 0; k < kAtOnce; ++k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool y = held[i] && m[k][i] != 0 && (window == 0 || at - s.pos[i] < window);
-                const uint32_t word = __ballot_sync(0xffffffffu, y);
-                if (me) s.rows[i] = word;
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t word = __ballot_sync(0xffffffffu, m[k][i] != 0);
+                    if (tok == t + k) s.rows[i] &= word;
+                }
             }
         }
+    } else if (!shared) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.rows[i] &= first_bits(first + tok - b_tok + 1 - (j0 + i * 32));
     }
+    if (window > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t near = 0;
+#pragma unroll 8
+            for (int c = 0; c < 32; ++c)
+                if (static_cast<long long>(pos_i) - __shfl_sync(0xffffffffu, s.pos[i], c) < window) near |= 1u << c;
+            s.rows[i] &= near;
+        }
+    }
+    if (!has) s.rows[0] = s.rows[1] = s.rows[2] = s.rows[3] = 0;
     return s;
 }
 
@@ -228,7 +252,7 @@ __device__ __forceinline__ void grow(Row &x, float top, bool wrote, uint32_t ot)
 // cheap to take again; then the weights.
 template <int D, bool E4M3, bool EXTRA>
 __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g, Row &x, int j0, bool whole, bool wrote,
-                                             uint32_t st, uint32_t ot, const float *fa) {
+                                             uint32_t st, uint32_t ot, const float *fa, const Seen &seen) {
     const bool linear = whole && (!EXTRA || a.cap == 0.0f);
     // The bias: slope * (position index - pos_i), in a whole tile linear in the column.
     const float base = EXTRA ? x.slope * static_cast<float>((g.shared ? 0 : a.shared_len) + j0 - x.pos_i) : 0.0f;
@@ -255,18 +279,16 @@ __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g
         }
         if (!E4M3 && !EXTRA) top *= x.rs;  // rs >= 0
     } else {
-        Seen seen = {{~0u, ~0u, ~0u, ~0u}, {}};
-        if (!whole)
-            seen = seen_columns(a.mask, a.pos, a.N, a.window, g.shared ? 0 : a.shared_len, g.shared, g.len, x.first, x.has,
-                                x.tok, x.b * a.N, x.pos_i, j0);
-        else
-            for (int c = 0; c < 4; ++c) seen.pos[c] = (g.shared ? 0 : a.shared_len) + j0 + c * 32 + (threadIdx.x & 31);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             tmem_load32(st + c * 32, t[0]);
             tmem_load_wait();
-            const uint32_t s = c == 0 ? seen.rows[0] : c == 1 ? seen.rows[1] : c == 2 ? seen.rows[2] : seen.rows[3];
-            const int p = c == 0 ? seen.pos[0] : c == 1 ? seen.pos[1] : c == 2 ? seen.pos[2] : seen.pos[3];
+            uint32_t s = ~0u;
+            int p = (g.shared ? 0 : a.shared_len) + j0 + c * 32 + (threadIdx.x & 31);
+            if (!whole) {
+                s = c == 0 ? seen.rows[0] : c == 1 ? seen.rows[1] : c == 2 ? seen.rows[2] : seen.rows[3];
+                p = c == 0 ? seen.pos[0] : c == 1 ? seen.pos[1] : c == 2 ? seen.pos[2] : seen.pos[3];
+            }
             top = fmaxf(top, scores32<E4M3, EXTRA, false>(a, x, base, c * 32, s, p, fa, t[0]));
             tmem_store32(st + c * 32, reinterpret_cast<const uint32_t *>(t[0]));
         }
@@ -572,25 +594,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!g.dual && (idx & 1) != w) continue;
                 const int j0 = t * kTile;
                 const bool whole = sees_whole(a, g, j0, last_pos);
-                live = bar_wait(smem_addr(&bar.s_full[w]), sn++ & 1, dead);
+                const uint32_t s_bar = smem_addr(&bar.s_full[w]), s_phase = sn++ & 1;
+                // What the masks leave of the tile is told while its scores are on their way,
+                // and its values cleaned.  (Where the tiles alternate, after the scores: only they
+                // tell that the slot's fill before this one is over.)
+                Seen seen;
+                if (!whole) {
+                    if (active)
+                        seen = seen_columns(a.mask, a.pos, a.N, a.window, g.shared ? 0 : a.shared_len, g.shared, g.len, x.first,
+                                            x.has, x.tok, x.b * a.N, x.pos_i, j0);
+                    // the tile's values: slot index as the loads number them
+                    const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
+                    if (!g.dual) live = bar_wait(s_bar, s_phase, dead);
+                    live = live && bar_wait(smem_addr(&bar.full[vi % S::kSlots]), (vi / S::kSlots) & 1, dead);
+                    live = __all_sync(0xffffffffu, live);
+                    if (!live) break;
+                    if (clean_values<D, E4M3>(ring + vi % S::kSlots * S::kSlot, row, j0 + row < g.len)) sh.odd[segs & 15] = 1;
+                    fence_async_proxy();
+                }
+                live = bar_wait(s_bar, s_phase, dead);
                 const float *fa = nullptr;
                 if (E4M3) {
                     const uint32_t s = (n_scale + idx) % kScaleRing;
                     live = live && bar_wait(smem_addr(&bar.scale_full[s]), ((n_scale + idx) / kScaleRing) & 1, dead);
                     fa = scales + s * 3 * kTile;
                 }
-                // the tile's values: slot index as the loads number them
-                const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
-                if (!whole) live = live && bar_wait(smem_addr(&bar.full[vi % S::kSlots]), (vi / S::kSlots) & 1, dead);
                 live = __all_sync(0xffffffffu, live);
                 if (!live) break;
                 fence_after_sync();
-                if (active) softmax_tile<D, E4M3, EXTRA>(a, g, x, j0, whole, wrote, st, ot, fa);
+                if (active) softmax_tile<D, E4M3, EXTRA>(a, g, x, j0, whole, wrote, st, ot, fa, seen);
                 wrote = true;
-                if (!whole) {
-                    if (clean_values<D, E4M3>(ring + vi % S::kSlots * S::kSlot, row, j0 + row < g.len)) sh.odd[segs & 15] = 1;
-                    fence_async_proxy();
-                }
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
