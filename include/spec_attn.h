@@ -141,8 +141,9 @@ int spec_attn_workspace_size(int B, int N, int Hq, int Hkv, int D, size_t *bytes
  *   out          [B, N, Hq, D] bf16, device, contiguous, 16-byte aligned
  *   out_lse      [B, N, Hq] fp32, device, or NULL
  *   workspace    >= spec_attn_workspace_size(...) bytes, 16-byte aligned, its
- *                first 4 bytes (the error word) zeroed before first use; a
- *                verification workspace will do if it is large enough
+ *                first 4 bytes (the error word) zeroed before first use, the
+ *                rest in any state.  One workspace per call in flight, and
+ *                not a verification call's: its counters would be lost
  */
 int spec_attn_tree(const spec_kv_cache *cache, const int32_t *page_table, int table_width,
                    const int32_t *lens, const void *q, int64_t q_stride, const uint8_t *mask,

@@ -89,7 +89,7 @@ __device__ __forceinline__ uint32_t byte_if(bool on, const uint8_t *at, uint32_t
 // A row's set depends on its token alone, so the warp, a lane a column, finds
 // the sets of its tokens (consecutive ones, from lo) four at a time, all their
 // mask bytes in flight together (3 thousand cycles for 8 tokens of 85 columns,
-where loads under branches took 13); without a mask it is arithmetic.  (Out of
+// where loads under branches took 13); without a mask it is arithmetic.  (Out of
 // line, with its arguments by value: inlined it would cost the main loop
 // registers.)
 __device__ __noinline__ Seen seen_columns(const uint8_t *mask, const int32_t *pos, int N, int window, int pos0, bool shared,
