@@ -20,6 +20,18 @@
 // terms, 2^-8 relative at worst).  A key's exponent multiplies its column of
 // S; a value's is added to t, so that the weight carries it, and taken back
 // in l.
+//
+// Bound by the chain softmax -> O += P V -> next S of a group, of which two are
+// in flight (TMEM holds no third S beside two O): a tile of 256 rows takes 3400
+// cycles in bf16, where its products are 2048 and a group's softmax 1400; in
+// e4m3 5600, where the two terms' split makes the softmax 3600.  Loads (64 KB a
+// bf16 tile) hold it up for a sixth.  Measured: 16 trees of 85 nodes, 8 heads of
+// 128, 4 query heads each, over bf16 caches of 3500 to 7001 with a distance
+// bias (0.12 PFLOP): 190 us; 64 chains of 6 over one e4m3 prefix of 16001 (0.10
+// PFLOP): 135 us.
+// Tried and dropped: tiles in halves of 64 columns, so that a half's scores are
+// made under the other's softmax (273 us against 246 at the time); the product
+// loops written out per mode (250); registers moved between warps (more spills).
 
 #include "attn_plan.cuh"
 

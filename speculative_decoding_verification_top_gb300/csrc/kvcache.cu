@@ -122,8 +122,8 @@ __device__ __forceinline__ void write_row(uint8_t *data, int8_t *exps, long long
 
 // A lane writes 16 elements of a row's keys and of its values.  Rows number
 // (entry, head): below 2^31, so 32-bit arithmetic.  Eight sequences of 4099
-// tokens, 8 heads of 128, e4m3 (202 MB): 8 elements a lane took 47 us, with
-// four rows a thread 85.
+// tokens, 8 heads of 128, e4m3 (202 MB): 41 us, 4.9 TB/s; 8 elements a lane
+// took 47, with four rows a thread 85.
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a) {
     constexpr int kLanes = D / kW;  // lanes a row
