@@ -24,11 +24,13 @@
 // Bound by the chain softmax -> O += P V -> next S of a group, of which two are
 // in flight (TMEM holds no third S beside two O): a tile of 256 rows takes 3400
 // cycles in bf16, where its products are 2048 and a group's softmax 1400; in
-// e4m3 5600, where the two terms' split makes the softmax 3600.  Loads (64 KB a
-// bf16 tile) hold it up for a sixth.  Measured: 16 trees of 85 nodes, 8 heads of
+// e4m3 5600, where the two terms' split makes the softmax 3600.  The first half
+// of P goes to its product while the second is made (16 trees of 85 nodes: 206
+// us a call against 214; 64 chains under one prefix: 213 against 220).  Loads
+// (64 KB a bf16 tile) hold it up for a sixth.  Measured: 16 trees of 85 nodes, 8 heads of
 // 128, 4 query heads each, over bf16 caches of 3500 to 7001 with a distance
-// bias (0.12 PFLOP): 190 us; 64 chains of 6 over one e4m3 prefix of 16001 (0.10
-// PFLOP): 135 us.
+// bias (0.12 PFLOP): 180 us; 64 chains of 6 over one e4m3 prefix of 16001 (0.10
+// PFLOP): 130 us.
 // Tried and dropped: tiles in halves of 64 columns, so that a half's scores are
 // made under the other's softmax (273 us against 246 at the time); the product
 // loops written out per mode (250); registers moved between warps (more spills).
@@ -43,7 +45,7 @@ constexpr int kScaleRing = 4;
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots];
     unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
-    unsigned long long q_full, left, o_full[2], s_full[2], p_full[2], drained;
+    unsigned long long q_full, left, o_full[2], s_full[2], p_half[2], p_full[2], drained;
 };
 
 struct Shared {
@@ -264,7 +266,7 @@ __device__ __forceinline__ void grow(Row &x, float top, bool wrote, uint32_t ot)
 // cheap to take again; then the weights.
 template <int D, bool E4M3, bool EXTRA>
 __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g, Row &x, int j0, bool whole, bool wrote,
-                                             uint32_t st, uint32_t ot, const float *fa, const Seen &seen) {
+                                             uint32_t st, uint32_t ot, const float *fa, const Seen &seen, uint32_t half_bar) {
     const bool linear = whole && (!EXTRA || a.cap == 0.0f);
     // The bias: slope * (position index - pos_i), in a whole tile linear in the column.
     const float base = EXTRA ? x.slope * static_cast<float>((g.shared ? 0 : a.shared_len) + j0 - x.pos_i) : 0.0f;
@@ -328,6 +330,12 @@ __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g
                 y[k] = fma2(v, mul_2, add_2);
         }
         x.l += weights32<E4M3>(st + c * 16, fa + 2 * kTile + c * 32, y);
+        if (c == 1) {  // the product may begin with these
+            tmem_store_wait();
+            fence_before_sync();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) bar_arrive(half_bar);
+        }
     }
     tmem_store_wait();
 }
@@ -382,6 +390,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int w = 0; w < 2; ++w) {
             bar_init(smem_addr(&bar.o_full[w]), 1);
             bar_init(smem_addr(&bar.s_full[w]), 1);
+            bar_init(smem_addr(&bar.p_half[w]), 4);
             bar_init(smem_addr(&bar.p_full[w]), 4);
         }
         bar_init(smem_addr(&bar.q_full), 8);
@@ -449,6 +458,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint32_t v0 = matrix_lo(smem_addr(ring), S::kMat);
             const uint32_t full0 = smem_addr(&bar.full[0]), empty0 = smem_addr(&bar.empty[0]);
             const uint32_t s_full = smem_addr(&bar.s_full[0]), p_full = smem_addr(&bar.p_full[0]);
+            const uint32_t p_half = smem_addr(&bar.p_half[0]);
             auto advance = [&] {
                 if (++slot == S::kSlots) {
                     slot = 0;
@@ -472,19 +482,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
             };
-            // O += P V of group w with the value tile in slot s
-            auto values = [&](uint32_t w, uint32_t s, bool first) {
+            // O += P V of group w with the value tile in slot s, of the positions of half z
+            auto values = [&](uint32_t w, uint32_t s, uint32_t z, bool first) {
                 const uint32_t v = v0 + s * (S::kSlot >> 4), d = tmem + 2 * kTile + w * D, pt = tmem + w * kTile;
                 if (E4M3) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t j = i % 4;
-                        mma_ts<true>(d, pt + j * 16 + (i / 4) * 8, v + (j * 32 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t j = 2 * z + i % 2;
+                        mma_ts<true>(d, pt + j * 16 + (i / 2) * 8, v + (j * 32 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma_ts<false>(d, pt + i * 8, v + (i * 16 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
+                    for (int i = 0; i < 4; ++i)
+                        mma_ts<false>(d, pt + (4 * z + i) * 8, v + ((4 * z + i) * 16 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
                 }
             };
             while (live && walk.next(&g)) {
@@ -514,9 +524,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (!(live = bar_wait(full0 + 8 * vs, vp, dead))) break;
                     const uint32_t w0 = g.dual ? 0 : t & 1, w1 = g.dual ? 1 : t & 1;
                     for (uint32_t w = w0; w <= w1; ++w) {
-                        if (!(live = bar_wait(p_full + 8 * w, pn[w]++ & 1, dead))) break;
+                        const uint32_t pp = pn[w]++ & 1;
+                        if (!(live = bar_wait(p_half + 8 * w, pp, dead))) break;
                         fence_after_sync();
-                        values(w, vs, g.dual ? t == 0 : t < 2);
+                        values(w, vs, 0, g.dual ? t == 0 : t < 2);
+                        if (!(live = bar_wait(p_full + 8 * w, pp, dead))) break;
+                        fence_after_sync();
+                        values(w, vs, 1, false);
                         if (w == w1) mma_commit(empty0 + 8 * vs);
                         if (!more) continue;
                         if (!(live = bar_wait(full0 + 8 * ks, kp, dead))) break;
@@ -634,7 +648,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 live = __all_sync(0xffffffffu, live);
                 if (!live) break;
                 fence_after_sync();
-                if (active) softmax_tile<D, E4M3, EXTRA>(a, g, x, j0, whole, wrote, st, ot, fa, seen);
+                if (active)
+                    softmax_tile<D, E4M3, EXTRA>(a, g, x, j0, whole, wrote, st, ot, fa, seen, smem_addr(&bar.p_half[w]));
+                else if (lane == 0)
+                    bar_arrive(smem_addr(&bar.p_half[w]));
                 wrote = true;
                 fence_before_sync();
                 __syncwarp();
