@@ -24,8 +24,8 @@
 // the first tile of a segment is rare, so maxima are reduced only then.  l is
 // kept per thread and summed once a segment.
 // Measured: 64 chains of 6 over e4m3 caches of 4100 to 8200 positions, 8 heads
-// of 128 (819 MB): 152 us, 5.4 TB/s, what its loads alone take; 128 chains of 4
-// over bf16 caches of 2500 to 5003, 4 heads of 64, capped (497 MB): 115 us (its
+// of 128 (819 MB): 153 us, 5.3 TB/s, its loads alone 152; 128 chains of 4
+// over bf16 caches of 2500 to 5003, 4 heads of 64, capped (497 MB): 119 us (its
 // loads alone 102).  Beside the loads a call costs about 20 us of launch, line
 // and first tiles, which is what a single token over 2049 positions takes.
 

@@ -29,8 +29,8 @@
 // us a call against 214; 64 chains under one prefix: 213 against 220).  Loads
 // (64 KB a bf16 tile) hold it up for a sixth.  Measured: 16 trees of 85 nodes, 8 heads of
 // 128, 4 query heads each, over bf16 caches of 3500 to 7001 with a distance
-// bias (0.12 PFLOP): 180 us; 64 chains of 6 over one e4m3 prefix of 16001 (0.10
-// PFLOP): 130 us.
+// bias (0.12 PFLOP): 174 us; 64 chains of 6 over one e4m3 prefix of 16001 (0.10
+// PFLOP): 133 us.
 // Tried and dropped: tiles in halves of 64 columns, so that a half's scores are
 // made under the other's softmax (273 us against 246 at the time); the product
 // loops written out per mode (250); registers moved between warps (more spills).
