@@ -44,7 +44,9 @@ constexpr float kNone = -FLT_MAX; // reference of a row that has seen nothing: b
 struct Barriers {
     unsigned long long k_full[kMaxKeys], v_full[kMaxSlots], v_empty[kMaxSlots];
     unsigned long long q_full[2], q_empty[2];
-    unsigned long long s_full[4], p_full[4], drained;
+    unsigned long long s_full[4], p_full[4];
+    unsigned long long done[2];  // a group's last product of a segment
+    unsigned long long drained;
 };
 
 template <int NR>
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&bar.q_full[i]), 1);
             bar_init(smem_addr(&bar.q_empty[i]), 9);  // the products, and eight softmax warps
+            bar_init(smem_addr(&bar.done[i]), 1);
         }
         for (int i = 0; i < 4; ++i) {
             bar_init(smem_addr(&bar.s_full[i]), 1);
@@ -337,6 +340,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                           i > 0 || first == 0);
                     }
                     mma_commit(v_empty + 8 * vs);
+                    if (left_v <= 2) mma_commit(smem_addr(&bar.done[iv & 1]));
                     if (++vs == S::kV) {
                         vs = 0;
                         vp ^= 1;
@@ -386,6 +390,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             return any_of(kGroupBarrier + w, 128, x);
         };
         uint32_t seg = 0, tile = 0, cnt = 0;  // segments, tiles of the CTA, tiles of this group
+        uint32_t ended = 0;                   // segments this group had a tile of
         bool live = true;
         // Exponents of this thread's position in tile t of segment s.
         auto exponents = [&](const Segment &s, int t, int *ek, int *ev) {
@@ -441,7 +446,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int c = j - (g.len - a.N);
                     if (!g.shared && c >= 0 && j < g.len && a.pos) pos_j = a.pos[static_cast<long long>(g.b) * a.N + c];
                     seen = seen_rows<NR>(a, g, rows, j, pos_j);
-                    ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
                 }
                 ok = ok && bar_wait(smem_addr(&bar.s_full[buf]), phase, dead);
                 fence_after_sync();
@@ -586,7 +590,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     *reinterpret_cast<uint4 *>(pb + o) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     *reinterpret_cast<uint4 *>(pb + o2) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }
-                if (!whole && clean_values<D, E4M3>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[seg & 15] = 1;
+                if (!whole) {
+                    // A wait by parity tells its fill of the slot from the one before only once that
+                    // one is known to be over.  These scores came after the product of tile vi - 3;
+                    // with two slots the one before is tile vi - 2, whose product is waited for.
+                    if (S::kV < 3 && vi >= S::kV)
+                        ok = ok && bar_wait(smem_addr(&bar.v_empty[vi % S::kV]), ((vi - S::kV) / S::kV) & 1, dead);
+                    ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
+                    if (ok && clean_values<D, E4M3>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[seg & 15] = 1;
+                }
                 fence_async_proxy();
                 fence_before_sync();
                 __syncwarp();
@@ -602,8 +614,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const Segment next = sh.seg[half ^ 1];
             if (E4M3 && ok && next.rows) exponents(next, next.t0 + ((tile + (g.t1 - g.t0) ^ w) & 1), &ek, &ev);
             if (wrote) {
-                const uint32_t vi = tile + ((g.t1 - 1 - first_tile) & ~1) + (first_tile - g.t0);  // the group's last tile
-                ok = ok && bar_wait(smem_addr(&bar.v_empty[vi % S::kV]), (vi / S::kV) & 1, dead);
+                ok = ok && bar_wait(smem_addr(&bar.done[w]), ended++ & 1, dead);
                 fence_after_sync();
                 __syncwarp();
                 float sum[NR / 32];
