@@ -592,10 +592,10 @@ def _tokens(t, name, H, D, dtypes):
     B, N = t.shape[:2]
     s = t.stride()
     step = s[1] if N > 1 else s[0] if B > 1 else H * D
-    if s[3] == 1 and (H == 1 or s[2] == D) and (B < 2 or s[0] == N * step):
+    if s[3] == 1 and (H == 1 or s[2] == D) and (B < 2 or s[0] == N * step) and step >= H * D:
         return step
-    raise ValueError("%s: each token's heads must be contiguous and tokens evenly spaced, got "
-                     "strides %s" % (name, s))
+    raise ValueError("%s: each token's heads must be contiguous and tokens evenly spaced, without "
+                     "overlap (no expanded tokens), got strides %s" % (name, s))
 
 
 def kv_append(cache, page_table, starts, k, v, rows=None, stream=None):
