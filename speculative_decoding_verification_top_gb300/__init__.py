@@ -24,6 +24,7 @@ negative status.
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -360,6 +361,13 @@ def _stream(stream):
     return s.cuda_stream
 
 
+def _made_on(stream):
+    """Where a call's own tensors are made: on the stream that works on them, so
+    that zeroing comes before that work and memory freed at return goes to later
+    work of the same stream only."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
 def _need(t, name, dtype, shape):
     if t.dtype != dtype or t.shape != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
         raise ValueError("%s must be a contiguous CUDA %s tensor of shape %s, got %s %s"
@@ -626,8 +634,9 @@ def kv_read(cache, page_table, starts, count, dtype=None, stream=None):
     B = starts.shape[0]
     _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
     _need(starts, "starts", torch.int32, (B,))
-    k, v = (torch.empty((B, count, c.Hkv, c.D), dtype=dtype or torch.bfloat16,
-                        device=starts.device) for _ in "kv")
+    with _made_on(stream):
+        k, v = (torch.empty((B, count, c.Hkv, c.D), dtype=dtype or torch.bfloat16,
+                            device=starts.device) for _ in "kv")
     spec_kv_read(c, _ptr(page_table), page_table.shape[1], _ptr(starts), _ptr(k), _ptr(v), B, count,
                  _dtype_code(k), _stream(stream))
     return k, v
@@ -647,15 +656,16 @@ def _attn(call, q, cache, before, page_table, lens, mask, pos, slopes, scale, ca
         _need(pos, "pos", torch.int32, (B, N))
     if slopes is not None:
         _need(slopes, "slopes", torch.float32, (Hq,))
-    if out is None:
-        out = torch.empty((B, N, Hq, c.D), dtype=q.dtype, device=q.device)
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((B, N, Hq, c.D), dtype=q.dtype, device=q.device)
+        if lse is True:
+            lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = new_workspace(spec_attn_workspace_size(B, N, Hq, c.Hkv, c.D), q.device)
     _need(out, "out", q.dtype, (B, N, Hq, c.D))
-    if lse is True:
-        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, N, Hq))
-    if workspace is None:
-        workspace = new_workspace(spec_attn_workspace_size(B, N, Hq, c.Hkv, c.D), q.device)
     call(c, *before, _ptr(page_table), page_table.shape[1], _ptr(lens), _ptr(q), step, _ptr(mask),
          _ptr(pos), _ptr(slopes), B, N, Hq, c.D ** -0.5 if scale is None else scale, cap, window,
          SPEC_BF16, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
@@ -667,7 +677,9 @@ def attn_tree(q, cache, page_table, lens, mask=None, pos=None, slopes=None, scal
     """Tensor-level spec_attn_tree: new tokens q [B, N, Hq, D] bf16 over a
     KVCache; mask and pos as tree_mask returns them (None: a chain); scale
     defaults to 1/sqrt(D).  Returns out [B, N, Hq, D], or (out, lse) with
-    lse=True or a tensor."""
+    lse=True or a tensor.  With ``stream``, what the call allocates belongs to
+    that stream.  Data errors (last_error) are in the workspace: give one to
+    read them."""
     return _attn(spec_attn_tree, q, cache, (), page_table, lens, mask, pos, slopes, scale, cap,
                  window, out, lse, workspace, stream)
 

@@ -1,4 +1,7 @@
 """The tensor-level helpers' own checks on the CPU: what the C entries are given."""
+import contextlib
+import types
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -47,3 +50,39 @@ def test_overlapping_and_uneven_tokens_are_refused():
         tokens(torch.as_strided(zeros(9000), (2, 3, 4, 64), (1000, 256, 64, 1)), 4, 64)
     with pytest.raises(ValueError):
         tokens(zeros(2, 3, 64, 4).transpose(2, 3), 4, 64)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_calls_own_tensors_are_made_on_its_stream(monkeypatch, given):
+    """With `stream`, the workspace is zeroed, and it and the outputs are
+    allocated, on that stream: made on the current one, the workspace would be
+    handed out again while the other stream still works on it."""
+    stream, within, made = types.SimpleNamespace(cuda_stream=5), [], []
+
+    @contextlib.contextmanager
+    def entered(s):
+        within.append(s)
+        yield
+        within.pop()
+
+    def note(real):
+        def f(*args, **kw):
+            made.append(list(within))
+            return OnGpu(real(*args, **kw))
+        return f
+
+    monkeypatch.setattr(torch.cuda, "stream", entered)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch, "empty", note(torch.empty))
+    monkeypatch.setattr(sv, "new_workspace", note(lambda n, device: torch.zeros(n, dtype=torch.uint8)))
+    calls = []
+    monkeypatch.setattr(sv, "spec_attn_tree", lambda *args: calls.append(args))
+    monkeypatch.setattr(sv, "spec_attn_workspace_size", lambda *args: 64)
+    monkeypatch.setattr(sv, "spec_kv_read", lambda *args: calls.append(args))
+    cache = types.SimpleNamespace(descriptor=sv.CacheDescriptor(None, None, None, None, 1, 2, 16, 64, 0))
+    ints = OnGpu(torch.zeros((2, 1), dtype=torch.int32))
+    one = OnGpu(torch.zeros(2, dtype=torch.int32))
+    sv.attn_tree(OnGpu(zeros(2, 3, 4, 64)), cache, ints, one, lse=True, stream=stream if given else None)
+    sv.kv_read(cache, ints, one, 4, stream=stream if given else None)
+    assert made == [[stream] if given else []] * 5  # out, lse, workspace; k, v
+    assert [c[-1] for c in calls] == [5 if given else 0] * 2
