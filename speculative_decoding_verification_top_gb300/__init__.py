@@ -574,6 +574,13 @@ class KVCache(collections.namedtuple("KVCache", "k v k_exp v_exp")):
             page, D, SPEC_E4M3 if e4m3 else SPEC_BF16)
         return self
 
+    @classmethod
+    def _make(cls, tensors):  # _replace comes here too
+        return cls(*tensors)
+
+    def __reduce__(self):  # a copy's descriptor is of the copy's tensors
+        return type(self), tuple(self)
+
 
 def new_cache(num_pages, Hkv, page, D, device, e4m3=False):
     """An empty (zeroed) cache of num_pages pages."""

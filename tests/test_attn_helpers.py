@@ -1,5 +1,6 @@
 """The tensor-level helpers' own checks on the CPU: what the C entries are given."""
 import contextlib
+import copy
 import types
 
 import pytest
@@ -17,6 +18,8 @@ class OnGpu:
         self._t = t
 
     def __getattr__(self, name):
+        if name.startswith("_"):
+            raise AttributeError(name)
         return getattr(self._t, name)
 
 
@@ -86,3 +89,17 @@ def test_a_calls_own_tensors_are_made_on_its_stream(monkeypatch, given):
     sv.kv_read(cache, ints, one, 4, stream=stream if given else None)
     assert made == [[stream] if given else []] * 5  # out, lse, workspace; k, v
     assert [c[-1] for c in calls] == [5 if given else 0] * 2
+
+
+def test_copies_of_a_cache_have_descriptors_of_their_own():
+    def pool():
+        return OnGpu(zeros(3, 2, 16, 64))
+
+    a, k = sv.KVCache(pool(), pool()), pool()
+    for b in (a._replace(k=k), sv.KVCache._make((k, a.v, None, None)), copy.deepcopy(a), copy.copy(a)):
+        assert type(b) is sv.KVCache
+        assert (b.descriptor.k, b.descriptor.v) == (b.k.data_ptr(), b.v.data_ptr())
+        assert (b.descriptor.num_pages, b.descriptor.page) == (3, 16)
+    assert a._replace(k=k).k is k
+    with pytest.raises(ValueError):
+        a._replace(k=OnGpu(zeros(3, 2, 16, 128)))
