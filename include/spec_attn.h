@@ -31,7 +31,8 @@
  *   NaN or infinite element is stored as the NaN byte and takes no part in
  *   the maximum.  Powers of two keep the scaling and the reading back
  *   exact, so the one rounding is the byte's own (nearest, ties to even).
- *   A page id outside [0, num_pages) in a table is never followed.
+ *   An exponent outside [-120, 120], which no append writes, counts as the
+ *   nearer end.  A page id outside [0, num_pages) in a table is never followed.
  */
 #ifndef SPEC_ATTN_H
 #define SPEC_ATTN_H

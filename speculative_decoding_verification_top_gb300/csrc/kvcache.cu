@@ -185,7 +185,7 @@ __device__ __forceinline__ void unpack(const Raw &r, float (&x)[kE]) {
         }
         return;
     }
-    const float f = exp2i(r.e);
+    const float f = exp2i(max(-120, min(120, r.e)));  // the range that is written
     const uint32_t w[2] = {r.u.x, r.u.y};
 #pragma unroll
     for (int i = 0; i < kE; i += 2) {
