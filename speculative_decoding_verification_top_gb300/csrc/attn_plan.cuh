@@ -427,7 +427,8 @@ __device__ __forceinline__ void stage_queries(const AttnArgs &a, const Segment &
             const uint32_t o = swizzled<kRow>(row, part * 16);
             *reinterpret_cast<uint4 *>(tile + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(tile + block + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (part == 0) factor[row] = exp2i(e);
+            // The conversion makes an infinite element a finite one: its row is NaN.
+            if (part == 0) factor[row] = top >= 0x7f80u ? NAN : exp2i(e);
         }
     }
 }

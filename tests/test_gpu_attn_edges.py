@@ -8,8 +8,7 @@ pytestmark = [
 ]
 
 import speculative_decoding_verification_top_gb300 as sv  # noqa: E402
-
-DEV = "cuda:0"
+from test_gpu_attn import DEV, Problem  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -31,3 +30,22 @@ def test_read_keeps_exponents_within_the_written_range():
         k, v = sv.kv_read(c, zero, zero[0], 8, dtype=dtype)
         assert torch.equal(k[0, :, 0].double().cpu(), want[:, None].expand(8, 64))
         assert torch.equal(v[0, :, 0].double().cpu(), -want[:, None].expand(8, 64))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("N,Hq,H", [(3, 4, 2), (24, 4, 2), (40, 8, 2)])
+def test_a_query_that_is_not_finite(N, Hq, H, e4m3, bad):
+    """Scores of both infinities, or NaN: no number comes out, whatever the
+    cache's type; the other rows are as before."""
+    p = Problem(30, [200, 90], N, Hq, H, 128, 32, e4m3)
+    if e4m3:  # small keys: no score overflows by itself
+        p.cache.k_exp -= 40
+    else:
+        p.cache.k.mul_(2.0 ** -40)
+    good, _ = p.run()
+    p.q[1, 2, 1, 5] = bad
+    out, lse = p.run()
+    assert torch.isnan(out[1, 2, 1]).all() and torch.isnan(lse[1, 2, 1])
+    good[1, 2, 1] = out[1, 2, 1] = 0
+    assert torch.equal(out, good)
