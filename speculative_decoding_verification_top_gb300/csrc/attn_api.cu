@@ -161,7 +161,9 @@ SPEC_EXPORT int spec_attn_shared(const spec_kv_cache *cache, const int32_t *shar
     a.Hq = Hq;
     a.G = Hq / a.c.Hkv;
     a.scale = scale;
-    a.cap = cap;
+    // From 2^64 on a cap is none: fp32 scores that it would change are past any
+    // difference that the softmax tells, and scale / cap would leave fp32's range.
+    a.cap = cap < 0x1p64f ? cap : 0.0f;
     a.window = window;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = out_lse;

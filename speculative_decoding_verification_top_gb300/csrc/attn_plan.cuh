@@ -357,9 +357,13 @@ __device__ __forceinline__ void e4m3_terms(float x0, float x1, uint32_t *hi, uin
     *lo = l;
 }
 
-// cap tanh(y) log2 e with capl = cap log2 e; tanh(y) = 1 - 2 / (1 + e^2y).
+// cap tanh(y) log2 e with capl = cap log2 e; tanh(y) = 1 - 2 / (1 + e^2y), and
+// where that loses digits the series y - y^3 / 3 + 2 y^5 / 15 - 17 y^7 / 315 (its
+// next term is under 2^-21 of y there).
 __device__ __forceinline__ float capped(float y, float capl) {
-    return capl - __fdividef(2.0f * capl, 1.0f + ex2(y * (2.0f * kLog2e)));
+    const float y2 = y * y, far = capl - __fdividef(2.0f * capl, 1.0f + ex2(y * (2.0f * kLog2e)));
+    const float near = capl * y * fmaf(y2, fmaf(y2, fmaf(y2, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
+    return fabsf(y) < 0.25f ? near : far;
 }
 
 // Stages the query rows [row0, row0 + rows) of a unit as the rows of a matrix

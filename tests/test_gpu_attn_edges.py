@@ -49,3 +49,11 @@ def test_a_query_that_is_not_finite(N, Hq, H, e4m3, bad):
     assert torch.isnan(out[1, 2, 1]).all() and torch.isnan(lse[1, 2, 1])
     good[1, 2, 1] = out[1, 2, 1] = 0
     assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("cap", [1e3, 1e5, 1e9, 1e20, 3e38])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("N", [3, 40])
+def test_a_cap_far_above_the_scores(N, e4m3, cap):
+    """cap tanh(s / cap) is then nearly s."""
+    Problem(31, [300, 129], N, 8, 2, 64, 64, e4m3).check(cap=cap)
