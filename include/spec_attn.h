@@ -159,7 +159,8 @@ int spec_attn_tree(const spec_kv_cache *cache, const int32_t *page_table, int ta
  * sequence's own cache is position shared_len + j of the sequence.  The
  * prefix's keys and values are read once for the whole batch, not once per
  * sequence.  shared_len >= 0; a bad page id in shared_table fails every
- * sequence.
+ * sequence.  With a window, what of the prefix no row reaches is not read, in
+ * whole blocks of 128 positions, and its page ids are not looked at.
  */
 int spec_attn_shared(const spec_kv_cache *cache, const int32_t *shared_table, int shared_len,
                      const int32_t *page_table, int table_width, const int32_t *lens,

@@ -132,9 +132,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             }
         }
     };
-    if (p.sT > 0)
-        join(p.shared, p.share[1], static_cast<long long>(h) * p.shared.head * (p.sT + p.shared.start), p.sT, h * p.shared.units,
-             b * p.own.rows + r0);
+    const int prefix = p.sT > 0 ? p.sT - static_cast<int>(p.share[2]) : 0;
+    if (prefix > 0)
+        join(p.shared, p.share[1], static_cast<long long>(h) * p.shared.head * (prefix + p.shared.start), prefix,
+             h * p.shared.units, b * p.own.rows + r0);
     if (s.t1 > s.t0)
         join(p.own, p.share[0], p.base[b] + static_cast<long long>(h) * p.own.head * (s.t1 - s.t0 + p.own.start), s.t1 - s.t0,
              bh * p.own.units, r0);
@@ -217,7 +218,7 @@ size_t carve_plan(Plan *p, int D, bool e4m3, char *work) {
     kind(&p->own, p->N * p->G, p->B * p->Hkv, true);
     kind(&p->shared, p->B * p->N * p->G, p->Hkv, false);
     p->base = reinterpret_cast<long long *>(take(p->B * sizeof(long long)));
-    p->share = reinterpret_cast<long long *>(take(2 * sizeof(long long)));
+    p->share = reinterpret_cast<long long *>(take(3 * sizeof(long long)));
     return off;
 }
 

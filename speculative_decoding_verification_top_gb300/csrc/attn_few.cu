@@ -204,13 +204,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (!ka.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     long long from, to;
-    find_share(p, sh.start, &from, &to);
+    const int prefix_first = find_share(p, sh.start, &from, &to);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = sh.tmem;
     volatile int *dead = &sh.dead;
-    Walk walk(p, from, to, sh.start.b0, sh.start.base0);
+    Walk walk(p, from, to, sh.start.b0, sh.start.base0, prefix_first);
     Segment g;
     const float mul = a.cap > 0.0f ? fabsf(a.scale) / a.cap : fabsf(a.scale) * kLog2e;
 

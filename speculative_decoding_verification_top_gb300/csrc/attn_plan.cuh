@@ -42,7 +42,7 @@ struct Plan {
     const int32_t *lens, *pos;
     int window;
     long long *base;      // [B] first cost of each sequence's units
-    long long *share;     // [2] a CTA's share of the launch that did the own, the prefix's units
+    long long *share;     // [3] a CTA's share of the launch that did the own, the prefix's units; prefix_first
 };
 
 struct KernelArgs {
@@ -102,11 +102,12 @@ struct Segment {
 struct Walk {
     long long ubase, x, end;
     int b, h, u;          // next unit; b = -1: the shared prefix
+    int prefix_first;     // the prefix's first tile that a row may see
     Tiles s;
     const Plan &p;
 
-    __device__ Walk(const Plan &plan, long long from, long long to, int b0, long long base0)
-        : ubase(0), x(from), end(to), b(b0), h(0), u(0), s(), p(plan) {
+    __device__ Walk(const Plan &plan, long long from, long long to, int b0, long long base0, int first)
+        : ubase(0), x(from), end(to), b(b0), h(0), u(0), prefix_first(first), s(), p(plan) {
         if (x >= end) {
             ubase = end;
             return;
@@ -114,7 +115,7 @@ struct Walk {
         const bool sh = b < 0;
         if (!sh) s = tiles_of(p, b);
         const Units &k = sh ? p.shared : p.own;
-        const int T = (sh ? p.sT : s.t1 - s.t0) + k.start;
+        const int T = (sh ? p.sT - prefix_first : s.t1 - s.t0) + k.start;
         const long long in = x - base0, head = static_cast<long long>(T) * k.head;
         if (in < INT_MAX && head < INT_MAX) {
             h = static_cast<int>(in) / static_cast<int>(head);
@@ -129,8 +130,8 @@ struct Walk {
     __device__ bool next(Segment *g) {
         while (ubase < end && b < p.B) {
             const bool sh = b < 0;
-            const int T = sh ? p.sT : s.t1 - s.t0;
-            if (T == 0) {  // a sequence without tiles
+            const int T = sh ? p.sT - prefix_first : s.t1 - s.t0;
+            if (T == 0) {  // a sequence, or a prefix, without tiles
                 advance_sequence();
                 continue;
             }
@@ -142,7 +143,7 @@ struct Walk {
             g->rows = min(k.rows - g->row0, 2 * kGroupRows);
             g->dual = g->rows > kGroupRows;
             const int c = u + 1 == k.units ? k.last : k.cost;
-            const int first = sh ? 0 : s.t0;
+            const int first = sh ? prefix_first : s.t0;
             tiles_in(x, end, ubase, T, k.start, c, &g->t0, &g->t1);
             g->len = sh ? p.Ls : s.len;
             g->slot = ((sh ? 0 : b) * p.Hkv + h) * k.units + u + static_cast<int>(blockIdx.x);
@@ -181,15 +182,34 @@ __device__ __forceinline__ int cost_of(const Units &u, const Tiles &s) {
 // The start of a CTA's share, found by all its threads together.
 struct Start {
     long long scan[kAttnThreads / 32];
+    int least[kAttnThreads / 32];
     long long base0;
     int b0;
 };
 
+// The least position index among this thread's part of all rows, for the
+// prefix's window.  A sequence whose length is out of range has none.
+__device__ __forceinline__ int least_position(const Plan &p) {
+    int least = INT_MAX;
+    if (p.pos) {
+        const int n = p.B * p.N;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += kAttnThreads) least = min(least, p.pos[i]);
+    } else {
+        for (int b = threadIdx.x; b < p.B; b += kAttnThreads) {
+            const int len = p.lens[b];
+            if (len >= 0 && len <= (p.width << p.page_shift)) least = min(least, p.Ls + len - p.N);
+        }
+    }
+    return least;
+}
+
 // The cost line: the prefix's units, then each sequence's.  Thread i sums a
 // contiguous run of the sequences; a scan places them.  Leaves this CTA's share
 // in *from, *to and where it starts in sh; CTA 0 writes the line down for the
-// join.  Contains block barriers; `sh` may be read after the next one.
-__device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *from, long long *to) {
+// join.  Returns the prefix's first tile that some row's window reaches.
+// Contains block barriers; `sh` may be read after the next one.
+__device__ __forceinline__ int find_share(const Plan &p, Start &sh, long long *from, long long *to) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = p.do_own ? ceil_div(p.B, kAttnThreads) : 0;
     const int bf = min(p.B, tid * each), bt = min(p.B, bf + each);
@@ -205,12 +225,25 @@ __device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *
         if (lane >= o) incl += y;
     }
     if (lane == 31) sh.scan[warp] = incl;
+    const bool trim = p.do_shared && p.window > 0;
+    if (trim) {
+        const int least = __reduce_min_sync(0xffffffffu, least_position(p));
+        if (lane == 0) sh.least[warp] = least;
+    }
     if (tid == 0) {
         sh.b0 = -1;
         sh.base0 = 0;
     }
     __syncthreads();
-    const long long prefix = p.do_shared ? static_cast<long long>(p.Hkv) * p.shared.head * (p.sT + p.shared.start) : 0;
+    int first = 0;
+    if (trim) {
+        int least = sh.least[0];
+        for (int w = 1; w < kAttnThreads / 32; ++w) least = min(least, sh.least[w]);
+        first = static_cast<int>(max(0ll, min(static_cast<long long>(p.sT), (static_cast<long long>(least) - p.window + 1) / kTile)));
+    }
+    const long long prefix = p.do_shared && first < p.sT
+                                 ? static_cast<long long>(p.Hkv) * p.shared.head * (p.sT - first + p.shared.start)
+                                 : 0;
     long long before = prefix, total = prefix;
     for (int w = 0; w < kAttnThreads / 32; ++w) {
         if (w < warp) before += sh.scan[w];
@@ -239,8 +272,12 @@ __device__ __forceinline__ void find_share(const Plan &p, Start &sh, long long *
     }
     if (blockIdx.x == 0 && tid == 0) {
         if (p.do_own) p.share[0] = share;
-        if (p.do_shared) p.share[1] = share;
+        if (p.do_shared) {
+            p.share[1] = share;
+            p.share[2] = first;
+        }
     }
+    return first;
 }
 
 // Bytes of the shared-memory matrices: keys, values and queries lie as rows of
