@@ -70,7 +70,7 @@ struct Shared {
     uint32_t tmem;
     int dead;              // a wait ran out: everyone leaves
     int fail[16];          // per segment (mod 16): a page id out of range
-    int odd[16];           // per segment (mod 16): a cleaned tile held values that are not finite
+    int odd[2][16];        // per group and segment (mod 16): a tile it cleaned held values that are not finite
 };
 
 template <int D, bool E4M3, int NR>
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         PageIds ids;
         bool live = true;
         for (uint32_t seg = 0; live && walk.next(&g); ++seg) {
-            if (lane == 0) sh.fail[seg & 15] = sh.odd[seg & 15] = 0;
+            if (lane == 0) sh.fail[seg & 15] = sh.odd[0][seg & 15] = sh.odd[1][seg & 15] = 0;
             __syncwarp();
             ids.begin(a, g);
             for (int t = g.t0; live && t < g.t1; ++t) {
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (S::kV < 3 && vi >= S::kV)
                         ok = ok && bar_wait(smem_addr(&bar.v_empty[vi % S::kV]), ((vi - S::kV) / S::kV) & 1, dead);
                     ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
-                    if (ok && clean_values<D, E4M3>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[seg & 15] = 1;
+                    if (ok && clean_values<D, E4M3>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[w][seg & 15] = 1;
                 }
                 fence_async_proxy();
                 fence_before_sync();
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // (A group without a tile of the segment has not waited for its loads: it
             // leaves the flags to the other.)
             const bool failed = wrote && reinterpret_cast<volatile int *>(sh.fail)[seg & 15] != 0;
-            const bool odd = wrote && reinterpret_cast<volatile int *>(sh.odd)[seg & 15] != 0;
+            const bool odd = wrote && reinterpret_cast<volatile int *>(sh.odd[w])[seg & 15] != 0;
             if (row < n_rows) {
                 const float m = ref[row];
                 const float sum = !wrote ? 0.0f : (sh.red[w][0][row] + sh.red[w][1][row]) + (sh.red[w][2][row] + sh.red[w][3][row]);
