@@ -383,7 +383,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // this warp's TMEM lanes
         const uint32_t ot = tmem + lanes + (4 + w) * NR;
         constexpr float kSlack = E4M3 ? kSlackE4M3 : kSlackBf16, kLift = E4M3 ? kLiftE4M3 : 0.0f;
-        const float capl = a.cap * kLog2e;
         float *ref = sh.ref[w], *keep = sh.keep[w];
         auto vote = [&](bool x) {
             __syncwarp();
@@ -467,8 +466,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (c0 >= n_rows) break;
                     if (cap) {
 #pragma unroll
-                        for (int c = c0; c < c0 + 16; ++c)
-                            s[c] = capped(E4M3 ? s[c] * fk * rows.rs[c] : s[c] * mul, capl);
+                        for (int c = c0; c < c0 + 16; ++c) s[c] *= E4M3 ? fk * rows.rs[c] : mul;
+                        cap_scores<16>(s + c0, a.cap);
                     }
                     float top[2] = {kNegInf, kNegInf};
 #pragma unroll

@@ -165,7 +165,6 @@ __device__ __noinline__ Seen seen_columns(const uint8_t *mask, const int32_t *po
 template <bool E4M3, bool EXTRA, bool WHOLE>
 __device__ __forceinline__ float scores32(const AttnArgs &a, const Row &x, float base, int col, uint32_t seen, int pos_col,
                                           const float *fa, float (&v)[32]) {
-    const float capl = a.cap * kLog2e;
     float top[2] = {kNegInf, kNegInf};
     if constexpr (WHOLE) {
         const F2 rs = pair_of(x.rs, x.rs), slope = pair_of(x.slope, x.slope), base2 = pair_of(base, base);
@@ -187,14 +186,17 @@ __device__ __forceinline__ float scores32(const AttnArgs &a, const Row &x, float
         }
         return fmaxf(top[0], top[1]);
     }
-    const bool cap = EXTRA && a.cap > 0.0f, by_pos = EXTRA && a.pos != nullptr;
+    const bool by_pos = EXTRA && a.pos != nullptr;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        if (E4M3) v[c] *= fa[col + c];
+        v[c] *= x.rs;
+    }
+    if (EXTRA && a.cap > 0.0f) cap_scores<32>(v, a.cap);
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
         float y = v[c];
-        if (E4M3) y *= fa[col + c];
-        y *= x.rs;
         if (EXTRA) {
-            if (cap) y = capped(y, capl);
             if (by_pos)
                 y = fmaf(x.slope, static_cast<float>(__shfl_sync(0xffffffffu, pos_col, c) - x.pos_i), y);
             else
