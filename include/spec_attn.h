@@ -120,9 +120,10 @@ int spec_attn_workspace_size(int B, int N, int Hq, int Hkv, int D, size_t *bytes
  *   lse_i  = ln sum_seen e^s_ij
  * A token that sees nothing gets zeros and lse -inf; an unseen position adds
  * nothing whatever its key and value hold.  Scores, sums and the output's
- * accumulation are fp32; the softmax weights are rounded to bf16 (or to two
- * e4m3 terms, about the same relative precision) for the product with the
- * values.  Results do not depend on timing: calls with the same inputs give
+ * accumulation are fp32; the softmax weights are rounded to bf16 for the product
+ * with the values, whatever the cache's type (an e4m3 cache's values are exact in
+ * bf16; its products q . k take the query to 2^-18 of its largest element).
+ * Results do not depend on timing: calls with the same inputs give
  * the same bits.
  *
  * Arguments

@@ -189,9 +189,10 @@ constexpr int kStartFew = 5, kStartWide = 8, kStartPrefix = 3;
 // A tile's cost in a unit of two row tiles and of one.  In bf16 one row tile is
 // held up by its loads (64 KB a tile) and by one chain of softmax and products
 // a group, and takes 0.9 of what two take: 4 to 3 gives 212 and 224 us on the
-// trees above, 2 to 1 217 and 240.  In e4m3 the softmax is what takes the time:
-// 2 to 1 gives 258 us on the trees over their own caches, 4 to 3 264.
-constexpr int kDualBf16 = 4, kSingleBf16 = 3, kDualE4M3 = 2, kSingleE4M3 = 1;
+// trees above, 2 to 1 217 and 240.  In e4m3 3 to 2 gives 247 and 286 us on the
+// trees over their own caches and under a prefix and 202 for 64 chains under one,
+// 2 to 1 254, 302 and 203, 4 to 3 247, 287 and 206.
+constexpr int kDualBf16 = 4, kSingleBf16 = 3, kDualE4M3 = 3, kSingleE4M3 = 2;
 
 // Fills the plan's sizes and carves its arrays; returns the bytes needed.
 size_t carve_plan(Plan *p, int D, bool e4m3, char *work) {

@@ -11,8 +11,11 @@
 // what 128 padded query rows would, gives a softmax thread a position and NR
 // scores, and leaves room in TMEM for two S ahead per group.
 //   warps 0-3, 4-7   two softmax groups, a thread per position, on alternate
-//                    tiles, each with its own (m, l, O)
-//   warps 8, 10      load key and value tiles page by page (TMA) into a ring each
+//                    tiles, each with its own (m, l, O); over an e4m3 cache they
+//                    widen the tile's values to bf16 first, while its scores are
+//                    on their way
+//   warps 8, 10      load key and value tiles page by page (TMA) into a ring each,
+//                    warp 10 an e4m3 tile's exponents too
 //   warp 9           issues the products (tcgen05); scores run up to two tiles
 //                    ahead of the values.  (Scores and values issued by two warps
 //                    took 70 us where this takes 62, one sequence of 131077 e4m3
@@ -24,10 +27,14 @@
 // the first tile of a segment is rare, so maxima are reduced only then.  l is
 // kept per thread and summed once a segment.
 // Measured: 64 chains of 6 over e4m3 caches of 4100 to 8200 positions, 8 heads
-// of 128 (819 MB): 153 us, 5.3 TB/s, its loads alone 152; 128 chains of 4
-// over bf16 caches of 2500 to 5003, 4 heads of 64, capped (497 MB): 119 us (its
-// loads alone 102).  Beside the loads a call costs about 20 us of launch, line
-// and first tiles, which is what a single token over 2049 positions takes.
+// of 128 (819 MB): 183 us, 4.5 TB/s; its loads alone 152, without the widening 145:
+// bound by what the groups issue.  128 chains of 4 over bf16 caches of 2500 to
+// 5003, 4 heads of 64, capped (497 MB): 110 us (its loads alone 102).  Beside the
+// loads a call costs about 20 us of launch, line and first tiles, which is what a
+// single token over 2049 positions takes.
+// Dropped: four warps more that widen (the groups' registers made room for by
+// setmaxnreg), all of it or a part: 234 to 271 us a call, where this takes 201; half
+// a tile at a time by them: 457.
 
 #include "attn_plan.cuh"
 
@@ -45,7 +52,7 @@ struct Barriers {
     unsigned long long k_full[kMaxKeys], v_full[kMaxSlots], v_empty[kMaxSlots];
     unsigned long long q_full[2], q_empty[2];
     unsigned long long s_full[4], p_full[4];
-    unsigned long long done[2];  // a group's last product of a segment
+    unsigned long long done[2];  // a group's last product of a segment; over e4m3 every one
     unsigned long long drained;
 };
 
@@ -63,7 +70,7 @@ struct Shared {
     Start start;
     Rows<NR> rows[2];
     Segment seg[2];        // the segment of each query tile; rows = 0: no more
-    alignas(16) float ref[2][NR];  // per group: reference maximum less the lift; +inf for no row
+    alignas(16) float ref[2][NR];  // per group: reference maximum; +inf for no row
     alignas(16) float keep[2][NR]; // per group: factor of the last growth
     float red[2][4][NR];   // per group and warp
     float factor[2][NR];   // e4m3: the query rows' own factors
@@ -78,14 +85,21 @@ struct Layout : Shape<D, E4M3> {
     using S = Shape<D, E4M3>;
     static constexpr int kQBlock = NR * S::kRow;                     // a block of the query tile
     static constexpr int kQ = kQBlock * (E4M3 ? 2 : S::kHalves);
-    static constexpr int kPRow = E4M3 ? NR : 2 * NR;                 // bytes of a row of weights
-    static constexpr int kPMat = kTile * kPRow;
-    static constexpr int kP = kPMat * (E4M3 ? 2 : 1);                // one buffer of weights
+    static constexpr int kPRow = 2 * NR;                             // bytes of a row of weights
+    static constexpr int kP = kTile * kPRow;                         // one buffer of weights
+    static constexpr int kPBufs = E4M3 ? 2 : 4;
+    static constexpr int kExps = E4M3 ? 2 * kTile : 0;               // a tile's exponents
+    static constexpr int kWide = E4M3 ? Shape<D, false>::kSlot : 0;  // a value tile widened to bf16
     static constexpr int kFixed = static_cast<int>((sizeof(Shared<NR>) + 127) / 128 * 128);
-    static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ - 4 * kP) / S::kSlot;
-    static constexpr int kSlots = kRoom < 2 * kMaxKeys + 4 ? kRoom : 2 * kMaxKeys + 4;
-    static constexpr int kK = kSlots / 2 < kMaxKeys ? kSlots / 2 : kMaxKeys, kV = kSlots - kK;  // of keys, of values
-    static constexpr int kBytes = kFixed + 2 * kQ + 4 * kP + kSlots * S::kSlot;
+    static constexpr int kMost = 2 * kMaxKeys + 4;
+    static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ - kPBufs * kP - 2 * kWide - kMost * kExps) / S::kSlot;
+    static constexpr int kSlots = kRoom < kMost ? kRoom : kMost;
+    static constexpr int kHalf = kSlots / 2 < kMaxKeys ? kSlots / 2 : kMaxKeys;
+    // Of values; over e4m3 an even number, so that a group's tiles have slots of their own.
+    static constexpr int kV = E4M3 ? (kSlots - kHalf) / 2 * 2 : kSlots - kHalf;
+    static constexpr int kK = kSlots - kV < kMaxKeys ? kSlots - kV : kMaxKeys;  // of keys
+    static constexpr int kBytes = kFixed + 2 * kQ + kPBufs * kP + 2 * kWide + (kK + kV) * S::kSlot + kV * kExps;
+    static_assert(kK >= 1 && kV >= 2, "two groups' value tiles");
     static constexpr uint32_t kColumns = NR == 32 ? 256 : 512;       // TMEM: 4 S and 2 O of NR columns
 };
 
@@ -173,16 +187,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const AttnArgs &a = ka.a;
     const Plan &p = ka.p;
-    uint8_t *k_ring = smem, *v_ring = k_ring + S::kK * S::kSlot, *pt = v_ring + S::kV * S::kSlot, *qt = pt + 4 * S::kP;
-    Shared<NR> &sh = *reinterpret_cast<Shared<NR> *>(qt + 2 * S::kQ);
+    uint8_t *k_ring = smem, *v_ring = k_ring + S::kK * S::kSlot, *wide = v_ring + S::kV * S::kSlot;
+    uint8_t *pt = wide + 2 * S::kWide, *qt = pt + S::kPBufs * S::kP;
+    int8_t *exps = reinterpret_cast<int8_t *>(qt + 2 * S::kQ);  // [kV][2][kTile]
+    Shared<NR> &sh = *reinterpret_cast<Shared<NR> *>(exps + S::kV * S::kExps);
     Barriers &bar = sh.bar;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
         for (int i = 0; i < S::kK; ++i) bar_init(smem_addr(&bar.k_full[i]), 1);
         for (int i = 0; i < S::kV; ++i) {
-            bar_init(smem_addr(&bar.v_full[i]), 1);
-            bar_init(smem_addr(&bar.v_empty[i]), 1);
+            bar_init(smem_addr(&bar.v_full[i]), E4M3 ? 33 : 1);  // the tile, and its exponents by 32 lanes
+            bar_init(smem_addr(&bar.v_empty[i]), E4M3 ? 4 : 1);  // the group's warps, or the product
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&bar.q_full[i]), 1);
@@ -257,19 +273,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ids.begin(a, g);
             for (int t = g.t0; live && t < g.t1; ++t)
                 live = load.tile(a, g, ids, t, &vmap, smem_addr(v_ring), bar.v_full, smem_addr(&bar.v_empty[load.slot]), dead,
-                                 nullptr);
+                                 nullptr, E4M3 ? smem_addr(exps) : 0);
         }
         if (!live) load.drain(bar.v_full);
     } else if (warp == 9) {
         // ---- products
         if (elect_one()) {
-            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kPv = mma_desc(E4M3, NR, true, true);
-            constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>;
+            using T = Shape<D, false>;  // the values as the product takes them
+            constexpr uint32_t kQk = mma_desc(E4M3, NR, false, false), kPv = mma_desc(false, NR, true, true);
+            constexpr uint32_t kHi = kMatrixHi<S::kRow>, kPHi = kMatrixHi<S::kPRow>, kVHi = kMatrixHi<T::kRow>;
             // Values narrower than 128 columns: the second block is the first again,
             // and its rows of O are not read.
-            constexpr uint32_t kLead = D == 128 && !E4M3 ? S::kMat : 0;
+            constexpr uint32_t kLead = D == 128 ? T::kMat : 0;
             const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(k_ring), 0);
-            const uint32_t v0 = matrix_lo(smem_addr(v_ring), kLead), p0 = matrix_lo(smem_addr(pt), 0);
+            const uint32_t v0 = matrix_lo(smem_addr(E4M3 ? wide : v_ring), kLead), p0 = matrix_lo(smem_addr(pt), 0);
             const uint32_t k_full = smem_addr(&bar.k_full[0]), v_full = smem_addr(&bar.v_full[0]);
             const uint32_t v_empty = smem_addr(&bar.v_empty[0]), q_full = smem_addr(&bar.q_full[0]);
             const uint32_t s_full = smem_addr(&bar.s_full[0]), p_full = smem_addr(&bar.p_full[0]);
@@ -322,25 +339,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                         continue;
                     }
-                    live = bar_wait(v_full + 8 * vs, vp, dead) && bar_wait(p_full + 8 * (iv & 3), (iv >> 2) & 1, dead);
+                    live = (E4M3 || bar_wait(v_full + 8 * vs, vp, dead)) && bar_wait(p_full + 8 * (iv & 3), (iv >> 2) & 1, dead);
                     fence_after_sync();
-                    const uint32_t v = v0 + vs * (S::kSlot >> 4), pb = p0 + (iv & 3) * (S::kP >> 4);
-                    const uint32_t d = tmem + (4 + (iv & 1)) * NR;
-                    if (E4M3) {
+                    const uint32_t v = v0 + (E4M3 ? (iv & 1) * (S::kWide >> 4) : vs * (S::kSlot >> 4));
+                    const uint32_t pb = p0 + (iv & (S::kPBufs - 1)) * (S::kP >> 4), d = tmem + (4 + (iv & 1)) * NR;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t j = i % 4;
-                            mma_ss<true>(d, v + (j * 32 * S::kRow >> 4), kHi,
-                                         pb + (((i / 4) * S::kPMat + j * 32 * S::kPRow) >> 4), kPHi, kPv, i > 0 || first == 0);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            mma_ss<false>(d, v + (i * 16 * S::kRow >> 4), kHi, pb + (i * 16 * S::kPRow >> 4), kPHi, kPv,
-                                          i > 0 || first == 0);
-                    }
-                    mma_commit(v_empty + 8 * vs);
-                    if (left_v <= 2) mma_commit(smem_addr(&bar.done[iv & 1]));
+                    for (int i = 0; i < 8; ++i)
+                        mma_ss<false>(d, v + (i * 16 * T::kRow >> 4), kVHi, pb + (i * 16 * S::kPRow >> 4), kPHi, kPv,
+                                      i > 0 || first == 0);
+                    if (!E4M3) mma_commit(v_empty + 8 * vs);
+                    if (E4M3 || left_v <= 2) mma_commit(smem_addr(&bar.done[iv & 1]));
                     if (++vs == S::kV) {
                         vs = 0;
                         vp ^= 1;
@@ -382,7 +390,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int w = warp >> 2, quad = warp & 3, row = tid & 127;  // row: the thread's position in a tile
         const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // this warp's TMEM lanes
         const uint32_t ot = tmem + lanes + (4 + w) * NR;
-        constexpr float kSlack = E4M3 ? kSlackE4M3 : kSlackBf16, kLift = E4M3 ? kLiftE4M3 : 0.0f;
         float *ref = sh.ref[w], *keep = sh.keep[w];
         auto vote = [&](bool x) {
             __syncwarp();
@@ -391,15 +398,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         uint32_t seg = 0, tile = 0, cnt = 0;  // segments, tiles of the CTA, tiles of this group
         uint32_t ended = 0;                   // segments this group had a tile of
         bool live = true;
-        // Exponents of this thread's position in tile t of segment s.
-        auto exponents = [&](const Segment &s, int t, int *ek, int *ev) {
-            const int j = t * kTile + row;
-            int slot = 0;
-            const int page = t < s.t1 && j < s.len ? page_of(a.c, pages_of(a, s), INT_MAX, j, &slot) : -1;
-            const long long at = cache_row(a.c, max(page, 0), s.h, slot);
-            *ek = page < 0 ? 0 : a.c.k_exp[at];
-            *ev = page < 0 ? 0 : a.c.v_exp[at];
-        };
         // The first segment's query tile: all eight warps, while the loads start.
         if (!walk.next(&g)) g.rows = 0;
         if (g.rows) stage(0, tid, 256);
@@ -412,8 +410,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         any_of(kFirstBarrier, 256, false);
         if (tid == 0) bar_arrive(smem_addr(&bar.q_full[0]));
         bool ok = true;
-        int ek = 0, ev = 0;
-        if (E4M3 && g.rows) exponents(g, g.t0 + w, &ek, &ev);
         while (g.rows) {
             const uint32_t half = seg & 1;
             const Units &u = g.shared ? p.shared : p.own;
@@ -434,8 +430,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int t = first_tile; t < g.t1; t += 2, ++cnt) {
                 const int j0 = t * kTile, j = j0 + row;
                 const uint32_t buf = w + 2 * (cnt & 1), phase = (cnt >> 1) & 1;
-                int ek_next = 0, ev_next = 0;
-                if (E4M3) exponents(g, t + 2, &ek_next, &ev_next);
+                float fk = 1.0f;  // e4m3: 2^(the key's exponent)
                 const bool whole = sees_whole(a, g, j0, last_pos);
                 // Position index of this thread's position, and the rows that see it.
                 int pos_j = (g.shared ? 0 : a.shared_len) + j;
@@ -446,6 +441,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (!g.shared && c >= 0 && j < g.len && a.pos) pos_j = a.pos[static_cast<long long>(g.b) * a.N + c];
                     seen = seen_rows<NR>(a, g, rows, j, pos_j);
                 }
+                if constexpr (E4M3) {
+                    // The values widened, while the scores are on their way.  Their buffer, and the
+                    // weights', is free after the group's last product; the slot's earlier fill was
+                    // this group's.
+                    if (cnt > 0) ok = ok && bar_wait(smem_addr(&bar.done[w]), (cnt - 1) & 1, dead);
+                    ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
+                    const int8_t *e = exps + vi % S::kV * S::kExps + row;
+                    fk = power_of(e[0]);
+                    if (ok && widen_values<D, 4>(v_ring + vi % S::kV * S::kSlot, wide + w * S::kWide, row, power_of(e[kTile]),
+                                              j < g.len, !whole))
+                        sh.odd[w][seg & 15] = 1;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(smem_addr(&bar.v_empty[vi % S::kV]));
+                }
                 ok = ok && bar_wait(smem_addr(&bar.s_full[buf]), phase, dead);
                 fence_after_sync();
                 __syncwarp();
@@ -453,12 +462,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                 for (int c = 0; c < NR; c += 32) tmem_load32(tmem + lanes + buf * NR + c, s + c);
                 tmem_load_wait();
-                const float fk = E4M3 ? exp2i(max(-120, min(120, ek))) : 1.0f;
-                const float fb = E4M3 ? static_cast<float>(max(-120, min(120, ev))) : 0.0f;
-                const float fl = E4M3 ? exp2i(-max(-120, min(120, ev))) : 1.0f;
                 const float at = static_cast<float>(pos_j - origin);
                 const bool cap = EXTRA && a.cap > 0.0f;
-                const F2 fk2 = pair_of(fk, fk), fb2 = pair_of(fb, fb), rs2 = pair_of(mul, mul), at2 = pair_of(at, at);
+                const F2 fk2 = pair_of(fk, fk), rs2 = pair_of(mul, mul), at2 = pair_of(at, at);
                 const F2 minus = pair_of(-1.0f, -1.0f);
                 float over = kNegInf;
 #pragma unroll
@@ -491,10 +497,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             y[0] = fma2(F2{s4.x}, fma2(F2{a4.x}, minus, at2), y[0]);
                             y[1] = fma2(F2{s4.y}, fma2(F2{a4.y}, minus, at2), y[1]);
                         }
-                        if (E4M3) {
-                            y[0] = add2(y[0], fb2);
-                            y[1] = add2(y[1], fb2);
-                        }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             float2 t2 = parts_of(y[k]);
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     over = max3(over, top[0], top[1]);
                 }
-                const bool grown = vote(!ok || over > kSlack + kLift);
+                const bool grown = vote(!ok || over > kSlack);
                 if (grown) {
                     if (vote(!ok)) {
                         live = false;
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (row < NR) {
                         const float m0 = ref[row];
                         const float m1 = fmaxf(fmaxf(sh.red[w][0][row], sh.red[w][1][row]),
-                                               fmaxf(sh.red[w][2][row], sh.red[w][3][row])) - kLift;
+                                               fmaxf(sh.red[w][2][row], sh.red[w][3][row]));
                         const bool up = m1 > m0 && (m0 == kNone || m1 - m0 > kSlack);
                         keep[row] = !up ? 1.0f : m0 == kNone ? 0.0f : ex2(m0 - m1);
                         if (up) ref[row] = m1;
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     vote(false);
                     const bool wrote = t >= g.t0 + 2;
                     if (wrote) {  // the products so far have to be in
-                        ok = bar_wait(smem_addr(&bar.v_empty[(vi - 2) % S::kV]), ((vi - 2) / S::kV) & 1, dead);
+                        if (!E4M3) ok = bar_wait(smem_addr(&bar.v_empty[(vi - 2) % S::kV]), ((vi - 2) / S::kV) & 1, dead);
                         ok = __all_sync(0xffffffffu, ok);
                         fence_after_sync();
                     }
@@ -557,12 +559,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
                 // Weights, and their place as the product's operand: a row per position.
-                // (Their buffer is free: these scores came after the product that read it.)
-                uint8_t *pb = pt + buf * S::kP;
+                // (Over bf16 their buffer is free: these scores came after the product that read it.)
+                uint8_t *pb = pt + (E4M3 ? w : buf) * S::kP;
 #pragma unroll
                 for (int c0 = 0; c0 < NR; c0 += 16) {
                     if (c0 >= n_rows) break;
-                    uint32_t pk[8];  // bf16 pairs, or four words of first and four of second terms
+                    uint32_t pk[8];  // bf16 pairs
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int c = c0 + 4 * k;
@@ -570,50 +572,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         const float2 u = parts_of(fma2(F2{m4.x}, minus, pair_of(s[c], s[c + 1])));
                         const float2 v = parts_of(fma2(F2{m4.y}, minus, pair_of(s[c + 2], s[c + 3])));
                         const float x0 = ex2(u.x), x1 = ex2(u.y), x2 = ex2(v.x), x3 = ex2(v.y);
-                        if (E4M3) {
-                            l[c] = fmaf(x0, fl, l[c]), l[c + 1] = fmaf(x1, fl, l[c + 1]);
-                            l[c + 2] = fmaf(x2, fl, l[c + 2]), l[c + 3] = fmaf(x3, fl, l[c + 3]);
-                            uint32_t h0, l0, h1, l1;
-                            e4m3_terms(x0, x1, &h0, &l0);
-                            e4m3_terms(x2, x3, &h1, &l1);
-                            pk[k] = h0 | h1 << 16;
-                            pk[4 + k] = l0 | l1 << 16;
-                        } else {
-                            l[c] += x0, l[c + 1] += x1, l[c + 2] += x2, l[c + 3] += x3;
-                            pk[2 * k] = bf16_pair(x0, x1);
-                            pk[2 * k + 1] = bf16_pair(x2, x3);
-                        }
+                        l[c] += x0, l[c + 1] += x1, l[c + 2] += x2, l[c + 3] += x3;
+                        pk[2 * k] = bf16_pair(x0, x1);
+                        pk[2 * k + 1] = bf16_pair(x2, x3);
                     }
-                    const uint32_t o = swizzled<S::kPRow>(row, E4M3 ? c0 : 2 * c0);
-                    const uint32_t o2 = E4M3 ? o + S::kPMat : swizzled<S::kPRow>(row, 2 * c0 + 16);
-                    *reinterpret_cast<uint4 *>(pb + o) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    *reinterpret_cast<uint4 *>(pb + o2) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    *reinterpret_cast<uint4 *>(pb + swizzled<S::kPRow>(row, 2 * c0)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    *reinterpret_cast<uint4 *>(pb + swizzled<S::kPRow>(row, 2 * c0 + 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }
-                if (!whole) {
-                    // A wait by parity tells its fill of the slot from the one before only once that
-                    // one is known to be over.  These scores came after the product of tile vi - 3;
-                    // with two slots the one before is tile vi - 2, whose product is waited for.
-                    if (S::kV < 3 && vi >= S::kV)
-                        ok = ok && bar_wait(smem_addr(&bar.v_empty[vi % S::kV]), ((vi - S::kV) / S::kV) & 1, dead);
-                    ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
-                    if (ok && clean_values<D, E4M3>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[w][seg & 15] = 1;
+                if constexpr (!E4M3) {
+                    if (!whole) {
+                        // A wait by parity tells its fill of the slot from the one before only once
+                        // that one is known to be over.  These scores came after the product of tile
+                        // vi - 3; with two slots the one before is tile vi - 2, whose product is waited for.
+                        if (S::kV < 3 && vi >= S::kV)
+                            ok = ok && bar_wait(smem_addr(&bar.v_empty[vi % S::kV]), ((vi - S::kV) / S::kV) & 1, dead);
+                        ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
+                        if (ok && clean_values<D>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[w][seg & 15] = 1;
+                    }
                 }
                 fence_async_proxy();
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) bar_arrive(smem_addr(&bar.p_full[buf]));
-                ek = ek_next;
-                ev = ev_next;
             }
             if (!live) break;
             // ---- the group's partial result of the segment
             const bool wrote = first_tile < g.t1;
-            // What comes next, and its first exponents, while the last product runs.
+            // What comes next, while the last product runs.
             ok = ok && bar_wait(smem_addr(&bar.q_full[half ^ 1]), ((seg + 1) >> 1) & 1, dead);
             const Segment next = sh.seg[half ^ 1];
-            if (E4M3 && ok && next.rows) exponents(next, next.t0 + ((tile + (g.t1 - g.t0) ^ w) & 1), &ek, &ev);
             if (wrote) {
-                ok = ok && bar_wait(smem_addr(&bar.done[w]), ended++ & 1, dead);
+                ok = ok && bar_wait(smem_addr(&bar.done[w]), (E4M3 ? cnt - 1 : ended++) & 1, dead);
                 fence_after_sync();
                 __syncwarp();
                 float sum[NR / 32];

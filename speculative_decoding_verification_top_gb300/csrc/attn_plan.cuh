@@ -18,9 +18,8 @@ constexpr int kSmemMax = 232448;  // bytes a CTA may have
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Growth of t over the reference maximum that is let stand: a weight stays
-// under 2^8 (bf16), or 2^5 * 2^3.75 < 448 (e4m3, whose weights are scaled by
-// 2^5 so that small ones keep their second term).
-constexpr float kSlackBf16 = 8.0f, kSlackE4M3 = 3.75f, kLiftE4M3 = 5.0f;
+// under 2^8.
+constexpr float kSlack = 8.0f;
 
 // The units of one kind (the prefix's, or the sequences' own).
 struct Units {
@@ -380,20 +379,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// Two weights as two e4m3 terms each: x = hi + lo up to 2^-8 of x.  The
-// remainder is taken in fp16, which holds x to 2^-11 (x is at most 2^9).
-__device__ __forceinline__ void e4m3_terms(float x0, float x1, uint32_t *hi, uint32_t *lo) {
-    const __half2 x = __floats2half2_rn(x0, x1);
-    uint16_t h, l;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
-    uint32_t y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(h));
-    const __half2 d = __hsub2(x, *reinterpret_cast<const __half2 *>(&y));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t *>(&d)));
-    *hi = h;
-    *lo = l;
-}
-
 // cap tanh(y) log2 e of n scores in place, capl = cap log2 e.  tanh(y) = 1 - 2 /
 // (1 + e^2y) is good to a rounding of the cap, 2^-22 of capl: under 2^-11 for caps
 // up to 1000, where weights are rounded to 2^-9.  Above, arguments under 1/4 go by
@@ -488,18 +473,17 @@ __device__ __forceinline__ void stage_queries(const AttnArgs &a, const Segment &
     }
 }
 
-// Row `row` of a value tile whose positions some rows do not see: zeros where
+// Row `row` of a bf16 value tile whose positions some rows do not see: zeros where
 // the position is not held (the slot has whatever was there), and zeros for
 // elements that are not finite, so that an unseen one does not reach a row
 // through 0 * inf.  Returns whether a held element was not finite.
-template <int D, bool E4M3>
+template <int D>
 __device__ __forceinline__ bool clean_values(uint8_t *tile, int row, bool held) {
-    using S = Shape<D, E4M3>;
+    using S = Shape<D, false>;
     bool odd = false;
 #pragma unroll
-    for (int i = 0; i < D * (E4M3 ? 1 : 2) / 16; ++i) {
-        uint4 *at = reinterpret_cast<uint4 *>(tile + (i * 16 / S::kRow) * S::kMat +
-                                              swizzled<S::kRow>(row, i * 16 % S::kRow));
+    for (int i = 0; i < D / 8; ++i) {
+        uint4 *at = reinterpret_cast<uint4 *>(tile + (i / 8) * S::kMat + swizzled<S::kRow>(row, i % 8 * 16));
         if (!held) {
             *at = make_uint4(0, 0, 0, 0);
             continue;
@@ -509,15 +493,8 @@ __device__ __forceinline__ bool clean_values(uint8_t *tile, int row, bool held) 
         bool here = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint32_t keep;
-            if (E4M3) {
-                // 0x80 in each byte that is 0x7f or 0xff
-                const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                keep = ~((nan >> 7) * 0xffu);
-            } else {
-                keep = ((w[k] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
-                       ((w[k] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
-            }
+            const uint32_t keep = ((w[k] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                                  ((w[k] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
             here |= keep != 0xffffffffu;
             w[k] &= keep;
         }
@@ -527,6 +504,65 @@ __device__ __forceinline__ bool clean_values(uint8_t *tile, int row, bool held) 
     return odd;
 }
 
+// Row `row` of an e4m3 value tile as bf16 values times f, a power of two, into a
+// bf16 tile: exact.  (With the weights in two e4m3 terms instead, as the other
+// operand of a product of bytes, those under 2^-15 of the largest were lost.)
+// CLEAN: some query rows do not see all positions; as above.  AT_ONCE pieces of 16
+// columns are worked on together: 4, unrolled, in the few-row kernel, whose softmax
+// groups do it (64 chains of 6: 200 us, 2 in a loop 213); 2 in a loop for the wide
+// kernel's helper warps, whose code then stays in the instruction cache (16 trees
+// of 85 nodes: 243 us, 4 unrolled 262).
+template <int D, int AT_ONCE, bool CLEAN>
+__device__ __forceinline__ bool widen_row(const uint8_t *from, uint8_t *to, int row, float f, bool held) {
+    using S = Shape<D, true>;
+    using T = Shape<D, false>;
+    constexpr int kUnroll = AT_ONCE == 4 ? D / 64 : 1;
+    const F2 f2 = pair_of(f, f);
+    bool odd = false;
+#pragma unroll kUnroll
+    for (int i0 = 0; i0 < D / 16; i0 += AT_ONCE) {
+        uint4 u[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+            u[i] = *reinterpret_cast<const uint4 *>(from + swizzled<S::kRow>(row, (i0 + i) * 16));
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, y[8];
+            if (CLEAN) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // 0x80 in each byte that is 0x7f or 0xff
+                    const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    odd |= held && nan != 0;
+                    w[k] = held ? w[k] & ~((nan >> 7) * 0xffu) : 0u;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 v = e4m3_values(w[k / 2] >> (k % 2 * 16) & 0xffffu);
+                const float2 x = parts_of(mul2(pair_of(v.x, v.y), f2));
+                y[k] = bf16_pair(x.x, x.y);
+            }
+            uint8_t *at = to + ((i0 + i) / 4) * T::kMat;
+            *reinterpret_cast<uint4 *>(at + swizzled<T::kRow>(row, (i0 + i) % 4 * 32)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4 *>(at + swizzled<T::kRow>(row, (i0 + i) % 4 * 32 + 16)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+    }
+    return odd;
+}
+
+template <int D>
+__device__ __noinline__ bool widen_clean(const uint8_t *from, uint8_t *to, int row, float f, bool held) {
+    return widen_row<D, 1, true>(from, to, row, f, held);
+}
+
+template <int D, int AT_ONCE>
+__device__ __forceinline__ bool widen_values(const uint8_t *from, uint8_t *to, int row, float f, bool held, bool clean) {
+    if (!clean) return widen_row<D, AT_ONCE, false>(from, to, row, f, true);
+    // A tile in ten and fewer; a call would cost the few-row kernel registers.
+    return AT_ONCE == 4 ? widen_row<D, 1, true>(from, to, row, f, held) : widen_clean<D>(from, to, row, f, held);
+}
+
 // Element `at` of the cached values where it is not finite, else anything finite.
 template <bool E4M3>
 __device__ __forceinline__ float odd_value(const CacheView &c, long long at) {
@@ -534,10 +570,8 @@ __device__ __forceinline__ float odd_value(const CacheView &c, long long at) {
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(c.v)[at]);
 }
 
-// Exponent i of four packed ones, kept in the range the cache is written with.
-__device__ __forceinline__ int exponent_of(uint32_t four, int i) {
-    return max(-120, min(120, static_cast<int>(static_cast<int8_t>(four >> 8 * i))));
-}
+// 2^e of a cached exponent, kept in the range the cache is written with.
+__device__ __forceinline__ float power_of(int e) { return exp2i(max(-120, min(120, e))); }
 
 __device__ __forceinline__ const int32_t *pages_of(const AttnArgs &a, const Segment &g) {
     return g.shared ? a.shared_table : a.table + static_cast<long long>(g.b) * a.width;
@@ -580,9 +614,11 @@ struct Loader {
     // Tile t of segment g (keys or values) into the next slot, once `empty` (if
     // given) has completed its last use: in the ring's own phase.  False when a
     // wait ran out.  *fail is set where a page id is out of range (that page's
-    // rows keep what the slot had; the segment's results are failed).
+    // rows keep what the slot had; the segment's results are failed).  `exps`, if
+    // given: the ring of the tiles' key and value exponents, 2 kTile bytes a slot,
+    // whose copies arrive at the same barrier (one arrival a lane).
     __device__ bool tile(const AttnArgs &a, const Segment &g, PageIds &from, int t, const CUtensorMap *map, uint32_t ring,
-                         unsigned long long *full_bar, uint32_t empty, volatile int *dead, int *fail) {
+                         unsigned long long *full_bar, uint32_t empty, volatile int *dead, int *fail, uint32_t exps = 0) {
         const int lane = threadIdx.x & 31, shift = a.c.page_shift, first = t * (kTile >> shift);
         const int pages = min(kTile >> shift, ((g.len - t * kTile) + (1 << shift) - 1) >> shift);
         from.turn(a, g, first);
@@ -605,6 +641,14 @@ struct Loader {
 #pragma unroll
             for (int x = 0; x < S::kHalves; ++x)
                 tma_load(dst + x * S::kMat, map, full, x * 64, 0, id * a.c.Hkv + g.h);
+        }
+        if (exps) {  // four positions a lane
+            const int page = __shfl_sync(0xffffffffu, id, lane * 4 >> shift);
+            const long long at = cache_row(a.c, max(page, 0), g.h, lane * 4 & ((1 << shift) - 1));
+            const uint32_t dst = exps + slot * 2 * kTile + lane * 4;
+            copy4(dst, a.c.k_exp + at, page >= 0);
+            copy4(dst + kTile, a.c.v_exp + at, page >= 0);
+            copies_arrive(full);
         }
         ++n;
         if (++slot == kSlots) {

@@ -8,7 +8,8 @@
 //   warp 8           loads key and value tiles page by page (TMA)
 //   warp 9           issues the products (tcgen05, M = 128 rows): S = Q K^T,
 //                    then O += P V with P in TMEM
-//   warp 10          the e4m3 cache's exponents, as factors
+//   warps 10, 11     over an e4m3 cache: the keys' exponents as factors, and the
+//                    value tiles widened to bf16, half a tile's positions each
 //   (the softmax groups stage the query tiles of their next segment)
 // A unit of over 128 rows gives each group 128 rows of its own and both work
 // on every tile; a smaller one alternates its tiles between the groups, so
@@ -16,21 +17,18 @@
 // 128 columns and two O of D.
 //
 // e4m3 cache: S = Q1 K^T + Q2 K^T with the query's two e4m3 terms, at the
-// e4m3 rate, costs what one bf16 product does; the weights likewise (two
-// terms, 2^-8 relative at worst).  A key's exponent multiplies its column of
-// S; a value's is added to t, so that the weight carries it, and taken back
-// in l.
+// e4m3 rate, costs what one bf16 product does.  A key's exponent multiplies its
+// column of S.  Values are multiplied as bf16, their exponent in them, so that
+// weights are what they are over a bf16 cache.
 //
 // Bound by the chain softmax -> O += P V -> next S of a group, of which two are
-// in flight (TMEM holds no third S beside two O): a tile of 256 rows takes 3400
-// cycles in bf16, where its products are 2048 and a group's softmax 1400; in
-// e4m3 5600, where the two terms' split makes the softmax 3600.  The first half
-// of P goes to its product while the second is made (16 trees of 85 nodes: 206
-// us a call against 214; 64 chains under one prefix: 213 against 220).  Loads
-// (64 KB a bf16 tile) hold it up for a sixth.  Measured: 16 trees of 85 nodes, 8 heads of
-// 128, 4 query heads each, over bf16 caches of 3500 to 7001 with a distance
-// bias (0.12 PFLOP): 174 us; 64 chains of 6 over one e4m3 prefix of 16001 (0.10
-// PFLOP): 133 us.
+// in flight: a tile of 256 rows takes 3400 cycles in bf16, where its products are
+// 2048 and a group's softmax 1400.  The first half of P goes to its product while
+// the second is made (16 trees of 85 nodes: 206 us a call against 214).  Loads
+// (64 KB a bf16 tile) hold it up for a sixth.  Measured: 16 trees of 85 nodes, 8
+// heads of 128, 4 query heads each, over bf16 caches of 3500 to 7001 with a distance
+// bias (0.12 PFLOP): 178 us; 64 chains of 6 over one e4m3 prefix of 16001 (0.10
+// PFLOP): 122 us.
 // Tried and dropped: tiles in halves of 64 columns, so that a half's scores are
 // made under the other's softmax (273 us against 246 at the time); the product
 // loops written out per mode (250); registers moved between warps (more spills).
@@ -41,10 +39,12 @@ namespace specv {
 namespace {
 
 constexpr int kScaleRing = 4;
+constexpr int kHelperBarrier = 1;  // hardware barrier of the e4m3 cache's two warps
 
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots];
     unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
+    unsigned long long wide_full[2], wide_empty[2];
     unsigned long long q_full, left, o_full[2], s_full[2], p_half[2], p_full[2], drained;
 };
 
@@ -61,12 +61,14 @@ template <int D, bool E4M3>
 struct Layout : Shape<D, E4M3> {
     using S = Shape<D, E4M3>;
     static constexpr int kQ = E4M3 ? 2 * S::kMat : S::kSlot;  // a group's query tile
+    static constexpr int kWide = E4M3 ? Shape<D, false>::kSlot : 0;  // a value tile widened to bf16
     // factors of the positions, and of the query rows
-    static constexpr int kScale = E4M3 ? (kScaleRing * 3 * kTile + 2 * kGroupRows) * 4 : 0;
+    static constexpr int kScale = E4M3 ? (kScaleRing * kTile + 2 * kGroupRows) * 4 : 0;
     static constexpr int kFixed = kScale + static_cast<int>((sizeof(Shared) + 127) / 128 * 128);
-    static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ) / S::kSlot;
+    static constexpr int kRoom = (kSmemMax - kFixed - 2 * kQ - 2 * kWide) / S::kSlot;
     static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
-    static constexpr int kBytes = kFixed + 2 * kQ + kSlots * S::kSlot;
+    static constexpr int kBytes = kFixed + 2 * kQ + 2 * kWide + kSlots * S::kSlot;
+    static_assert(kSlots >= 5, "a tile's fill of a slot is told from the one before by what was multiplied since");
 };
 
 // What a softmax thread holds of its row.
@@ -172,13 +174,8 @@ __device__ __forceinline__ float scores32(const AttnArgs &a, const Row &x, float
         for (int c = 0; c < 32; c += 2) {
             F2 y = pair_of(v[c], v[c + 1]);
             F2 b;
-            if (E4M3) {
-                y = mul2(y, *reinterpret_cast<const F2 *>(fa + col + c));
-                b = *reinterpret_cast<const F2 *>(fa + kTile + col + c);
-                if (EXTRA) b = add2(b, fma2(slope, pair_of(col + c, col + c + 1), base2));
-            } else {
-                b = EXTRA ? fma2(slope, pair_of(col + c, col + c + 1), base2) : pair_of(0.0f, 0.0f);
-            }
+            if (E4M3) y = mul2(y, *reinterpret_cast<const F2 *>(fa + col + c));
+            b = EXTRA ? fma2(slope, pair_of(col + c, col + c + 1), base2) : pair_of(0.0f, 0.0f);
             const float2 t = parts_of(fma2(y, rs, b));
             v[c] = t.x;
             v[c + 1] = t.y;
@@ -202,7 +199,6 @@ __device__ __forceinline__ float scores32(const AttnArgs &a, const Row &x, float
             else
                 y += fmaf(x.slope, static_cast<float>(col + c), base);
         }
-        if (E4M3) y += fa[kTile + col + c];
         if (!(seen >> c & 1u)) y = kNegInf;
         v[c] = y;
         top[c & 1] = fmaxf(top[c & 1], y);
@@ -211,31 +207,18 @@ __device__ __forceinline__ float scores32(const AttnArgs &a, const Row &x, float
 }
 
 // Weights 2^t of 32 columns, t already less the reference, into TMEM as the
-// product's operand: 16 columns of bf16 pairs, or 8 of first and 8 of second
-// e4m3 terms.  Returns their sum, in e4m3 without the values' exponents (fc:
-// 2^-ev).
-template <bool E4M3>
-__device__ __forceinline__ float weights32(uint32_t dst, const float *fc, const F2 (&t)[16]) {
+// product's operand, 16 columns of bf16 pairs.  Returns their sum.
+__device__ __forceinline__ float weights32(uint32_t dst, const F2 (&t)[16]) {
     F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
     uint32_t pk[16];
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
         const float2 u = parts_of(t[c]), v = parts_of(t[c + 1]);
         const float x0 = ex2(u.x), x1 = ex2(u.y), x2 = ex2(v.x), x3 = ex2(v.y);
-        if (E4M3) {
-            sum[0] = fma2(pair_of(x0, x1), *reinterpret_cast<const F2 *>(fc + 2 * c), sum[0]);
-            sum[1] = fma2(pair_of(x2, x3), *reinterpret_cast<const F2 *>(fc + 2 * c + 2), sum[1]);
-            uint32_t h0, l0, h1, l1;
-            e4m3_terms(x0, x1, &h0, &l0);
-            e4m3_terms(x2, x3, &h1, &l1);
-            pk[c / 2] = h0 | h1 << 16;
-            pk[8 + c / 2] = l0 | l1 << 16;
-        } else {
-            sum[0] = add2(sum[0], pair_of(x0, x1));
-            sum[1] = add2(sum[1], pair_of(x2, x3));
-            pk[c] = bf16_pair(x0, x1);
-            pk[c + 1] = bf16_pair(x2, x3);
-        }
+        sum[0] = add2(sum[0], pair_of(x0, x1));
+        sum[1] = add2(sum[1], pair_of(x2, x3));
+        pk[c] = bf16_pair(x0, x1);
+        pk[c + 1] = bf16_pair(x2, x3);
     }
     tmem_store16(dst, pk);
     const float2 s = parts_of(add2(sum[0], sum[1]));
@@ -244,9 +227,9 @@ __device__ __forceinline__ float weights32(uint32_t dst, const float *fc, const 
 
 // Moves the row's reference maximum up to `top` where that is needed,
 // rescaling the sum and, if there is one, the accumulator in TMEM.
-template <int D, bool E4M3>
+template <int D>
 __device__ __forceinline__ void grow(Row &x, float top, bool wrote, uint32_t ot) {
-    const bool up = top > x.m + (E4M3 ? kSlackE4M3 : kSlackBf16);
+    const bool up = top > x.m + kSlack;
     if (!__any_sync(0xffffffffu, up)) return;
     const float keep = up ? ex2(x.m - top) : 1.0f;
     if (up) x.m = top;
@@ -309,8 +292,8 @@ __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g
             tmem_store32(st + c * 32, reinterpret_cast<const uint32_t *>(t[0]));
         }
     }
-    grow<D, E4M3>(x, top, wrote, ot);
-    const float ref = x.m == kNegInf ? 0.0f : x.m - (E4M3 ? kLiftE4M3 : 0.0f);
+    grow<D>(x, top, wrote, ot);
+    const float ref = x.m == kNegInf ? 0.0f : x.m;
     const bool stored = E4M3 || !linear;
     const float mul = stored ? 1.0f : x.rs, slope = stored ? 0.0f : x.slope, add = (stored ? 0.0f : base) - ref;
     const F2 mul_2 = pair_of(mul, mul), slope_2 = pair_of(slope, slope), add_2 = pair_of(add, add);
@@ -331,7 +314,7 @@ __device__ __forceinline__ void softmax_tile(const AttnArgs &a, const Segment &g
             else
                 y[k] = fma2(v, mul_2, add_2);
         }
-        x.l += weights32<E4M3>(st + c * 16, fa + 2 * kTile + c * 32, y);
+        x.l += weights32(st + c * 16, y);
         if (c == 1) {  // the product may begin with these
             tmem_store_wait();
             fence_before_sync();
@@ -373,9 +356,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const AttnArgs &a = ka.a;
     const Plan &p = ka.p;
-    uint8_t *qt = smem, *ring = qt + 2 * S::kQ;
-    float *scales = reinterpret_cast<float *>(ring + S::kSlots * S::kSlot);
-    float *q_factor = scales + kScaleRing * 3 * kTile;  // [2][kGroupRows], e4m3
+    uint8_t *qt = smem, *ring = qt + 2 * S::kQ, *wide = ring + S::kSlots * S::kSlot;
+    float *scales = reinterpret_cast<float *>(wide + 2 * S::kWide);  // [kScaleRing][kTile], e4m3
+    float *q_factor = scales + kScaleRing * kTile;                    // [2][kGroupRows], e4m3
     Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(scales) + S::kScale);
     Barriers &bar = sh.bar;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -386,10 +369,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_init(smem_addr(&bar.empty[i]), 1);
         }
         for (int i = 0; i < kScaleRing; ++i) {
-            bar_init(smem_addr(&bar.scale_full[i]), 1);
+            bar_init(smem_addr(&bar.scale_full[i]), 2);
             bar_init(smem_addr(&bar.scale_empty[i]), 8);
         }
         for (int w = 0; w < 2; ++w) {
+            bar_init(smem_addr(&bar.wide_full[w]), 1);
+            bar_init(smem_addr(&bar.wide_empty[w]), 1);
             bar_init(smem_addr(&bar.o_full[w]), 1);
             bar_init(smem_addr(&bar.s_full[w]), 1);
             bar_init(smem_addr(&bar.p_half[w]), 4);
@@ -451,13 +436,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else if (warp == 9) {
         // ---- products
         if (elect_one()) {
-            constexpr uint32_t kQk = mma_desc(E4M3, kTile, false, false), kPv = mma_desc(E4M3, D, false, true);
-            constexpr uint32_t kHi = kMatrixHi<S::kRow>;
-            uint32_t segs = 0, pn[2] = {0, 0};
+            using T = Shape<D, false>;  // the values as the product takes them
+            constexpr uint32_t kQk = mma_desc(E4M3, kTile, false, false), kPv = mma_desc(false, D, false, true);
+            constexpr uint32_t kHi = kMatrixHi<S::kRow>, kVHi = kMatrixHi<T::kRow>;
+            uint32_t segs = 0, pn[2] = {0, 0}, vn = 0;
             uint32_t slot = 0, phase = 0;  // the ring, in the order it is filled
             bool live = true;
             const uint32_t q0 = matrix_lo(smem_addr(qt), 0), k0 = matrix_lo(smem_addr(ring), 0);
-            const uint32_t v0 = matrix_lo(smem_addr(ring), S::kMat);
+            const uint32_t v0 = matrix_lo(smem_addr(E4M3 ? wide : ring), T::kMat);
             const uint32_t full0 = smem_addr(&bar.full[0]), empty0 = smem_addr(&bar.empty[0]);
             const uint32_t s_full = smem_addr(&bar.s_full[0]), p_full = smem_addr(&bar.p_full[0]);
             const uint32_t p_half = smem_addr(&bar.p_half[0]);
@@ -484,23 +470,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
             };
-            // O += P V of group w with the value tile in slot s, of the positions of half z
+            // O += P V of group w with the value tile in slot (or wide buffer) s, of the positions of half z
             auto values = [&](uint32_t w, uint32_t s, uint32_t z, bool first) {
-                const uint32_t v = v0 + s * (S::kSlot >> 4), d = tmem + 2 * kTile + w * D, pt = tmem + w * kTile;
-                if (E4M3) {
+                const uint32_t v = v0 + s * (T::kSlot >> 4), d = tmem + 2 * kTile + w * D, pt = tmem + w * kTile;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t j = 2 * z + i % 2;
-                        mma_ts<true>(d, pt + j * 16 + (i / 2) * 8, v + (j * 32 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_ts<false>(d, pt + (4 * z + i) * 8, v + ((4 * z + i) * 16 * S::kRow >> 4), kHi, kPv, i > 0 || !first);
-                }
+                for (int i = 0; i < 4; ++i)
+                    mma_ts(d, pt + (4 * z + i) * 8, v + ((4 * z + i) * 16 * T::kRow >> 4), kVHi, kPv, i > 0 || !first);
             };
             while (live && walk.next(&g)) {
-                const int T = g.t1 - g.t0, lead = g.dual ? 1 : min(2, T);
+                const int n = g.t1 - g.t0, lead = g.dual ? 1 : min(2, n);
                 live = bar_wait(smem_addr(&bar.q_full), segs & 1, dead);
                 for (int t = 0; live && t < lead; ++t) {  // scores of each group's first tile
                     if (!(live = bar_wait(full0 + 8 * slot, phase, dead))) break;
@@ -517,13 +495,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     mma_commit(empty0 + 8 * slot);
                     advance();
                 }
-                for (int t = 0; live && t < T; ++t) {
-                    const uint32_t vs = slot, vp = phase;
+                for (int t = 0; live && t < n; ++t, ++vn) {
+                    // Over e4m3 the two helper warps take the tile from the ring.
+                    const uint32_t vs = E4M3 ? vn & 1 : slot, vp = E4M3 ? (vn >> 1) & 1 : phase;
+                    const uint32_t v_full = E4M3 ? smem_addr(&bar.wide_full[vs]) : full0 + 8 * vs;
+                    const uint32_t v_empty = E4M3 ? smem_addr(&bar.wide_empty[vs]) : empty0 + 8 * vs;
                     advance();
-                    const bool more = t + lead < T;
+                    const bool more = t + lead < n;
                     const uint32_t ks = slot, kp = phase;
                     if (more) advance();
-                    if (!(live = bar_wait(full0 + 8 * vs, vp, dead))) break;
+                    if (!(live = bar_wait(v_full, vp, dead))) break;
                     const uint32_t w0 = g.dual ? 0 : t & 1, w1 = g.dual ? 1 : t & 1;
                     for (uint32_t w = w0; w <= w1; ++w) {
                         const uint32_t pp = pn[w]++ & 1;
@@ -533,7 +514,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (!(live = bar_wait(p_full + 8 * w, pp, dead))) break;
                         fence_after_sync();
                         values(w, vs, 1, false);
-                        if (w == w1) mma_commit(empty0 + 8 * vs);
+                        if (w == w1) mma_commit(v_empty);
                         if (!more) continue;
                         if (!(live = bar_wait(full0 + 8 * ks, kp, dead))) break;
                         scores(w, g.dual ? w : 0, ks);
@@ -551,37 +532,78 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 10) {
-        // ---- the e4m3 exponents as factors: 2^ek, ev, 2^-ev of every position
-        if (E4M3) {
-            uint32_t n = 0;
+    } else if (warp >= 10) {
+        // ---- the e4m3 cache, a warp for each half of a tile's positions, two rows a
+        // thread: 2^ek of every position, a tile ahead, and the value tile widened.
+        // A thread's page ids are read three tiles ahead, its exponents two.
+        if constexpr (E4M3) {
+            const int half = warp - 10, row = half * 64 + lane;
+            uint32_t n = 0, n_ring = 0, seg = 0;
             bool live = true;
+            auto page_ids = [&](int t, int (&id)[2]) {
+                for (int i = 0; i < 2; ++i) {
+                    const int j = t * kTile + row + 32 * i;
+                    id[i] = t < g.t1 && j < g.len ? pages_of(a, g)[j >> a.c.page_shift] : -1;
+                    if (id[i] >= a.c.num_pages) id[i] = -1;
+                }
+            };
+            auto exponents = [&](int t, const int (&id)[2], int (&e)[2][2]) {
+                for (int i = 0; i < 2; ++i) {
+                    const long long at =
+                        cache_row(a.c, max(id[i], 0), g.h, (t * kTile + row + 32 * i) & ((1 << a.c.page_shift) - 1));
+                    e[i][0] = id[i] < 0 ? 0 : a.c.k_exp[at];
+                    e[i][1] = id[i] < 0 ? 0 : a.c.v_exp[at];
+                }
+            };
+            auto factors = [&](uint32_t m, const int (&e)[2][2]) {
+                const uint32_t s = m % kScaleRing;
+                live = live && bar_wait(smem_addr(&bar.scale_empty[s]), ((m / kScaleRing) & 1) ^ 1, dead);
+                live = __all_sync(0xffffffffu, live);
+                for (int i = 0; i < 2; ++i) scales[s * kTile + row + 32 * i] = power_of(e[i][0]);
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.scale_full[s]));
+            };
             while (live && walk.next(&g)) {
+                const int T = g.t1 - g.t0, last_pos = a.window > 0 ? last_position(a, g) : 0;
+                int id[2], now[2][2], next[2][2], after[2][2];
+                page_ids(g.t0, id);
+                exponents(g.t0, id, now);
+                page_ids(g.t0 + 1, id);
+                factors(n, now);
+                exponents(g.t0 + 1, id, next);
+                page_ids(g.t0 + 2, id);
                 for (int t = g.t0; t < g.t1; ++t, ++n) {
-                    const int j = t * kTile + lane * 4;
-                    int slot = 0;
-                    const int page = j < g.len ? page_of(a.c, pages_of(a, g), INT_MAX, j, &slot) : -1;
-                    uint32_t ek = 0, ev = 0;
-                    if (page >= 0) {
-                        const long long row = cache_row(a.c, page, g.h, slot);
-                        ek = __ldg(reinterpret_cast<const uint32_t *>(a.c.k_exp + row));
-                        ev = __ldg(reinterpret_cast<const uint32_t *>(a.c.v_exp + row));
-                    }
-                    const uint32_t s = n % kScaleRing;
-                    live = bar_wait(smem_addr(&bar.scale_empty[s]), ((n / kScaleRing) & 1) ^ 1, dead);
-                    live = __all_sync(0xffffffffu, live);
-                    if (!live) break;
-                    float *f = scales + s * 3 * kTile + lane * 4;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int x = exponent_of(ek, i), y = exponent_of(ev, i);
-                        f[i] = exp2i(x);
-                        f[kTile + i] = static_cast<float>(y);
-                        f[2 * kTile + i] = exp2i(-y);
+                    if (t + 1 < g.t1) factors(n + 1, next);
+                    exponents(t + 2, id, after);
+                    page_ids(t + 3, id);
+                    const int idx = t - g.t0;
+                    // The tile's slot as the loads number them.  The buffer is free once the product of
+                    // the tile two before is over: all fills before the slot's present one then are.
+                    const uint32_t vi = n_ring + (g.dual || idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
+                    live = live && bar_wait(smem_addr(&bar.wide_empty[n & 1]), ((n >> 1) & 1) ^ 1, dead) &&
+                           bar_wait(smem_addr(&bar.full[vi % S::kSlots]), (vi / S::kSlots) & 1, dead);
+                    if (live) {
+                        const bool clean = !sees_whole(a, g, t * kTile, last_pos);
+                        bool odd = false;
+                        for (int i = 0; i < 2; ++i)
+                            odd |= widen_values<D, 2>(ring + vi % S::kSlots * S::kSlot, wide + (n & 1) * S::kWide, row + 32 * i,
+                                                   power_of(now[i][1]), t * kTile + row + 32 * i < g.len, clean);
+                        if (odd) sh.odd[seg & 15] = 1;
+                        fence_async_proxy();
                     }
                     __syncwarp();
-                    if (lane == 0) bar_arrive(smem_addr(&bar.scale_full[s]));
+                    // The two warps leave together: this barrier's wait has no bound of its own.
+                    live = !any_of(kHelperBarrier, 64, !live);
+                    if (!live) break;
+                    if (warp == 10 && lane == 0) {
+                        bar_arrive(smem_addr(&bar.empty[vi % S::kSlots]));
+                        bar_arrive(smem_addr(&bar.wide_full[n & 1]));
+                    }
+                    for (int i = 0; i < 2; ++i)
+                        for (int k = 0; k < 2; ++k) now[i][k] = next[i][k], next[i][k] = after[i][k];
                 }
+                n_ring += 2 * T;
+                ++seg;
             }
         }
     } else if (warp < 8) {
@@ -631,21 +653,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (active)
                         seen = seen_columns(a.mask, a.pos, a.N, a.window, g.shared ? 0 : a.shared_len, g.shared, g.len, x.first,
                                             x.has, x.tok, x.b * a.N, x.pos_i, j0);
-                    // the tile's values: slot index as the loads number them
-                    const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
-                    if (!g.dual) live = bar_wait(s_bar, s_phase, dead);
-                    live = live && bar_wait(smem_addr(&bar.full[vi % S::kSlots]), (vi / S::kSlots) & 1, dead);
-                    live = __all_sync(0xffffffffu, live);
-                    if (!live) break;
-                    if (clean_values<D, E4M3>(ring + vi % S::kSlots * S::kSlot, row, j0 + row < g.len)) sh.odd[segs & 15] = 1;
-                    fence_async_proxy();
+                    if constexpr (!E4M3) {
+                        // the tile's values: slot index as the loads number them
+                        const uint32_t vi = n_ring + (g.dual ? 2 * idx + 1 : idx == T - 1 ? 2 * idx + 1 : 2 * idx + 2);
+                        if (!g.dual) live = bar_wait(s_bar, s_phase, dead);
+                        live = live && bar_wait(smem_addr(&bar.full[vi % S::kSlots]), (vi / S::kSlots) & 1, dead);
+                        live = __all_sync(0xffffffffu, live);
+                        if (!live) break;
+                        if (clean_values<D>(ring + vi % S::kSlots * S::kSlot, row, j0 + row < g.len)) sh.odd[segs & 15] = 1;
+                        fence_async_proxy();
+                    }
                 }
                 live = bar_wait(s_bar, s_phase, dead);
                 const float *fa = nullptr;
                 if (E4M3) {
                     const uint32_t s = (n_scale + idx) % kScaleRing;
                     live = live && bar_wait(smem_addr(&bar.scale_full[s]), ((n_scale + idx) / kScaleRing) & 1, dead);
-                    fa = scales + s * 3 * kTile;
+                    fa = scales + s * kTile;
                 }
                 live = __all_sync(0xffffffffu, live);
                 if (!live) break;
@@ -675,7 +699,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const bool failed = reinterpret_cast<volatile int *>(sh.fail)[segs & 15] != 0;
             const bool odd = reinterpret_cast<volatile int *>(sh.odd)[segs & 15] != 0;
             if (has)
-                k.ml[at] = make_float2(x.m == kNegInf ? kNegInf : x.m - (E4M3 ? kLiftE4M3 : 0.0f), failed ? NAN : x.l);
+                k.ml[at] = make_float2(x.m, failed ? NAN : x.l);
             if (active && wrote) {
                 // Rows go out through this warp's part of the query tile's memory (its
                 // products are done), so that a store instruction covers whole lines.

@@ -112,6 +112,16 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Four bytes (zeros where not `on`), and their arrival at `bar` once this
+// thread's copies so far are there (the barrier's count includes it).
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool on) {
+    asm volatile("cp.async.ca.shared::cta.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4u : 0u) : "memory");
+}
+
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // -------------------------------------------------------------- tcgen05
 
 __device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t columns) {
@@ -140,7 +150,7 @@ __device__ __forceinline__ void fence_after_sync() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// D[tmem] (+)= A B with A and B in shared memory, or A in TMEM.  F8: both
+// D[tmem] (+)= A B with A and B in shared memory.  F8: both
 // operands e4m3, 32 deep; else both bf16, 16 deep.  A matrix descriptor comes
 // as its low word (which moves along the matrix) and its high word.
 template <bool F8>
@@ -160,18 +170,12 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, ui
             "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
 }
 
-template <bool F8>
+// Both bf16, A in TMEM.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool add) {
-    if (F8)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-            "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-            "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u));
 }
 
 // 32 consecutive TMEM columns of this thread's lane (a warp reads its own 32
