@@ -77,7 +77,7 @@ struct Shared {
     uint32_t tmem;
     int dead;              // a wait ran out: everyone leaves
     int fail[16];          // per segment (mod 16): a page id out of range
-    int odd[2][16];        // per group and segment (mod 16): a tile it cleaned held values that are not finite
+    int odd[2][2];         // per group and segment (mod 2): a tile it cleaned held values that are not finite
 };
 
 template <int D, bool E4M3, int NR>
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         PageIds ids;
         bool live = true;
         for (uint32_t seg = 0; live && walk.next(&g); ++seg) {
-            if (lane == 0) sh.fail[seg & 15] = sh.odd[0][seg & 15] = sh.odd[1][seg & 15] = 0;
+            if (lane == 0) sh.fail[seg & 15] = 0;
             __syncwarp();
             ids.begin(a, g);
             for (int t = g.t0; live && t < g.t1; ++t) {
@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int i = 0; i < NR; ++i) l[i] = 0.0f;
             if (row < NR) ref[row] = row < n_rows ? kNone : INFINITY;
-            if (vote(!ok)) {  // the reference is set
+            if (row == 0) sh.odd[w][half] = 0;
+            if (vote(!ok)) {  // the reference and the flag are set
                 live = false;
                 break;
             }
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     fk = power_of(e[0]);
                     if (ok && widen_values<D, 4>(v_ring + vi % S::kV * S::kSlot, wide + w * S::kWide, row, power_of(e[kTile]),
                                               j < g.len, !whole))
-                        sh.odd[w][seg & 15] = 1;
+                        sh.odd[w][half] = 1;
                     __syncwarp();
                     if (lane == 0) bar_arrive(smem_addr(&bar.v_empty[vi % S::kV]));
                 }
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (S::kV < 3 && vi >= S::kV)
                             ok = ok && bar_wait(smem_addr(&bar.v_empty[vi % S::kV]), ((vi - S::kV) / S::kV) & 1, dead);
                         ok = ok && bar_wait(smem_addr(&bar.v_full[vi % S::kV]), (vi / S::kV) & 1, dead);
-                        if (ok && clean_values<D>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[w][seg & 15] = 1;
+                        if (ok && clean_values<D>(v_ring + vi % S::kV * S::kSlot, row, j < g.len)) sh.odd[w][half] = 1;
                     }
                 }
                 fence_async_proxy();
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // (A group without a tile of the segment has not waited for its loads: it
             // leaves the flags to the other.)
             const bool failed = wrote && reinterpret_cast<volatile int *>(sh.fail)[seg & 15] != 0;
-            const bool odd = wrote && reinterpret_cast<volatile int *>(sh.odd[w])[seg & 15] != 0;
+            const bool odd = wrote && reinterpret_cast<volatile int *>(sh.odd[w])[half] != 0;
             if (row < n_rows) {
                 const float m = ref[row];
                 const float sum = !wrote ? 0.0f : (sh.red[w][0][row] + sh.red[w][1][row]) + (sh.red[w][2][row] + sh.red[w][3][row]);
