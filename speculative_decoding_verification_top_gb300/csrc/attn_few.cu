@@ -27,8 +27,8 @@
 // the first tile of a segment is rare, so maxima are reduced only then.  l is
 // kept per thread and summed once a segment.
 // Measured: 64 chains of 6 over e4m3 caches of 4100 to 8200 positions, 8 heads
-// of 128 (819 MB): 183 us, 4.5 TB/s; its loads alone 152, without the widening 145:
-// bound by what the groups issue.  128 chains of 4 over bf16 caches of 2500 to
+// of 128 (819 MB): 183 us, 4.5 TB/s (its loads alone 152): bound by what the groups
+// issue (the call takes 202 us, without the widening 164).  128 chains of 4 over bf16 caches of 2500 to
 // 5003, 4 heads of 64, capped (497 MB): 110 us (its loads alone 102).  Beside the
 // loads a call costs about 20 us of launch, line and first tiles, which is what a
 // single token over 2049 positions takes.
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int8_t *e = exps + vi % S::kV * S::kExps + row;
                     fk = power_of(e[0]);
                     if (ok && widen_values<D, 4>(v_ring + vi % S::kV * S::kSlot, wide + w * S::kWide, row, power_of(e[kTile]),
-                                              j < g.len, !whole))
+                                                 j < g.len, !whole))
                         sh.odd[w][half] = 1;
                     __syncwarp();
                     if (lane == 0) bar_arrive(smem_addr(&bar.v_empty[vi % S::kV]));

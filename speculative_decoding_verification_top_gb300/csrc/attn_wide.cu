@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         bool odd = false;
                         for (int i = 0; i < 2; ++i)
                             odd |= widen_values<D, 2>(ring + vi % S::kSlots * S::kSlot, wide + (n & 1) * S::kWide, row + 32 * i,
-                                                   power_of(now[i][1]), t * kTile + row + 32 * i < g.len, clean);
+                                                      power_of(now[i][1]), t * kTile + row + 32 * i < g.len, clean);
                         if (odd) sh.odd[seg & 15] = 1;
                         fence_async_proxy();
                     }
