@@ -138,7 +138,8 @@ int spec_attn_workspace_size(int B, int N, int Hq, int Hkv, int D, size_t *bytes
  *                index is its place in the sequence.
  *   slopes       [Hq] fp32, device, or NULL
  *   B >= 0, 1 <= N <= SPEC_MAX_TREE_NODES, Hq a multiple of Hkv
- *   scale        finite; cap >= 0 and finite (0: none); window >= 0 (0: none)
+ *   scale        finite; cap >= 0 and finite (0: none, as 2^64 and more are);
+ *                window >= 0 (0: none)
  *   dtype        type of q and out: SPEC_BF16
  *   out          [B, N, Hq, D] bf16, device, contiguous, 16-byte aligned
  *   out_lse      [B, N, Hq] fp32, device, or NULL
