@@ -171,6 +171,143 @@ int spec_attn_shared(const spec_kv_cache *cache, const int32_t *shared_table, in
                      int dtype, void *out, float *out_lse, void *workspace,
                      size_t workspace_bytes, spec_stream_t stream);
 
+/*
+ * Rotary positions.  A head's `rot` elements from element `first` on are rot / 2
+ * pairs; pair i of a token at position index p is turned by the angle
+ * p * theta_i and multiplied by `amplitude`:
+ *   (u, v) -> amplitude (u cos - v sin, v cos + u sin)
+ * SPEC_ROPE_HALF: pair i is elements (i, i + rot / 2) of the part;
+ * SPEC_ROPE_INTERLEAVED: (2 i, 2 i + 1).  The head's other elements stay.
+ * Angles are held as fractions of a turn in 64-bit fixed point: a frequency is
+ * 2^64 theta_i / (2 pi), its product with p modulo 2^64 is exact, so that a far
+ * position costs no digits.  Positions are any int32.
+ */
+enum { SPEC_ROPE_HALF = 0, SPEC_ROPE_INTERLEAVED = 1 };
+
+/* How frequencies theta_i = base^(-2 i / rot) are scaled for contexts longer
+ * than `original` by `factor`:
+ *   SPEC_ROPE_PLAIN   not at all
+ *   SPEC_ROPE_LINEAR  theta / factor
+ *   SPEC_ROPE_TURNS   theta (w + (1 - w) / factor), w = (t - low) / (high - low)
+ *                     clamped to [0, 1], t = original theta / (2 pi): the turns
+ *                     that the pair makes in the original context
+ *   SPEC_ROPE_INDEX   the same with w = 1 - (i - a) / max(b - a, 1/1000) clamped,
+ *                     a = max(0, floor(at(high))), b = min(rot - 1, ceil(at(low))),
+ *                     at(t) = rot ln(original / (2 pi t)) / (2 ln base): the pair
+ *                     that makes t turns there */
+enum { SPEC_ROPE_PLAIN = 0, SPEC_ROPE_LINEAR = 1, SPEC_ROPE_TURNS = 2, SPEC_ROPE_INDEX = 3 };
+
+/*
+ * The frequencies, computed on the host into freqs [rot / 2] (HOST memory; copy
+ * them to the device for the calls below).  rot: a multiple of 16, 16..1024;
+ * base > 1, at most 1e30; factor >= 1 (unread for SPEC_ROPE_PLAIN); original,
+ * low and high only for the last two: original >= 1, 0 < low < high, each at
+ * most 1e30.  All finite.
+ */
+int spec_rope_freqs(int rot, double base, int scaling, double factor, double original, double low,
+                    double high, uint64_t *freqs);
+
+/*
+ * Rotary positions of B * N tokens of H heads of D elements.
+ *   x, out       [B, N, H, D] dtype, device, 16-byte aligned; consecutive tokens
+ *                (across sequences too) at x_stride / out_stride elements (0: H * D;
+ *                at least that, a multiple of 8), a token's heads contiguous.
+ *                out may be x, with the same stride (then only the turned part is
+ *                written); otherwise they do not overlap
+ *   freqs        [rot / 2], device, 16-byte aligned
+ *   pos          [B, N] int32, device
+ *   D, rot, first  multiples of 16: 16 <= D <= 1024, first + rot <= D
+ *   amplitude    finite; a negative angle (`inverse` != 0) takes the turn back
+ *   layout       SPEC_ROPE_HALF or SPEC_ROPE_INTERLEAVED
+ *   dtype        SPEC_F32 or SPEC_BF16 (computed in fp32, rounded once)
+ */
+int spec_rope(const void *x, int64_t x_stride, void *out, int64_t out_stride, const uint64_t *freqs,
+              int rot, int first, float amplitude, int layout, int inverse, const int32_t *pos,
+              int B, int N, int H, int D, int dtype, spec_stream_t stream);
+
+/*
+ * spec_kv_append with the keys rotated on the way: token r of sequence b is
+ * turned (its first `rot` elements a head) to position index pos[b][r], then
+ * written as spec_kv_append writes it (an e4m3 cache takes the turned values
+ * unrounded).  Without pos the index is the cache position.  The values are
+ * written as they are.
+ * With q, the same tokens' queries are rotated in the same launch: out_q gets
+ * token n of q at index pos[b][n], or starts[b] + n.
+ *   pos          [B, N] int32, device, or NULL
+ *   freqs, rot, amplitude, layout  as for spec_rope; rot <= D
+ *   q, out_q     [B, N, Hq, D] dtype, device, as x and out of spec_rope, or both
+ *                NULL; with `rows` NULL only (SPEC_ERR_PARAM)
+ * Other arguments as for spec_kv_append.
+ */
+int spec_kv_append_rope(const spec_kv_cache *cache, const int32_t *page_table, int table_width,
+                        const int32_t *starts, const void *k, const void *v, int64_t token_stride,
+                        const int32_t *rows, const int32_t *pos, const uint64_t *freqs, int rot,
+                        float amplitude, int layout, const void *q, int64_t q_stride, void *out_q,
+                        int64_t out_q_stride, int B, int N, int M, int Hq, int dtype,
+                        spec_stream_t stream);
+
+/*
+ * A latent cache: one row of C + R bf16 elements a position, shared by all
+ * heads.  The first C are the latent vector, values and the keys' first part at
+ * once; the R after them are the keys' rotary part.  Pages and tables as above.
+ */
+typedef struct spec_latent_cache {
+    void *data;     /* [num_pages, page, C + R] bf16, 16-byte aligned          */
+    int num_pages;  /* >= 1                                                    */
+    int page;       /* 16, 32, 64 or 128 positions                             */
+    int C;          /* 128, 256 or 512                                         */
+    int R;          /* 64                                                      */
+} spec_latent_cache;
+
+/*
+ * Write M new tokens per sequence into a latent cache: positions, rows and what
+ * is skipped as in spec_kv_append.  c [B, N, C] and r [B, N, R] dtype, device,
+ * 16-byte aligned, tokens at c_stride and r_stride elements (0: C, R; at least
+ * that, multiples of 8: both may be parts of one projection).  r is rotated
+ * (all R elements) to pos[b][r], or to the cache position without pos; freqs
+ * NULL: r as it is (pos is then ignored).
+ */
+int spec_latent_append(const spec_latent_cache *cache, const int32_t *page_table, int table_width,
+                       const int32_t *starts, const void *c, int64_t c_stride, const void *r,
+                       int64_t r_stride, const int32_t *rows, const int32_t *pos,
+                       const uint64_t *freqs, float amplitude, int layout, int B, int N, int M,
+                       int dtype, spec_stream_t stream);
+
+/* Workspace bytes of spec_latent_attn for B sequences of N new tokens and H
+ * heads (any cache lengths). */
+int spec_latent_workspace_size(int B, int N, int H, int C, size_t *bytes);
+
+/*
+ * Attention of N new tokens per sequence to a latent cache, in the absorbed
+ * form: every head's query comes with its own key projection multiplied in
+ * (C elements) and its rotary part (R elements, rotated), so that all heads
+ * read one row (c_j, r_j) a position.  For token i, head h, position j:
+ *   s_ij  = scale * q_ih . (c_j, r_j)
+ *   out_ih = sum_seen e^s_ij c_j / sum_seen e^s_ij     (C elements: the head's value
+ *                                        projection is applied by the caller)
+ *   lse_ih = ln sum_seen e^s_ij
+ * seen as in spec_attn_tree: the context always, new token j where
+ * mask[b][i][j] != 0, or j <= i without a mask.  A token that sees nothing gets
+ * zeros and lse -inf; an unseen position adds nothing whatever it holds.
+ * Scores, sums and accumulators are fp32, the softmax weights are rounded to
+ * bf16 for the product with the latents.  Calls with the same inputs give the
+ * same bits.
+ *   lens         [B] int32, device: cached positions, the new tokens included
+ *   q            [B, N, H, C + R] bf16, device, 16-byte aligned, tokens at
+ *                q_stride elements (0: H * (C + R); a multiple of 8)
+ *   mask         [B, N, N] uint8, device, or NULL (a chain)
+ *   1 <= N <= SPEC_MAX_TREE_NODES, 1 <= H <= 1024; scale finite
+ *   out          [B, N, H, C] bf16, device, contiguous, 16-byte aligned
+ *   out_lse      [B, N, H] fp32, device, or NULL
+ *   workspace    >= spec_latent_workspace_size(...) bytes, as for spec_attn_tree
+ * A length outside [0, table_width * page] or a bad page id fails its sequence:
+ * outputs NaN, SPEC_DATA_PAGE_RANGE in the workspace's error word.
+ */
+int spec_latent_attn(const spec_latent_cache *cache, const int32_t *page_table, int table_width,
+                     const int32_t *lens, const void *q, int64_t q_stride, const uint8_t *mask,
+                     int B, int N, int H, float scale, void *out, float *out_lse, void *workspace,
+                     size_t workspace_bytes, spec_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -420,6 +420,49 @@ int spec_verify_acceptance(const void *target_logits, const void *draft_logits, 
                            float *out_beta, float *out_tv, void *workspace,
                            size_t workspace_bytes, spec_stream_t stream);
 
+/*
+ * Log probabilities of emitted tokens, as a server reports them beside the
+ * tokens: [LZ] "Notation" gives p_i = softmax(logits / temperature); of it, for
+ * entry t of sequence b with token x = tokens[b][t],
+ *   logprob   ln p(x)
+ *   entropy   -sum_v p(v) ln p(v)
+ *   rank      how many tokens come before x by logit, equal ones by index
+ *   top       the `top` first tokens in that order, and their ln p
+ * of the whole row (no top-k, no top-p).  An entry's row is target row
+ * t of its sequence, or rows[b][t]: for spec_verify_sample the tokens are
+ * out_tokens and M = N = k + 1; for spec_verify_tree the tokens are out_tokens and
+ * the rows out_path, M = D + 1.
+ * A token of -1 (the pad of out_tokens) is no entry: its row is not read, its
+ * numbers are 0 and its rank and ids -1, so that a sequence's log probabilities
+ * can be summed as they are.
+ *
+ * Arguments
+ *   target_logits    [B, N, V] dtype, device
+ *   tokens           [B, M] int32, device
+ *   rows             [B, M] int32, device, or NULL (then M <= N)
+ *   B, M >= 0, N >= 1, 1 <= V <= SPEC_MAX_V; temperature > 0, finite
+ *   top              0 <= top <= SPEC_MAX_TOP, at most V
+ *   out_logprob      [B, M] fp32, device
+ *   out_entropy      [B, M] fp32, device, or NULL
+ *   out_rank         [B, M] int32, device, or NULL
+ *   out_top_ids      [B, M, top] int32, device (top > 0)
+ *   out_top_logprobs [B, M, top] fp32, device (top > 0)
+ *   workspace        >= spec_verify_logprobs_workspace_size() bytes, zeroed before
+ *                    first use; only its error word is used, so it may be a
+ *                    verification call's
+ * Data errors: a row with NaN or +inf or of -inf alone, a token neither -1 nor
+ * in [0, V), or a row outside [0, N) (SPEC_DATA_TOKEN_RANGE) gives that entry NaN
+ * numbers, rank and ids -1.
+ * Returns SPEC_OK or a negative status.
+ */
+#define SPEC_MAX_TOP 32
+int spec_verify_logprobs_workspace_size(size_t *bytes);
+int spec_verify_logprobs(const void *target_logits, const int32_t *tokens, const int32_t *rows,
+                         int B, int N, int M, int V, float temperature, int top, int dtype,
+                         float *out_logprob, float *out_entropy, int32_t *out_rank,
+                         int32_t *out_top_ids, float *out_top_logprobs, void *workspace,
+                         size_t workspace_bytes, spec_stream_t stream);
+
 /* Static, human-readable description of a status or data-error bit. */
 const char *spec_verify_status_string(int status);
 

@@ -14,10 +14,15 @@ Entry points (same names as the C ABI):
     spec_verify_status_string,
     spec_kv_append, spec_kv_read, spec_attn_workspace_size, spec_attn_tree,
     spec_attn_shared (the target pass's cache and attention, declared in
-    ``include/spec_attn.h``)
+    ``include/spec_attn.h``),
+    spec_rope_freqs, spec_rope, spec_kv_append_rope (rotary positions),
+    spec_latent_append, spec_latent_workspace_size, spec_latent_attn (a latent
+    cache and its attention), spec_verify_logprobs_workspace_size,
+    spec_verify_logprobs
 plus tensor-level helpers ``verify_sample`` / ``verify_sample_probs`` /
-``verify_tree`` / ``acceptance`` / ``kv_append`` / ``kv_read`` /
-``attn_tree`` / ``attn_shared`` that take
+``verify_tree`` / ``acceptance`` / ``logprobs`` / ``kv_append`` / ``kv_read`` /
+``attn_tree`` / ``attn_shared`` / ``rope_freqs`` / ``rope`` /
+``kv_append_rope`` / ``latent_append`` / ``latent_attn`` that take
 torch CUDA tensors, allocate outputs and a zeroed workspace, and raise on a
 negative status.
 """
@@ -36,9 +41,11 @@ CSRC = os.path.join(_PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("api.cu", "rows.cu", "topp.cu", "final.cu", "noalloc.cu",
                      "accept.cu", "treemask.cu", "treesample.cu", "select.cu",
-                     "kvcache.cu", "attn.cu", "attn_few.cu", "attn_wide.cu", "attn_api.cu")]
+                     "kvcache.cu", "attn.cu", "attn_few.cu", "attn_wide.cu", "attn_api.cu",
+                     "rope.cu", "latent.cu", "target_api.cu", "logprobs.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh", "attn.cuh",
-                                             "attn_plan.cuh", "tensor.cuh")]
+                                             "attn_plan.cuh", "tensor.cuh", "checks.cuh",
+                                             "kvrows.cuh", "target.cuh", "logprobs.cuh")]
 INCLUDE = os.path.join(_ROOT, "include")
 HEADER = os.path.join(INCLUDE, "spec_verify.h")
 ATTN_HEADER = os.path.join(INCLUDE, "spec_attn.h")
@@ -56,6 +63,9 @@ SPEC_DATA_PROB_RANGE = 1 << 6
 SPEC_DATA_PAGE_RANGE = 1 << 7
 SPEC_DATA_STALL = 1 << 8
 SPEC_MAX_K = 31
+SPEC_MAX_TOP = 32
+SPEC_ROPE_HALF, SPEC_ROPE_INTERLEAVED = 0, 1
+SPEC_ROPE_PLAIN, SPEC_ROPE_LINEAR, SPEC_ROPE_TURNS, SPEC_ROPE_INDEX = 0, 1, 2, 3
 
 EXPORTED = (
     "spec_verify_workspace_size",
@@ -79,6 +89,14 @@ EXPORTED = (
     "spec_attn_workspace_size",
     "spec_attn_tree",
     "spec_attn_shared",
+    "spec_rope_freqs",
+    "spec_rope",
+    "spec_kv_append_rope",
+    "spec_latent_append",
+    "spec_latent_workspace_size",
+    "spec_latent_attn",
+    "spec_verify_logprobs_workspace_size",
+    "spec_verify_logprobs",
     "spec_verify_status_string",
 )
 
@@ -92,6 +110,12 @@ class CacheDescriptor(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
                 ("v_exp", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("Hkv", ctypes.c_int),
                 ("page", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class LatentDescriptor(ctypes.Structure):
+    """struct spec_latent_cache of include/spec_attn.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page", ctypes.c_int),
+                ("C", ctypes.c_int), ("R", ctypes.c_int)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -160,6 +184,16 @@ def lib():
         L.spec_attn_tree.argtypes = [C, P, I, P, P, S, P, P, P, I, I, I, F, F, I, I, P, P, P, Z, P]
         L.spec_attn_shared.argtypes = [C, P, I, P, I, P, P, S, P, P, P, I, I, I, F, F, I, I, P, P,
                                        P, Z, P]
+        D, A = ctypes.c_double, ctypes.POINTER(LatentDescriptor)
+        L.spec_rope_freqs.argtypes = [I, D, I, D, D, D, D, P]
+        L.spec_rope.argtypes = [P, S, P, S, P, I, I, F, I, I, P, I, I, I, I, I, P]
+        L.spec_kv_append_rope.argtypes = [C, P, I, P, P, P, S, P, P, P, I, F, I, P, S, P, S, I, I, I,
+                                          I, I, P]
+        L.spec_latent_append.argtypes = [A, P, I, P, P, S, P, S, P, P, P, F, I, I, I, I, I, P]
+        L.spec_latent_workspace_size.argtypes = [I, I, I, I, ctypes.POINTER(Z)]
+        L.spec_latent_attn.argtypes = [A, P, I, P, P, S, P, I, I, I, F, P, P, P, Z, P]
+        L.spec_verify_logprobs_workspace_size.argtypes = [ctypes.POINTER(Z)]
+        L.spec_verify_logprobs.argtypes = [P, P, P, I, I, I, I, F, I, I, P, P, P, P, P, P, Z, P]
         L.spec_verify_status_string.argtypes = [I]
         L.spec_verify_status_string.restype = ctypes.c_char_p
         for name in EXPORTED[:-1]:
@@ -329,6 +363,63 @@ def spec_attn_shared(cache, shared_table_ptr, shared_len, table_ptr, table_width
         cache, shared_table_ptr, shared_len, table_ptr, table_width, lens_ptr, q_ptr, q_stride,
         mask_ptr, pos_ptr, slopes_ptr, B, N, Hq, float(scale), float(cap), window, dtype, out_ptr,
         out_lse_ptr, workspace_ptr, workspace_bytes, stream))
+
+
+def spec_rope_freqs(rot, base, scaling, factor, original, low, high, freqs_ptr):
+    """`freqs_ptr`: host memory for rot / 2 uint64."""
+    return _check(lib().spec_rope_freqs(rot, base, scaling, factor, original, low, high, freqs_ptr))
+
+
+def spec_rope(x_ptr, x_stride, out_ptr, out_stride, freqs_ptr, rot, first, amplitude, layout, inverse,
+              pos_ptr, B, N, H, D, dtype, stream=0):
+    return _check(lib().spec_rope(x_ptr, x_stride, out_ptr, out_stride, freqs_ptr, rot, first,
+                                  float(amplitude), layout, inverse, pos_ptr, B, N, H, D, dtype,
+                                  stream))
+
+
+def spec_kv_append_rope(cache, table_ptr, table_width, starts_ptr, k_ptr, v_ptr, token_stride, rows_ptr,
+                        pos_ptr, freqs_ptr, rot, amplitude, layout, q_ptr, q_stride, out_q_ptr,
+                        out_q_stride, B, N, M, Hq, dtype, stream=0):
+    return _check(lib().spec_kv_append_rope(
+        cache, table_ptr, table_width, starts_ptr, k_ptr, v_ptr, token_stride, rows_ptr, pos_ptr,
+        freqs_ptr, rot, float(amplitude), layout, q_ptr, q_stride, out_q_ptr, out_q_stride, B, N, M, Hq,
+        dtype, stream))
+
+
+def spec_latent_append(cache, table_ptr, table_width, starts_ptr, c_ptr, c_stride, r_ptr, r_stride,
+                       rows_ptr, pos_ptr, freqs_ptr, amplitude, layout, B, N, M, dtype, stream=0):
+    """`cache`: a LatentDescriptor, here and below."""
+    return _check(lib().spec_latent_append(
+        cache, table_ptr, table_width, starts_ptr, c_ptr, c_stride, r_ptr, r_stride, rows_ptr, pos_ptr,
+        freqs_ptr, float(amplitude), layout, B, N, M, dtype, stream))
+
+
+def spec_latent_workspace_size(B, N, H, C):
+    out = ctypes.c_size_t(0)
+    _check(lib().spec_latent_workspace_size(B, N, H, C, ctypes.byref(out)))
+    return out.value
+
+
+def spec_latent_attn(cache, table_ptr, table_width, lens_ptr, q_ptr, q_stride, mask_ptr, B, N, H, scale,
+                     out_ptr, out_lse_ptr, workspace_ptr, workspace_bytes, stream=0):
+    return _check(lib().spec_latent_attn(
+        cache, table_ptr, table_width, lens_ptr, q_ptr, q_stride, mask_ptr, B, N, H, float(scale), out_ptr,
+        out_lse_ptr, workspace_ptr, workspace_bytes, stream))
+
+
+def spec_verify_logprobs_workspace_size():
+    out = ctypes.c_size_t(0)
+    _check(lib().spec_verify_logprobs_workspace_size(ctypes.byref(out)))
+    return out.value
+
+
+def spec_verify_logprobs(target_ptr, tokens_ptr, rows_ptr, B, N, M, V, temperature, top, dtype,
+                         out_logprob_ptr, out_entropy_ptr, out_rank_ptr, out_top_ids_ptr,
+                         out_top_logprobs_ptr, workspace_ptr, workspace_bytes, stream=0):
+    return _check(lib().spec_verify_logprobs(
+        target_ptr, tokens_ptr, rows_ptr, B, N, M, V, float(temperature), top, dtype, out_logprob_ptr,
+        out_entropy_ptr, out_rank_ptr, out_top_ids_ptr, out_top_logprobs_ptr, workspace_ptr,
+        workspace_bytes, stream))
 
 
 def spec_verify_status_string(status):
@@ -550,6 +641,39 @@ def verify_tree_sample(target, draft, parents, node_tokens, uniforms, depth, tem
     return out_t, out_n, out_p, workspace
 
 
+LogProbs = collections.namedtuple("LogProbs", "logprob entropy rank top_ids top_logprobs")
+
+
+def logprobs(target, tokens, rows=None, temperature=1.0, top=0, entropy=True, rank=True,
+             workspace=None, stream=None):
+    """Tensor-level spec_verify_logprobs: target logits [B, N, V], emitted
+    tokens [B, M] int32 (verify_sample's out_tokens; -1: no entry) and, after
+    verify_tree, rows = its out_path.  Returns LogProbs: logprob, entropy [B, M]
+    fp32, rank [B, M] int32 (None where not asked for), and with top > 0 top_ids
+    int32 and top_logprobs fp32 [B, M, top].  Data errors (last_error) are in the
+    workspace: give one to read them."""
+    torch = _torch()
+    B, N, V = target.shape
+    M = tokens.shape[1]
+    _need(target, "target", target.dtype, (B, N, V))
+    _need(tokens, "tokens", torch.int32, (B, M))
+    if rows is not None:
+        _need(rows, "rows", torch.int32, (B, M))
+    dev = target.device
+    with _made_on(stream):
+        f = torch.empty((2 if entropy else 1, B, M), dtype=torch.float32, device=dev)
+        r = torch.empty((B, M), dtype=torch.int32, device=dev) if rank else None
+        ids = torch.empty((B, M, top), dtype=torch.int32, device=dev) if top else None
+        best = torch.empty((B, M, top), dtype=torch.float32, device=dev) if top else None
+        if workspace is None:
+            workspace = new_workspace(spec_verify_logprobs_workspace_size(), dev)
+    out = LogProbs(f[0], f[1] if entropy else None, r, ids, best)
+    spec_verify_logprobs(_ptr(target), _ptr(tokens), _ptr(rows), B, N, M, V, temperature, top,
+                         _dtype_code(target), *map(_ptr, out), _ptr(workspace), workspace.numel(),
+                         _stream(stream))
+    return out
+
+
 # ------------------------------------------- the target pass's cache and attention
 
 class KVCache(collections.namedtuple("KVCache", "k v k_exp v_exp")):
@@ -703,3 +827,179 @@ def attn_shared(q, cache, shared_table, shared_len, page_table, lens, mask=None,
                          % (shared_table.numel(), shared_len))
     return _attn(spec_attn_shared, q, cache, (_ptr(shared_table), shared_len), page_table, lens,
                  mask, pos, slopes, scale, cap, window, out, lse, workspace, stream)
+
+
+# ------------------------------------------------------------- rotary positions
+
+SCALINGS = {"plain": SPEC_ROPE_PLAIN, "linear": SPEC_ROPE_LINEAR, "turns": SPEC_ROPE_TURNS,
+            "index": SPEC_ROPE_INDEX}
+
+
+def rope_freqs(rot, base=10000.0, scaling="plain", factor=1.0, original=0, low=0.0, high=0.0,
+               device="cuda"):
+    """The frequencies of spec_rope_freqs, made once, as an int64 tensor [rot / 2]
+    on `device`.  scaling: "plain", "linear", "turns" or "index" (the header's
+    SPEC_ROPE_*)."""
+    torch = _torch()
+    if scaling not in SCALINGS:
+        raise ValueError("scaling must be one of %s, got %r" % (", ".join(SCALINGS), scaling))
+    host = torch.empty((max(int(rot), 2) // 2,), dtype=torch.int64)
+    spec_rope_freqs(rot, base, SCALINGS[scaling], factor, original, low, high, _ptr(host))
+    return host.to(device)
+
+
+def _turn(freqs, interleaved):
+    if freqs.dtype != _torch().int64 or freqs.dim() != 1 or not freqs.is_contiguous() or not freqs.is_cuda:
+        raise ValueError("freqs must be what rope_freqs returns, on the GPU")
+    return 2 * freqs.numel(), SPEC_ROPE_INTERLEAVED if interleaved else SPEC_ROPE_HALF
+
+
+def _turned(x, out, name, D, stream):
+    """out of a rotation of x [B, N, H, D] (None: a new tensor); both strides."""
+    torch = _torch()
+    H = x.shape[2]
+    step = _tokens(x, name, H, D, (torch.bfloat16, torch.float32))
+    if out is None:
+        with _made_on(stream):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape:
+        raise ValueError("out must have the shape of %s, got %s" % (name, tuple(out.shape)))
+    return out, step, _tokens(out, "out", H, D, (x.dtype,))
+
+
+def rope(x, freqs, pos, first=0, amplitude=1.0, interleaved=False, inverse=False, out=None,
+         stream=None):
+    """Tensor-level spec_rope: x [B, N, H, D] (bf16 or fp32) at position indices
+    pos [B, N] int32; the elements from `first` on that freqs (rope_freqs) covers
+    are turned.  Returns out (out=x: in place)."""
+    torch = _torch()
+    B, N, H, D = x.shape
+    rot, layout = _turn(freqs, interleaved)
+    _need(pos, "pos", torch.int32, (B, N))
+    out, step, out_step = _turned(x, out, "x", D, stream)
+    spec_rope(_ptr(x), step, _ptr(out), out_step, _ptr(freqs), rot, first, amplitude, layout,
+              1 if inverse else 0, _ptr(pos), B, N, H, D, _dtype_code(x), _stream(stream))
+    return out
+
+
+def kv_append_rope(cache, page_table, starts, k, v, freqs, q=None, rows=None, pos=None, amplitude=1.0,
+                   interleaved=False, out_q=None, stream=None):
+    """Tensor-level spec_kv_append_rope: kv_append with k turned to position
+    indices pos [B, N] int32 (None: cache positions) on the way, and with q
+    [B, N, Hq, D] the queries too.  Returns out_q, or None without q."""
+    torch = _torch()
+    c = cache.descriptor
+    B, N = k.shape[:2]
+    rot, layout = _turn(freqs, interleaved)
+    step = _tokens(k, "k", c.Hkv, c.D, (torch.bfloat16, torch.float32))
+    if _tokens(v, "v", c.Hkv, c.D, (k.dtype,)) != step or v.shape != k.shape:
+        raise ValueError("k and v must have one shape and token stride")
+    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
+    _need(starts, "starts", torch.int32, (B,))
+    M = N
+    if rows is not None:
+        M = rows.shape[1]
+        _need(rows, "rows", torch.int32, (B, M))
+    if pos is not None:
+        _need(pos, "pos", torch.int32, (B, N))
+    q_step = out_step = Hq = 0
+    if q is not None:
+        if q.dtype != k.dtype or q.shape[:2] != (B, N):
+            raise ValueError("q must be of k's type and tokens")
+        Hq = q.shape[2]
+        out_q, q_step, out_step = _turned(q, out_q, "q", c.D, stream)
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    spec_kv_append_rope(c, _ptr(page_table), page_table.shape[1], _ptr(starts), _ptr(k), _ptr(v), step,
+                        _ptr(rows), _ptr(pos), _ptr(freqs), rot, amplitude, layout, _ptr(q), q_step,
+                        _ptr(out_q), out_step, B, N, M, Hq, _dtype_code(k), _stream(stream))
+    return out_q
+
+
+# ---------------------------------------------------------------- a latent cache
+
+class LatentCache(collections.namedtuple("LatentCache", "data R")):
+    """A paged latent cache: data [num_pages, page, C + R] bf16, the last R
+    elements of a row the rotary part.  Checked once, here; the calls pass its C
+    descriptor."""
+
+    def __new__(cls, data, R=64):
+        self = super().__new__(cls, data, R)
+        n, page, width = data.shape
+        _need(data, "data", _torch().bfloat16, (n, page, width))
+        self.descriptor = LatentDescriptor(_ptr(data), n, page, width - R, R)
+        return self
+
+    @classmethod
+    def _make(cls, fields):  # _replace comes here too
+        return cls(*fields)
+
+    def __reduce__(self):  # a copy's descriptor is of the copy's tensor
+        return type(self), tuple(self)
+
+
+def new_latent_cache(num_pages, page, C, device, R=64):
+    """An empty (zeroed) latent cache of num_pages pages."""
+    torch = _torch()
+    return LatentCache(torch.zeros((num_pages, page, C + R), dtype=torch.bfloat16, device=device), R)
+
+
+def latent_append(cache, page_table, starts, c, r, freqs=None, rows=None, pos=None, amplitude=1.0,
+                  interleaved=False, stream=None):
+    """Tensor-level spec_latent_append: tokens c [B, N, C] and r [B, N, R] (fp32 or
+    bf16; parts of one projection, or tensors of their own) to positions
+    starts[b] + t of a LatentCache, r turned to pos [B, N] (None: the cache
+    positions) where freqs (rope_freqs(R)) are given; rows as in kv_append."""
+    torch = _torch()
+    d = cache.descriptor
+    B, N = c.shape[:2]
+    types = (torch.bfloat16, torch.float32)
+    c_step = _tokens(c.unsqueeze(2), "c", 1, d.C, types)
+    r_step = _tokens(r.unsqueeze(2), "r", 1, d.R, (c.dtype,))
+    if r.shape[:2] != (B, N):
+        raise ValueError("c and r must hold the same tokens")
+    rot, layout = (d.R, SPEC_ROPE_HALF) if freqs is None else _turn(freqs, interleaved)
+    if rot != d.R:
+        raise ValueError("freqs are of %d elements, the cache's rotary part has %d" % (rot, d.R))
+    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
+    _need(starts, "starts", torch.int32, (B,))
+    M = N
+    if rows is not None:
+        M = rows.shape[1]
+        _need(rows, "rows", torch.int32, (B, M))
+    if pos is not None:
+        _need(pos, "pos", torch.int32, (B, N))
+    spec_latent_append(d, _ptr(page_table), page_table.shape[1], _ptr(starts), _ptr(c), c_step, _ptr(r),
+                       r_step, _ptr(rows), _ptr(pos), _ptr(freqs), amplitude, layout, B, N, M,
+                       _dtype_code(c), _stream(stream))
+
+
+def latent_attn(q, cache, page_table, lens, scale, mask=None, out=None, lse=None, workspace=None,
+                stream=None):
+    """Tensor-level spec_latent_attn: new tokens q [B, N, H, C + R] bf16 (each
+    head's query with its key projection multiplied in, then the rotary part)
+    over a LatentCache; mask as tree_mask returns it (None: a chain).  Returns out
+    [B, N, H, C], or (out, lse) with lse=True or a tensor.  With ``stream``, what
+    the call allocates belongs to that stream.  Data errors (last_error) are in
+    the workspace: give one to read them."""
+    torch = _torch()
+    d = cache.descriptor
+    B, N, H = q.shape[:3]
+    step = _tokens(q, "q", H, d.C + d.R, (torch.bfloat16,))
+    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
+    _need(lens, "lens", torch.int32, (B,))
+    if mask is not None:
+        _need(mask, "mask", torch.uint8, (B, N, N))
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((B, N, H, d.C), dtype=q.dtype, device=q.device)
+        if lse is True:
+            lse = torch.empty((B, N, H), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = new_workspace(spec_latent_workspace_size(B, N, H, d.C), q.device)
+    _need(out, "out", q.dtype, (B, N, H, d.C))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, N, H))
+    spec_latent_attn(d, _ptr(page_table), page_table.shape[1], _ptr(lens), _ptr(q), step, _ptr(mask), B, N,
+                     H, scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
+    return out if lse is None else (out, lse)

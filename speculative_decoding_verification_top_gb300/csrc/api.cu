@@ -2,6 +2,7 @@
 // argument validation, workspace layout and kernel dispatch.  No compute.
 
 #include "common.cuh"
+#include "logprobs.cuh"
 #include "spec_attn.h"
 
 #define SPEC_EXPORT extern "C" __attribute__((visibility("default")))
@@ -514,6 +515,50 @@ SPEC_EXPORT int spec_verify_acceptance(const void *target_logits, const void *dr
     a.beta = out_beta;
     a.tv = out_tv;
     return launch_accept(a, dtype, masked, reinterpret_cast<cudaStream_t>(stream));
+}
+
+SPEC_EXPORT int spec_verify_logprobs_workspace_size(size_t *bytes) {
+    if (!bytes) return SPEC_ERR_NULL;
+    *bytes = kAlign;
+    return SPEC_OK;
+}
+
+SPEC_EXPORT int spec_verify_logprobs(const void *target_logits, const int32_t *tokens, const int32_t *rows, int B, int N,
+                                     int M, int V, float temperature, int top, int dtype, float *out_logprob,
+                                     float *out_entropy, int32_t *out_rank, int32_t *out_top_ids, float *out_top_logprobs,
+                                     void *workspace, size_t workspace_bytes, spec_stream_t stream) {
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+    if (B < 0 || N < 1 || M < 0 || V < 1 || V > SPEC_MAX_V || top < 0 || top > SPEC_MAX_TOP || top > V ||
+        (!rows && M > N) || static_cast<long long>(B) * M > INT_MAX / 64 || static_cast<long long>(B) * N > INT_MAX)
+        return SPEC_ERR_SHAPE;
+    if (!std::isfinite(temperature) || temperature <= 0.0f || !std::isfinite(1.4426950408889634f / temperature))
+        return SPEC_ERR_PARAM;
+    if (B == 0 || M == 0) return SPEC_OK;
+    if (!target_logits || !tokens || !out_logprob || (top > 0 && (!out_top_ids || !out_top_logprobs))) return SPEC_ERR_NULL;
+    auto off = [](const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; };
+    if (off(target_logits, dtype == SPEC_F32 ? 4 : 2) || off(tokens, 4) || off(rows, 4) || off(out_logprob, 4) ||
+        off(out_entropy, 4) || off(out_rank, 4) || off(out_top_ids, 4) || off(out_top_logprobs, 4))
+        return SPEC_ERR_ALIGN;
+    if (!workspace || workspace_bytes < kAlign) return SPEC_ERR_WORKSPACE;
+    if (off(workspace, 4)) return SPEC_ERR_ALIGN;
+    LogprobArgs a = {};
+    a.logits = target_logits;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.B = B;
+    a.N = N;
+    a.M = M;
+    a.V = V;
+    a.top = top;
+    a.c = 1.4426950408889634f / temperature;
+    a.inv_t = 1.0f / temperature;
+    a.logprob = out_logprob;
+    a.entropy = out_entropy;
+    a.rank = out_rank;
+    a.top_ids = out_top_ids;
+    a.top_logprobs = out_top_logprobs;
+    a.err = static_cast<uint32_t *>(workspace);
+    return launch_logprobs(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 SPEC_EXPORT const char *spec_verify_status_string(int status) {
