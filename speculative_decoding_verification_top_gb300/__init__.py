@@ -45,7 +45,8 @@ SOURCES = [os.path.join(CSRC, f)
                      "rope.cu", "latent.cu", "target_api.cu", "logprobs.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh", "attn.cuh",
                                              "attn_plan.cuh", "tensor.cuh", "checks.cuh",
-                                             "kvrows.cuh", "target.cuh", "logprobs.cuh")]
+                                             "kvrows.cuh", "target.cuh", "logprobs.cuh", "util.cuh",
+                                             "latent_plan.cuh")]
 INCLUDE = os.path.join(_ROOT, "include")
 HEADER = os.path.join(INCLUDE, "spec_verify.h")
 ATTN_HEADER = os.path.join(INCLUDE, "spec_attn.h")

@@ -223,23 +223,6 @@ size_t carve_plan(Plan *p, int D, bool e4m3, char *work) {
     return off;
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static EncodeFn fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeFn>(f);
-    }();
-    return fn;
-}
-
 // The cache as [num_pages * Hkv][page][D]; a box is one page's head, in
 // columns of one shared-memory row.
 bool make_map(CUtensorMap *map, void *data, const CacheView &c) {
@@ -270,17 +253,6 @@ int launch_join(const KernelArgs &ka, int grid, cudaStream_t st) {
 }
 
 }  // namespace
-
-// The current device's multiprocessors, asked for once a device.
-static int multiprocessors() {
-    static int known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if ((n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
-    return n;
-}
 
 size_t attn_work_bytes(int B, int N, int Hq, int Hkv, int D) {
     Plan p = {};

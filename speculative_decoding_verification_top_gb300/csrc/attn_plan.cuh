@@ -5,6 +5,7 @@
 
 #include "attn.cuh"
 #include "tensor.cuh"
+#include "util.cuh"
 
 namespace specv {
 
@@ -13,14 +14,6 @@ constexpr int kGroupRows = 128;   // query rows a softmax group of the wide kern
 constexpr int kFewRows = 64;      // units of at most this many rows go to the few-row kernel
 constexpr int kAttnThreads = 384;
 constexpr int kMaxSlots = 16;
-constexpr int kMaxGrid = 152;
-constexpr int kSmemMax = 232448;  // bytes a CTA may have
-constexpr float kLog2e = 1.4426950408889634f;
-
-// Growth of t over the reference maximum that is let stand: a weight stays
-// under 2^8.
-constexpr float kSlack = 8.0f;
-
 // The units of one kind (the prefix's, or the sequences' own).
 struct Units {
     int rows;             // query rows a (sequence, head); of all sequences for the prefix
@@ -321,12 +314,6 @@ __device__ __forceinline__ bool sees_whole(const AttnArgs &a, const Segment &g, 
     return a.window == 0 || static_cast<long long>(last_pos) - (g.shared ? 0 : a.shared_len) - j0 < a.window;
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -336,47 +323,6 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
 __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-
-// Two fp32 operations an instruction (sm_100 and later).
-struct F2 {
-    unsigned long long v;
-};
-
-__device__ __forceinline__ F2 pair_of(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ float2 parts_of(F2 x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
-    return r;
-}
-
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // cap tanh(y) log2 e of n scores in place, capl = cap log2 e.  tanh(y) = 1 - 2 /
@@ -667,34 +613,5 @@ struct Loader {
 
 int launch_wide(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
 int launch_few(KernelArgs &ka, int grid, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
-
-// A launch that may start before the kernel ahead of it in the stream has ended
-// (each kernel here waits for that itself before it touches memory).
-template <typename... Params, typename... Args>
-bool launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
-}
-
-// Raises the kernel's shared-memory limit, once per kernel and device (`done`
-// is the kernel's own).
-template <typename Kernel>
-bool allow_smem(Kernel kernel, int bytes, int (&done)[64]) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    if (__atomic_load_n(&done[dev], __ATOMIC_RELAXED)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    __atomic_store_n(&done[dev], 1, __ATOMIC_RELAXED);
-    return true;
-}
 
 }  // namespace specv

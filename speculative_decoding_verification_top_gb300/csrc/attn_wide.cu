@@ -87,11 +87,6 @@ struct Seen {
     int pos[4];
 };
 
-// The first n of 32 bits, n clamped to 0..32.
-__device__ __forceinline__ uint32_t first_bits(int n) {
-    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
 // Loads that are not taken leave `otherwise`; no branch, so that many are in
 // flight together.
 __device__ __forceinline__ uint32_t byte_if(bool on, const uint8_t *at, uint32_t otherwise) {

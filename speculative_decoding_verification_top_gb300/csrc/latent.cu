@@ -3,79 +3,747 @@
 // For one query row (token i, head h) over the positions j it sees:
 //   t_j = log2(e) scale q . (c_j, r_j);  m = max t_j;  l = sum 2^(t_j - m);
 //   out = sum 2^(t_j - m) c_j / l.
+// All heads read the same rows (c_j, r_j), and c_j is key and value at once: a
+// tile of 64 positions is loaded once for both products.
 //
-// A warp takes a row and goes through its positions one at a time.
+// A unit is 64 of a sequence's N H query rows; its keys are up to 72 KB a tile and
+// its accumulator 64 x C in fp32.  The products are laid out so that both fit:
+//   S = Q K^T     M = 64 rows, N = 64 positions; Q in shared memory, for C = 512
+//                 its first 256 columns in TMEM, which leaves room for 2.5 tiles
+//   O^T += C^T P^T   M = 128 elements of the latent, N = 64 rows: the tile's own
+//                 bytes are the first operand, its positions their rows, and an
+//                 accumulator of 512 x 64 is 256 columns of TMEM
+// latent_kernel      persistent, one CTA per SM; its share of the tiles segment by
+//                    segment
+//   warps 0-3        softmax, a thread per row and half a tile's positions (an
+//                    accumulator of 64 rows fills 16 of a warp's 32 lanes; the
+//                    load gives the other lanes its second half); the query tile;
+//                    the results
+//   warp 4           loads tiles page by page (TMA), in slots of 128 columns
+//   warp 5           issues the products, S a tile ahead of O
+// latent_join_kernel joins the partial results of units cut between CTAs
+//
+// The work: a sequence's units are taken `width` at a time, by as many CTAs that go
+// through its tiles together, so that a tile comes from memory once for them.  All
+// (sequence, band of `width` units) lie on one line, a cost of one a tile and
+// `start` for beginning; it is cut into equal shares, one per group of CTAs.  A
+// unit that one share holds whole is written out at once, the others' parts (m, l,
+// O) are joined in the line's order: results do not depend on timing.
 
-#include "target.cuh"
+#include "latent_plan.cuh"
 
 namespace specv {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+struct Barriers {
+    unsigned long long full[kMaxSlots], empty[kMaxSlots];     // the latent's slots
+    unsigned long long r_full[kMaxRopes], r_empty[kMaxRopes]; // the rotary part's
+    unsigned long long q_full, s_full[2], p_full, pv_done, drained;
+};
+
+struct Shared {
+    Barriers bar;
+    Begin begin;
+    uint32_t tmem;
+    int dead;            // a wait ran out: everyone leaves
+    int quit;            // the vote at which the softmax warps leave, or 0
+    int fail[kAhead];    // per segment (mod kAhead): a page id out of range
+    int odd;             // of the segment: cleaned elements that were not finite
+    float row[kRows];    // factors of the rows: of a rescaling, or 1 / l
+};
 
 template <int C>
-__global__ void __launch_bounds__(kThreads) latent_kernel(const LatentArgs a) {
-    constexpr int kW = C + 64, kPairs = kW / 64, kOut = C / 64;  // element pairs a lane
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= a.B * a.N * a.H) return;
-    const int token = row / a.H, b = token / a.N, n = token - b * a.N, len = a.lens[b];
-    uint32_t *out = reinterpret_cast<uint32_t *>(a.out + static_cast<long long>(row) * C);
-    bool bad = len < 0 || len > a.width << a.c.page_shift;
-    float2 q[kPairs], o[kOut] = {};
-    const __nv_bfloat162 *pq =
-        reinterpret_cast<const __nv_bfloat162 *>(a.q + token * a.q_stride + static_cast<long long>(row - token * a.H) * kW);
-    for (int i = 0; i < kPairs; ++i) q[i] = __bfloat1622float2(pq[i * 32 + lane]);
-    const float mul = a.scale * kLog2e;
+struct Layout {
+    static constexpr int kPairs = C / 128;                       // slots a tile, and accumulators of 128 elements
+    static constexpr int kInTmem = C == 512 ? 4 : 0;             // 64-column blocks of Q in TMEM
+    static constexpr int kInSmem = C / 64 + 1 - kInTmem;         // and in shared memory, the rotary one last
+    static constexpr int kRopes = C == 512 ? 2 : C == 256 ? 5 : 8;
+    static constexpr int kFixed = (kInSmem + 1 + kRopes) * kBlock + static_cast<int>((sizeof(Shared) + 127) / 128 * 128);
+    static constexpr int kRoom = (kSmemMax - kFixed) / (2 * kBlock);
+    static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
+    static constexpr int kBytes = kFixed + kSlots * 2 * kBlock;
+    // TMEM columns: O^T from 0, two S, Q
+    static constexpr int kS = 256, kQ = 384;
+    static_assert(kSlots >= 2 * kPairs && kRopes >= 2 && kRopes <= kMaxRopes, "S of a tile is made before O of the one before");
+};
+
+constexpr int kVoteBarrier = 1, kRowBarrier = 2;  // hardware barriers of the softmax warps
+constexpr int kSoftmax = 128;                     // their threads
+
+__device__ __forceinline__ void meet(int id) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(kSoftmax) : "memory"); }
+
+// 32 columns of 16 lanes for lanes 0-15, and the 32 columns from `kSecond` on of
+// the same 16 for lanes 16-31.
+template <int kSecond>
+__device__ __forceinline__ void tmem_load_halves(uint32_t addr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32], %33;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr), "n"(kSecond)
+        : "memory");
+}
+
+template <int kSecond>
+__device__ __forceinline__ void tmem_store_halves(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], %33, "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "n"(kSecond)
+        : "memory");
+}
+
+// Instruction descriptor with M = 64 rows (tensor.cuh's has 128).
+__host__ __device__ constexpr uint32_t mma_desc64(int n) {
+    return (mma_desc(false, n, false, false) & ~(0x1fu << 24)) | (64u >> 4) << 24;
+}
+
+// Where the query row `row` of a segment lies; null past its rows.
+__device__ __forceinline__ const uint4 *query_row(const LatentArgs &a, const Segment &g, int row) {
+    if (row >= g.rows) return nullptr;
+    const int r = g.row0 + row, n = r / a.H;
+    return reinterpret_cast<const uint4 *>(a.q + (static_cast<long long>(g.b) * a.N + n) * a.q_stride +
+                                           static_cast<long long>(r - n * a.H) * (a.c.C + a.c.R));
+}
+
+// The segment's query tile, zeros past its rows; the scale's sign goes into it.
+template <int C>
+__device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment &g, uint8_t *tile, uint32_t tmem) {
+    using L = Layout<C>;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    constexpr int kParts = L::kInSmem * 8;  // 16-byte parts of a row
+#pragma unroll 4
+    for (int i = tid; i < kRows * kParts; i += kSoftmax) {
+        const int row = i / kParts, part = i - row * kParts;
+        const uint4 *q = query_row(a, g, row);
+        uint4 u = q ? __ldg(q + L::kInTmem * 8 + part) : zero;
+        u = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
+        *reinterpret_cast<uint4 *>(tile + part / 8 * kBlock + swizzled<128>(row, part % 8 * 16)) = u;
+    }
+    if constexpr (L::kInTmem > 0) {
+        // Lanes 0-15 hold a row's columns from 0 on (two elements a column), 16-31 from 64.
+        const uint4 *q = query_row(a, g, warp * 16 + (lane & 15));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 u = q ? __ldg(q + (lane >> 4) * 16 + k * 8 + i) : zero;
+                w[4 * i] = u.x ^ flip;
+                w[4 * i + 1] = u.y ^ flip;
+                w[4 * i + 2] = u.z ^ flip;
+                w[4 * i + 3] = u.w ^ flip;
+            }
+            tmem_store_halves<64>(tmem + L::kQ + (static_cast<uint32_t>(warp) << 21) + k * 32, w);
+        }
+        tmem_store_wait();
+    }
+    fence_async_proxy();
+    fence_before_sync();
+}
+
+// The columns of 32 from position j on that token n of sequence b sees.
+__device__ __forceinline__ uint32_t seen_columns(const LatentArgs &a, const Segment &g, int n, bool has, int j) {
+    const int first = g.len - a.N;
+    uint32_t s = first_bits(g.len - j);
+    if (!has) return 0;
+    if (!a.mask) return s & first_bits(first + n + 1 - j);
+    const uint8_t *at = a.mask + (static_cast<long long>(g.b) * a.N + n) * a.N + (j - first);
+    uint32_t m[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        m[i] = 1;
+        if (j + i >= first && j + i < g.len) m[i] = at[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (m[i] == 0) s &= ~(1u << i);
+    return s;
+}
+
+// Clears, in a tile that some rows do not see whole, the positions past the end
+// and the elements that are not finite, so that neither reaches a row through
+// 0 * inf; whether an element of a held position was not finite.
+template <int C>
+__device__ __forceinline__ bool clean_tile(uint8_t *slots, uint32_t slot0, int held) {
+    using L = Layout<C>;
+    bool odd = false;
+    for (int i = threadIdx.x; i < kTile * (C / 8); i += kSoftmax) {
+        const int row = i / (C / 8), part = i - row * (C / 8);
+        const uint32_t slot = (slot0 + part / 16) % L::kSlots;
+        uint4 *at = reinterpret_cast<uint4 *>(slots + slot * 2 * kBlock + part / 8 % 2 * kBlock + swizzled<128>(row, part % 8 * 16));
+        if (row >= held) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 u = *at;
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        bool here = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t keep = ((w[k] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                                  ((w[k] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+            here |= keep != 0xffffffffu;
+            w[k] &= keep;
+        }
+        if (here) *at = make_uint4(w[0], w[1], w[2], w[3]);
+        odd |= here;
+    }
+    return odd;
+}
+
+// What clean_tile took from element d of row `row`'s result: the elements that are
+// not finite of the positions it sees in the segment's cleaned tiles.
+__device__ __noinline__ float odd_values(const LatentArgs &a, const Segment g, int row, int d) {
+    float y = 0.0f;
+    const int n = (g.row0 + row) / a.H, first = g.len - a.N;
+    for (int t = g.t0; t < g.t1; ++t) {
+        if (sees_whole(a, g, t * kTile)) continue;
+        for (int j = t * kTile; j < min(g.len, (t + 1) * kTile); ++j) {
+            const int c = j - first;
+            if (c >= 0 && (a.mask ? a.mask[(static_cast<long long>(g.b) * a.N + n) * a.N + c] == 0 : c > n)) continue;
+            const int page = a.table[static_cast<long long>(g.b) * a.width + (j >> a.c.page_shift)];
+            if (page < 0 || page >= a.c.num_pages) continue;
+            const long long at = (static_cast<long long>(page) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
+            const float x = __bfloat162float(a.c.data[at * (a.c.C + a.c.R) + d]);
+            if (!isfinite(x)) y += x;
+        }
+    }
+    return y;
+}
+
+template <int C>
+__global__ void __launch_bounds__(kLatentThreads, 1)
+    latent_kernel(const __grid_constant__ LatentKernelArgs ka, const __grid_constant__ CUtensorMap map) {
+    using L = Layout<C>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const LatentArgs &a = ka.a;
+    const LatentPlan &p = ka.p;
+    uint8_t *qt = smem, *pt = qt + L::kInSmem * kBlock, *ropes = pt + kBlock, *slots = ropes + L::kRopes * kBlock;
+    Shared &sh = *reinterpret_cast<Shared *>(slots + L::kSlots * 2 * kBlock);
+    Barriers &bar = sh.bar;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < L::kSlots; ++i) {
+            bar_init(smem_addr(&bar.full[i]), 1);
+            bar_init(smem_addr(&bar.empty[i]), 1);
+        }
+        for (int i = 0; i < L::kRopes; ++i) {
+            bar_init(smem_addr(&bar.r_full[i]), 1);
+            bar_init(smem_addr(&bar.r_empty[i]), 1);
+        }
+        bar_init(smem_addr(&bar.q_full), 4);
+        bar_init(smem_addr(&bar.s_full[0]), 1);
+        bar_init(smem_addr(&bar.s_full[1]), 1);
+        bar_init(smem_addr(&bar.p_full), 4);
+        bar_init(smem_addr(&bar.pv_done), 1);
+        bar_init(smem_addr(&bar.drained), 1);
+        sh.dead = sh.quit = sh.odd = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_proxy();
+    }
+    if (warp == 5) tmem_alloc(smem_addr(&sh.tmem), 512);
+    // Up to here this may run beside the kernel before it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    long long from, to;
+    find_begin(p, sh.begin, &from, &to);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    volatile int *dead = &sh.dead;
+    Walk walk(p, from, to, sh.begin);
+    Segment g;
+
+    if (warp == 4) {
+        // ---- loads: of each tile the rotary part, then the latent
+        const int box = min(kTile, 1 << a.c.page_shift), boxes = kTile / box;  // positions of a copy, copies of a tile
+        uint32_t slot = 0, phase = 1, rope = 0, r_phase = 1, n = 0, rn = 0, seg = 0;
+        bool live = true;
+        for (; live && walk.next(&g); ++seg) {
+            if (lane == 0) sh.fail[seg % kAhead] = 0;
+            __syncwarp();
+            const int32_t *table = a.table + static_cast<long long>(g.b) * a.width;
+            auto page_at = [&](int t) {  // this lane's page of tile t; -2: none
+                const int j = t * kTile + lane * box;
+                return t < g.t1 && lane < boxes && j < g.len ? table[j >> a.c.page_shift] : -2;
+            };
+            int next = page_at(g.t0);
+            for (int t = g.t0; live && t < g.t1; ++t) {
+                int id = next;
+                next = page_at(t + 1);
+                if (id != -2 && (id < 0 || id >= a.c.num_pages)) {
+                    sh.fail[seg % kAhead] = 1;
+                    atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
+                    id = -1;
+                }
+                const bool here = id >= 0;
+                const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, here)) * box) * 128u;
+                const int y = (t * kTile + lane * box) & ((1 << a.c.page_shift) - 1);
+                for (int i = -1; i < L::kPairs; ++i) {
+                    const uint32_t full = i < 0 ? smem_addr(&bar.r_full[rope]) : smem_addr(&bar.full[slot]);
+                    live = i < 0 ? bar_wait(smem_addr(&bar.r_empty[rope]), r_phase, dead)
+                                 : bar_wait(smem_addr(&bar.empty[slot]), phase, dead);
+                    live = __all_sync(0xffffffffu, live);
+                    if (!live) break;
+                    if (lane == 0) bar_arrive_tx(full, i < 0 ? bytes : 2 * bytes);
+                    __syncwarp();
+                    const uint32_t dst = smem_addr(i < 0 ? ropes + rope * kBlock : slots + slot * 2 * kBlock) + lane * box * 128;
+                    if (here) {
+                        tma_load(dst, &map, full, i < 0 ? C : i * 128, y, id);
+                        if (i >= 0) tma_load(dst + kBlock, &map, full, i * 128 + 64, y, id);
+                    }
+                    if (i < 0) {
+                        ++rn;
+                        if (++rope == L::kRopes) rope = 0, r_phase ^= 1;
+                    } else {
+                        ++n;
+                        if (++slot == L::kSlots) slot = 0, phase ^= 1;
+                    }
+                }
+            }
+        }
+        if (!live) {  // the copies in flight land before the CTA's memory goes
+            for (uint32_t i = n > L::kSlots ? n - L::kSlots : 0; i < n; ++i)
+                bar_drain(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
+            for (uint32_t i = rn > L::kRopes ? rn - L::kRopes : 0; i < rn; ++i)
+                bar_drain(smem_addr(&bar.r_full[i % L::kRopes]), (i / L::kRopes) & 1);
+        }
+    } else if (warp == 5) {
+        // ---- products
+        if (elect_one()) {
+            constexpr uint32_t kQk = mma_desc64(kTile), kPv = mma_desc(false, kRows, true, false), kHi = kMatrixHi<128>;
+            const uint32_t q0 = matrix_lo(smem_addr(qt), 0), r0 = matrix_lo(smem_addr(ropes), 0);
+            const uint32_t k0 = matrix_lo(smem_addr(slots), 0), v0 = matrix_lo(smem_addr(slots), kBlock);
+            const uint32_t p0 = matrix_lo(smem_addr(pt), 0);
+            uint32_t slot = 0, phase = 0, rope = 0, r_phase = 0, vslot = 0, segs = 0, pn = 0, sn = 0;
+            bool live = true;
+            // S of the next tile, rotary part first
+            auto scores = [&] {
+                const uint32_t d = tmem + L::kS + (sn & 1) * kTile;
+                if (!(live = bar_wait(smem_addr(&bar.r_full[rope]), r_phase, dead))) return;
+                fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss<false>(d, q0 + (((L::kInSmem - 1) * kBlock + k * 32) >> 4), kHi, r0 + ((rope * kBlock + k * 32) >> 4), kHi, kQk,
+                                  k > 0);
+                mma_commit(smem_addr(&bar.r_empty[rope]));
+                if (++rope == L::kRopes) rope = 0, r_phase ^= 1;
+#pragma unroll
+                for (int i = 0; i < L::kPairs; ++i) {
+                    if (!(live = bar_wait(smem_addr(&bar.full[slot]), phase, dead))) return;
+                    fence_after_sync();
+                    const uint32_t b = k0 + (slot * 2 * kBlock >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int block = 2 * i + k / 4;
+                        const uint32_t bk = b + ((k / 4 * kBlock + k % 4 * 32) >> 4);
+                        if (block < L::kInTmem)
+                            mma_ts(d, tmem + L::kQ + block * 32 + k % 4 * 8, bk, kHi, kQk, true);
+                        else
+                            mma_ss<false>(d, q0 + (((block - L::kInTmem) * kBlock + k % 4 * 32) >> 4), kHi, bk, kHi, kQk, true);
+                    }
+                    if (++slot == L::kSlots) slot = 0, phase ^= 1;
+                }
+                mma_commit(smem_addr(&bar.s_full[sn++ & 1]));
+            };
+            while (live && walk.next(&g)) {
+                live = bar_wait(smem_addr(&bar.q_full), segs++ & 1, dead);
+                fence_after_sync();
+                if (live) scores();
+                for (int t = g.t0; live && t < g.t1; ++t) {
+                    if (t + 1 < g.t1) scores();
+                    if (!live || !(live = bar_wait(smem_addr(&bar.p_full), pn++ & 1, dead))) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < L::kPairs; ++i) {
+                        const uint32_t v = v0 + (vslot * 2 * kBlock >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss<false>(tmem + i * kRows, v + (k * 16 * 128 >> 4), kHi, p0 + (k * 32 >> 4), kHi, kPv, t > g.t0 || k > 0);
+                        mma_commit(smem_addr(&bar.empty[vslot]));
+                        if (++vslot == L::kSlots) vslot = 0;
+                    }
+                    mma_commit(smem_addr(&bar.pv_done));
+                }
+            }
+            if (!live) {  // products in flight end before TMEM is freed
+                mma_commit(smem_addr(&bar.drained));
+                bar_drain(smem_addr(&bar.drained), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ---- softmax
+        const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+        const int row = warp * 16 + (lane & 15), half = lane >> 4;
+        const float mul = fabsf(a.scale) * kLog2e;
+        uint32_t n = 0, seg = 0;  // tiles and segments so far
+        int votes = 0;
+        bool ok = true, live = true;
+        if (tid == 0) p.head[blockIdx.x].parts = 0;
+        // A warp whose wait ran out says so, and all leave at its next vote (a vote's
+        // own wait has no bound: they must come to it together).
+        auto waited = [&](uint32_t b, uint32_t parity) {
+            ok = ok && bar_wait(b, parity, dead);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                *reinterpret_cast<volatile int *>(&sh.quit) = votes + 1;
+            }
+        };
+        auto vote = [&](bool x) {
+            ++votes;
+            return any_of(kVoteBarrier, kSoftmax, x || !ok);
+        };
+        auto leaving = [&] {
+            const int quit = *reinterpret_cast<volatile int *>(&sh.quit);
+            return quit != 0 && quit <= votes;
+        };
+        for (; live && walk.next(&g); ++seg) {
+            stage_queries<C>(a, g, qt, tmem);
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
+            const bool has = row < g.rows;
+            const int token = has ? (g.row0 + row) / a.H : 0;
+            float m = kNegInf, l = 0.0f;
+            for (int t = g.t0; t < g.t1; ++t, ++n) {
+                const int j0 = t * kTile + half * 32;
+                const bool whole = sees_whole(a, g, t * kTile);
+                uint32_t seen = ~0u;
+                if (!whole) seen = seen_columns(a, g, token, has, j0);
+                waited(smem_addr(&bar.s_full[n & 1]), (n >> 1) & 1);
+                fence_after_sync();
+                float v[32];
+                tmem_load_halves<32>(tmem + lanes + L::kS + (n & 1) * kTile, v);
+                tmem_load_wait();
+                float top[2] = {kNegInf, kNegInf};
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        top[0] = max3(top[0], v[c], v[c + 1]);
+                        top[1] = max3(top[1], v[c + 2], v[c + 3]);
+                    }
+                    top[0] = fmaxf(top[0], top[1]) * mul;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float y = v[c] * mul;
+                        if (seen >> c & 1u) top[c & 1] = fmaxf(top[c & 1], y);
+                    }
+                    top[0] = fmaxf(top[0], top[1]);
+                }
+                const float most = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], 16));
+                const bool up = most > m + kSlack;
+                const uint32_t before = smem_addr(&bar.pv_done), before_phase = (n - 1) & 1;
+                bool free = t == g.t0;  // the tile before is multiplied
+                if (vote(up)) {
+                    if (leaving()) {
+                        live = false;
+                        break;
+                    }
+                    // Some row's reference moves up: its sum and its column of O^T are rescaled.
+                    const float keep = up ? ex2(m - most) : 1.0f;
+                    if (up) m = most;
+                    l *= keep;
+                    if (!free) {
+                        waited(before, before_phase);
+                        free = true;
+                        fence_after_sync();
+                        if (half == 0) sh.row[row] = keep;
+                        meet(kRowBarrier);
+#pragma unroll 1
+                        for (int c = 0; c < L::kPairs * kRows; c += 32) {
+                            float o[32];
+                            tmem_load32(tmem + lanes + c, o);
+                            tmem_load_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] *= sh.row[c % kRows + k];
+                            tmem_store32(tmem + lanes + c, reinterpret_cast<const uint32_t *>(o));
+                        }
+                        tmem_store_wait();
+                        meet(kRowBarrier);
+                    }
+                }
+                const float ref = m == kNegInf ? 0.0f : m;
+                uint32_t w[16];
+                {
+                    F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
+                    const F2 mul2 = pair_of(mul, mul), ref2 = pair_of(-ref, -ref);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float2 y = parts_of(fma2(pair_of(v[c], v[c + 1]), mul2, ref2));
+                        if (!whole) {
+                            y.x = seen >> c & 1u ? y.x : kNegInf;
+                            y.y = seen >> (c + 1) & 1u ? y.y : kNegInf;
+                        }
+                        y = make_float2(ex2(y.x), ex2(y.y));
+                        sum[c / 2 & 1] = add2(sum[c / 2 & 1], pair_of(y.x, y.y));
+                        w[c / 2] = bf16_pair(y.x, y.y);
+                    }
+                    const float2 s = parts_of(add2(sum[0], sum[1]));
+                    l += s.x + s.y;
+                }
+                if (!free) waited(before, before_phase);
+                if (!whole && ok) {  // the products of S are done with the tile
+                    const uint32_t fill = n * L::kPairs;
+                    for (uint32_t i = fill; i < fill + L::kPairs; ++i)
+                        waited(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
+                    if (clean_tile<C>(slots, fill % L::kSlots, g.len - t * kTile)) sh.odd = 1;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(pt + swizzled<128>(row, half * 64 + i * 16)) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                fence_async_proxy();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.p_full));
+            }
+            if (!live) break;
+            waited(smem_addr(&bar.pv_done), (n - 1) & 1);
+            fence_after_sync();
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            // All warps are past the segment's tiles: what they and the loads noted is there.
+            if (vote(false) && leaving()) {
+                live = false;
+                break;
+            }
+            const bool failed = *reinterpret_cast<volatile int *>(&sh.fail[seg % kAhead]) != 0;
+            const bool odd = *reinterpret_cast<volatile int *>(&sh.odd) != 0;
+            if (failed) l = NAN;
+            const bool alone = g.t0 == 0 && g.t1 == g.tiles;
+            const int part = 2 * static_cast<int>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
+            if (half == 0) {
+                sh.row[row] = !alone ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const long long at = static_cast<long long>(g.b) * a.N * a.H + g.row0 + row;
+                if (alone && a.lse && has) a.lse[at] = l == 0.0f ? kNegInf : (m + log2f(l)) / kLog2e;
+                if (!alone && has) p.ml[part * p.rc + row] = make_float2(m, l);
+            }
+            if (tid == 0 && !alone && g.t0 == 0) p.head[blockIdx.x] = {g.b, g.row0, g.rows, g.parts};
+            meet(kRowBarrier);
+            // ---- the rows' results: a lane holds an element, of each row in turn
+            const long long row_at = static_cast<long long>(g.b) * a.N * a.H + g.row0;
+            for (int c = 0; c < L::kPairs * 2; ++c) {
+                const int r0 = c % 2 * 32, d = c / 2 * 128 + warp * 32 + lane;
+                if (r0 >= g.rows) continue;
+                float o[32];
+                tmem_load32(tmem + lanes + c * 32, o);
+                tmem_load_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    if (r0 + k >= g.rows) break;
+                    float y = o[k];
+                    if (odd) y += odd_values(a, g, r0 + k, d);
+                    if (alone) {
+                        const float f = sh.row[r0 + k];
+                        a.out[(row_at + r0 + k) * C + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : y * f);
+                    } else {
+                        p.o[(static_cast<long long>(part) * p.rc + r0 + k) * C + d] = y;
+                    }
+                }
+            }
+            fence_before_sync();
+            meet(kRowBarrier);
+            if (tid == 0) sh.odd = 0;  // before its next vote, after which the others may set it
+        }
+        if (!live && tid == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 5) tmem_free(tmem, 512);
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+
+// A row's running result: a lane holds C / 32 elements, four at a time.
+template <int C>
+struct Running {
     float m = kNegInf, l = 0.0f;
-    const int first = len - a.N;
-    for (int j = 0; j < len && !bad; ++j) {
-        const int page = a.table[static_cast<long long>(b) * a.width + (j >> a.c.page_shift)];
-        if (page < 0 || page >= a.c.num_pages) {
-            bad = true;
-            break;
-        }
-        if (j >= first && (a.mask ? a.mask[static_cast<long long>(token) * a.N + j - first] == 0 : j - first > n)) continue;
-        const long long at = (static_cast<long long>(page) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
-        const __nv_bfloat162 *pk = reinterpret_cast<const __nv_bfloat162 *>(a.c.data + at * kW);
-        float2 k[kPairs];
-        float s = 0.0f;
-        for (int i = 0; i < kPairs; ++i) {
-            k[i] = __bfloat1622float2(pk[i * 32 + lane]);
-            s = fmaf(q[i].x, k[i].x, fmaf(q[i].y, k[i].y, s));
-        }
-        for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= mul;
-        const float top = fmaxf(m, s), keep = m == kNegInf ? 0.0f : ex2(m - top), w = ex2(s - top);
+    float4 o[C / 128] = {};
+
+    __device__ void add(float2 ml, const float4 (&y)[C / 128]) {
+        if (isnan(ml.y)) l = NAN;
+        const float top = fmaxf(m, ml.x);
+        if (top == kNegInf) return;
+        const float keep = ex2(m - top), f = ml.x == kNegInf ? 0.0f : ex2(ml.x - top);
         m = top;
-        l = l * keep + w;
-        for (int i = 0; i < kOut; ++i) o[i] = make_float2(fmaf(w, k[i].x, o[i].x * keep), fmaf(w, k[i].y, o[i].y * keep));
+        l = fmaf(f, ml.y, l * keep);
+#pragma unroll
+        for (int i = 0; i < C / 128; ++i) {
+            o[i].x = fmaf(f, y[i].x, o[i].x * keep);
+            o[i].y = fmaf(f, y[i].y, o[i].y * keep);
+            o[i].z = fmaf(f, y[i].z, o[i].z * keep);
+            o[i].w = fmaf(f, y[i].w, o[i].w * keep);
+        }
     }
-    if (bad) {
-        l = NAN;
-        if (lane == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
+};
+
+// Blocks [0, joins): the rows of units cut between CTAs, a warp a row, or (SPLIT) a
+// block a row, its warps the parts in turn, for units cut into many.  The other
+// blocks: sequences without positions, and those whose length is out of range.
+template <int C, bool SPLIT>
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentKernelArgs ka, int joins) {
+    constexpr int kV = C / 128;
+    const LatentArgs &a = ka.a;
+    const LatentPlan &p = ka.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (static_cast<int>(blockIdx.x) >= joins) {
+        for (int b = blockIdx.x - joins; b < p.B; b += gridDim.x - joins) {
+            const int len = a.lens[b];
+            if (len > 0 && len <= p.most) continue;
+            const uint32_t fill = len == 0 ? 0u : 0x7fff7fffu;  // NaN
+            uint32_t *out = reinterpret_cast<uint32_t *>(a.out + static_cast<long long>(b) * p.rows * C);
+            for (int i = threadIdx.x; i < p.rows * (C / 2); i += kJoinThreads) out[i] = fill;
+            if (a.lse)
+                for (int i = threadIdx.x; i < p.rows; i += kJoinThreads)
+                    a.lse[static_cast<long long>(b) * p.rows + i] = len == 0 ? kNegInf : NAN;
+            if (len != 0 && threadIdx.x == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
+        }
+        return;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int i = 0; i < kOut; ++i) {
-        const __nv_bfloat162 y = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv);
-        out[i * 32 + lane] = *reinterpret_cast<const uint32_t *>(&y);
+    constexpr int kBlockRows = SPLIT ? 1 : kJoinWarps;
+    const int chunks = p.rc / kBlockRows, cta = blockIdx.x / chunks;
+    const int row = (blockIdx.x - cta * chunks) * kBlockRows + (SPLIT ? 0 : warp);
+    const Head h = p.head[cta];
+    if (h.parts == 0 || row >= h.rows) return;
+    Running<C> x;
+#pragma unroll 2
+    for (int i = SPLIT ? warp : 0; i < h.parts; i += SPLIT ? kJoinWarps : 1) {
+        const long long at = (2ll * (cta + i * p.width) + (i == 0 ? 1 : 0)) * p.rc + row;
+        const float2 ml = p.ml[at];
+        float4 y[kV];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) y[k] = *reinterpret_cast<const float4 *>(p.o + at * C + k * 128 + lane * 4);
+        x.add(ml, y);
     }
-    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? kNegInf : (m + log2f(l)) / kLog2e;
+    if constexpr (SPLIT) {
+        __shared__ float2 ml[kJoinWarps];
+        __shared__ float4 part[kJoinWarps][32][kV];
+        if (lane == 0) ml[warp] = make_float2(x.m, x.l);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) part[warp][lane][k] = x.o[k];
+        __syncthreads();
+        if (warp > 0) return;
+        for (int w = 1; w < kJoinWarps; ++w) x.add(ml[w], part[w][lane]);
+    }
+    const long long at = static_cast<long long>(h.b) * p.rows + h.row0 + row;
+    const float inv = x.l == 0.0f ? 0.0f : 1.0f / x.l;  // nothing seen: every accumulator is 0
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+        *reinterpret_cast<uint2 *>(a.out + at * C + k * 128 + lane * 4) =
+            make_uint2(bf16_pair(x.o[k].x * inv, x.o[k].y * inv), bf16_pair(x.o[k].z * inv, x.o[k].w * inv));
+    if (a.lse && lane == 0) a.lse[at] = x.l == 0.0f ? kNegInf : (x.m + log2f(x.l)) / kLog2e;
+}
+
+// ------------------------------------------------------------------ host
+
+// What beginning a band costs, in tiles.
+constexpr int kStart = 4;
+
+// Fills the plan's sizes and carves its arrays; returns the bytes needed.
+size_t carve_plan(LatentPlan *p, int N, int H, int C, char *work) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = (off + bytes + 255) / 256 * 256;
+        return work + at;
+    };
+    p->N = N;
+    p->rows = N * H;
+    p->units = (p->rows + kRows - 1) / kRows;
+    p->start = kStart;
+    p->rc = p->rows < kRows ? (p->rows + 7) / 8 * 8 : kRows;
+    const size_t parts = 2 * kMaxGrid * static_cast<size_t>(p->rc);
+    p->head = reinterpret_cast<Head *>(take(kMaxGrid * sizeof(Head)));
+    p->ml = reinterpret_cast<float2 *>(take(parts * sizeof(float2)));
+    p->o = reinterpret_cast<float *>(take(parts * C * sizeof(float)));
+    return off;
+}
+
+// How many units go through a sequence's tiles together.  Taken one by one, each
+// reads the tiles for itself, which memory delivers in 1.6 times what their products
+// take; taken together, a last band of fewer units and CTAs left over idle.
+void choose_width(LatentPlan *p, int grid) {
+    double best = 0.0;
+    for (int w = 1; w <= 8 && w <= p->units && w <= grid; ++w) {
+        const int bands = (p->units + w - 1) / w, groups = grid / w;
+        const double busy = static_cast<double>(p->units) / (bands * w) * (groups * w) / grid;
+        const double score = w == 1 ? busy / 1.6 : busy;
+        if (score < best) continue;
+        best = score;
+        p->width = w;
+        p->bands = bands;
+        p->groups = groups;
+    }
+}
+
+// The cache as [num_pages][page][C + R]; a box is up to 64 positions of 64 columns.
+bool make_map(CUtensorMap *map, const LatentView &c) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t page = 1ull << c.page_shift, W = c.C + c.R;
+    const cuuint64_t dims[3] = {W, page, static_cast<cuuint64_t>(c.num_pages)};
+    const cuuint64_t strides[2] = {W * 2, W * 2 * page};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page < kTile ? page : kTile), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.data, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int C>
+int launch_shape(const LatentKernelArgs &ka, const CUtensorMap &map, cudaStream_t st) {
+    static int done[64];
+    const LatentPlan &p = ka.p;
+    const int grid = p.groups * p.width;
+    if (!allow_smem(latent_kernel<C>, Layout<C>::kBytes, done)) return SPEC_ERR_CUDA;
+    if (!launch_early(latent_kernel<C>, dim3(grid), dim3(kLatentThreads), Layout<C>::kBytes, st, ka, map)) return SPEC_ERR_CUDA;
+    // Bands over four groups and more each: few rows, many parts.
+    const bool split = 4ll * p.B * p.bands <= p.groups;
+    const int joins = grid * (split ? p.rc : p.rc / kJoinWarps), fills = p.B < 152 ? p.B : 152;
+    return launch_early(split ? latent_join_kernel<C, true> : latent_join_kernel<C, false>, dim3(joins + fills), dim3(kJoinThreads), 0,
+                        st, ka, joins)
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
 }
 
 }  // namespace
 
-size_t latent_work_bytes(int, int, int, int) { return 0; }
+size_t latent_work_bytes(int, int N, int H, int C) {
+    LatentPlan p = {};
+    return carve_plan(&p, N, H, C, nullptr);
+}
 
 int launch_latent(const LatentArgs &a, cudaStream_t st) {
-    const unsigned grid = (static_cast<unsigned>(a.B) * a.N * a.H + kWarps - 1) / kWarps;
-    if (a.c.C == 512)
-        latent_kernel<512><<<grid, kThreads, 0, st>>>(a);
-    else if (a.c.C == 256)
-        latent_kernel<256><<<grid, kThreads, 0, st>>>(a);
-    else
-        latent_kernel<128><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    LatentKernelArgs ka = {};
+    ka.a = a;
+    ka.p.B = a.B;
+    ka.p.lens = a.lens;
+    ka.p.most = a.width << a.c.page_shift;
+    carve_plan(&ka.p, a.N, a.H, a.c.C, a.work);
+    const int sms = multiprocessors();
+    CUtensorMap map;
+    if (sms <= 0 || !make_map(&map, a.c)) return SPEC_ERR_CUDA;
+    choose_width(&ka.p, sms < kMaxGrid ? sms : kMaxGrid);
+    return a.c.C == 512 ? launch_shape<512>(ka, map, st) : a.c.C == 256 ? launch_shape<256>(ka, map, st) : launch_shape<128>(ka, map, st);
 }
 
 }  // namespace specv
