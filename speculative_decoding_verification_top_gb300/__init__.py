@@ -466,6 +466,30 @@ def _need(t, name, dtype, shape):
                          % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
 
+def _made(stream, make, *args, **kw):
+    """make(...) on the call's stream (as _made_on)."""
+    if stream is None:
+        return make(*args, **kw)
+    with _torch().cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _lies(t, name, dtype, shape, device):
+    """_need for a tensor beside others on the device of index `device`."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d, got %s %s on %s"
+                         % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+
+
+def _launch(device, stream):
+    """The handle of the stream that a call on tensors of this device runs on: the
+    given one, else the current one (by its handle: a Stream object takes 3 us)."""
+    c = _torch()._C
+    if c._cuda_getDevice() != device:
+        raise ValueError("the tensors are on cuda:%d, which is not the current device" % device)
+    return c._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 def new_workspace(nbytes, device):
     """A zero-filled workspace tensor (zeroing is the required first-use init)."""
     torch = _torch()
@@ -656,23 +680,30 @@ def logprobs(target, tokens, rows=None, temperature=1.0, top=0, entropy=True, ra
     torch = _torch()
     B, N, V = target.shape
     M = tokens.shape[1]
-    _need(target, "target", target.dtype, (B, N, V))
-    _need(tokens, "tokens", torch.int32, (B, M))
+    if not (target.is_contiguous() and target.is_cuda):
+        raise ValueError("target must be a contiguous CUDA tensor")
+    device = target.get_device()
+    _lies(tokens, "tokens", torch.int32, (B, M), device)
     if rows is not None:
-        _need(rows, "rows", torch.int32, (B, M))
-    dev = target.device
-    with _made_on(stream):
-        f = torch.empty((2 if entropy else 1, B, M), dtype=torch.float32, device=dev)
-        r = torch.empty((B, M), dtype=torch.int32, device=dev) if rank else None
-        ids = torch.empty((B, M, top), dtype=torch.int32, device=dev) if top else None
-        best = torch.empty((B, M, top), dtype=torch.float32, device=dev) if top else None
-        if workspace is None:
-            workspace = new_workspace(spec_verify_logprobs_workspace_size(), dev)
-    out = LogProbs(f[0], f[1] if entropy else None, r, ids, best)
-    spec_verify_logprobs(_ptr(target), _ptr(tokens), _ptr(rows), B, N, M, V, temperature, top,
-                         _dtype_code(target), *map(_ptr, out), _ptr(workspace), workspace.numel(),
-                         _stream(stream))
+        _lies(rows, "rows", torch.int32, (B, M), device)
+    handle = _launch(device, stream)
+    out = _made(stream, _new_logprobs, B, M, top, entropy, rank, target.device)
+    if workspace is None:
+        workspace = _made(stream, new_workspace, spec_verify_logprobs_workspace_size(), target.device)
+    spec_verify_logprobs(target.data_ptr(), tokens.data_ptr(), _ptr(rows), B, N, M, V, temperature, top,
+                         _dtype_code(target), out.logprob.data_ptr(), _ptr(out.entropy), _ptr(out.rank),
+                         _ptr(out.top_ids), _ptr(out.top_logprobs), workspace.data_ptr(),
+                         workspace.numel(), handle)
     return out
+
+
+def _new_logprobs(B, M, top, entropy, rank, device):
+    empty, f, i = _torch().empty, _torch().float32, _torch().int32
+    return LogProbs(empty((B, M), dtype=f, device=device),
+                    empty((B, M), dtype=f, device=device) if entropy else None,
+                    empty((B, M), dtype=i, device=device) if rank else None,
+                    empty((B, M, top), dtype=i, device=device) if top else None,
+                    empty((B, M, top), dtype=f, device=device) if top else None)
 
 
 # ------------------------------------------- the target pass's cache and attention
@@ -849,22 +880,22 @@ def rope_freqs(rot, base=10000.0, scaling="plain", factor=1.0, original=0, low=0
     return host.to(device)
 
 
-def _turn(freqs, interleaved):
-    if freqs.dtype != _torch().int64 or freqs.dim() != 1 or not freqs.is_contiguous() or not freqs.is_cuda:
-        raise ValueError("freqs must be what rope_freqs returns, on the GPU")
+def _turn(freqs, interleaved, device):
+    if (freqs.dtype != _torch().int64 or freqs.dim() != 1 or not freqs.is_contiguous() or
+            freqs.get_device() != device):
+        raise ValueError("freqs must be what rope_freqs returns, on cuda:%d" % device)
     return 2 * freqs.numel(), SPEC_ROPE_INTERLEAVED if interleaved else SPEC_ROPE_HALF
 
 
-def _turned(x, out, name, D, stream):
+def _turned(x, out, name, H, D, stream):
     """out of a rotation of x [B, N, H, D] (None: a new tensor); both strides."""
     torch = _torch()
-    H = x.shape[2]
     step = _tokens(x, name, H, D, (torch.bfloat16, torch.float32))
     if out is None:
-        with _made_on(stream):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape:
-        raise ValueError("out must have the shape of %s, got %s" % (name, tuple(out.shape)))
+        return _made(stream, torch.empty_like, x, memory_format=torch.contiguous_format), step, H * D
+    if out.shape != x.shape or out.get_device() != x.get_device():
+        raise ValueError("out must have the shape and device of %s, got %s on %s"
+                         % (name, tuple(out.shape), out.device))
     return out, step, _tokens(out, "out", H, D, (x.dtype,))
 
 
@@ -875,11 +906,13 @@ def rope(x, freqs, pos, first=0, amplitude=1.0, interleaved=False, inverse=False
     are turned.  Returns out (out=x: in place)."""
     torch = _torch()
     B, N, H, D = x.shape
-    rot, layout = _turn(freqs, interleaved)
-    _need(pos, "pos", torch.int32, (B, N))
-    out, step, out_step = _turned(x, out, "x", D, stream)
-    spec_rope(_ptr(x), step, _ptr(out), out_step, _ptr(freqs), rot, first, amplitude, layout,
-              1 if inverse else 0, _ptr(pos), B, N, H, D, _dtype_code(x), _stream(stream))
+    out, step, out_step = _turned(x, out, "x", H, D, stream)
+    device = x.get_device()
+    rot, layout = _turn(freqs, interleaved, device)
+    _lies(pos, "pos", torch.int32, (B, N), device)
+    spec_rope(x.data_ptr(), step, out.data_ptr(), out_step, freqs.data_ptr(), rot, first, amplitude,
+              layout, 1 if inverse else 0, pos.data_ptr(), B, N, H, D, _dtype_code(x),
+              _launch(device, stream))
     return out
 
 
@@ -890,30 +923,35 @@ def kv_append_rope(cache, page_table, starts, k, v, freqs, q=None, rows=None, po
     [B, N, Hq, D] the queries too.  Returns out_q, or None without q."""
     torch = _torch()
     c = cache.descriptor
-    B, N = k.shape[:2]
-    rot, layout = _turn(freqs, interleaved)
-    step = _tokens(k, "k", c.Hkv, c.D, (torch.bfloat16, torch.float32))
-    if _tokens(v, "v", c.Hkv, c.D, (k.dtype,)) != step or v.shape != k.shape:
+    H, D = c.Hkv, c.D
+    step = _tokens(k, "k", H, D, (torch.bfloat16, torch.float32))
+    if _tokens(v, "v", H, D, (k.dtype,)) != step or v.shape != k.shape:
         raise ValueError("k and v must have one shape and token stride")
-    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
-    _need(starts, "starts", torch.int32, (B,))
-    M = N
+    B, N = k.shape[:2]
+    device = k.get_device()
+    if v.get_device() != device or cache.k.get_device() != device:
+        raise ValueError("k, v and the cache must be on one device")
+    rot, layout = _turn(freqs, interleaved, device)
+    M, width = N, page_table.shape[1]
+    _lies(page_table, "page_table", torch.int32, (B, width), device)
+    _lies(starts, "starts", torch.int32, (B,), device)
     if rows is not None:
         M = rows.shape[1]
-        _need(rows, "rows", torch.int32, (B, M))
+        _lies(rows, "rows", torch.int32, (B, M), device)
     if pos is not None:
-        _need(pos, "pos", torch.int32, (B, N))
+        _lies(pos, "pos", torch.int32, (B, N), device)
     q_step = out_step = Hq = 0
     if q is not None:
-        if q.dtype != k.dtype or q.shape[:2] != (B, N):
-            raise ValueError("q must be of k's type and tokens")
+        if q.dtype != k.dtype or q.shape[:2] != (B, N) or q.get_device() != device:
+            raise ValueError("q must be of k's type, tokens and device")
         Hq = q.shape[2]
-        out_q, q_step, out_step = _turned(q, out_q, "q", c.D, stream)
+        out_q, q_step, out_step = _turned(q, out_q, "q", Hq, D, stream)
     elif out_q is not None:
         raise ValueError("out_q without q")
-    spec_kv_append_rope(c, _ptr(page_table), page_table.shape[1], _ptr(starts), _ptr(k), _ptr(v), step,
-                        _ptr(rows), _ptr(pos), _ptr(freqs), rot, amplitude, layout, _ptr(q), q_step,
-                        _ptr(out_q), out_step, B, N, M, Hq, _dtype_code(k), _stream(stream))
+    spec_kv_append_rope(c, page_table.data_ptr(), width, starts.data_ptr(), k.data_ptr(), v.data_ptr(),
+                        step, _ptr(rows), _ptr(pos), freqs.data_ptr(), rot, amplitude, layout, _ptr(q),
+                        q_step, _ptr(out_q), out_step, B, N, M, Hq, _dtype_code(k),
+                        _launch(device, stream))
     return out_q
 
 
@@ -954,25 +992,32 @@ def latent_append(cache, page_table, starts, c, r, freqs=None, rows=None, pos=No
     torch = _torch()
     d = cache.descriptor
     B, N = c.shape[:2]
-    types = (torch.bfloat16, torch.float32)
-    c_step = _tokens(c.unsqueeze(2), "c", 1, d.C, types)
-    r_step = _tokens(r.unsqueeze(2), "r", 1, d.R, (c.dtype,))
-    if r.shape[:2] != (B, N):
-        raise ValueError("c and r must hold the same tokens")
-    rot, layout = (d.R, SPEC_ROPE_HALF) if freqs is None else _turn(freqs, interleaved)
+    c_step = _parts(c, "c", d.C, (torch.bfloat16, torch.float32))
+    r_step = _parts(r, "r", d.R, (c.dtype,))
+    device = c.get_device()
+    if r.shape[:2] != (B, N) or r.get_device() != device or cache.data.get_device() != device:
+        raise ValueError("c and r must hold the same tokens, on the cache's device")
+    rot, layout = (d.R, SPEC_ROPE_HALF) if freqs is None else _turn(freqs, interleaved, device)
     if rot != d.R:
         raise ValueError("freqs are of %d elements, the cache's rotary part has %d" % (rot, d.R))
-    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
-    _need(starts, "starts", torch.int32, (B,))
-    M = N
+    M, width = N, page_table.shape[1]
+    _lies(page_table, "page_table", torch.int32, (B, width), device)
+    _lies(starts, "starts", torch.int32, (B,), device)
     if rows is not None:
         M = rows.shape[1]
-        _need(rows, "rows", torch.int32, (B, M))
+        _lies(rows, "rows", torch.int32, (B, M), device)
     if pos is not None:
-        _need(pos, "pos", torch.int32, (B, N))
-    spec_latent_append(d, _ptr(page_table), page_table.shape[1], _ptr(starts), _ptr(c), c_step, _ptr(r),
-                       r_step, _ptr(rows), _ptr(pos), _ptr(freqs), amplitude, layout, B, N, M,
-                       _dtype_code(c), _stream(stream))
+        _lies(pos, "pos", torch.int32, (B, N), device)
+    spec_latent_append(d, page_table.data_ptr(), width, starts.data_ptr(), c.data_ptr(), c_step,
+                       r.data_ptr(), r_step, _ptr(rows), _ptr(pos), _ptr(freqs), amplitude, layout, B, N,
+                       M, _dtype_code(c), _launch(device, stream))
+
+
+def _parts(t, name, D, dtypes):
+    """_tokens for [B, N, D], one vector a token."""
+    if t.dim() == 3 and t.is_contiguous() and t.dtype in dtypes and t.is_cuda and t.shape[2] == D:
+        return D
+    return _tokens(t.unsqueeze(2), name, 1, D, dtypes)
 
 
 def latent_attn(q, cache, page_table, lens, scale, mask=None, out=None, lse=None, workspace=None,
@@ -986,21 +1031,27 @@ def latent_attn(q, cache, page_table, lens, scale, mask=None, out=None, lse=None
     torch = _torch()
     d = cache.descriptor
     B, N, H = q.shape[:3]
-    step = _tokens(q, "q", H, d.C + d.R, (torch.bfloat16,))
-    _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
-    _need(lens, "lens", torch.int32, (B,))
+    C = d.C
+    step = _tokens(q, "q", H, C + d.R, (torch.bfloat16,))
+    device, width = q.get_device(), page_table.shape[1]
+    if cache.data.get_device() != device:
+        raise ValueError("q must be on the cache's device")
+    _lies(page_table, "page_table", torch.int32, (B, width), device)
+    _lies(lens, "lens", torch.int32, (B,), device)
     if mask is not None:
-        _need(mask, "mask", torch.uint8, (B, N, N))
-    with _made_on(stream):
-        if out is None:
-            out = torch.empty((B, N, H, d.C), dtype=q.dtype, device=q.device)
-        if lse is True:
-            lse = torch.empty((B, N, H), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = new_workspace(spec_latent_workspace_size(B, N, H, d.C), q.device)
-    _need(out, "out", q.dtype, (B, N, H, d.C))
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (B, N, H))
-    spec_latent_attn(d, _ptr(page_table), page_table.shape[1], _ptr(lens), _ptr(q), step, _ptr(mask), B, N,
-                     H, scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
+        _lies(mask, "mask", torch.uint8, (B, N, N), device)
+    handle = _launch(device, stream)
+    if out is None:
+        out = _made(stream, torch.empty, (B, N, H, C), dtype=q.dtype, device=q.device)
+    else:
+        _lies(out, "out", q.dtype, (B, N, H, C), device)
+    if lse is True:
+        lse = _made(stream, torch.empty, (B, N, H), dtype=torch.float32, device=q.device)
+    elif lse is not None:
+        _lies(lse, "lse", torch.float32, (B, N, H), device)
+    if workspace is None:
+        workspace = _made(stream, new_workspace, spec_latent_workspace_size(B, N, H, C), q.device)
+    spec_latent_attn(d, page_table.data_ptr(), width, lens.data_ptr(), q.data_ptr(), step, _ptr(mask), B,
+                     N, H, scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
+                     handle)
     return out if lse is None else (out, lse)

@@ -22,7 +22,7 @@ namespace {
 
 using Key = unsigned long long;
 
-constexpr int kVecs = 8;               // vectors a thread holds of a chunk
+constexpr int kVecs = 10;              // vectors a thread holds of a chunk
 constexpr int kChunk = kThreads * kVecs;
 constexpr int kGroups = kThreads / 4;  // groups of threads whose maxima bound the first chunk
 constexpr int kCap = 1024;             // candidates kept of a chunk
@@ -203,7 +203,7 @@ __device__ __forceinline__ void take_first(Shared &sh, const Held<T> &h, float m
 
 // SOME: top > 0.
 template <typename T, bool SOME>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs a) {
     constexpr int E = Elem<T>::kPerVec;
     __shared__ Shared sh;
     const int size = a.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -278,8 +278,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
                 const float2 e = make_float2(ex2(y.x), ex2(y.y));
                 z = add2(z, e);
                 s = fma2(e, y, s);
-                before += (f[k] > bar) + (f[k + 1] > bar);
             }
+            if (!(h.top[i] >= lt)) continue;  // nothing of the vector comes before the token
+#pragma unroll
+            for (int k = 0; k < E; ++k) before += f[k] > bar;
             if (lowest || (at <= token && token < at + E)) {  // equal ones before it
 #pragma unroll
                 for (int k = 0; k < E; ++k)
@@ -392,7 +394,8 @@ int launch_logprobs(LogprobArgs &a, int dtype, cudaStream_t st) {
     const int E = dtype == SPEC_F32 ? 4 : 8;
     const long long entries = static_cast<long long>(a.B) * a.M;
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && a.V > a.cluster * kThreads * E && entries * a.cluster < 152 * 8) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && (a.V > a.cluster * kChunk * E || (a.V > a.cluster * kThreads * E && entries * a.cluster < 152 * 8)))
+        a.cluster *= 2;
     if (dtype == SPEC_F32) return a.top ? launch_size<float, true>(a, st) : launch_size<float, false>(a, st);
     return a.top ? launch_size<uint16_t, true>(a, st) : launch_size<uint16_t, false>(a, st);
 }

@@ -10,7 +10,9 @@
 // A unit is 16 elements of a head, two vectors of 8: eight pairs, or 16
 // elements that stay.  A thread takes one unit of up to four heads of a token, so
 // that eight sines and cosines (about 30 instructions each) serve 32 pairs.
-// All kernels are bound by memory: each element read once and written once.
+// All kernels are bound by memory: each element read once and written once.  What
+// a thread loads is held as it came until its turn, so that a multiprocessor has
+// room for 16 and more warps with 128 bytes a thread on their way.
 
 #include "kvrows.cuh"
 #include "target.cuh"
@@ -18,29 +20,35 @@
 namespace specv {
 namespace {
 
-// A unit's two vectors in its head, and its first pair (-1: not turned).
+// A unit's two vectors in its head, and whether they are turned; the vectors lie
+// half a part (the turned one, or what stays before or after it) apart, so that
+// neighbouring lanes' vectors lie side by side in either layout.
 struct Unit {
-    int at0, at1, pair;
+    int at0, at1, turned;
 };
 
-__device__ __forceinline__ Unit unit_of(const Turn &t, int unit) {
-    const int e = unit * kW, i = e - t.first;
-    if (i < 0 || i >= t.rot) return {e, e + kE, -1};
-    if (t.interleaved) return {e, e + kE, i / 2};
-    return {t.first + i / 2, t.first + i / 2 + t.rot / 2, i / 2};
+__device__ __forceinline__ Unit unit_of(const Turn &t, int D, int unit) {
+    const int e = unit * kW, end = t.first + t.rot;
+    const int part = e < t.first ? 0 : e < end ? t.first : end;
+    const int size = e < t.first ? t.first : e < end ? t.rot : D - end;
+    const int at = part + (e - part) / 2;
+    return {at, at + size / 2, e >= t.first && e < end};
 }
 
-// a cos and a sin of pairs pair .. pair + 7 at index p.
+// a cos and a sin of a unit's pairs at index p, in the order of its vectors.
 struct Angles {
     float c[kE], s[kE];
 };
 
-__device__ __forceinline__ Angles angles_of(const Turn &t, int pair, long long p) {
+__device__ __forceinline__ Angles angles_of(const Turn &t, const Unit &u, long long p) {
     Angles a = {};
-    if (pair < 0) return a;
+    if (!u.turned) return a;
+    // Half: the first vector's eight pairs.  Interleaved: each vector's four.
+    const int i0 = u.at0 - t.first, p0 = t.interleaved ? i0 / 2 : i0, p1 = t.interleaved ? i0 / 2 + t.rot / 4 : i0 + kE / 2;
     ulonglong2 f[kE / 2];
 #pragma unroll
-    for (int i = 0; i < kE / 2; ++i) f[i] = __ldg(reinterpret_cast<const ulonglong2 *>(t.freqs + pair) + i);
+    for (int i = 0; i < kE / 2; ++i)
+        f[i] = __ldg(reinterpret_cast<const ulonglong2 *>(t.freqs + (i < kE / 4 ? p0 : p1)) + i % (kE / 4));
     const long long index = t.inverse ? -p : p;
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
@@ -69,42 +77,73 @@ __device__ __forceinline__ void turn(float (&x)[2][kE], const Angles &a, bool in
     }
 }
 
-// Eight elements of a tensor that the same kernel may write: not by the
-// read-only path.
-__device__ __forceinline__ void fetch8(const float *p, float (&x)[kE]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw;
+
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void widen(float (&x)[kE]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void widen(float (&x)[kE]) const { widen8(a, x); }
+};
+
+// Not by the read-only path: the same kernel may write the tensor.
+__device__ __forceinline__ Raw<float> fetch(const float *p) {
+    return {*reinterpret_cast<const float4 *>(p), *(reinterpret_cast<const float4 *>(p) + 1)};
 }
 
-__device__ __forceinline__ void fetch8(const __nv_bfloat16 *p, float (&x)[kE]) {
-    widen8(*reinterpret_cast<const uint4 *>(p), x);
-}
+__device__ __forceinline__ Raw<__nv_bfloat16> fetch(const __nv_bfloat16 *p) { return {*reinterpret_cast<const uint4 *>(p)}; }
+
+// A unit of up to HC heads from head h0 on, of `n` heads, as it lies in memory.
+template <typename T, int HC>
+struct Heads {
+    Raw<T> x[HC][2];
+
+    __device__ __forceinline__ void load(const T *from, int D, const Unit &u, int h0, int n) {
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+            if (h0 + i >= n) break;
+            x[i][0] = fetch(from + (h0 + i) * D + u.at0);
+            x[i][1] = fetch(from + (h0 + i) * D + u.at1);
+        }
+    }
+
+    // Head i's elements, turned if the unit is.
+    __device__ __forceinline__ void get(int i, const Turn &t, const Unit &u, const Angles &a, float (&y)[2][kE]) const {
+        x[i][0].widen(y[0]);
+        x[i][1].widen(y[1]);
+        if (!u.turned) return;
+        if (t.interleaved)
+            turn(y, a, true);
+        else
+            turn(y, a, false);
+    }
+};
 
 // The heads h0 .. of one token, this thread's unit of each.
 template <typename T, int HC>
 __device__ __forceinline__ void turn_heads(const T *x, T *out, const Turn &t, int H, int D, int unit, int h0, long long p) {
-    const Unit u = unit_of(t, unit);
-    if (u.pair < 0 && x == out) return;
-    float y[HC][2][kE];
+    const Unit u = unit_of(t, D, unit);
+    if (!u.turned && x == out) return;
+    Heads<T, HC> heads;
+    heads.load(x, D, u, h0, H);
+    const Angles a = angles_of(t, u, p);
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
         if (h0 + i >= H) break;
-        fetch8(x + (h0 + i) * D + u.at0, y[i][0]);
-        fetch8(x + (h0 + i) * D + u.at1, y[i][1]);
-    }
-    const Angles a = angles_of(t, u.pair, p);
-#pragma unroll
-    for (int i = 0; i < HC; ++i) {
-        if (h0 + i >= H) break;
-        if (u.pair >= 0) {
-            if (t.interleaved)
-                turn(y[i], a, true);
-            else
-                turn(y[i], a, false);
-        }
-        store8(out + (h0 + i) * D + u.at0, y[i][0]);
-        store8(out + (h0 + i) * D + u.at1, y[i][1]);
+        float y[2][kE];
+        heads.get(i, t, u, a, y);
+        store8(out + (h0 + i) * D + u.at0, y[0]);
+        store8(out + (h0 + i) * D + u.at1, y[1]);
     }
 }
 
@@ -140,15 +179,16 @@ __device__ __forceinline__ void write_unit(uint8_t *data, int8_t *exps, long lon
     if (part == 0) exps[row] = static_cast<int8_t>(e);
 }
 
-// The first kv_blocks blocks write keys and values, the others turn queries.
+// The first kv_blocks blocks write keys, the next as many values, the others turn
+// queries.
 template <typename T, int D, bool E4M3, int HC>
 __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRopeArgs ar) {
     constexpr int kUnits = D / kW;
     const AppendArgs &a = ar.a;
     const int unit = threadIdx.x % kUnits;
-    if (blockIdx.x >= ar.kv_blocks) {
+    if (blockIdx.x >= 2 * ar.kv_blocks) {
         const uint32_t chunks = (ar.Hq + HC - 1) / HC;
-        const uint32_t item = (blockIdx.x - ar.kv_blocks) * (kThreads / kUnits) + threadIdx.x / kUnits;
+        const uint32_t item = (blockIdx.x - 2 * ar.kv_blocks) * (kThreads / kUnits) + threadIdx.x / kUnits;
         const uint32_t token = item / chunks;
         if (token >= static_cast<uint32_t>(a.B) * a.N) return;
         const uint32_t b = token / a.N;
@@ -157,94 +197,93 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
                           ar.t, ar.Hq, D, unit, (item - token * chunks) * HC, p);
         return;
     }
+    const bool values = blockIdx.x >= ar.kv_blocks;
     const uint32_t chunks = (a.c.Hkv + HC - 1) / HC;
-    const uint32_t item = blockIdx.x * (kThreads / kUnits) + threadIdx.x / kUnits;
+    const uint32_t item = (values ? blockIdx.x - ar.kv_blocks : blockIdx.x) * (kThreads / kUnits) + threadIdx.x / kUnits;
     const uint32_t bt = item / chunks;
-    const Unit u = unit_of(ar.t, unit);
+    Unit u = unit_of(ar.t, D, unit);
+    if (values) u.turned = 0;
     int page = -1, slot = 0, h0 = 0, p = 0;
-    float k[HC][2][kE] = {}, v[HC][2][kE] = {};
+    Heads<T, HC> heads = {};
     if (bt < static_cast<uint32_t>(a.B) * a.M) {
         const uint32_t b = bt / a.M;
         const int t = static_cast<int>(bt - b * a.M), r = a.rows ? a.rows[bt] : t;
         h0 = static_cast<int>(item - bt * chunks) * HC;
-        const long long at = static_cast<long long>(a.starts[b]) + t;
-        if (r >= 0 && r < a.N && at <= INT_MAX) {
-            const long long token = static_cast<long long>(b) * a.N + r;
-            const T *pk = static_cast<const T *>(a.k) + token * a.stride, *pv = static_cast<const T *>(a.v) + token * a.stride;
+        if (r >= 0 && r < a.N) {
+            const long long token = static_cast<long long>(b) * a.N + r, at = static_cast<long long>(a.starts[b]) + t;
+            heads.load(static_cast<const T *>(values ? a.v : a.k) + token * a.stride, D, u, h0, a.c.Hkv);
             p = ar.pos ? ar.pos[token] : static_cast<int>(at);
-            page = page_of(a.c, a.table + static_cast<long long>(b) * a.width, a.width, static_cast<int>(at), &slot);
-            if (page >= 0) {
-#pragma unroll
-                for (int i = 0; i < HC; ++i) {
-                    if (h0 + i >= a.c.Hkv) break;
-                    load8(pk + (h0 + i) * D + u.at0, k[i][0]);
-                    load8(pk + (h0 + i) * D + u.at1, k[i][1]);
-                    load8(pv + (h0 + i) * D + u.at0, v[i][0]);
-                    load8(pv + (h0 + i) * D + u.at1, v[i][1]);
-                }
-            }
+            if (at <= INT_MAX)
+                page = page_of(a.c, a.table + static_cast<long long>(b) * a.width, a.width, static_cast<int>(at), &slot);
         }
     }
-    const Angles an = angles_of(ar.t, u.pair, p);
+    const Angles an = angles_of(ar.t, u, p);
+    uint8_t *data = values ? a.c.v : a.c.k;
+    int8_t *exps = values ? a.c.v_exp : a.c.k_exp;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
         const bool live = page >= 0 && h0 + i < a.c.Hkv;
         const long long row = live ? cache_row(a.c, page, h0 + i, slot) : 0;
-        if (u.pair >= 0) {
-            if (ar.t.interleaved)
-                turn(k[i], an, true);
-            else
-                turn(k[i], an, false);
-        }
+        float y[2][kE];
+        heads.get(i, ar.t, u, an, y);
         __syncwarp();
-        write_unit<D, E4M3>(a.c.k, a.c.k_exp, row, u, unit, live, k[i]);
-        write_unit<D, E4M3>(a.c.v, a.c.v_exp, row, u, unit, live, v[i]);
+        write_unit<D, E4M3>(data, exps, row, u, unit, live, y);
     }
 }
 
-// Rows of a latent cache, a unit a thread: C / 16 of the latent, then the rotary
-// part's.
+// Rows of a latent cache.  The first c_blocks blocks copy the latent, 32 elements a
+// thread; the others turn the rotary part, a unit a thread (in warps of their own:
+// beside the copies its sines and cosines would hold up every warp).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentAppendArgs a) {
-    const uint32_t units = (a.c.C + a.c.R) / kW;
-    const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentAppendArgs a, unsigned c_blocks) {
+    const bool rotary = blockIdx.x >= c_blocks;
+    const uint32_t units = rotary ? a.c.R / kW : a.c.C / (2 * kW);
+    const uint32_t item = (rotary ? blockIdx.x - c_blocks : blockIdx.x) * kThreads + threadIdx.x;
     const uint32_t bt = item / units;
     if (bt >= static_cast<uint32_t>(a.B) * a.M) return;
     const int unit = static_cast<int>(item - bt * units);
     const uint32_t b = bt / a.M;
     const int t = static_cast<int>(bt - b * a.M), r = a.rows ? a.rows[bt] : t;
-    const long long at = static_cast<long long>(a.starts[b]) + t;
-    if (r < 0 || r >= a.N || at < 0 || at > INT_MAX) return;
-    const int i = static_cast<int>(at) >> a.c.page_shift;
-    if (i >= a.width) return;
-    const int page = a.table[static_cast<long long>(b) * a.width + i];
-    if (page < 0 || page >= a.c.num_pages) return;
-    const long long token = static_cast<long long>(b) * a.N + r;
-    const long long row = (static_cast<long long>(page) << a.c.page_shift) + (at & ((1 << a.c.page_shift) - 1));
-    __nv_bfloat16 *to = a.c.data + row * (a.c.C + a.c.R);
-    float x[2][kE];
-    if (unit * kW < a.c.C) {
-        const T *from = static_cast<const T *>(a.x) + token * a.x_stride + unit * kW;
-        load8(from, x[0]);
-        load8(from + kE, x[1]);
-        store8(to + unit * kW, x[0]);
-        store8(to + unit * kW + kE, x[1]);
+    if (r < 0 || r >= a.N) return;
+    const long long at = static_cast<long long>(a.starts[b]) + t, token = static_cast<long long>(b) * a.N + r;
+    // Where the token goes; null: nowhere.
+    auto target = [&]() -> __nv_bfloat16 * {
+        if (at < 0 || at > INT_MAX) return nullptr;
+        const int i = static_cast<int>(at) >> a.c.page_shift;
+        if (i >= a.width) return nullptr;
+        const int page = a.table[static_cast<long long>(b) * a.width + i];
+        if (page < 0 || page >= a.c.num_pages) return nullptr;
+        const long long row = (static_cast<long long>(page) << a.c.page_shift) + (at & ((1 << a.c.page_shift) - 1));
+        return a.c.data + row * (a.c.C + a.c.R);
+    };
+    if (!rotary) {
+        constexpr int kV = 2 * kW / kE;  // vectors, a quarter of the row apart
+        const int step = a.c.C / kV;
+        const T *from = static_cast<const T *>(a.x) + token * a.x_stride + unit * kE;
+        Raw<T> x[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) x[i] = fetch(from + i * step);
+        __nv_bfloat16 *to = target();
+        if (!to) return;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            float y[kE];
+            x[i].widen(y);
+            store8(to + unit * kE + i * step, y);
+        }
         return;
     }
-    const Unit u = unit_of(a.t, unit - a.c.C / kW);
-    const T *from = static_cast<const T *>(a.r) + token * a.r_stride;
-    load8(from + u.at0, x[0]);
-    load8(from + u.at1, x[1]);
-    if (u.pair >= 0) {
-        const Angles an = angles_of(a.t, u.pair, a.pos ? a.pos[token] : static_cast<int>(at));
-        if (a.t.interleaved)
-            turn(x, an, true);
-        else
-            turn(x, an, false);
-    }
-    store8(to + a.c.C + u.at0, x[0]);
-    store8(to + a.c.C + u.at1, x[1]);
+    const Unit u = unit_of(a.t, a.c.R, unit);
+    Heads<T, 1> part;
+    part.load(static_cast<const T *>(a.r) + token * a.r_stride, 0, u, 0, 1);
+    __nv_bfloat16 *to = target();
+    if (!to) return;
+    const Angles an = angles_of(a.t, u, a.pos ? a.pos[token] : static_cast<int>(at));
+    float y[2][kE];
+    part.get(0, a.t, u, an, y);
+    store8(to + a.c.C + u.at0, y[0]);
+    store8(to + a.c.C + u.at1, y[1]);
 }
 
 // Heads a thread: four where that leaves every multiprocessor full, else one.
@@ -269,7 +308,7 @@ int append_heads(AppendRopeArgs &a, cudaStream_t st) {
     const long long entries = static_cast<long long>(a.a.B) * a.a.M, tokens = a.q ? static_cast<long long>(a.a.B) * a.a.N : 0;
     a.kv_blocks = blocks_for(entries * ((a.a.c.Hkv + HC - 1) / HC) * (D / kW));
     const unsigned q_blocks = blocks_for(tokens * ((a.Hq + HC - 1) / HC) * (D / kW));
-    kv_append_rope_kernel<T, D, E4M3, HC><<<a.kv_blocks + q_blocks, kThreads, 0, st>>>(a);
+    kv_append_rope_kernel<T, D, E4M3, HC><<<2 * a.kv_blocks + q_blocks, kThreads, 0, st>>>(a);
     return launched();
 }
 
@@ -298,11 +337,12 @@ int launch_kv_append_rope(AppendRopeArgs &a, int dtype, cudaStream_t st) {
 }
 
 int launch_latent_append(const LatentAppendArgs &a, int dtype, cudaStream_t st) {
-    const long long threads = static_cast<long long>(a.B) * a.M * ((a.c.C + a.c.R) / kW);
+    const long long entries = static_cast<long long>(a.B) * a.M;
+    const unsigned c_blocks = blocks_for(entries * (a.c.C / (2 * kW))), blocks = c_blocks + blocks_for(entries * (a.c.R / kW));
     if (dtype == SPEC_F32)
-        latent_append_kernel<float><<<blocks_for(threads), kThreads, 0, st>>>(a);
+        latent_append_kernel<float><<<blocks, kThreads, 0, st>>>(a, c_blocks);
     else
-        latent_append_kernel<__nv_bfloat16><<<blocks_for(threads), kThreads, 0, st>>>(a);
+        latent_append_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a, c_blocks);
     return launched();
 }
 
