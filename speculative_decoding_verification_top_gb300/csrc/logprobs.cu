@@ -8,25 +8,33 @@
 // complement, so that keys differ and equal logits go by index.
 //
 // A row is cut into slices, one per CTA of a cluster; a CTA goes through its slice
-// in chunks of 2048 vectors of 16 bytes that it holds in registers: the sums, the
-// count of tokens before the emitted one, and the chunk's candidates for the
-// slice's `top` first: those above the top-th of what was seen before or, in the
-// first chunk, from the top-th largest of 64 groups' maxima on (at least `top`
-// elements reach it, and few more do).  The slices' sums and lists meet in the
-// first CTA's shared memory.
+// in chunks of 10240 vectors of 16 bytes: the sums, the count of tokens before the
+// emitted one, and each vector's maximum.  The chunk's candidates for the slice's
+// `top` first come from the vectors (read once more, from L2) whose maximum is from
+// a bar on: the top-th of what was seen before or, in the first chunk, the top-th
+// largest of 64 groups' maxima (at least `top` elements reach it, and few more do).
+// The slices' sums and lists meet in the first CTA's shared memory.
+// Bound by what is issued (about 6 instructions an element, an exponential among
+// them) and, where rows are few, by the chain load, sums, bar, candidates, cluster.
+// Kept in registers instead of read again, a chunk takes 80 registers and code that
+// the instruction cache does not hold.
 
 #include "logprobs.cuh"
+#include "util.cuh"
 
 namespace specv {
 namespace {
 
 using Key = unsigned long long;
 
-constexpr int kVecs = 10;              // vectors a thread holds of a chunk
+constexpr int kVecs = 40;              // vectors a thread takes of a chunk
+constexpr int kBatch = 4;              // of them at a time, the next ones in flight
 constexpr int kChunk = kThreads * kVecs;
 constexpr int kGroups = kThreads / 4;  // groups of threads whose maxima bound the first chunk
+constexpr int kQueue = 512;            // vectors of a chunk that may hold candidates
 constexpr int kCap = 1024;             // candidates kept of a chunk
 constexpr int kMaxCluster = 8;
+constexpr int kResident = 3;           // CTAs a multiprocessor has room for
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFar = -200.0f;        // 2^y is 0 from here down
 
@@ -42,10 +50,11 @@ struct Shared {
     Key mine[SPEC_MAX_TOP];              // this slice's so far, sorted
     Key cand[kCap];
     Key best[kWarps];
+    uint16_t top[kChunk];                // the chunk's vectors' maxima (up_bits)
+    uint16_t queue[kQueue];
     float group[kGroups];
-    float warp[3][kWarps];
-    uint32_t before[kWarps];
-    uint32_t bad, n, n_mine;
+    Part warp[kWarps];
+    uint32_t n, n_mine, n_queue;
     float bound;
 };
 
@@ -55,18 +64,11 @@ __device__ __forceinline__ Key key_of(float v, int index) {
 
 __device__ __forceinline__ Key max_key(Key a, Key b) { return a > b ? a : b; }
 
-// The largest float below a finite x.
-__device__ __forceinline__ float below(float x) {
-    const int u = __float_as_int(x);
-    return x == 0.0f ? __int_as_float(static_cast<int>(0x80000001u)) : __int_as_float(u + (u < 0 ? 1 : -1));
-}
-
-// A row's vectors lie on 16-byte boundaries: the first starts up to `head`
-// elements before the row.  What lies outside the row is not read, and -inf.
+// A vector of which elements [at, at + E) some lie outside the row: those are not
+// read, and -inf.
 template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T *row, int at, int V) {
+__device__ __noinline__ uint4 edge_vec(const T *row, int at, int V) {
     constexpr int E = Elem<T>::kPerVec;
-    if (at >= 0 && at + E <= V) return ld_stream(row + at);
     uint32_t w[4] = {Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord};
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -80,6 +82,14 @@ __device__ __forceinline__ uint4 load_vec(const T *row, int at, int V) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A row's vectors lie on 16-byte boundaries: the first starts up to `head`
+// elements before the row.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T *row, int at, int V) {
+    if (at >= 0 && at + Elem<T>::kPerVec <= V) return ld_stream(row + at);
+    return edge_vec(row, at, V);
+}
+
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -91,80 +101,129 @@ __device__ __forceinline__ X *remote(X *p) {
     return r;
 }
 
-// What a thread holds of a chunk.
-template <typename T>
-struct Held {
-    uint4 q[kVecs];
-    float top[kVecs];  // the vectors' maxima
-    int at;            // index of vector 0's first element; the others follow kThreads vectors apart
-    int end;           // first index past the slice (and the row)
+// The largest float below a finite x.
+__device__ __forceinline__ float below(float x) {
+    const int u = __float_as_int(x);
+    return x == 0.0f ? __int_as_float(static_cast<int>(0x80000001u)) : __int_as_float(u + (u < 0 ? 1 : -1));
+}
 
-    // fn(element, index) of those from `bar` on.
-    template <typename Fn>
-    __device__ __forceinline__ void from(float bar, Fn fn) const {
+// x in 16 bits, rounded up (a bf16 as it is), and back.
+__device__ __forceinline__ uint16_t up_bits(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return static_cast<uint16_t>((u + (u >> 31 ? 0u : 0xffffu)) >> 16);
+}
+
+__device__ __forceinline__ float of_bits(uint16_t u) { return __uint_as_float(static_cast<uint32_t>(u) << 16); }
+
+// The token whose rank is counted.
+struct Emitted {
+    int id;
+    float logit, under;  // under: the largest float below the logit
+
+    // How many of a vector's elements, from index `at` on, come before it: those
+    // above its logit, and equal ones ahead of it.
+    template <typename T>
+    __device__ __forceinline__ uint32_t before(const uint4 &q, int at, int end) const {
         constexpr int E = Elem<T>::kPerVec;
+        float f[E];
+        unpack<T>(q, f);
+        uint32_t n = 0;
+        if (logit == kNegInf || (at <= id && id < at + E)) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (!(top[i] >= bar)) continue;
-            uint4 u = q[i];
-            // Unpacked anew: kept from the sums, the floats would take 100 registers more.
-            asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
-            float f[E];
-            unpack<T>(u, f);
+            for (int k = 0; k < E; ++k) n += f[k] > logit || (f[k] == logit && at + k >= 0 && at + k < min(id, end));
+        } else {
+            const float bar = at < id ? under : logit;
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const int x = at + i * kThreads * E + k;
-                if (f[k] >= bar && x >= 0 && x < end) fn(f[k], x);
-            }
+            for (int k = 0; k < E; ++k) n += f[k] > bar;
+        }
+        return n;
+    }
+};
+
+// The row as vectors, and the slice's end.
+template <typename T>
+struct Slice {
+    const T *row;
+    int head, V, end;  // end: first element past the slice (and the row)
+
+    __device__ __forceinline__ int at(int vec) const { return vec * Elem<T>::kPerVec - head; }
+
+    // fn(element, key) of a vector's elements from `bar` on whose keys are above `least`.
+    template <typename Fn>
+    __device__ __forceinline__ void from(int vec, float bar, Key least, Fn fn) const {
+        constexpr int E = Elem<T>::kPerVec;
+        float f[E];
+        unpack<T>(load_vec(row, at(vec), V), f);
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const int x = at(vec) + k;
+            if (!(f[k] >= bar) || x < 0 || x >= end) continue;
+            const Key y = key_of(f[k], x);
+            if (y > least) fn(y);
         }
     }
 };
 
-// Brings the slice's list sh.mine up to date with a chunk.  All threads call it;
-// contains block barriers, the last thing it does is one.
+// Brings the slice's list sh.mine up to date with the chunk from vector v on, of
+// which a thread took `count`, with maximum `most`.  All threads call it; contains
+// block barriers, the last thing it does is one.
 template <typename T>
-__device__ __forceinline__ void take_first(Shared &sh, const Held<T> &h, float most, int top) {
+__device__ __forceinline__ void take_first(Shared &sh, const Slice<T> &slice, int v, int count, float most, int top) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int held = static_cast<int>(sh.n_mine);  // the last barrier was after its write
     float bar;
     Key least = 0;  // keys above it are candidates
+    if (tid < held) sh.cand[tid] = sh.mine[tid];
+    if (tid == 0) {
+        sh.n = held;
+        sh.n_queue = 0;
+    }
     if (held < top) {
         float g = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
         if (lane % 4 == 0) sh.group[tid / 4] = g;
         if (tid == 0) sh.bound = kNegInf;
         __syncthreads();
-        if (tid < kGroups) {
-            const float x = sh.group[tid];
-            int n = 0;
-#pragma unroll 8
-            for (int j = 0; j < kGroups; ++j) {
-                const float y = sh.group[j];
-                n += y > x || (y == x && j < tid);
-            }
-            if (n == top - 1) sh.bound = x;
+        // Four threads count for a group: those above it, and equal ones ahead of it.
+        const float x = sh.group[tid / 4];
+        int n = 0;
+#pragma unroll 4
+        for (int i = 0; i < kGroups / 4; ++i) {
+            const int j = i * 4 + tid % 4;
+            const float y = sh.group[j];
+            n += y > x || (y == x && j < tid / 4);
         }
-        if (tid < held) sh.cand[tid] = sh.mine[tid];
-        if (tid == 0) sh.n = held;
+        n += __shfl_xor_sync(0xffffffffu, n, 1);
+        n += __shfl_xor_sync(0xffffffffu, n, 2);
+        if (n == top - 1) sh.bound = x;
         __syncthreads();
         bar = sh.bound;
     } else {
         least = sh.mine[top - 1];
         bar = key_float(static_cast<uint32_t>(least >> 32));
-        if (tid < held) sh.cand[tid] = sh.mine[tid];
-        if (tid == 0) sh.n = held;
         __syncthreads();
     }
-    if (most >= bar)
-        h.from(bar, [&](float v, int x) {
-            const Key k = key_of(v, x);
-            if (k <= least) return;
-            const uint32_t n = atomicAdd(&sh.n, 1);
-            if (n < kCap) sh.cand[n] = k;
-        });
+    if (most >= bar) {
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+            if (!(of_bits(sh.top[i * kThreads + tid]) >= bar)) continue;
+            const uint32_t n = atomicAdd(&sh.n_queue, 1);
+            if (n < kQueue) sh.queue[n] = static_cast<uint16_t>(i * kThreads + tid);
+        }
+    }
+    __syncthreads();
+    const int vecs = static_cast<int>(sh.n_queue);
+    if (vecs <= kQueue) {
+#pragma unroll 1
+        for (int i = tid; i < vecs; i += kThreads)
+            slice.from(v + sh.queue[i], bar, least, [&](Key k) {
+                const uint32_t n = atomicAdd(&sh.n, 1);
+                if (n < kCap) sh.cand[n] = k;
+            });
+    }
     __syncthreads();
     const int n = static_cast<int>(sh.n);
-    if (n <= kCap) {
+    if (vecs <= kQueue && n <= kCap) {
         for (int i = tid; i < n; i += kThreads) {
             const Key x = sh.cand[i];
             int place = 0;
@@ -180,13 +239,16 @@ __device__ __forceinline__ void take_first(Shared &sh, const Held<T> &h, float m
     const Key old = tid < held ? sh.mine[tid] : 0;
     Key last = ~0ull;
     int k = 0;
+#pragma unroll 1
     for (; k < top; ++k) {
         Key best = old < last ? old : 0;
-        if (most >= bar)
-            h.from(bar, [&](float v, int x) {
-                const Key y = key_of(v, x);
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+            if (!(of_bits(sh.top[i * kThreads + tid]) >= bar)) continue;
+            slice.from(v + i * kThreads + tid, bar, 0, [&](Key y) {
                 if (y < last) best = max_key(best, y);
             });
+        }
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) best = max_key(best, __shfl_xor_sync(0xffffffffu, best, o));
         __syncthreads();
@@ -201,15 +263,27 @@ __device__ __forceinline__ void take_first(Shared &sh, const Held<T> &h, float m
     __syncthreads();
 }
 
+// Adds one part's sums to another's.
+__device__ __forceinline__ void join_part(Part &p, const Part &x, float c) {
+    const float top = fmaxf(p.m, x.m);
+    const float y0 = p.m == kNegInf ? kFar : fmaxf((p.m - top) * c, kFar), k0 = ex2(y0);
+    const float y1 = x.m == kNegInf ? kFar : fmaxf((x.m - top) * c, kFar), k1 = ex2(y1);
+    p.a = k0 * fmaf(p.z, y0, p.a) + k1 * fmaf(x.z, y1, x.a);
+    p.z = k0 * p.z + k1 * x.z;
+    p.m = top;
+    p.before += x.before;
+    p.bad |= x.bad;
+}
+
 // SOME: top > 0.
 template <typename T, bool SOME>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const LogprobArgs a) {
     constexpr int E = Elem<T>::kPerVec;
     __shared__ Shared sh;
     const int size = a.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long entry = blockIdx.x / static_cast<unsigned>(size);
+    const uint32_t entry = blockIdx.x / static_cast<uint32_t>(size);
     const int rank = static_cast<int>(blockIdx.x - entry * size);
-    const int b = static_cast<int>(entry / a.M), t = static_cast<int>(entry - static_cast<long long>(b) * a.M);
+    const int b = static_cast<int>(entry / a.M), t = static_cast<int>(entry - static_cast<uint32_t>(b) * a.M);
     const int token = a.tokens[entry];
     const int r = a.rows && token != -1 ? a.rows[entry] : t;
     if (token < 0 || token >= a.V || r < 0 || r >= a.N) {  // the whole cluster alike
@@ -222,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
             if (token != -1) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_TOKEN_RANGE));
         }
         if (SOME && tid < a.top) {
-            a.top_ids[entry * a.top + tid] = -1;
-            a.top_logprobs[entry * a.top + tid] = x;
+            a.top_ids[static_cast<long long>(entry) * a.top + tid] = -1;
+            a.top_logprobs[static_cast<long long>(entry) * a.top + tid] = x;
         }
         return;
     }
@@ -233,97 +307,107 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
     const int vecs = (head + a.V + E - 1) / E, per = (vecs + size - 1) / size;
     const int v0 = min(vecs, rank * per), v1 = min(vecs, v0 + per);
     const float lt = to_f32(row[token]), c = a.c;
-    // An element before the token comes before it from lt on, one after it above lt.
-    const bool lowest = lt == kNegInf;
-    const float under = lowest ? kNegInf : below(lt);
+    const Emitted emitted = {token, lt, lt == kNegInf ? kNegInf : below(lt)};
     float m = kNegInf;
-    float2 z = make_float2(0.0f, 0.0f), s = z;
+    F2 z = pair_of(0.0f, 0.0f), s = z;
+    const F2 c2 = pair_of(c, c);
+    // Vectors [inner0, inner1) of the slice lie in the row whole.
+    const int inner0 = head > 0 && v0 == 0 ? 1 : v0, inner1 = min(v1, (head + a.V) / E);
     uint32_t before = 0;
     bool odd = false;
-    if (tid == 0) sh.n_mine = sh.bad = 0;
-    __syncthreads();
+    const Slice<T> slice = {row, head, a.V, min(a.V, v1 * E - head)};
+    if (SOME) {
+        if (tid == 0) sh.n_mine = 0;
+        __syncthreads();
+    }
+#pragma unroll 1
     for (int v = v0; v < v1; v += kChunk) {
-        Held<T> h;
-        h.at = (v + tid) * E - head;
-        h.end = min(a.V, v1 * E - head);
+        float most = kNegInf;  // of the chunk
+        int count = 0;
+        auto batch = [&](int from, uint4 (&q)[kBatch]) {  // vectors from + i kThreads + tid
+            if (from >= inner0 && min(v1, from + kBatch * kThreads) <= inner1) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-            h.q[i] = v + i * kThreads + tid < v1 ? load_vec(row, h.at + i * kThreads * E, a.V) : neg_inf_vec<T>();
-        float top = kNegInf;
+                for (int i = 0; i < kBatch; ++i) {
+                    q[i] = neg_inf_vec<T>();
+                    if (from + i * kThreads + tid < v1) q[i] = ld_stream(row + slice.at(from + i * kThreads + tid));
+                }
+            } else {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            h.top[i] = batch_max1<T>(h.q[i]);
-            top = max_nan(top, h.top[i]);
-        }
-        odd |= !(top < INFINITY);
-        // ---- sums, against this thread's own reference
-        if (top > m) {
-            const float y = m == kNegInf ? kFar : fmaxf((m - top) * c, kFar), keep = ex2(y);
-            s = make_float2(keep * fmaf(z.x, y, s.x), keep * fmaf(z.y, y, s.y));
-            z = make_float2(keep * z.x, keep * z.y);
-            m = top;
-        }
-        const float ref = m == kNegInf ? 0.0f : m;
-        const float2 ref2 = make_float2(-ref, -ref), c2 = make_float2(c, c), none = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            float f[E];
-            unpack<T>(h.q[i], f);
-            const int at = h.at + i * kThreads * E;
-            const float bar = at + E <= token ? under : lt;
-#pragma unroll
-            for (int k = 0; k < E; k += 2) {
-                float2 y = fma2(add2(make_float2(f[k], f[k + 1]), ref2), c2, none);
-                y = make_float2(fmaxf(y.x, kFar), fmaxf(y.y, kFar));
-                const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                z = add2(z, e);
-                s = fma2(e, y, s);
+                for (int i = 0; i < kBatch; ++i) {
+                    const int x = from + i * kThreads + tid;
+                    q[i] = x < v1 ? load_vec(row, slice.at(x), a.V) : neg_inf_vec<T>();
+                }
             }
-            if (!(h.top[i] >= lt)) continue;  // nothing of the vector comes before the token
+        };
+        const int until = min(v1, v + kChunk);
+        uint4 q[kBatch], next[kBatch];
+        batch(v, next);
+#pragma unroll 1
+        for (; v + count * kThreads < until; count += kBatch) {
+            const int first = v + count * kThreads + tid;
 #pragma unroll
-            for (int k = 0; k < E; ++k) before += f[k] > bar;
-            if (lowest || (at <= token && token < at + E)) {  // equal ones before it
+            for (int i = 0; i < kBatch; ++i) q[i] = next[i];
+            if (v + (count + kBatch) * kThreads < until) batch(v + (count + kBatch) * kThreads, next);
+            float tops[kBatch], top = kNegInf;
 #pragma unroll
-                for (int k = 0; k < E; ++k)
-                    before += f[k] == lt && at + k >= 0 && at + k < min(token, h.end) && (lowest || at + E > token);
+            for (int i = 0; i < kBatch; ++i) {
+                tops[i] = batch_max1<T>(q[i]);
+                top = max_nan(top, tops[i]);
+                if (SOME) sh.top[(count + i) * kThreads + tid] = up_bits(tops[i]);
+            }
+            odd |= !(top < INFINITY);
+            most = fmaxf(most, top);
+            // ---- sums, against this thread's own reference
+            if (top > m) {
+                const float y = m == kNegInf ? kFar : fmaxf((m - top) * c, kFar), keep = ex2(y);
+                s = mul2(pair_of(keep, keep), fma2(z, pair_of(y, y), s));
+                z = mul2(pair_of(keep, keep), z);
+                m = top;
+            }
+            const float ref = m == kNegInf ? 0.0f : m;
+            const F2 ref2 = pair_of(-ref, -ref);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                float f[E];
+                unpack<T>(q[i], f);
+#pragma unroll
+                for (int k = 0; k < E; k += 2) {
+                    const float2 y = parts_of(mul2(add2(pair_of(f[k], f[k + 1]), ref2), c2));
+                    const F2 y2 = pair_of(fmaxf(y.x, kFar), fmaxf(y.y, kFar));
+                    const F2 e = pair_of(ex2(parts_of(y2).x), ex2(parts_of(y2).y));
+                    z = add2(z, e);
+                    s = fma2(e, y2, s);
+                }
+            }
+            if (top >= lt) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (tops[i] >= lt) before += emitted.before<T>(q[i], slice.at(first + i * kThreads), slice.end);
             }
         }
-        if (SOME) take_first<T>(sh, h, top, a.top);
+        if (SOME) take_first<T>(sh, slice, v, count, most, a.top);
     }
     // ---- the slice's sums
-    float most = m;
+    Part mine = {m, parts_of(z).x + parts_of(z).y, parts_of(s).x + parts_of(s).y, __reduce_add_sync(0xffffffffu, before),
+                 __any_sync(0xffffffffu, odd) ? kFlagNonFinite : 0u};
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (__any_sync(0xffffffffu, odd) && lane == 0) sh.bad = kFlagNonFinite;
-    if (lane == 0) sh.warp[0][warp] = most;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) most = fmaxf(most, sh.warp[0][w]);
-    float zs = z.x + z.y, as = s.x + s.y;
+    for (int o = 16; o > 0; o /= 2) mine.m = fmaxf(mine.m, __shfl_xor_sync(0xffffffffu, mine.m, o));
     {
-        const float y = m == kNegInf ? kFar : fmaxf((m - most) * c, kFar), keep = ex2(y);
-        as = keep * fmaf(zs, y, as);
-        zs *= keep;
+        const float y = m == kNegInf ? kFar : fmaxf((m - mine.m) * c, kFar), keep = ex2(y);
+        mine.a = keep * fmaf(mine.z, y, mine.a);
+        mine.z *= keep;
     }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
-        zs += __shfl_xor_sync(0xffffffffu, zs, o);
-        as += __shfl_xor_sync(0xffffffffu, as, o);
+        mine.z += __shfl_xor_sync(0xffffffffu, mine.z, o);
+        mine.a += __shfl_xor_sync(0xffffffffu, mine.a, o);
     }
-    before = __reduce_add_sync(0xffffffffu, before);
-    if (lane == 0) {
-        sh.warp[1][warp] = zs;
-        sh.warp[2][warp] = as;
-        sh.before[warp] = before;
-    }
+    if (lane == 0) sh.warp[warp] = mine;
     __syncthreads();
     cluster_wait();
     if (tid == 0) {
-        Part p = {most, 0.0f, 0.0f, 0, sh.bad};
-        for (int w = 0; w < kWarps; ++w) {
-            p.z += sh.warp[1][w];
-            p.a += sh.warp[2][w];
-            p.before += sh.before[w];
-        }
+        Part p = sh.warp[0];
+        for (int w = 1; w < kWarps; ++w) join_part(p, sh.warp[w], c);
         *remote(&sh.part[rank]) = p;
     }
     if (SOME && tid < a.top) *remote(&sh.list[rank][tid]) = tid < static_cast<int>(sh.n_mine) ? sh.mine[tid] : 0;
@@ -331,32 +415,22 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
     cluster_wait();
     if (rank) return;
     // ---- the row
-    float R = kNegInf, Z = 0.0f, A = 0.0f;
-    uint32_t bad = 0, place = 0;
-    for (int i = 0; i < size; ++i) {
-        R = fmaxf(R, sh.part[i].m);
-        bad |= sh.part[i].bad;
-    }
-    if (!bad && R == kNegInf) bad = kFlagAllNegInf;
-    for (int i = 0; i < size; ++i) {
-        const Part p = sh.part[i];
-        place += p.before;
-        const float y = p.m == kNegInf ? kFar : fmaxf((p.m - R) * c, kFar), keep = ex2(y);
-        A = fmaf(keep, fmaf(p.z, y, p.a), A);
-        Z = fmaf(keep, p.z, Z);
-    }
+    Part p = sh.part[0];
+    for (int i = 1; i < size; ++i) join_part(p, sh.part[i], c);
+    const float R = p.m, Z = p.z, A = p.a;
+    const uint32_t bad = p.bad ? p.bad : R == kNegInf ? kFlagAllNegInf : 0u;
     const float lz = log2f(Z);
     if (tid == 0) {
         if (bad) atomicOr(a.err, bad);
         a.logprob[entry] = bad ? NAN : (lt - R) * a.inv_t - kLn2 * lz;
         if (a.entropy) a.entropy[entry] = bad ? NAN : kLn2 * (lz - A / Z);
-        if (a.rank) a.rank[entry] = bad ? -1 : static_cast<int32_t>(place);
+        if (a.rank) a.rank[entry] = bad ? -1 : static_cast<int32_t>(p.before);
     }
     if (!SOME) return;
     if (bad) {
         if (tid < a.top) {
-            a.top_ids[entry * a.top + tid] = -1;
-            a.top_logprobs[entry * a.top + tid] = NAN;
+            a.top_ids[static_cast<long long>(entry) * a.top + tid] = -1;
+            a.top_logprobs[static_cast<long long>(entry) * a.top + tid] = NAN;
         }
         return;
     }
@@ -369,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
             for (int e = 0; e < a.top && sh.list[j][e] > x; ++e) ++k;
         }
         if (k >= a.top || x == 0) continue;
-        a.top_ids[entry * a.top + k] = static_cast<int32_t>(~static_cast<uint32_t>(x));
-        a.top_logprobs[entry * a.top + k] = (key_float(static_cast<uint32_t>(x >> 32)) - R) * a.inv_t - kLn2 * lz;
+        a.top_ids[static_cast<long long>(entry) * a.top + k] = static_cast<int32_t>(~static_cast<uint32_t>(x));
+        a.top_logprobs[static_cast<long long>(entry) * a.top + k] = (key_float(static_cast<uint32_t>(x >> 32)) - R) * a.inv_t - kLn2 * lz;
     }
 }
 
@@ -394,8 +468,7 @@ int launch_logprobs(LogprobArgs &a, int dtype, cudaStream_t st) {
     const int E = dtype == SPEC_F32 ? 4 : 8;
     const long long entries = static_cast<long long>(a.B) * a.M;
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && (a.V > a.cluster * kChunk * E || (a.V > a.cluster * kThreads * E && entries * a.cluster < 152 * 8)))
-        a.cluster *= 2;
+    while (a.cluster < kMaxCluster && a.V > a.cluster * kThreads * E && entries * a.cluster < 152 * kResident) a.cluster *= 2;
     if (dtype == SPEC_F32) return a.top ? launch_size<float, true>(a, st) : launch_size<float, false>(a, st);
     return a.top ? launch_size<uint16_t, true>(a, st) : launch_size<uint16_t, false>(a, st);
 }
