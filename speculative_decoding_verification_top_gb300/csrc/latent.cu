@@ -20,7 +20,9 @@
 //                    load gives the other lanes its second half); the query tile;
 //                    the results
 //   warp 4           loads tiles page by page (TMA), in slots of 128 columns
-//   warp 5           issues the products, S a tile ahead of O
+//   warps 5, 6       issue the products, S and O: each as soon as its operands are
+//                    there.  (One warp for both has O wait for the loads of the S
+//                    ahead of it: 3600 cycles a tile, of 2040 that the products take.)
 // latent_join_kernel joins the partial results of units cut between CTAs
 //
 // The work: a sequence's units are taken `width` at a time, by as many CTAs that go
@@ -38,7 +40,7 @@ namespace {
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots];     // the latent's slots
     unsigned long long r_full[kMaxRopes], r_empty[kMaxRopes]; // the rotary part's
-    unsigned long long q_full, s_full[2], p_full, pv_done, drained;
+    unsigned long long q_full, s_full[2], s_empty[2], p_full, pv_done, drained[2];
 };
 
 struct Shared {
@@ -49,7 +51,7 @@ struct Shared {
     int quit;            // the vote at which the softmax warps leave, or 0
     int fail[kAhead];    // per segment (mod kAhead): a page id out of range
     int odd;             // of the segment: cleaned elements that were not finite
-    float row[kRows];    // factors of the rows: of a rescaling, or 1 / l
+    alignas(16) float row[kRows];  // factors of the rows: of a rescaling, or 1 / l
 };
 
 template <int C>
@@ -66,6 +68,9 @@ struct Layout {
     static constexpr int kS = 256, kQ = 384;
     static_assert(kSlots >= 2 * kPairs && kRopes >= 2 && kRopes <= kMaxRopes, "S of a tile is made before O of the one before");
 };
+
+constexpr int kRotary = 64;     // rotary elements of a row
+constexpr int kFarAhead = 4;    // tiles between their prefetch and their load
 
 constexpr int kVoteBarrier = 1, kRowBarrier = 2;  // hardware barriers of the softmax warps
 constexpr int kSoftmax = 128;                     // their threads
@@ -125,7 +130,7 @@ __device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     constexpr int kParts = L::kInSmem * 8;  // 16-byte parts of a row
-#pragma unroll 4
+#pragma unroll 10
     for (int i = tid; i < kRows * kParts; i += kSoftmax) {
         const int row = i / kParts, part = i - row * kParts;
         const uint4 *q = query_row(a, g, row);
@@ -172,6 +177,34 @@ __device__ __forceinline__ uint32_t seen_columns(const LatentArgs &a, const Segm
     for (int i = 0; i < 32; ++i)
         if (m[i] == 0) s &= ~(1u << i);
     return s;
+}
+
+// A row's 32 weights 2^(v mul - ref), two bf16 a word; their sum.
+__device__ __forceinline__ float weights(const float (&v)[32], float mul, float ref, uint32_t (&w)[16]) {
+    F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
+    const F2 mul2 = pair_of(mul, mul), ref2 = pair_of(-ref, -ref);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const float2 y = parts_of(fma2(pair_of(v[c], v[c + 1]), mul2, ref2));
+        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        sum[c / 2 & 1] = add2(sum[c / 2 & 1], pair_of(e.x, e.y));
+        w[c / 2] = bf16_pair(e.x, e.y);
+    }
+    const float2 s = parts_of(add2(sum[0], sum[1]));
+    return s.x + s.y;
+}
+
+// The same, 0 where it does not see the position.
+__device__ __forceinline__ float weights(const float (&v)[32], float mul, float ref, uint32_t (&w)[16], uint32_t seen) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const float2 e = make_float2(seen >> c & 1u ? ex2(fmaf(v[c], mul, -ref)) : 0.0f,
+                                     seen >> (c + 1) & 1u ? ex2(fmaf(v[c + 1], mul, -ref)) : 0.0f);
+        sum += e.x + e.y;
+        w[c / 2] = bf16_pair(e.x, e.y);
+    }
+    return sum;
 }
 
 // Clears, in a tile that some rows do not see whole, the positions past the end
@@ -225,6 +258,32 @@ __device__ __noinline__ float odd_values(const LatentArgs &a, const Segment g, i
     return y;
 }
 
+// An element times its row's factor; 0 where the row sees nothing.
+__device__ __forceinline__ __nv_bfloat16 scaled(float y, float factor) {
+    return __float2bfloat16_rn(factor == 0.0f ? 0.0f : y * factor);
+}
+
+// Writes this lane's element of up to 32 rows (`left` are there): rounded, times the
+// row's factor, or as it is.
+template <int C>
+__device__ __forceinline__ void write_rows(__nv_bfloat16 *out, const float (&o)[32], int left, const float *factor) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(factor + k);
+        if (k < left) out[k * C] = scaled(o[k], f.x);
+        if (k + 1 < left) out[(k + 1) * C] = scaled(o[k + 1], f.y);
+        if (k + 2 < left) out[(k + 2) * C] = scaled(o[k + 2], f.z);
+        if (k + 3 < left) out[(k + 3) * C] = scaled(o[k + 3], f.w);
+    }
+}
+
+template <int C>
+__device__ __forceinline__ void write_rows(float *out, const float (&o)[32], int left, const float *) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        if (k < left) out[k * C] = o[k];
+}
+
 template <int C>
 __global__ void __launch_bounds__(kLatentThreads, 1)
     latent_kernel(const __grid_constant__ LatentKernelArgs ka, const __grid_constant__ CUtensorMap map) {
@@ -249,9 +308,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         bar_init(smem_addr(&bar.q_full), 4);
         bar_init(smem_addr(&bar.s_full[0]), 1);
         bar_init(smem_addr(&bar.s_full[1]), 1);
+        bar_init(smem_addr(&bar.s_empty[0]), 4);
+        bar_init(smem_addr(&bar.s_empty[1]), 4);
         bar_init(smem_addr(&bar.p_full), 4);
         bar_init(smem_addr(&bar.pv_done), 1);
-        bar_init(smem_addr(&bar.drained), 1);
+        bar_init(smem_addr(&bar.drained[0]), 1);
+        bar_init(smem_addr(&bar.drained[1]), 1);
         sh.dead = sh.quit = sh.odd = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_proxy();
@@ -273,6 +335,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     if (warp == 4) {
         // ---- loads: of each tile the rotary part, then the latent
         const int box = min(kTile, 1 << a.c.page_shift), boxes = kTile / box;  // positions of a copy, copies of a tile
+        const int turn = static_cast<int>(blockIdx.x) % p.width;
         uint32_t slot = 0, phase = 1, rope = 0, r_phase = 1, n = 0, rn = 0, seg = 0;
         bool live = true;
         for (; live && walk.next(&g); ++seg) {
@@ -283,10 +346,22 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 const int j = t * kTile + lane * box;
                 return t < g.t1 && lane < boxes && j < g.len ? table[j >> a.c.page_shift] : -2;
             };
-            int next = page_at(g.t0);
+            // The group's CTAs ask for its tiles, in turn, kFarAhead tiles before they
+            // are loaded: what a slot waits for is then L2, not memory.
+            auto ask = [&](int t, int id) {
+                if (t % p.width == turn && id >= 0 && id < a.c.num_pages) {
+                    const int y = (t * kTile + lane * box) & ((1 << a.c.page_shift) - 1);
+                    const long long at = (static_cast<long long>(id) << a.c.page_shift) + y;
+                    prefetch_l2(a.c.data + at * (C + kRotary), static_cast<uint32_t>(box) * (C + kRotary) * 2);
+                }
+            };
+            for (int t = g.t0 + 1; t < g.t0 + kFarAhead; ++t) ask(t, page_at(t));
+            int next = page_at(g.t0), far = page_at(g.t0 + kFarAhead);
             for (int t = g.t0; live && t < g.t1; ++t) {
                 int id = next;
                 next = page_at(t + 1);
+                ask(t + kFarAhead, far);
+                far = page_at(t + kFarAhead + 1);
                 if (id != -2 && (id < 0 || id >= a.c.num_pages)) {
                     sh.fail[seg % kAhead] = 1;
                     atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
@@ -325,66 +400,78 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 bar_drain(smem_addr(&bar.r_full[i % L::kRopes]), (i / L::kRopes) & 1);
         }
     } else if (warp == 5) {
-        // ---- products
+        // ---- S, rotary part first
         if (elect_one()) {
-            constexpr uint32_t kQk = mma_desc64(kTile), kPv = mma_desc(false, kRows, true, false), kHi = kMatrixHi<128>;
+            constexpr uint32_t kQk = mma_desc64(kTile), kHi = kMatrixHi<128>;
             const uint32_t q0 = matrix_lo(smem_addr(qt), 0), r0 = matrix_lo(smem_addr(ropes), 0);
-            const uint32_t k0 = matrix_lo(smem_addr(slots), 0), v0 = matrix_lo(smem_addr(slots), kBlock);
-            const uint32_t p0 = matrix_lo(smem_addr(pt), 0);
-            uint32_t slot = 0, phase = 0, rope = 0, r_phase = 0, vslot = 0, segs = 0, pn = 0, sn = 0;
+            const uint32_t k0 = matrix_lo(smem_addr(slots), 0);
+            uint32_t slot = 0, phase = 0, rope = 0, r_phase = 0, segs = 0, n = 0;
             bool live = true;
-            // S of the next tile, rotary part first
-            auto scores = [&] {
-                const uint32_t d = tmem + L::kS + (sn & 1) * kTile;
-                if (!(live = bar_wait(smem_addr(&bar.r_full[rope]), r_phase, dead))) return;
-                fence_after_sync();
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ss<false>(d, q0 + (((L::kInSmem - 1) * kBlock + k * 32) >> 4), kHi, r0 + ((rope * kBlock + k * 32) >> 4), kHi, kQk,
-                                  k > 0);
-                mma_commit(smem_addr(&bar.r_empty[rope]));
-                if (++rope == L::kRopes) rope = 0, r_phase ^= 1;
-#pragma unroll
-                for (int i = 0; i < L::kPairs; ++i) {
-                    if (!(live = bar_wait(smem_addr(&bar.full[slot]), phase, dead))) return;
-                    fence_after_sync();
-                    const uint32_t b = k0 + (slot * 2 * kBlock >> 4);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int block = 2 * i + k / 4;
-                        const uint32_t bk = b + ((k / 4 * kBlock + k % 4 * 32) >> 4);
-                        if (block < L::kInTmem)
-                            mma_ts(d, tmem + L::kQ + block * 32 + k % 4 * 8, bk, kHi, kQk, true);
-                        else
-                            mma_ss<false>(d, q0 + (((block - L::kInTmem) * kBlock + k % 4 * 32) >> 4), kHi, bk, kHi, kQk, true);
-                    }
-                    if (++slot == L::kSlots) slot = 0, phase ^= 1;
-                }
-                mma_commit(smem_addr(&bar.s_full[sn++ & 1]));
-            };
             while (live && walk.next(&g)) {
                 live = bar_wait(smem_addr(&bar.q_full), segs++ & 1, dead);
-                fence_after_sync();
-                if (live) scores();
-                for (int t = g.t0; live && t < g.t1; ++t) {
-                    if (t + 1 < g.t1) scores();
-                    if (!live || !(live = bar_wait(smem_addr(&bar.p_full), pn++ & 1, dead))) break;
+                for (int t = g.t0; live && t < g.t1; ++t, ++n) {
+                    if (!(live = bar_wait(smem_addr(&bar.s_empty[n & 1]), (n >> 1 & 1) ^ 1, dead))) break;
+                    const uint32_t d = tmem + L::kS + (n & 1) * kTile;
+                    if (!(live = bar_wait(smem_addr(&bar.r_full[rope]), r_phase, dead))) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss<false>(d, q0 + (((L::kInSmem - 1) * kBlock + k * 32) >> 4), kHi, r0 + ((rope * kBlock + k * 32) >> 4), kHi, kQk,
+                                      k > 0);
+                    mma_commit(smem_addr(&bar.r_empty[rope]));
+                    if (++rope == L::kRopes) rope = 0, r_phase ^= 1;
+#pragma unroll
+                    for (int i = 0; i < L::kPairs; ++i) {
+                        if (!(live = bar_wait(smem_addr(&bar.full[slot]), phase, dead))) break;
+                        fence_after_sync();
+                        const uint32_t b = k0 + (slot * 2 * kBlock >> 4);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int block = 2 * i + k / 4;
+                            const uint32_t bk = b + ((k / 4 * kBlock + k % 4 * 32) >> 4);
+                            if (block < L::kInTmem)
+                                mma_ts(d, tmem + L::kQ + block * 32 + k % 4 * 8, bk, kHi, kQk, true);
+                            else
+                                mma_ss<false>(d, q0 + (((block - L::kInTmem) * kBlock + k % 4 * 32) >> 4), kHi, bk, kHi, kQk, true);
+                        }
+                        if (++slot == L::kSlots) slot = 0, phase ^= 1;
+                    }
+                    if (!live) break;
+                    mma_commit(smem_addr(&bar.s_full[n & 1]));
+                }
+            }
+            if (!live) {  // products in flight end before TMEM is freed
+                mma_commit(smem_addr(&bar.drained[0]));
+                bar_drain(smem_addr(&bar.drained[0]), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ---- O^T
+        if (elect_one()) {
+            constexpr uint32_t kPv = mma_desc(false, kRows, true, false), kHi = kMatrixHi<128>;
+            const uint32_t v0 = matrix_lo(smem_addr(slots), kBlock), p0 = matrix_lo(smem_addr(pt), 0);
+            uint32_t slot = 0, n = 0;
+            bool live = true;
+            while (live && walk.next(&g)) {
+                for (int t = g.t0; t < g.t1; ++t) {
+                    if (!(live = bar_wait(smem_addr(&bar.p_full), n++ & 1, dead))) break;
                     fence_after_sync();
 #pragma unroll
                     for (int i = 0; i < L::kPairs; ++i) {
-                        const uint32_t v = v0 + (vslot * 2 * kBlock >> 4);
+                        const uint32_t v = v0 + (slot * 2 * kBlock >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_ss<false>(tmem + i * kRows, v + (k * 16 * 128 >> 4), kHi, p0 + (k * 32 >> 4), kHi, kPv, t > g.t0 || k > 0);
-                        mma_commit(smem_addr(&bar.empty[vslot]));
-                        if (++vslot == L::kSlots) vslot = 0;
+                        mma_commit(smem_addr(&bar.empty[slot]));
+                        if (++slot == L::kSlots) slot = 0;
                     }
                     mma_commit(smem_addr(&bar.pv_done));
                 }
             }
-            if (!live) {  // products in flight end before TMEM is freed
-                mma_commit(smem_addr(&bar.drained));
-                bar_drain(smem_addr(&bar.drained), 0);
+            if (!live) {
+                mma_commit(smem_addr(&bar.drained[1]));
+                bar_drain(smem_addr(&bar.drained[1]), 0);
             }
         }
         __syncwarp();
@@ -414,10 +501,18 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             const int quit = *reinterpret_cast<volatile int *>(&sh.quit);
             return quit != 0 && quit <= votes;
         };
-        for (; live && walk.next(&g); ++seg) {
-            stage_queries<C>(a, g, qt, tmem);
+        // The next segment's queries are laid down once the last scores are made, so
+        // that its first ones are made while this one's results are written.
+        Segment ahead;
+        auto more = [&] {
+            if (!walk.next(&ahead)) return false;
+            stage_queries<C>(a, ahead, qt, tmem);
             __syncwarp();
             if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
+            return true;
+        };
+        for (bool some = more(); live && some; ++seg) {
+            g = ahead;
             const bool has = row < g.rows;
             const int token = has ? (g.row0 + row) / a.H : 0;
             float m = kNegInf, l = 0.0f;
@@ -431,6 +526,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 float v[32];
                 tmem_load_halves<32>(tmem + lanes + L::kS + (n & 1) * kTile, v);
                 tmem_load_wait();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.s_empty[n & 1]));
                 float top[2] = {kNegInf, kNegInf};
                 if (whole) {
 #pragma unroll
@@ -481,23 +579,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 }
                 const float ref = m == kNegInf ? 0.0f : m;
                 uint32_t w[16];
-                {
-                    F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
-                    const F2 mul2 = pair_of(mul, mul), ref2 = pair_of(-ref, -ref);
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        float2 y = parts_of(fma2(pair_of(v[c], v[c + 1]), mul2, ref2));
-                        if (!whole) {
-                            y.x = seen >> c & 1u ? y.x : kNegInf;
-                            y.y = seen >> (c + 1) & 1u ? y.y : kNegInf;
-                        }
-                        y = make_float2(ex2(y.x), ex2(y.y));
-                        sum[c / 2 & 1] = add2(sum[c / 2 & 1], pair_of(y.x, y.y));
-                        w[c / 2] = bf16_pair(y.x, y.y);
-                    }
-                    const float2 s = parts_of(add2(sum[0], sum[1]));
-                    l += s.x + s.y;
-                }
+                if (whole)
+                    l += weights(v, mul, ref, w);
+                else
+                    l += weights(v, mul, ref, w, seen);
                 if (!free) waited(before, before_phase);
                 if (!whole && ok) {  // the products of S are done with the tile
                     const uint32_t fill = n * L::kPairs;
@@ -515,6 +600,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 if (lane == 0) bar_arrive(smem_addr(&bar.p_full));
             }
             if (!live) break;
+            some = more();
             waited(smem_addr(&bar.pv_done), (n - 1) & 1);
             fence_after_sync();
             l += __shfl_xor_sync(0xffffffffu, l, 16);
@@ -537,23 +623,27 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             if (tid == 0 && !alone && g.t0 == 0) p.head[blockIdx.x] = {g.b, g.row0, g.rows, g.parts};
             meet(kRowBarrier);
             // ---- the rows' results: a lane holds an element, of each row in turn
-            const long long row_at = static_cast<long long>(g.b) * a.N * a.H + g.row0;
+            const long long first = alone ? static_cast<long long>(g.b) * a.N * a.H + g.row0 : static_cast<long long>(part) * p.rc;
+#pragma unroll 1
             for (int c = 0; c < L::kPairs * 2; ++c) {
                 const int r0 = c % 2 * 32, d = c / 2 * 128 + warp * 32 + lane;
                 if (r0 >= g.rows) continue;
                 float o[32];
                 tmem_load32(tmem + lanes + c * 32, o);
                 tmem_load_wait();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    if (r0 + k >= g.rows) break;
-                    float y = o[k];
-                    if (odd) y += odd_values(a, g, r0 + k, d);
-                    if (alone) {
-                        const float f = sh.row[r0 + k];
-                        a.out[(row_at + r0 + k) * C + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : y * f);
-                    } else {
-                        p.o[(static_cast<long long>(part) * p.rc + r0 + k) * C + d] = y;
+                if (alone)
+                    write_rows<C>(a.out + (first + r0) * C + d, o, g.rows - r0, sh.row + r0);
+                else
+                    write_rows<C>(p.o + (first + r0) * C + d, o, g.rows - r0, sh.row + r0);
+                if (odd) {  // not finite: they decide an element whatever its finite part
+                    for (int k = 0; k < min(32, g.rows - r0); ++k) {
+                        const float y = odd_values(a, g, r0 + k, d);
+                        const long long at = (first + r0 + k) * C + d;
+                        if (y == 0.0f) continue;
+                        if (alone)
+                            a.out[at] = __float2bfloat16_rn(__bfloat162float(a.out[at]) + y);
+                        else
+                            p.o[at] += y;
                     }
                 }
             }
