@@ -19,10 +19,12 @@
 //                    accumulator of 64 rows fills 16 of a warp's 32 lanes; the
 //                    load gives the other lanes its second half); the query tile;
 //                    the results
-//   warp 4           loads tiles page by page (TMA), in slots of 128 columns
-//   warps 5, 6       issue the products, S and O: each as soon as its operands are
+//   warps 4, 5       issue the products, S and O: each as soon as its operands are
 //                    there.  (One warp for both has O wait for the loads of the S
 //                    ahead of it: 3600 cycles a tile, of 2040 that the products take.)
+//   warps 6-9        load tiles page by page (TMA), in slots of 128 columns: a thread's
+//                    wait, arrival and copy take 300 cycles whatever the copy's size,
+//                    so that one thread's nine copies a tile would be the bound
 // latent_join_kernel joins the partial results of units cut between CTAs
 //
 // The work: a sequence's units are taken `width` at a time, by as many CTAs that go
@@ -69,8 +71,8 @@ struct Layout {
     static_assert(kSlots >= 2 * kPairs && kRopes >= 2 && kRopes <= kMaxRopes, "S of a tile is made before O of the one before");
 };
 
-constexpr int kRotary = 64;     // rotary elements of a row
-constexpr int kFarAhead = 4;    // tiles between their prefetch and their load
+constexpr int kScores = 4, kValues = 5, kLoaders = 6;  // the warps that issue products, and the first that loads
+constexpr int kBoxes = 4;                              // pages of a tile, at most
 
 constexpr int kVoteBarrier = 1, kRowBarrier = 2;  // hardware barriers of the softmax warps
 constexpr int kSoftmax = 128;                     // their threads
@@ -315,10 +317,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         bar_init(smem_addr(&bar.drained[0]), 1);
         bar_init(smem_addr(&bar.drained[1]), 1);
         sh.dead = sh.quit = sh.odd = 0;
+        for (int i = 0; i < kAhead; ++i) sh.fail[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_proxy();
     }
-    if (warp == 5) tmem_alloc(smem_addr(&sh.tmem), 512);
+    if (warp == kScores) tmem_alloc(smem_addr(&sh.tmem), 512);
     // Up to here this may run beside the kernel before it.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -332,74 +335,70 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     Walk walk(p, from, to, sh.begin);
     Segment g;
 
-    if (warp == 4) {
-        // ---- loads: of each tile the rotary part, then the latent
-        const int box = min(kTile, 1 << a.c.page_shift), boxes = kTile / box;  // positions of a copy, copies of a tile
-        const int turn = static_cast<int>(blockIdx.x) % p.width;
-        uint32_t slot = 0, phase = 1, rope = 0, r_phase = 1, n = 0, rn = 0, seg = 0;
-        bool live = true;
-        for (; live && walk.next(&g); ++seg) {
-            if (lane == 0) sh.fail[seg % kAhead] = 0;
-            __syncwarp();
-            const int32_t *table = a.table + static_cast<long long>(g.b) * a.width;
-            auto page_at = [&](int t) {  // this lane's page of tile t; -2: none
-                const int j = t * kTile + lane * box;
-                return t < g.t1 && lane < boxes && j < g.len ? table[j >> a.c.page_shift] : -2;
-            };
-            // The group's CTAs ask for its tiles, in turn, kFarAhead tiles before they
-            // are loaded: what a slot waits for is then L2, not memory.
-            auto ask = [&](int t, int id) {
-                if (t % p.width == turn && id >= 0 && id < a.c.num_pages) {
-                    const int y = (t * kTile + lane * box) & ((1 << a.c.page_shift) - 1);
-                    const long long at = (static_cast<long long>(id) << a.c.page_shift) + y;
-                    prefetch_l2(a.c.data + at * (C + kRotary), static_cast<uint32_t>(box) * (C + kRotary) * 2);
-                }
-            };
-            for (int t = g.t0 + 1; t < g.t0 + kFarAhead; ++t) ask(t, page_at(t));
-            int next = page_at(g.t0), far = page_at(g.t0 + kFarAhead);
-            for (int t = g.t0; live && t < g.t1; ++t) {
-                int id = next;
-                next = page_at(t + 1);
-                ask(t + kFarAhead, far);
-                far = page_at(t + kFarAhead + 1);
-                if (id != -2 && (id < 0 || id >= a.c.num_pages)) {
-                    sh.fail[seg % kAhead] = 1;
-                    atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
-                    id = -1;
-                }
-                const bool here = id >= 0;
-                const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, here)) * box) * 128u;
-                const int y = (t * kTile + lane * box) & ((1 << a.c.page_shift) - 1);
-                for (int i = -1; i < L::kPairs; ++i) {
-                    const uint32_t full = i < 0 ? smem_addr(&bar.r_full[rope]) : smem_addr(&bar.full[slot]);
-                    live = i < 0 ? bar_wait(smem_addr(&bar.r_empty[rope]), r_phase, dead)
-                                 : bar_wait(smem_addr(&bar.empty[slot]), phase, dead);
-                    live = __all_sync(0xffffffffu, live);
-                    if (!live) break;
-                    if (lane == 0) bar_arrive_tx(full, i < 0 ? bytes : 2 * bytes);
-                    __syncwarp();
-                    const uint32_t dst = smem_addr(i < 0 ? ropes + rope * kBlock : slots + slot * 2 * kBlock) + lane * box * 128;
-                    if (here) {
-                        tma_load(dst, &map, full, i < 0 ? C : i * 128, y, id);
-                        if (i >= 0) tma_load(dst + kBlock, &map, full, i * 128 + 64, y, id);
+    if (warp >= kLoaders) {
+        // ---- loads: of each tile the rotary part and the latent, by slots in turn
+        if (elect_one()) {
+            const uint32_t mine = warp - kLoaders;
+            const int box = min(kTile, 1 << a.c.page_shift), boxes = kTile / box;  // positions of a copy, copies of a tile
+            uint32_t seg = 0, n = 0, uses = 0, r_uses = 0;  // segments and tiles so far; uses of the rings
+            bool live = true;
+            for (; live && walk.next(&g); ++seg) {
+                const int32_t *table = a.table + static_cast<long long>(g.b) * a.width;
+                int next[kBoxes];
+                auto fetch = [&](int t) {  // the pages of tile t; -2: none
+#pragma unroll
+                    for (int k = 0; k < kBoxes; ++k) {
+                        const int j = t * kTile + k * box;
+                        next[k] = k < boxes && t < g.t1 && j < g.len ? table[j >> a.c.page_shift] : -2;
                     }
-                    if (i < 0) {
-                        ++rn;
-                        if (++rope == L::kRopes) rope = 0, r_phase ^= 1;
-                    } else {
-                        ++n;
-                        if (++slot == L::kSlots) slot = 0, phase ^= 1;
+                };
+                fetch(g.t0);
+                for (int t = g.t0; live && t < g.t1; ++t, ++n) {
+                    int id[kBoxes];
+                    uint32_t bytes = 0;
+                    bool bad = false;
+#pragma unroll
+                    for (int k = 0; k < kBoxes; ++k) {
+                        const bool in = next[k] >= 0 && next[k] < a.c.num_pages;
+                        id[k] = in ? next[k] : -1;
+                        bad |= !in && next[k] != -2;
+                        if (in) bytes += box * 128u;
+                    }
+                    fetch(t + 1);
+                    const int y = (t * kTile) & ((1 << a.c.page_shift) - 1);  // 0 where a tile has several pages
+                    for (uint32_t i = 0; i <= L::kPairs; ++i) {  // the rotary part, then its slots
+                        const bool rotary = i == 0;
+                        const uint32_t use = rotary ? n : n * L::kPairs + i - 1, ring = rotary ? L::kRopes : L::kSlots;
+                        if (use % kLoadWarps != mine) continue;
+                        const uint32_t slot = use % ring, full = smem_addr(rotary ? &bar.r_full[slot] : &bar.full[slot]);
+                        live = bar_wait(smem_addr(rotary ? &bar.r_empty[slot] : &bar.empty[slot]), (use / ring & 1) ^ 1, dead);
+                        if (!live) break;
+                        (rotary ? r_uses : uses) = use + 1;
+                        if (bad) {  // by one whose part of the tile is waited for
+                            *reinterpret_cast<volatile int *>(&sh.fail[seg % kAhead]) = 1;
+                            atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_PAGE_RANGE));
+                        }
+                        bar_arrive_tx(full, rotary ? bytes : 2 * bytes);
+                        const uint32_t dst = smem_addr(rotary ? ropes + slot * kBlock : slots + slot * 2 * kBlock);
+                        const int x = rotary ? C : static_cast<int>(i - 1) * 128;
+#pragma unroll
+                        for (int k = 0; k < kBoxes; ++k) {
+                            if (id[k] < 0) continue;
+                            tma_load(dst + k * box * 128, &map, full, x, y, id[k]);
+                            if (!rotary) tma_load(dst + kBlock + k * box * 128, &map, full, x + 64, y, id[k]);
+                        }
                     }
                 }
             }
+            if (!live) {  // the copies in flight land before the CTA's memory goes
+                for (uint32_t i = uses > L::kSlots ? uses - L::kSlots : 0; i < uses; ++i)
+                    if (i % kLoadWarps == mine) bar_drain(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
+                for (uint32_t i = r_uses > L::kRopes ? r_uses - L::kRopes : 0; i < r_uses; ++i)
+                    if (i % kLoadWarps == mine) bar_drain(smem_addr(&bar.r_full[i % L::kRopes]), (i / L::kRopes) & 1);
+            }
         }
-        if (!live) {  // the copies in flight land before the CTA's memory goes
-            for (uint32_t i = n > L::kSlots ? n - L::kSlots : 0; i < n; ++i)
-                bar_drain(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
-            for (uint32_t i = rn > L::kRopes ? rn - L::kRopes : 0; i < rn; ++i)
-                bar_drain(smem_addr(&bar.r_full[i % L::kRopes]), (i / L::kRopes) & 1);
-        }
-    } else if (warp == 5) {
+        __syncwarp();
+    } else if (warp == kScores) {
         // ---- S, rotary part first
         if (elect_one()) {
             constexpr uint32_t kQk = mma_desc64(kTile), kHi = kMatrixHi<128>;
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == kValues) {
         // ---- O^T
         if (elect_one()) {
             constexpr uint32_t kPv = mma_desc(false, kRows, true, false), kHi = kMatrixHi<128>;
@@ -649,14 +648,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
             fence_before_sync();
             meet(kRowBarrier);
-            if (tid == 0) sh.odd = 0;  // before its next vote, after which the others may set it
+            if (tid == 0) sh.fail[seg % kAhead] = sh.odd = 0;  // before its next vote, after which the others may set it
         }
         if (!live && tid == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
     }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (warp == 5) tmem_free(tmem, 512);
+    if (warp == kScores) tmem_free(tmem, 512);
 }
 
 constexpr int kJoinThreads = 256;
