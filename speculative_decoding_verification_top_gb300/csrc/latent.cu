@@ -22,9 +22,10 @@
 //   warps 4, 5       issue the products, S and O: each as soon as its operands are
 //                    there.  (One warp for both has O wait for the loads of the S
 //                    ahead of it: 3600 cycles a tile, of 2040 that the products take.)
-//   warps 6-9        load tiles page by page (TMA), in slots of 128 columns: a thread's
-//                    wait, arrival and copy take 300 cycles whatever the copy's size,
-//                    so that one thread's nine copies a tile would be the bound
+//   warps 6-9, 10    load tiles page by page (TMA), in slots of 128 columns, and the
+//                    rotary part: a thread's wait, arrival and copy take 300 cycles
+//                    whatever the copy's size, and one thread's nine copies a tile
+//                    would be the bound
 // latent_join_kernel joins the partial results of units cut between CTAs
 //
 // The work: a sequence's units are taken `width` at a time, by as many CTAs that go
@@ -42,7 +43,7 @@ namespace {
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots];     // the latent's slots
     unsigned long long r_full[kMaxRopes], r_empty[kMaxRopes]; // the rotary part's
-    unsigned long long q_full, s_full[2], s_empty[2], p_full, pv_done, drained[2];
+    unsigned long long q_full, s_full[2], s_empty[2], p_full[2], pv_done[2], drained[2];
 };
 
 struct Shared {
@@ -61,14 +62,14 @@ struct Layout {
     static constexpr int kPairs = C / 128;                       // slots a tile, and accumulators of 128 elements
     static constexpr int kInTmem = C == 512 ? 4 : 0;             // 64-column blocks of Q in TMEM
     static constexpr int kInSmem = C / 64 + 1 - kInTmem;         // and in shared memory, the rotary one last
-    static constexpr int kRopes = C == 512 ? 2 : C == 256 ? 5 : 8;
-    static constexpr int kFixed = (kInSmem + 1 + kRopes) * kBlock + static_cast<int>((sizeof(Shared) + 127) / 128 * 128);
+    static constexpr int kRopes = C == 512 ? 1 : C == 256 ? 4 : 7;
+    static constexpr int kFixed = (kInSmem + 2 + kRopes) * kBlock + static_cast<int>((sizeof(Shared) + 127) / 128 * 128);
     static constexpr int kRoom = (kSmemMax - kFixed) / (2 * kBlock);
     static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
     static constexpr int kBytes = kFixed + kSlots * 2 * kBlock;
     // TMEM columns: O^T from 0, two S, Q
     static constexpr int kS = 256, kQ = 384;
-    static_assert(kSlots >= 2 * kPairs && kRopes >= 2 && kRopes <= kMaxRopes, "S of a tile is made before O of the one before");
+    static_assert(kSlots >= 2 * kPairs && kRopes <= kMaxRopes, "S of a tile is made before O of the one before");
 };
 
 constexpr int kScores = 4, kValues = 5, kLoaders = 6;  // the warps that issue products, and the first that loads
@@ -124,31 +125,46 @@ __device__ __forceinline__ const uint4 *query_row(const LatentArgs &a, const Seg
                                            static_cast<long long>(r - n * a.H) * (a.c.C + a.c.R));
 }
 
-// The segment's query tile, zeros past its rows; the scale's sign goes into it.
+// The segment's query tile, zeros past its rows; the scale's sign goes into it.  A
+// warp takes 16 rows.
 template <int C>
 __device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment &g, uint8_t *tile, uint32_t tmem) {
     using L = Layout<C>;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    constexpr int kParts = L::kInSmem * 8;  // 16-byte parts of a row
-#pragma unroll 10
-    for (int i = tid; i < kRows * kParts; i += kSoftmax) {
-        const int row = i / kParts, part = i - row * kParts;
-        const uint4 *q = query_row(a, g, row);
-        uint4 u = q ? __ldg(q + L::kInTmem * 8 + part) : zero;
-        u = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
-        *reinterpret_cast<uint4 *>(tile + part / 8 * kBlock + swizzled<128>(row, part % 8 * 16)) = u;
-    }
+    const uint4 *q = query_row(a, g, warp * 16 + (lane & 15));
+    uint4 head[L::kInTmem > 0 ? 16 : 1];
     if constexpr (L::kInTmem > 0) {
         // Lanes 0-15 hold a row's columns from 0 on (two elements a column), 16-31 from 64.
-        const uint4 *q = query_row(a, g, warp * 16 + (lane & 15));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) head[i] = q ? __ldg(q + (lane >> 4) * 16 + i) : zero;
+    }
+    constexpr int kParts = L::kInSmem * 8, kTurns = kParts / 2, kBatch = kTurns / 4;  // 16-byte parts of a row, turns of a warp
+    const unsigned long long at = reinterpret_cast<unsigned long long>(q);
+#pragma unroll
+    for (int i0 = 0; i0 < kTurns; i0 += kBatch) {
+        uint4 u[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int x = (i0 + i) * 32 + lane, row = x / kParts, part = x - row * kParts;
+            const uint4 *from = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, at, row));
+            u[i] = from ? __ldg(from + L::kInTmem * 8 + part) : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int x = (i0 + i) * 32 + lane, row = x / kParts, part = x - row * kParts;
+            *reinterpret_cast<uint4 *>(tile + part / 8 * kBlock + swizzled<128>(warp * 16 + row, part % 8 * 16)) =
+                make_uint4(u[i].x ^ flip, u[i].y ^ flip, u[i].z ^ flip, u[i].w ^ flip);
+        }
+    }
+    if constexpr (L::kInTmem > 0) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint4 u = q ? __ldg(q + (lane >> 4) * 16 + k * 8 + i) : zero;
+                const uint4 u = head[k * 8 + i];
                 w[4 * i] = u.x ^ flip;
                 w[4 * i + 1] = u.y ^ flip;
                 w[4 * i + 2] = u.z ^ flip;
@@ -293,7 +309,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const LatentArgs &a = ka.a;
     const LatentPlan &p = ka.p;
-    uint8_t *qt = smem, *pt = qt + L::kInSmem * kBlock, *ropes = pt + kBlock, *slots = ropes + L::kRopes * kBlock;
+    uint8_t *qt = smem, *pt = qt + L::kInSmem * kBlock, *ropes = pt + 2 * kBlock, *slots = ropes + L::kRopes * kBlock;
     Shared &sh = *reinterpret_cast<Shared *>(slots + L::kSlots * 2 * kBlock);
     Barriers &bar = sh.bar;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -308,14 +324,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             bar_init(smem_addr(&bar.r_empty[i]), 1);
         }
         bar_init(smem_addr(&bar.q_full), 4);
-        bar_init(smem_addr(&bar.s_full[0]), 1);
-        bar_init(smem_addr(&bar.s_full[1]), 1);
-        bar_init(smem_addr(&bar.s_empty[0]), 4);
-        bar_init(smem_addr(&bar.s_empty[1]), 4);
-        bar_init(smem_addr(&bar.p_full), 4);
-        bar_init(smem_addr(&bar.pv_done), 1);
-        bar_init(smem_addr(&bar.drained[0]), 1);
-        bar_init(smem_addr(&bar.drained[1]), 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_addr(&bar.s_full[i]), 1);
+            bar_init(smem_addr(&bar.s_empty[i]), 4);
+            bar_init(smem_addr(&bar.p_full[i]), 4);
+            bar_init(smem_addr(&bar.pv_done[i]), 1);
+            bar_init(smem_addr(&bar.drained[i]), 1);
+        }
         sh.dead = sh.quit = sh.odd = 0;
         for (int i = 0; i < kAhead; ++i) sh.fail[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     for (uint32_t i = 0; i <= L::kPairs; ++i) {  // the rotary part, then its slots
                         const bool rotary = i == 0;
                         const uint32_t use = rotary ? n : n * L::kPairs + i - 1, ring = rotary ? L::kRopes : L::kSlots;
-                        if (use % kLoadWarps != mine) continue;
+                        if (mine != (rotary ? kRopeLoader : use % kRopeLoader)) continue;
                         const uint32_t slot = use % ring, full = smem_addr(rotary ? &bar.r_full[slot] : &bar.full[slot]);
                         live = bar_wait(smem_addr(rotary ? &bar.r_empty[slot] : &bar.empty[slot]), (use / ring & 1) ^ 1, dead);
                         if (!live) break;
@@ -392,9 +407,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
             if (!live) {  // the copies in flight land before the CTA's memory goes
                 for (uint32_t i = uses > L::kSlots ? uses - L::kSlots : 0; i < uses; ++i)
-                    if (i % kLoadWarps == mine) bar_drain(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
+                    if (i % kRopeLoader == mine) bar_drain(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
                 for (uint32_t i = r_uses > L::kRopes ? r_uses - L::kRopes : 0; i < r_uses; ++i)
-                    if (i % kLoadWarps == mine) bar_drain(smem_addr(&bar.r_full[i % L::kRopes]), (i / L::kRopes) & 1);
+                    bar_drain(smem_addr(&bar.r_full[i % L::kRopes]), (i / L::kRopes) & 1);
             }
         }
         __syncwarp();
@@ -453,19 +468,20 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             uint32_t slot = 0, n = 0;
             bool live = true;
             while (live && walk.next(&g)) {
-                for (int t = g.t0; t < g.t1; ++t) {
-                    if (!(live = bar_wait(smem_addr(&bar.p_full), n++ & 1, dead))) break;
+                for (int t = g.t0; t < g.t1; ++t, ++n) {
+                    if (!(live = bar_wait(smem_addr(&bar.p_full[n & 1]), n >> 1 & 1, dead))) break;
                     fence_after_sync();
+                    const uint32_t pn = p0 + ((n & 1) * kBlock >> 4);
 #pragma unroll
                     for (int i = 0; i < L::kPairs; ++i) {
                         const uint32_t v = v0 + (slot * 2 * kBlock >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_ss<false>(tmem + i * kRows, v + (k * 16 * 128 >> 4), kHi, p0 + (k * 32 >> 4), kHi, kPv, t > g.t0 || k > 0);
+                            mma_ss<false>(tmem + i * kRows, v + (k * 16 * 128 >> 4), kHi, pn + (k * 32 >> 4), kHi, kPv, t > g.t0 || k > 0);
                         mma_commit(smem_addr(&bar.empty[slot]));
                         if (++slot == L::kSlots) slot = 0;
                     }
-                    mma_commit(smem_addr(&bar.pv_done));
+                    mma_commit(smem_addr(&bar.pv_done[n & 1]));
                 }
             }
             if (!live) {
@@ -546,8 +562,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 }
                 const float most = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], 16));
                 const bool up = most > m + kSlack;
-                const uint32_t before = smem_addr(&bar.pv_done), before_phase = (n - 1) & 1;
-                bool free = t == g.t0;  // the tile before is multiplied
                 if (vote(up)) {
                     if (leaving()) {
                         live = false;
@@ -557,9 +571,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     const float keep = up ? ex2(m - most) : 1.0f;
                     if (up) m = most;
                     l *= keep;
-                    if (!free) {
-                        waited(before, before_phase);
-                        free = true;
+                    if (t > g.t0) {
+                        waited(smem_addr(&bar.pv_done[(n - 1) & 1]), (n - 1) >> 1 & 1);
                         fence_after_sync();
                         if (half == 0) sh.row[row] = keep;
                         meet(kRowBarrier);
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     l += weights(v, mul, ref, w);
                 else
                     l += weights(v, mul, ref, w, seen);
-                if (!free) waited(before, before_phase);
+                waited(smem_addr(&bar.pv_done[n & 1]), (n >> 1 & 1) ^ 1);  // of two tiles before
                 if (!whole && ok) {  // the products of S are done with the tile
                     const uint32_t fill = n * L::kPairs;
                     for (uint32_t i = fill; i < fill + L::kPairs; ++i)
@@ -591,16 +604,16 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(pt + swizzled<128>(row, half * 64 + i * 16)) =
+                    *reinterpret_cast<uint4 *>(pt + (n & 1) * kBlock + swizzled<128>(row, half * 64 + i * 16)) =
                         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 fence_async_proxy();
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) bar_arrive(smem_addr(&bar.p_full));
+                if (lane == 0) bar_arrive(smem_addr(&bar.p_full[n & 1]));
             }
             if (!live) break;
             some = more();
-            waited(smem_addr(&bar.pv_done), (n - 1) & 1);
+            waited(smem_addr(&bar.pv_done[(n - 1) & 1]), (n - 1) >> 1 & 1);
             fence_after_sync();
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             // All warps are past the segment's tiles: what they and the loads noted is there.

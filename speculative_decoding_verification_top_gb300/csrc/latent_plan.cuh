@@ -11,7 +11,7 @@ namespace specv {
 constexpr int kTile = 64;             // positions a tile
 constexpr int kRows = 64;             // query rows a unit
 constexpr int kBlock = 64 * 128;      // bytes of 64 rows of 64 columns
-constexpr int kLoadWarps = 4;
+constexpr int kLoadWarps = 5, kRopeLoader = kLoadWarps - 1;
 constexpr int kLatentThreads = 192 + 32 * kLoadWarps;
 constexpr int kMaxSlots = 16, kMaxRopes = 8;
 constexpr int kAhead = 32;            // segments that the loads may be ahead, and more
