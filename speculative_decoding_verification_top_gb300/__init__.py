@@ -429,9 +429,15 @@ def spec_verify_status_string(status):
 
 # ------------------------------------------------- torch tensor helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t):
@@ -755,7 +761,8 @@ def _tokens(t, name, H, D, dtypes):
     """[B, N, H, D] with packed tokens; returns their stride in elements.
     Consecutive tokens may lie further apart (slices of a wider projection),
     evenly over the whole batch."""
-    if t.dtype not in dtypes or t.dim() != 4 or t.shape[2:] != (H, D) or not t.is_cuda:
+    shape = t.shape
+    if t.dtype not in dtypes or len(shape) != 4 or shape[2] != H or shape[3] != D or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor [B, N, %d, %d] of %s, got %s %s"
                          % (name, H, D, "/".join(map(str, dtypes)), t.dtype, tuple(t.shape)))
     if t.is_contiguous():
@@ -925,9 +932,9 @@ def kv_append_rope(cache, page_table, starts, k, v, freqs, q=None, rows=None, po
     c = cache.descriptor
     H, D = c.Hkv, c.D
     step = _tokens(k, "k", H, D, (torch.bfloat16, torch.float32))
-    if _tokens(v, "v", H, D, (k.dtype,)) != step or v.shape != k.shape:
+    if v.shape != k.shape or _tokens(v, "v", H, D, (k.dtype,)) != step:
         raise ValueError("k and v must have one shape and token stride")
-    B, N = k.shape[:2]
+    B, N, _, _ = k.shape
     device = k.get_device()
     if v.get_device() != device or cache.k.get_device() != device:
         raise ValueError("k, v and the cache must be on one device")

@@ -33,6 +33,7 @@ constexpr int kChunk = kThreads * kVecs;
 constexpr int kGroups = kThreads / 4;  // groups of threads whose maxima bound the first chunk
 constexpr int kQueue = 512;            // vectors of a chunk that may hold candidates
 constexpr int kCap = 1024;             // candidates kept of a chunk
+constexpr int kTies = SPEC_MAX_TOP * 8;  // equal ones among them that are taken at a time, at most
 constexpr int kMaxCluster = 8;
 constexpr int kResident = 3;           // CTAs a multiprocessor has room for
 constexpr float kLn2 = 0.6931471805599453f;
@@ -54,6 +55,7 @@ struct Shared {
     uint16_t queue[kQueue];
     float group[kGroups];
     Part warp[kWarps];
+    uint32_t ties[kWarps];
     uint32_t n, n_mine, n_queue;
     float bound;
 };
@@ -106,6 +108,9 @@ __device__ __forceinline__ float below(float x) {
     const int u = __float_as_int(x);
     return x == 0.0f ? __int_as_float(static_cast<int>(0x80000001u)) : __int_as_float(u + (u < 0 ? 1 : -1));
 }
+
+// The smallest float above x; +inf above the largest finite one.
+__device__ __forceinline__ float above(float x) { return -below(-x); }
 
 // x in 16 bits, rounded up (a bf16 as it is), and back.
 __device__ __forceinline__ uint16_t up_bits(float x) {
@@ -203,27 +208,65 @@ __device__ __forceinline__ void take_first(Shared &sh, const Slice<T> &slice, in
         bar = key_float(static_cast<uint32_t>(least >> 32));
         __syncthreads();
     }
-    if (most >= bar) {
+    // Candidates: the elements from the bar on, or (where equal logits make those too
+    // many, as in a masked row) above it, then equal ones by index until there are
+    // `top`.
+    bool fits = false, ties = false;
 #pragma unroll 1
-        for (int i = 0; i < count; ++i) {
-            if (!(of_bits(sh.top[i * kThreads + tid]) >= bar)) continue;
-            const uint32_t n = atomicAdd(&sh.n_queue, 1);
-            if (n < kQueue) sh.queue[n] = static_cast<uint16_t>(i * kThreads + tid);
+    for (int pass = 0; pass < 2 && !fits; ++pass) {
+        ties = pass == 1;
+        if (ties) {
+            __syncthreads();
+            if (tid == 0) {
+                sh.n = held;
+                sh.n_queue = 0;
+            }
+            __syncthreads();
+        }
+        const float from = ties ? above(bar) : bar;
+        if (most >= from) {
+#pragma unroll 1
+            for (int i = 0; i < count; ++i) {
+                if (!(of_bits(sh.top[i * kThreads + tid]) >= from)) continue;
+                const uint32_t n = atomicAdd(&sh.n_queue, 1);
+                if (n < kQueue) sh.queue[n] = static_cast<uint16_t>(i * kThreads + tid);
+            }
+        }
+        __syncthreads();
+        const int vecs = static_cast<int>(sh.n_queue);
+        if (vecs <= kQueue) {
+#pragma unroll 1
+            for (int i = tid; i < vecs; i += kThreads)
+                slice.from(v + sh.queue[i], from, least, [&](Key k) {
+                    const uint32_t n = atomicAdd(&sh.n, 1);
+                    if (n < kCap) sh.cand[n] = k;
+                });
+        }
+        __syncthreads();
+        fits = vecs <= kQueue && static_cast<int>(sh.n) <= (ties ? kCap - kTies : kCap);
+    }
+    if (fits && ties) {
+        const uint32_t equal = okey<float>(bar);
+#pragma unroll 1
+        for (int i = 0; i < count && static_cast<int>(sh.n) < top; ++i) {  // sh.n as the last barrier left it
+            const bool near = of_bits(sh.top[i * kThreads + tid]) >= bar;
+            bool some = false;
+            if (near)
+                slice.from(v + i * kThreads + tid, bar, least, [&](Key k) { some |= static_cast<uint32_t>(k >> 32) == equal; });
+            const uint32_t mask = __ballot_sync(0xffffffffu, some);
+            if (lane == 0) sh.ties[warp] = static_cast<uint32_t>(__popc(mask));
+            __syncthreads();
+            int place = __popc(mask & ((1u << lane) - 1u));
+            for (int w = 0; w < warp; ++w) place += static_cast<int>(sh.ties[w]);
+            if (some && place < top)  // the first `top` threads with any: by index
+                slice.from(v + i * kThreads + tid, bar, least, [&](Key k) {
+                    if (static_cast<uint32_t>(k >> 32) == equal) sh.cand[atomicAdd(&sh.n, 1)] = k;
+                });
+            __syncthreads();
         }
     }
-    __syncthreads();
-    const int vecs = static_cast<int>(sh.n_queue);
-    if (vecs <= kQueue) {
-#pragma unroll 1
-        for (int i = tid; i < vecs; i += kThreads)
-            slice.from(v + sh.queue[i], bar, least, [&](Key k) {
-                const uint32_t n = atomicAdd(&sh.n, 1);
-                if (n < kCap) sh.cand[n] = k;
-            });
-    }
-    __syncthreads();
-    const int n = static_cast<int>(sh.n);
-    if (vecs <= kQueue && n <= kCap) {
+    if (fits) {
+        const int n = static_cast<int>(sh.n);
         for (int i = tid; i < n; i += kThreads) {
             const Key x = sh.cand[i];
             int place = 0;
@@ -235,7 +278,7 @@ __device__ __forceinline__ void take_first(Shared &sh, const Slice<T> &slice, in
         __syncthreads();
         return;
     }
-    // Too many at once (equal logits): the first `top` of list and chunk one by one.
+    // Too many above the bar: the first `top` of list and chunk one by one.
     const Key old = tid < held ? sh.mine[tid] : 0;
     Key last = ~0ull;
     int k = 0;

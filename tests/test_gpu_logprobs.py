@@ -201,3 +201,40 @@ def test_after_verification_and_captured():
     assert bool((got.rank >= 0).sum(1).eq(num + 1).all())
     want, _, _ = sv.verify_sample(target, draft, toks, uni, workspace=ws)
     assert torch.equal(want, out) and sv.last_error(ws) == 0
+
+
+def some_of(x, tokens, top, got, picked):
+    """check() of the picked sequences."""
+    at = torch.from_numpy(picked).to(DEV)
+    part = sv.LogProbs(*(None if t is None else t[at] for t in got))
+    check(x[at].double().cpu().numpy(), tokens[picked], None, 1.0, top, part)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low", ["-inf", "lowest"])
+def test_masked_rows_of_a_batch(dtype, low):
+    """Rows that a mask leaves few tokens of, in calls of few and of many entries (one CTA or many a row)."""
+    rng = np.random.default_rng(5)
+    V = 50001
+    low = -float("inf") if low == "-inf" else torch.finfo(dtype).min
+    for B in (1, 500):
+        x = torch.full((B, 1, V), low, dtype=dtype, device=DEV)
+        keep = rng.choice(V, 12, replace=False)
+        x[:, 0, torch.from_numpy(keep).to(DEV)] = torch.randn((B, 12), device=DEV).to(dtype)
+        x[:, 0, 33:40] = 0.25  # equal ones among those left
+        tokens = rng.integers(0, V, (B, 1)).astype(np.int32)
+        tokens[:, 0] = np.where(np.arange(B) % 2 == 0, keep[0], tokens[:, 0])
+        got = sv.logprobs(x, dev(tokens), top=32)
+        some_of(x, tokens, 32, got, np.unique([0, B // 3, B - 1]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_above_the_bar(dtype):
+    """The largest logits in so few threads' vectors that the bar lies far below them."""
+    V, E = 60000, 4 if dtype == torch.float32 else 8
+    vec = torch.arange(V, device=DEV) // E % 256
+    x = torch.randn((500, 1, V), device=DEV) + torch.where(vec < 124, 100.0, 0.0)
+    x = x.to(dtype)
+    tokens = np.full((500, 1), 17, np.int32)
+    got = sv.logprobs(x, dev(tokens), top=32)
+    some_of(x, tokens, 32, got, np.array([0, 499]))
