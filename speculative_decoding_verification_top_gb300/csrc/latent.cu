@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
     const Head h = p.head[cta];
     if (h.parts == 0 || row >= h.rows) return;
     Running<C> x;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = SPLIT ? warp : 0; i < h.parts; i += SPLIT ? kJoinWarps : 1) {
         const long long at = (2ll * (cta + i * p.width) + (i == 0 ? 1 : 0)) * p.rc + row;
         const float2 ml = p.ml[at];

@@ -260,3 +260,48 @@ def test_append_attend_verify():
     one = sv.latent_attn(q[:, on].contiguous(), plain, table, start + 4, 0.1)
     # the same values in another order of positions: twice the forms' own distance
     assert float((out[:, on] - one).float().abs().max()) <= 2.0 ** -6 * float(one.float().abs().max())
+
+
+@pytest.mark.parametrize("C,page", [(128, 16), (256, 64), (512, 32), (512, 128)])
+def test_bad_pages_among_many_sequences(C, page):
+    """Many short sequences a CTA, some with a bad page: those fail, and no others, call after call."""
+    rng = np.random.default_rng([C, page])
+    B = 700
+    lens = rng.integers(1, 150, B).tolist()
+    lens[3] = lens[-1] = 140
+    cache, table, q, _ = make(rng, B, 2, 16, C, page, lens)
+    want, wl, err = call(q, cache, table, lens, 0.05)
+    assert err == 0
+    bad = np.zeros(B, bool)
+    bad[[3, B - 1]] = bad[rng.choice(B, 40, replace=False)] = True
+    broken = table.copy()
+    for b in np.flatnonzero(bad):
+        broken[b, rng.integers(0, -(-lens[b] // page))] = rng.choice([-1, cache.descriptor.num_pages])
+    at = torch.from_numpy(bad).to(DEV)
+    for _ in range(3):
+        out, lse, err = call(q, cache, broken, lens, 0.05)
+        assert err == sv.SPEC_DATA_PAGE_RANGE
+        assert bool(torch.isnan(out[at]).all()) and bool(torch.isnan(lse[at]).all())
+        assert torch.equal(out[~at], want[~at]) and torch.equal(lse[~at], wl[~at])
+
+
+@pytest.mark.parametrize("B,N,H,C,page,longest,tree", [
+    (30, 6, 32, 512, 64, 4000, False), (9, 40, 20, 512, 16, 3000, True), (64, 1, 16, 256, 32, 2500, False),
+    (12, 24, 64, 128, 128, 5000, True)])
+def test_same_bits(B, N, H, C, page, longest, tree):
+    """Results do not depend on timing: calls back to back, with others between, give the same bits."""
+    rng = np.random.default_rng([B, N, H, C, 7])
+    lens = rng.integers(N, longest, B).tolist()
+    mask = trees(rng, B, N) if tree else None
+    cache, table, q, m = make(rng, B, N, H, C, page, lens, mask)
+    t, n = dev(table), dev(np.array(lens, np.int32))
+    ws = sv.new_workspace(sv.spec_latent_workspace_size(B, N, H, C), DEV)
+    out, lse = sv.latent_attn(q, cache, t, n, 0.06, mask=m, lse=True, workspace=ws)
+    check(out[:2], lse[:2], cache, table[:2], q[:2], lens[:2], 0.06, None if mask is None else mask[:2], some=range(0, H, 7))
+    short = dev(np.minimum(lens, N + 3).astype(np.int32))
+    for i in range(25):
+        if i % 3 == 0:
+            sv.latent_attn(q, cache, t, short, 0.06, mask=m, workspace=ws)
+        again, again_lse = sv.latent_attn(q, cache, t, n, 0.06, mask=m, lse=True, workspace=ws)
+        assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    assert sv.last_error(ws) == 0
