@@ -15,7 +15,7 @@
 //                 accumulator of 512 x 64 is 256 columns of TMEM
 // latent_kernel      persistent, one CTA per SM; its share of the tiles segment by
 //                    segment
-//   warps 0-3        softmax, a thread per row and half a tile's positions (an
+//   warps 0-3 (0-7)  softmax, a thread per row and half a tile's positions (an
 //                    accumulator of 64 rows fills 16 of a warp's 32 lanes; the
 //                    load gives the other lanes its second half); the query tile;
 //                    the results
@@ -50,11 +50,11 @@ struct Shared {
     Barriers bar;
     Begin begin;
     uint32_t tmem;
-    int dead;            // a wait ran out: everyone leaves
-    int quit;            // the vote at which the softmax warps leave, or 0
-    int fail[kAhead];    // per segment (mod kAhead): a page id out of range
-    int odd;             // of the segment: cleaned elements that were not finite
-    alignas(16) float row[kRows];  // factors of the rows: of a rescaling, or 1 / l
+    int dead;               // a wait ran out: nobody waits any more
+    int fail[kAhead];       // per segment (mod kAhead): a page id out of range
+    int odd[2];             // of the segment, by group: cleaned elements that were not finite
+    float2 ml[2][kRows];    // a group's maxima and sums
+    alignas(16) float row[2][kRows];  // its factors of the rows: of a rescaling, or for the results
 };
 
 template <int C>
@@ -67,18 +67,31 @@ struct Layout {
     static constexpr int kRoom = (kSmemMax - kFixed) / (2 * kBlock);
     static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
     static constexpr int kBytes = kFixed + kSlots * 2 * kBlock;
+    // Softmax groups: each takes every kGroups-th tile, with an O^T of its own.  Under
+    // 512 elements there is room for two, and the chain scores, weights, products
+    // (1400 cycles a tile) is the bound with one.
+    static constexpr int kGroups = C == 512 ? 1 : 2;
+    static constexpr int kSoftmax = 128 * kGroups;               // their threads
+    // Warps: softmax, the two that issue products, the slots' loaders, the rotary part's
+    static constexpr int kScores = 4 * kGroups, kValues = kScores + 1, kLoaders = kScores + 2;
+    static constexpr int kSlotLoaders = C == 512 ? 4 : 2;
+    static constexpr int kThreads = 32 * (kLoaders + kSlotLoaders + 1);
     // TMEM columns: O^T from 0, two S, Q
     static constexpr int kS = 256, kQ = 384;
     static_assert(kSlots >= 2 * kPairs && kRopes <= kMaxRopes, "S of a tile is made before O of the one before");
 };
 
-constexpr int kScores = 4, kValues = 5, kLoaders = 6;  // the warps that issue products, and the first that loads
-constexpr int kBoxes = 4;                              // pages of a tile, at most
+constexpr int kBoxes = 4;    // pages of a tile, at most
+constexpr int kGroup = 128;  // threads of a softmax group
 
-constexpr int kVoteBarrier = 1, kRowBarrier = 2;  // hardware barriers of the softmax warps
-constexpr int kSoftmax = 128;                     // their threads
+// Hardware barriers: of a group's votes and rows (the next one of either is the
+// second group's), and of all groups.
+constexpr int kVoteBarrier = 1, kRowBarrier = 3, kAllBarrier = 5;
 
-__device__ __forceinline__ void meet(int id) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(kSoftmax) : "memory"); }
+template <int kThreads>
+__device__ __forceinline__ void meet(int id) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
 
 // 32 columns of 16 lanes for lanes 0-15, and the 32 columns from `kSecond` on of
 // the same 16 for lanes 16-31.
@@ -126,11 +139,11 @@ __device__ __forceinline__ const uint4 *query_row(const LatentArgs &a, const Seg
 }
 
 // The segment's query tile, zeros past its rows; the scale's sign goes into it.  A
-// warp takes 16 rows.
+// group lays it down, a warp 16 rows.
 template <int C>
 __device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment &g, uint8_t *tile, uint32_t tmem) {
     using L = Layout<C>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & 3;
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const uint4 *q = query_row(a, g, warp * 16 + (lane & 15));
@@ -232,7 +245,7 @@ template <int C>
 __device__ __forceinline__ bool clean_tile(uint8_t *slots, uint32_t slot0, int held) {
     using L = Layout<C>;
     bool odd = false;
-    for (int i = threadIdx.x; i < kTile * (C / 8); i += kSoftmax) {
+    for (int i = threadIdx.x % kGroup; i < kTile * (C / 8); i += kGroup) {
         const int row = i / (C / 8), part = i - row * (C / 8);
         const uint32_t slot = (slot0 + part / 16) % L::kSlots;
         uint4 *at = reinterpret_cast<uint4 *>(slots + slot * 2 * kBlock + part / 8 % 2 * kBlock + swizzled<128>(row, part % 8 * 16));
@@ -277,33 +290,32 @@ __device__ __noinline__ float odd_values(const LatentArgs &a, const Segment g, i
 }
 
 // An element times its row's factor; 0 where the row sees nothing.
-__device__ __forceinline__ __nv_bfloat16 scaled(float y, float factor) {
-    return __float2bfloat16_rn(factor == 0.0f ? 0.0f : y * factor);
-}
+__device__ __forceinline__ float scaled(float y, float factor) { return factor == 0.0f ? 0.0f : y * factor; }
 
-// Writes this lane's element of up to 32 rows (`left` are there): rounded, times the
-// row's factor, or as it is.
-template <int C>
-__device__ __forceinline__ void write_rows(__nv_bfloat16 *out, const float (&o)[32], int left, const float *factor) {
+__device__ __forceinline__ void scale_rows(float (&o)[32], const float *factor) {
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
         const float4 f = *reinterpret_cast<const float4 *>(factor + k);
-        if (k < left) out[k * C] = scaled(o[k], f.x);
-        if (k + 1 < left) out[(k + 1) * C] = scaled(o[k + 1], f.y);
-        if (k + 2 < left) out[(k + 2) * C] = scaled(o[k + 2], f.z);
-        if (k + 3 < left) out[(k + 3) * C] = scaled(o[k + 3], f.w);
+        o[k] = scaled(o[k], f.x);
+        o[k + 1] = scaled(o[k + 1], f.y);
+        o[k + 2] = scaled(o[k + 2], f.z);
+        o[k + 3] = scaled(o[k + 3], f.w);
     }
 }
 
-template <int C>
-__device__ __forceinline__ void write_rows(float *out, const float (&o)[32], int left, const float *) {
+__device__ __forceinline__ void put(__nv_bfloat16 *out, float y) { *out = __float2bfloat16_rn(y); }
+__device__ __forceinline__ void put(float *out, float y) { *out = y; }
+
+// Writes this lane's element of up to 32 rows; `left` are there.
+template <int C, typename T>
+__device__ __forceinline__ void write_rows(T *out, const float (&o)[32], int left) {
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-        if (k < left) out[k * C] = o[k];
+        if (k < left) put(out + k * C, o[k]);
 }
 
 template <int C>
-__global__ void __launch_bounds__(kLatentThreads, 1)
+__global__ void __launch_bounds__(Layout<C>::kThreads, 1)
     latent_kernel(const __grid_constant__ LatentKernelArgs ka, const __grid_constant__ CUtensorMap map) {
     using L = Layout<C>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -331,17 +343,17 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             bar_init(smem_addr(&bar.pv_done[i]), 1);
             bar_init(smem_addr(&bar.drained[i]), 1);
         }
-        sh.dead = sh.quit = sh.odd = 0;
+        sh.dead = sh.odd[0] = sh.odd[1] = 0;
         for (int i = 0; i < kAhead; ++i) sh.fail[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_proxy();
     }
-    if (warp == kScores) tmem_alloc(smem_addr(&sh.tmem), 512);
+    if (warp == L::kScores) tmem_alloc(smem_addr(&sh.tmem), 512);
     // Up to here this may run beside the kernel before it.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     long long from, to;
-    find_begin(p, sh.begin, &from, &to);
+    find_begin<L::kThreads>(p, sh.begin, &from, &to);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -350,10 +362,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     Walk walk(p, from, to, sh.begin);
     Segment g;
 
-    if (warp >= kLoaders) {
+    if (warp >= L::kLoaders) {
         // ---- loads: of each tile the rotary part and the latent, by slots in turn
         if (elect_one()) {
-            const uint32_t mine = warp - kLoaders;
+            const uint32_t mine = warp - L::kLoaders;
             const int box = min(kTile, 1 << a.c.page_shift), boxes = kTile / box;  // positions of a copy, copies of a tile
             uint32_t seg = 0, n = 0, uses = 0, r_uses = 0;  // segments and tiles so far; uses of the rings
             bool live = true;
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     for (uint32_t i = 0; i <= L::kPairs; ++i) {  // the rotary part, then its slots
                         const bool rotary = i == 0;
                         const uint32_t use = rotary ? n : n * L::kPairs + i - 1, ring = rotary ? L::kRopes : L::kSlots;
-                        if (mine != (rotary ? kRopeLoader : use % kRopeLoader)) continue;
+                        if (mine != (rotary ? L::kSlotLoaders : use % L::kSlotLoaders)) continue;
                         const uint32_t slot = use % ring, full = smem_addr(rotary ? &bar.r_full[slot] : &bar.full[slot]);
                         live = bar_wait(smem_addr(rotary ? &bar.r_empty[slot] : &bar.empty[slot]), (use / ring & 1) ^ 1, dead);
                         if (!live) break;
@@ -407,13 +419,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
             if (!live) {  // the copies in flight land before the CTA's memory goes
                 for (uint32_t i = uses > L::kSlots ? uses - L::kSlots : 0; i < uses; ++i)
-                    if (i % kRopeLoader == mine) bar_drain(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
+                    if (i % L::kSlotLoaders == mine) bar_drain(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
                 for (uint32_t i = r_uses > L::kRopes ? r_uses - L::kRopes : 0; i < r_uses; ++i)
                     bar_drain(smem_addr(&bar.r_full[i % L::kRopes]), (i / L::kRopes) & 1);
             }
         }
         __syncwarp();
-    } else if (warp == kScores) {
+    } else if (warp == L::kScores) {
         // ---- S, rotary part first
         if (elect_one()) {
             constexpr uint32_t kQk = mma_desc64(kTile), kHi = kMatrixHi<128>;
@@ -460,7 +472,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == kValues) {
+    } else if (warp == L::kValues) {
         // ---- O^T
         if (elect_one()) {
             constexpr uint32_t kPv = mma_desc(false, kRows, true, false), kHi = kMatrixHi<128>;
@@ -471,13 +483,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 for (int t = g.t0; t < g.t1; ++t, ++n) {
                     if (!(live = bar_wait(smem_addr(&bar.p_full[n & 1]), n >> 1 & 1, dead))) break;
                     fence_after_sync();
-                    const uint32_t pn = p0 + ((n & 1) * kBlock >> 4);
+                    const uint32_t pn = p0 + ((n & 1) * kBlock >> 4), d = tmem + n % L::kGroups * (L::kPairs * kRows);
+                    const bool more = t - L::kGroups >= g.t0;  // the accumulator holds some of the segment
 #pragma unroll
                     for (int i = 0; i < L::kPairs; ++i) {
                         const uint32_t v = v0 + (slot * 2 * kBlock >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_ss<false>(tmem + i * kRows, v + (k * 16 * 128 >> 4), kHi, pn + (k * 32 >> 4), kHi, kPv, t > g.t0 || k > 0);
+                            mma_ss<false>(d + i * kRows, v + (k * 16 * 128 >> 4), kHi, pn + (k * 32 >> 4), kHi, kPv, more || k > 0);
                         mma_commit(smem_addr(&bar.empty[slot]));
                         if (++slot == L::kSlots) slot = 0;
                     }
@@ -490,48 +503,43 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else {
         // ---- softmax
-        const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
-        const int row = warp * 16 + (lane & 15), half = lane >> 4;
+        const int group = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(quarter) << 21, acc = tmem + lanes + group * (L::kPairs * kRows);
+        const int row = quarter * 16 + (lane & 15), half = lane >> 4;
         const float mul = fabsf(a.scale) * kLog2e;
-        uint32_t n = 0, seg = 0;  // tiles and segments so far
-        int votes = 0;
-        bool ok = true, live = true;
+        uint32_t n0 = 0, seg = 0;  // tiles before the segment, segments so far
+        bool ok = true;
         if (tid == 0) p.head[blockIdx.x].parts = 0;
-        // A warp whose wait ran out says so, and all leave at its next vote (a vote's
-        // own wait has no bound: they must come to it together).
+        // Once a wait ran out nobody waits, and all go through the rest as it is: the
+        // hardware barriers have no bound, so that all must come to each.
         auto waited = [&](uint32_t b, uint32_t parity) {
-            ok = ok && bar_wait(b, parity, dead);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                *reinterpret_cast<volatile int *>(&sh.quit) = votes + 1;
-            }
+            if (ok) ok = bar_try(b, parity) || (*dead == 0 && bar_wait_on(b, parity, dead));
+            ok = __all_sync(0xffffffffu, ok);
         };
-        auto vote = [&](bool x) {
-            ++votes;
-            return any_of(kVoteBarrier, kSoftmax, x || !ok);
-        };
-        auto leaving = [&] {
-            const int quit = *reinterpret_cast<volatile int *>(&sh.quit);
-            return quit != 0 && quit <= votes;
-        };
-        // The next segment's queries are laid down once the last scores are made, so
-        // that its first ones are made while this one's results are written.
+        // The next segment's queries are laid down once the last scores are made, by the
+        // group that saw them, so that its first ones are made while this one's results
+        // are written.
         Segment ahead;
-        auto more = [&] {
+        auto more = [&](bool stage) {
             if (!walk.next(&ahead)) return false;
-            stage_queries<C>(a, ahead, qt, tmem);
-            __syncwarp();
-            if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
+            if (stage) {
+                stage_queries<C>(a, ahead, qt, tmem);
+                __syncwarp();
+                if (lane == 0) bar_arrive(smem_addr(&bar.q_full));
+            }
             return true;
         };
-        for (bool some = more(); live && some; ++seg) {
+        for (bool some = more(group == 0); some; ++seg) {
             g = ahead;
             const bool has = row < g.rows;
             const int token = has ? (g.row0 + row) / a.H : 0;
             float m = kNegInf, l = 0.0f;
+            uint32_t n = n0;
             for (int t = g.t0; t < g.t1; ++t, ++n) {
+                if (n % L::kGroups != group) continue;
+                const bool later = t - L::kGroups >= g.t0;  // not this group's first of the segment
                 const int j0 = t * kTile + half * 32;
                 const bool whole = sees_whole(a, g, t * kTile);
                 uint32_t seen = ~0u;
@@ -562,31 +570,28 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 }
                 const float most = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], 16));
                 const bool up = most > m + kSlack;
-                if (vote(up)) {
-                    if (leaving()) {
-                        live = false;
-                        break;
-                    }
+                if (any_of(kVoteBarrier + group, kGroup, up)) {
                     // Some row's reference moves up: its sum and its column of O^T are rescaled.
                     const float keep = up ? ex2(m - most) : 1.0f;
                     if (up) m = most;
                     l *= keep;
-                    if (t > g.t0) {
-                        waited(smem_addr(&bar.pv_done[(n - 1) & 1]), (n - 1) >> 1 & 1);
+                    if (later) {
+                        const uint32_t before = n - L::kGroups;
+                        waited(smem_addr(&bar.pv_done[before & 1]), before >> 1 & 1);
                         fence_after_sync();
-                        if (half == 0) sh.row[row] = keep;
-                        meet(kRowBarrier);
+                        if (half == 0) sh.row[group][row] = keep;
+                        meet<kGroup>(kRowBarrier + group);
 #pragma unroll 1
                         for (int c = 0; c < L::kPairs * kRows; c += 32) {
                             float o[32];
-                            tmem_load32(tmem + lanes + c, o);
+                            tmem_load32(acc + c, o);
                             tmem_load_wait();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= sh.row[c % kRows + k];
-                            tmem_store32(tmem + lanes + c, reinterpret_cast<const uint32_t *>(o));
+                            for (int k = 0; k < 32; ++k) o[k] *= sh.row[group][c % kRows + k];
+                            tmem_store32(acc + c, reinterpret_cast<const uint32_t *>(o));
                         }
                         tmem_store_wait();
-                        meet(kRowBarrier);
+                        meet<kGroup>(kRowBarrier + group);
                     }
                 }
                 const float ref = m == kNegInf ? 0.0f : m;
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     const uint32_t fill = n * L::kPairs;
                     for (uint32_t i = fill; i < fill + L::kPairs; ++i)
                         waited(smem_addr(&bar.full[i % L::kSlots]), (i / L::kSlots) & 1);
-                    if (clean_tile<C>(slots, fill % L::kSlots, g.len - t * kTile)) sh.odd = 1;
+                    if (clean_tile<C>(slots, fill % L::kSlots, g.len - t * kTile)) sh.odd[group] = 1;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -611,42 +616,65 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 __syncwarp();
                 if (lane == 0) bar_arrive(smem_addr(&bar.p_full[n & 1]));
             }
-            if (!live) break;
-            some = more();
-            waited(smem_addr(&bar.pv_done[(n - 1) & 1]), (n - 1) >> 1 & 1);
+            some = more((n - 1) % L::kGroups == group);
+            // This group's last tile; none where the segment's one tile was the other's.
+            const uint32_t last = (n - 1) % L::kGroups == group ? n - 1 : n - 2;
+            const bool any = static_cast<int>(last - n0) >= 0;
+            if (any) waited(smem_addr(&bar.pv_done[last & 1]), last >> 1 & 1);
             fence_after_sync();
             l += __shfl_xor_sync(0xffffffffu, l, 16);
-            // All warps are past the segment's tiles: what they and the loads noted is there.
-            if (vote(false) && leaving()) {
-                live = false;
-                break;
-            }
+            if (half == 0) sh.ml[group][row] = make_float2(m, l);
+            fence_before_sync();
+            meet<L::kSoftmax>(kAllBarrier);
+            fence_after_sync();
+            // All are past the segment's tiles: what they and the loads noted is there.
             const bool failed = *reinterpret_cast<volatile int *>(&sh.fail[seg % kAhead]) != 0;
-            const bool odd = *reinterpret_cast<volatile int *>(&sh.odd) != 0;
-            if (failed) l = NAN;
+            bool odd = false;
+            float most = kNegInf, sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < L::kGroups; ++i) {
+                odd |= *reinterpret_cast<volatile int *>(&sh.odd[i]) != 0;
+                most = fmaxf(most, sh.ml[i][row].x);
+            }
+            const float ref = most == kNegInf ? 0.0f : most;
+#pragma unroll
+            for (int i = 0; i < L::kGroups; ++i) sum += sh.ml[i][row].y * ex2(sh.ml[i][row].x - ref);
+            if (failed) sum = NAN;
             const bool alone = g.t0 == 0 && g.t1 == g.tiles;
             const int part = 2 * static_cast<int>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
             if (half == 0) {
-                sh.row[row] = !alone ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const float whole = !alone ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+                sh.row[group][row] = whole * ex2(m - ref);
                 const long long at = static_cast<long long>(g.b) * a.N * a.H + g.row0 + row;
-                if (alone && a.lse && has) a.lse[at] = l == 0.0f ? kNegInf : (m + log2f(l)) / kLog2e;
-                if (!alone && has) p.ml[part * p.rc + row] = make_float2(m, l);
+                if (group == 0 && alone && a.lse && has) a.lse[at] = sum == 0.0f ? kNegInf : (most + log2f(sum)) / kLog2e;
+                if (group == 0 && !alone && has) p.ml[part * p.rc + row] = make_float2(most, sum);
             }
             if (tid == 0 && !alone && g.t0 == 0) p.head[blockIdx.x] = {g.b, g.row0, g.rows, g.parts};
-            meet(kRowBarrier);
+            meet<L::kSoftmax>(kAllBarrier);
             // ---- the rows' results: a lane holds an element, of each row in turn
             const long long first = alone ? static_cast<long long>(g.b) * a.N * a.H + g.row0 : static_cast<long long>(part) * p.rc;
+            const bool both = L::kGroups == 2 && g.t1 - g.t0 > 1;
+            const int of = L::kGroups == 2 ? static_cast<int>(n0 & 1) : 0;  // the group of the first tile
 #pragma unroll 1
-            for (int c = 0; c < L::kPairs * 2; ++c) {
-                const int r0 = c % 2 * 32, d = c / 2 * 128 + warp * 32 + lane;
+            for (int c = group; c < L::kPairs * 2; c += L::kGroups) {
+                const int r0 = c % 2 * 32, d = c / 2 * 128 + quarter * 32 + lane;
                 if (r0 >= g.rows) continue;
                 float o[32];
-                tmem_load32(tmem + lanes + c * 32, o);
+                tmem_load32(tmem + lanes + of * (L::kPairs * kRows) + c * 32, o);
                 tmem_load_wait();
+                scale_rows(o, sh.row[of] + r0);
+                if (both) {
+                    float x[32];
+                    tmem_load32(tmem + lanes + (of ^ 1) * (L::kPairs * kRows) + c * 32, x);
+                    tmem_load_wait();
+                    scale_rows(x, sh.row[of ^ 1] + r0);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] += x[k];
+                }
                 if (alone)
-                    write_rows<C>(a.out + (first + r0) * C + d, o, g.rows - r0, sh.row + r0);
+                    write_rows<C>(a.out + (first + r0) * C + d, o, g.rows - r0);
                 else
-                    write_rows<C>(p.o + (first + r0) * C + d, o, g.rows - r0, sh.row + r0);
+                    write_rows<C>(p.o + (first + r0) * C + d, o, g.rows - r0);
                 if (odd) {  // not finite: they decide an element whatever its finite part
                     for (int k = 0; k < min(32, g.rows - r0); ++k) {
                         const float y = odd_values(a, g, r0 + k, d);
@@ -660,15 +688,18 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 }
             }
             fence_before_sync();
-            meet(kRowBarrier);
-            if (tid == 0) sh.fail[seg % kAhead] = sh.odd = 0;  // before its next vote, after which the others may set it
+            meet<L::kSoftmax>(kAllBarrier);
+            // Before this thread's next vote, after which its group may set it again.
+            if (tid % kGroup == 0) sh.odd[group] = 0;
+            if (tid == 0) sh.fail[seg % kAhead] = 0;
+            n0 = n;
         }
-        if (!live && tid == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
+        if (!ok && lane == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
     }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (warp == kScores) tmem_free(tmem, 512);
+    if (warp == L::kScores) tmem_free(tmem, 512);
 }
 
 constexpr int kJoinThreads = 256;
@@ -817,7 +848,7 @@ int launch_shape(const LatentKernelArgs &ka, const CUtensorMap &map, cudaStream_
     const LatentPlan &p = ka.p;
     const int grid = p.groups * p.width;
     if (!allow_smem(latent_kernel<C>, Layout<C>::kBytes, done)) return SPEC_ERR_CUDA;
-    if (!launch_early(latent_kernel<C>, dim3(grid), dim3(kLatentThreads), Layout<C>::kBytes, st, ka, map)) return SPEC_ERR_CUDA;
+    if (!launch_early(latent_kernel<C>, dim3(grid), dim3(Layout<C>::kThreads), Layout<C>::kBytes, st, ka, map)) return SPEC_ERR_CUDA;
     // Bands over four groups and more each: few rows, many parts.
     const bool split = 4ll * p.B * p.bands <= p.groups;
     const int joins = grid * (split ? p.rc : p.rc / kJoinWarps), fills = p.B < 152 ? p.B : 152;

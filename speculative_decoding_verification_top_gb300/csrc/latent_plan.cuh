@@ -11,8 +11,7 @@ namespace specv {
 constexpr int kTile = 64;             // positions a tile
 constexpr int kRows = 64;             // query rows a unit
 constexpr int kBlock = 64 * 128;      // bytes of 64 rows of 64 columns
-constexpr int kLoadWarps = 5, kRopeLoader = kLoadWarps - 1;
-constexpr int kLatentThreads = 192 + 32 * kLoadWarps;
+constexpr int kMaxThreads = 512;
 constexpr int kMaxSlots = 16, kMaxRopes = 8;
 constexpr int kAhead = 32;            // segments that the loads may be ahead, and more
 
@@ -54,15 +53,16 @@ __device__ __forceinline__ long long cost_of(const LatentPlan &p, int len) {
 
 // Where a CTA's share begins, found by all its threads together.
 struct Begin {
-    long long scan[kLatentThreads / 32];
+    long long scan[kMaxThreads / 32];
     long long base, share;
     int b;
 };
 
 // Contains block barriers; `at` may be read after the next one.
+template <int kThreads>
 __device__ __forceinline__ void find_begin(const LatentPlan &p, Begin &at, long long *from, long long *to) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int each = (p.B + kLatentThreads - 1) / kLatentThreads;
+    const int each = (p.B + kThreads - 1) / kThreads;
     const int bf = min(p.B, tid * each), bt = min(p.B, bf + each);
     long long mine = 0;
     for (int b = bf; b < bt; ++b) mine += cost_of(p, length_of(p, b));
@@ -79,7 +79,7 @@ __device__ __forceinline__ void find_begin(const LatentPlan &p, Begin &at, long 
     }
     __syncthreads();
     long long before = incl - mine, total = 0;
-    for (int w = 0; w < kLatentThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += at.scan[w];
         total += at.scan[w];
     }

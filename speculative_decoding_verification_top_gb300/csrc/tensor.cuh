@@ -42,11 +42,9 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 
 constexpr uint32_t kTries = 1u << 21;  // a wait gives up after this many (each may suspend): seconds
 
-// Waits for the phase `parity`; false when the tries ran out: *dead is set and
-// the caller leaves its loops (others then run out of theirs).  The loop is one
-// asm statement: the thread that issues the products is bound by its own
-// instructions, and this is most of what it does.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
+// Waits on; false when the tries ran out: *dead is set and the caller leaves its
+// loops (others then run out of theirs).  The loop is one asm statement.
+__device__ __forceinline__ bool bar_wait_on(uint32_t bar, uint32_t parity, volatile int *dead) {
     uint32_t tries;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -64,6 +62,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     if (tries < kTries) return true;
     *dead = 1;
     return false;
+}
+
+// Waits for the phase `parity`.  A phase that has completed is seen by a try of its
+// own: 70 cycles where the loop takes 200, and the threads that load and that issue
+// products do little else.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
+    return bar_try(bar, parity) || bar_wait_on(bar, parity, dead);
 }
 
 // The same without the flag.
