@@ -81,6 +81,7 @@ struct Layout {
     static_assert(kSlots >= 2 * kPairs && kRopes <= kMaxRopes, "S of a tile is made before O of the one before");
 };
 
+constexpr int kRotary = 64;  // rotary elements of a row
 constexpr int kBoxes = 4;    // pages of a tile, at most
 constexpr int kGroup = 128;  // threads of a softmax group
 
@@ -371,6 +372,12 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
             bool live = true;
             for (; live && walk.next(&g); ++seg) {
                 const int32_t *table = a.table + static_cast<long long>(g.b) * a.width;
+                // The queries, where they lie side by side, are asked for a tile or two
+                // before the softmax warps come to them.
+                const long long token = static_cast<long long>(a.H) * (C + kRotary);
+                if (mine == L::kSlotLoaders && a.q_stride == token)
+                    prefetch_l2(a.q + g.b * (a.N * token) + static_cast<long long>(g.row0) * (C + kRotary),
+                                static_cast<uint32_t>(g.rows) * (C + kRotary) * 2);
                 int next[kBoxes];
                 auto fetch = [&](int t) {  // the pages of tile t; -2: none
 #pragma unroll

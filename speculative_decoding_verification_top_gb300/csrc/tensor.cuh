@@ -117,6 +117,11 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Bytes that will be read (16-byte aligned, whole 16 bytes), into L2.
+__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // Four bytes (zeros where not `on`), and their arrival at `bar` once this
 // thread's copies so far are there (the barrier's count includes it).
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool on) {
