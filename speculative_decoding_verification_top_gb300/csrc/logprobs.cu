@@ -321,6 +321,7 @@ __device__ __forceinline__ void join_part(Part &p, const Part &x, float c) {
 // SOME: top > 0.
 template <typename T, bool SOME>
 __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const LogprobArgs a) {
+    started_early();
     constexpr int E = Elem<T>::kPerVec;
     __shared__ Shared sh;
     const int size = a.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -493,16 +494,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
 
 template <typename T, bool SOME>
 int launch_size(const LogprobArgs &a, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.M * a.cluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {static_cast<unsigned>(a.cluster), 1, 1};
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, SOME>, a) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(a.B) * a.M * a.cluster);
+    return launch_early_clusters(logprobs_kernel<T, SOME>, a.cluster, grid, dim3(kThreads), 0, st, a) ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace

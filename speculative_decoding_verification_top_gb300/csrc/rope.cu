@@ -16,6 +16,7 @@
 
 #include "kvrows.cuh"
 #include "target.cuh"
+#include "util.cuh"
 
 namespace specv {
 namespace {
@@ -149,6 +150,7 @@ __device__ __forceinline__ void turn_heads(const T *x, T *out, const Turn &t, in
 
 template <typename T, int HC>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+    started_early();
     const uint32_t units = a.D / kW, chunks = (a.H + HC - 1) / HC;
     const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
     const uint32_t token = item / (units * chunks), rest = item - token * units * chunks;
@@ -183,6 +185,7 @@ __device__ __forceinline__ void write_unit(uint8_t *data, int8_t *exps, long lon
 // queries.
 template <typename T, int D, bool E4M3, int HC>
 __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRopeArgs ar) {
+    started_early();
     constexpr int kUnits = D / kW;
     const AppendArgs &a = ar.a;
     const int unit = threadIdx.x % kUnits;
@@ -237,6 +240,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
 // beside the copies its sines and cosines would hold up every warp).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentAppendArgs a, unsigned c_blocks) {
+    started_early();
     const bool rotary = blockIdx.x >= c_blocks;
     const uint32_t units = rotary ? a.c.R / kW : a.c.C / (2 * kW);
     const uint32_t item = (rotary ? blockIdx.x - c_blocks : blockIdx.x) * kThreads + threadIdx.x;
@@ -291,16 +295,17 @@ constexpr long long kFull = 152ll * 2048;
 
 unsigned blocks_for(long long threads) { return static_cast<unsigned>((threads + kThreads - 1) / kThreads); }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
+template <typename... Params, typename... Args>
+int launch(void (*kernel)(Params...), unsigned blocks, cudaStream_t st, const Args &...args) {
+    return launch_early(kernel, dim3(blocks), dim3(kThreads), 0, st, args...) ? SPEC_OK : SPEC_ERR_CUDA;
+}
 
 template <typename T>
 int rope_heads(const RopeArgs &a, cudaStream_t st) {
     const long long each = static_cast<long long>(a.tokens) * (a.D / kW);
     if (each * a.H > 4 * kFull)
-        rope_kernel<T, 4><<<blocks_for(each * ((a.H + 3) / 4)), kThreads, 0, st>>>(a);
-    else
-        rope_kernel<T, 1><<<blocks_for(each * a.H), kThreads, 0, st>>>(a);
-    return launched();
+        return launch(rope_kernel<T, 4>, blocks_for(each * ((a.H + 3) / 4)), st, a);
+    return launch(rope_kernel<T, 1>, blocks_for(each * a.H), st, a);
 }
 
 template <typename T, int D, bool E4M3, int HC>
@@ -308,8 +313,7 @@ int append_heads(AppendRopeArgs &a, cudaStream_t st) {
     const long long entries = static_cast<long long>(a.a.B) * a.a.M, tokens = a.q ? static_cast<long long>(a.a.B) * a.a.N : 0;
     a.kv_blocks = blocks_for(entries * ((a.a.c.Hkv + HC - 1) / HC) * (D / kW));
     const unsigned q_blocks = blocks_for(tokens * ((a.Hq + HC - 1) / HC) * (D / kW));
-    kv_append_rope_kernel<T, D, E4M3, HC><<<2 * a.kv_blocks + q_blocks, kThreads, 0, st>>>(a);
-    return launched();
+    return launch(kv_append_rope_kernel<T, D, E4M3, HC>, 2 * a.kv_blocks + q_blocks, st, a);
 }
 
 template <typename T, int D, bool E4M3>
@@ -339,11 +343,8 @@ int launch_kv_append_rope(AppendRopeArgs &a, int dtype, cudaStream_t st) {
 int launch_latent_append(const LatentAppendArgs &a, int dtype, cudaStream_t st) {
     const long long entries = static_cast<long long>(a.B) * a.M;
     const unsigned c_blocks = blocks_for(entries * (a.c.C / (2 * kW))), blocks = c_blocks + blocks_for(entries * (a.c.R / kW));
-    if (dtype == SPEC_F32)
-        latent_append_kernel<float><<<blocks, kThreads, 0, st>>>(a, c_blocks);
-    else
-        latent_append_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a, c_blocks);
-    return launched();
+    return dtype == SPEC_F32 ? launch(latent_append_kernel<float>, blocks, st, a, c_blocks)
+                             : launch(latent_append_kernel<__nv_bfloat16>, blocks, st, a, c_blocks);
 }
 
 }  // namespace specv

@@ -68,21 +68,37 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// First thing in a kernel that launch_early starts: waits for the kernel ahead of it,
+// and lets the one behind it start early in turn.
+__device__ __forceinline__ void started_early() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
 // A launch that may start before the kernel ahead of it in the stream has ended
 // (each kernel here waits for that itself before it touches memory).
 template <typename... Params, typename... Args>
-bool launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args &...args) {
+bool launch_early_clusters(void (*kernel)(Params...), int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                           const Args &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+// The same without clusters.
+template <typename... Params, typename... Args>
+bool launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args &...args) {
+    return launch_early_clusters(kernel, 0, grid, block, smem, st, args...);
 }
 
 // Raises the kernel's shared-memory limit, once per kernel and device (`done`
