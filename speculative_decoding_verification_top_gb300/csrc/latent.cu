@@ -15,14 +15,14 @@
 //                 accumulator of 512 x 64 is 256 columns of TMEM
 // latent_kernel      persistent, one CTA per SM; its share of the tiles segment by
 //                    segment
-//   warps 0-3 (0-7)  softmax, a thread per row and half a tile's positions (an
+//   4 or 8 warps     softmax, a thread per row and half a tile's positions (an
 //                    accumulator of 64 rows fills 16 of a warp's 32 lanes; the
 //                    load gives the other lanes its second half); the query tile;
 //                    the results
-//   warps 4, 5       issue the products, S and O: each as soon as its operands are
+//   2 warps          issue the products, S and O: each as soon as its operands are
 //                    there.  (One warp for both has O wait for the loads of the S
 //                    ahead of it: 3600 cycles a tile, of 2040 that the products take.)
-//   warps 6-9, 10    load tiles page by page (TMA), in slots of 128 columns, and the
+//   3 or 5 warps     load tiles page by page (TMA), in slots of 128 columns, and the
 //                    rotary part: a thread's wait, arrival and copy take 300 cycles
 //                    whatever the copy's size, and one thread's nine copies a tile
 //                    would be the bound
@@ -34,6 +34,18 @@
 // `start` for beginning; it is cut into equal shares, one per group of CTAs.  A
 // unit that one share holds whole is written out at once, the others' parts (m, l,
 // O) are joined in the line's order: results do not depend on timing.
+//
+// What bounds it.  C = 512: shared memory, which delivers 128 bytes a cycle.  A tile of
+// 64 positions and rows takes 112 KB for S, 96 KB for O, 82 KB that loads and weights
+// write: 2270 cycles, where the products alone take 36 x 34.5 + 16 x 50; a tile is
+// measured at 2400, and a segment's beginning and end at some 20000 (55 tiles).
+// 64 x 6 tokens of 32 heads over up to 8200 positions, 184 us (0.47 of the measured
+// product rate); 16 trees of 85 nodes, 16 heads, 7001 positions, 293 us (0.46); one
+// token each of 64 sequences, 16 heads, 91 us (0.74 of the copy rate).  C = 128: the
+// chain of a softmax group, 2000 cycles a tile of its own: 83 us of 25 (one group: 128).
+// Not taken: a cluster's CTAs loading a tile once for all of them (chains 312 us: a slot
+// is free only when the last of them is done), pairs of CTAs on one product (the halves of
+// keys and values that each must hold leave no room to load ahead).
 
 #include "latent_plan.cuh"
 
@@ -710,6 +722,7 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
 }
 
 constexpr int kJoinThreads = 256;
+static_assert(kMaxGrid <= kJoinThreads, "a thread per head");
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 // A row's running result: a lane holds C / 32 elements, four at a time.
@@ -736,11 +749,12 @@ struct Running {
 };
 
 // Blocks [0, joins): the rows of units cut between CTAs, a warp a row, or (SPLIT) a
-// block a row, its warps the parts in turn, for units cut into many.  The other
-// blocks: sequences without positions, and those whose length is out of range.
+// block 128 elements of a row, its warps the parts in turn, for units cut into many
+// (a token over 2049 positions, 33 parts: 8 us in blocks of a row for every CTA).
+// The other blocks: sequences without positions, and those whose length is out of range.
 template <int C, bool SPLIT>
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentKernelArgs ka, int joins) {
-    constexpr int kV = C / 128;
+    constexpr int kWidth = SPLIT ? 128 : C, kV = kWidth / 128;
     const LatentArgs &a = ka.a;
     const LatentPlan &p = ka.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -761,18 +775,32 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
         return;
     }
     constexpr int kBlockRows = SPLIT ? 1 : kJoinWarps;
-    const int chunks = p.rc / kBlockRows, cta = blockIdx.x / chunks;
-    const int row = (blockIdx.x - cta * chunks) * kBlockRows + (SPLIT ? 0 : warp);
+    const int chunks = p.rc / kBlockRows, chunk = blockIdx.x / (C / kWidth);
+    const int first = (blockIdx.x - chunk * (C / kWidth)) * kWidth + lane * 4;  // this lane's first element
+    const int row = chunk % chunks * kBlockRows + (SPLIT ? 0 : warp);
+    int cta = chunk / chunks;
+    if constexpr (SPLIT) {  // a unit's number so far: its head is looked up (a block for every CTA's would be thousands)
+        __shared__ int found;
+        const int unit = cta, b = unit / p.units, row0 = (unit - b * p.units) * kRows;
+        if (threadIdx.x == 0) found = -1;
+        __syncthreads();
+        if (threadIdx.x < static_cast<unsigned>(p.groups * p.width)) {
+            const Head h = p.head[threadIdx.x];
+            if (h.parts > 0 && h.b == b && h.row0 == row0) found = threadIdx.x;
+        }
+        __syncthreads();
+        if ((cta = found) < 0) return;
+    }
     const Head h = p.head[cta];
     if (h.parts == 0 || row >= h.rows) return;
-    Running<C> x;
+    Running<kWidth> x;
 #pragma unroll 4
     for (int i = SPLIT ? warp : 0; i < h.parts; i += SPLIT ? kJoinWarps : 1) {
         const long long at = (2ll * (cta + i * p.width) + (i == 0 ? 1 : 0)) * p.rc + row;
         const float2 ml = p.ml[at];
         float4 y[kV];
 #pragma unroll
-        for (int k = 0; k < kV; ++k) y[k] = *reinterpret_cast<const float4 *>(p.o + at * C + k * 128 + lane * 4);
+        for (int k = 0; k < kV; ++k) y[k] = *reinterpret_cast<const float4 *>(p.o + at * C + k * 128 + first);
         x.add(ml, y);
     }
     if constexpr (SPLIT) {
@@ -789,15 +817,16 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
     const float inv = x.l == 0.0f ? 0.0f : 1.0f / x.l;  // nothing seen: every accumulator is 0
 #pragma unroll
     for (int k = 0; k < kV; ++k)
-        *reinterpret_cast<uint2 *>(a.out + at * C + k * 128 + lane * 4) =
+        *reinterpret_cast<uint2 *>(a.out + at * C + k * 128 + first) =
             make_uint2(bf16_pair(x.o[k].x * inv, x.o[k].y * inv), bf16_pair(x.o[k].z * inv, x.o[k].w * inv));
-    if (a.lse && lane == 0) a.lse[at] = x.l == 0.0f ? kNegInf : (x.m + log2f(x.l)) / kLog2e;
+    if (a.lse && first == 0) a.lse[at] = x.l == 0.0f ? kNegInf : (x.m + log2f(x.l)) / kLog2e;
 }
 
 // ------------------------------------------------------------------ host
 
-// What beginning a band costs, in tiles.
-constexpr int kStart = 4;
+// What beginning a band costs, in tiles: its first queries, scores and products one
+// after the other, and its results (some 20000 cycles; of 4, 8, 12 and 18 the best).
+constexpr int start_of(int C) { return C == 512 ? 8 : 12; }
 
 // Fills the plan's sizes and carves its arrays; returns the bytes needed.
 size_t carve_plan(LatentPlan *p, int N, int H, int C, char *work) {
@@ -810,7 +839,7 @@ size_t carve_plan(LatentPlan *p, int N, int H, int C, char *work) {
     p->N = N;
     p->rows = N * H;
     p->units = (p->rows + kRows - 1) / kRows;
-    p->start = kStart;
+    p->start = start_of(C);
     p->rc = p->rows < kRows ? (p->rows + 7) / 8 * 8 : kRows;
     const size_t parts = 2 * kMaxGrid * static_cast<size_t>(p->rc);
     p->head = reinterpret_cast<Head *>(take(kMaxGrid * sizeof(Head)));
@@ -820,14 +849,15 @@ size_t carve_plan(LatentPlan *p, int N, int H, int C, char *work) {
 }
 
 // How many units go through a sequence's tiles together.  Taken one by one, each
-// reads the tiles for itself, which memory delivers in 1.6 times what their products
-// take; taken together, a last band of fewer units and CTAs left over idle.
+// reads the tiles for itself (1.03 times as long for 22 units, 1.2 for three); taken
+// together, a last band of fewer units and CTAs left over idle (three units by twos
+// leave a quarter idle: 257 us of 184).
 void choose_width(LatentPlan *p, int grid) {
     double best = 0.0;
     for (int w = 1; w <= 8 && w <= p->units && w <= grid; ++w) {
         const int bands = (p->units + w - 1) / w, groups = grid / w;
         const double busy = static_cast<double>(p->units) / (bands * w) * (groups * w) / grid;
-        const double score = w == 1 ? busy / 1.6 : busy;
+        const double score = w == 1 ? busy / 1.2 : busy;
         if (score < best) continue;
         best = score;
         p->width = w;
@@ -858,7 +888,7 @@ int launch_shape(const LatentKernelArgs &ka, const CUtensorMap &map, cudaStream_
     if (!launch_early(latent_kernel<C>, dim3(grid), dim3(Layout<C>::kThreads), Layout<C>::kBytes, st, ka, map)) return SPEC_ERR_CUDA;
     // Bands over four groups and more each: few rows, many parts.
     const bool split = 4ll * p.B * p.bands <= p.groups;
-    const int joins = grid * (split ? p.rc : p.rc / kJoinWarps), fills = p.B < 152 ? p.B : 152;
+    const int joins = split ? p.B * p.units * p.rc * (C / 128) : grid * (p.rc / kJoinWarps), fills = p.B < 152 ? p.B : 152;
     return launch_early(split ? latent_join_kernel<C, true> : latent_join_kernel<C, false>, dim3(joins + fills), dim3(kJoinThreads), 0,
                         st, ka, joins)
                ? SPEC_OK
