@@ -1,4 +1,6 @@
 """Attention over a latent cache on the GPU against the 64-bit form."""
+import types
+
 import numpy as np
 import pytest
 
@@ -305,3 +307,21 @@ def test_same_bits(B, N, H, C, page, longest, tree):
         again, again_lse = sv.latent_attn(q, cache, t, n, 0.06, mask=m, lse=True, workspace=ws)
         assert torch.equal(again, out) and torch.equal(again_lse, lse)
     assert sv.last_error(ws) == 0
+
+
+def test_past_32_bits():
+    """A cache of more than 2^31 elements, its last pages in use."""
+    C, page, n = 512, 64, 58300  # 58300 * 64 * 576 elements
+    cache = sv.LatentCache(torch.empty((n, page, C + 64), dtype=torch.bfloat16, device=DEV))
+    assert cache.data.numel() > 2 ** 31
+    rng = np.random.default_rng(8)
+    lens, table = [130], (n - 1 - np.arange(3, dtype=np.int32))[None]
+    c, r = dev(rng.normal(size=(1, 130, C)), torch.bfloat16), dev(rng.normal(size=(1, 130, 64)), torch.bfloat16)
+    sv.latent_append(cache, dev(table), dev(np.zeros(1, np.int32)), c, r)
+    got = cache.data[n - 3:].flip(0).flatten(0, 1)[:130]
+    assert torch.equal(got, torch.cat((c[0], r[0]), -1))
+    q = dev(rng.normal(size=(1, 2, 16, C + 64)), torch.bfloat16)
+    out, lse, err = call(q, cache, table, lens, 0.06)
+    assert err == 0
+    few = types.SimpleNamespace(data=cache.data[n - 3:], descriptor=cache.descriptor)
+    check(out, lse, few, table - (n - 3), q, lens, 0.06)

@@ -238,3 +238,16 @@ def test_many_above_the_bar(dtype):
     tokens = np.full((500, 1), 17, np.int32)
     got = sv.logprobs(x, dev(tokens), top=32)
     some_of(x, tokens, 32, got, np.array([0, 499]))
+
+
+def test_past_32_bits():
+    """More than 2^31 logits, rows at both ends."""
+    N, V = 16800, 128256
+    x = torch.empty((1, N, V), dtype=torch.bfloat16, device=DEV)
+    assert x.numel() > 2 ** 31
+    rows = np.array([[0, N - 1, N - 2]], np.int32)
+    x[0, rows[0].tolist()] = torch.randn((3, V), device=DEV).to(x.dtype)
+    tokens = np.array([[5, V - 1, 77]], np.int32)
+    got = sv.logprobs(x, dev(tokens), rows=dev(rows), top=6)
+    few = x[:, rows[0].tolist()].double().cpu().numpy()
+    check(few, tokens, np.arange(3)[None], 1.0, 6, got)

@@ -271,3 +271,27 @@ def test_captured():
     pos.fill_(77)
     graph.replay()
     assert torch.equal(out, sv.rope(x, freqs, pos))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_past_32_bits(e4m3):
+    """A cache of more than 2^31 elements, its last pages written and read back."""
+    n, Hkv, page, D = 33000, 8, 64, 128  # 65536 elements a page
+    shape = (n, Hkv, page, D)
+    if e4m3:
+        k, v = (torch.empty(shape, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in "kv")
+        ke, ve = (torch.empty(shape[:3], dtype=torch.int8, device=DEV) for _ in "kv")
+    else:
+        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=DEV) for _ in "kv")
+        ke = ve = None
+    assert k.numel() > 2 ** 31
+    big, small = sv.KVCache(k, v, ke, ve), sv.new_cache(2, Hkv, page, D, DEV, e4m3=e4m3)
+    x = torch.randn((1, 100, Hkv, D), device=DEV).to(torch.bfloat16)
+    freqs, zero = sv.rope_freqs(D), dev(np.zeros(1, np.int32))
+    got = []
+    for cache, table in ((big, [[n - 1, n - 2]]), (small, [[0, 1]])):
+        table = dev(np.array(table, np.int32))
+        q = sv.kv_append_rope(cache, table, zero, x, x, freqs, q=x)
+        got.append((q, *sv.kv_read(cache, table, zero, 100)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
