@@ -152,45 +152,37 @@ __device__ __forceinline__ const uint4 *query_row(const LatentArgs &a, const Seg
 }
 
 // The segment's query tile, zeros past its rows; the scale's sign goes into it.  A
-// group lays it down, a warp 16 rows.
+// group lays it down, a warp 16 rows, all of its loads on their way at once (through
+// registers, 20 vectors a lane in four turns, a segment's queries took 6500 cycles).
 template <int C>
 __device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment &g, uint8_t *tile, uint32_t tmem) {
     using L = Layout<C>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & 3;
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
     const uint4 *q = query_row(a, g, warp * 16 + (lane & 15));
-    uint4 head[L::kInTmem > 0 ? 16 : 1];
+    constexpr int kParts = L::kInSmem * 8, kTurns = kParts / 2;  // 16-byte parts of a row, turns of a warp
+    const unsigned long long at = reinterpret_cast<unsigned long long>(q);
+    auto place = [&](int turn, int *row, int *part) {
+        const int x = turn * 32 + lane;
+        *row = x / kParts;
+        *part = x - *row * kParts;
+        return tile + *part / 8 * kBlock + swizzled<128>(warp * 16 + *row, *part % 8 * 16);
+    };
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        int row, part;
+        uint8_t *to = place(i, &row, &part);
+        const uint4 *from = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, at, row));
+        copy16(smem_addr(to), from ? from + L::kInTmem * 8 + part : reinterpret_cast<const uint4 *>(a.q), from != nullptr);
+    }
     if constexpr (L::kInTmem > 0) {
         // Lanes 0-15 hold a row's columns from 0 on (two elements a column), 16-31 from 64.
-#pragma unroll
-        for (int i = 0; i < 16; ++i) head[i] = q ? __ldg(q + (lane >> 4) * 16 + i) : zero;
-    }
-    constexpr int kParts = L::kInSmem * 8, kTurns = kParts / 2, kBatch = kTurns / 4;  // 16-byte parts of a row, turns of a warp
-    const unsigned long long at = reinterpret_cast<unsigned long long>(q);
-#pragma unroll
-    for (int i0 = 0; i0 < kTurns; i0 += kBatch) {
-        uint4 u[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int x = (i0 + i) * 32 + lane, row = x / kParts, part = x - row * kParts;
-            const uint4 *from = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, at, row));
-            u[i] = from ? __ldg(from + L::kInTmem * 8 + part) : zero;
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int x = (i0 + i) * 32 + lane, row = x / kParts, part = x - row * kParts;
-            *reinterpret_cast<uint4 *>(tile + part / 8 * kBlock + swizzled<128>(warp * 16 + row, part % 8 * 16)) =
-                make_uint4(u[i].x ^ flip, u[i].y ^ flip, u[i].z ^ flip, u[i].w ^ flip);
-        }
-    }
-    if constexpr (L::kInTmem > 0) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint4 u = head[k * 8 + i];
+                const uint4 u = q ? __ldg(q + (lane >> 4) * 16 + k * 8 + i) : make_uint4(0, 0, 0, 0);
                 w[4 * i] = u.x ^ flip;
                 w[4 * i + 1] = u.y ^ flip;
                 w[4 * i + 2] = u.z ^ flip;
@@ -199,6 +191,15 @@ __device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment
             tmem_store_halves<64>(tmem + L::kQ + (static_cast<uint32_t>(warp) << 21) + k * 32, w);
         }
         tmem_store_wait();
+    }
+    copies_wait();
+    if (flip) {  // of the lane's own copies
+#pragma unroll 1
+        for (int i = 0; i < kTurns; ++i) {
+            int row, part;
+            uint4 *u = reinterpret_cast<uint4 *>(place(i, &row, &part));
+            *u = make_uint4(u->x ^ flip, u->y ^ flip, u->z ^ flip, u->w ^ flip);
+        }
     }
     fence_async_proxy();
     fence_before_sync();
