@@ -168,6 +168,11 @@ __device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment
         *part = x - *row * kParts;
         return tile + *part / 8 * kBlock + swizzled<128>(warp * 16 + *row, *part % 8 * 16);
     };
+    // In TMEM, lanes 0-15 hold a row's columns from 0 on (two elements a column), 16-31
+    // from 64.
+    uint4 head[L::kInTmem * 4 + 1];
+#pragma unroll
+    for (int i = 0; i < L::kInTmem * 4; ++i) head[i] = q ? __ldg(q + (lane >> 4) * 16 + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
         int row, part;
@@ -176,13 +181,12 @@ __device__ __forceinline__ void stage_queries(const LatentArgs &a, const Segment
         copy16(smem_addr(to), from ? from + L::kInTmem * 8 + part : reinterpret_cast<const uint4 *>(a.q), from != nullptr);
     }
     if constexpr (L::kInTmem > 0) {
-        // Lanes 0-15 hold a row's columns from 0 on (two elements a column), 16-31 from 64.
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint4 u = q ? __ldg(q + (lane >> 4) * 16 + k * 8 + i) : make_uint4(0, 0, 0, 0);
+                const uint4 u = head[k * 8 + i];
                 w[4 * i] = u.x ^ flip;
                 w[4 * i + 1] = u.y ^ flip;
                 w[4 * i + 2] = u.z ^ flip;
