@@ -529,7 +529,8 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
         __syncwarp();
     } else {
         // ---- softmax
-        const int group = warp >> 2, quarter = warp & 3;
+        const uint32_t group = warp >> 2;
+        const int quarter = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quarter) << 21, acc = tmem + lanes + group * (L::kPairs * kRows);
         const int row = quarter * 16 + (lane & 15), half = lane >> 4;
         const float mul = fabsf(a.scale) * kLog2e;
@@ -560,9 +561,9 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
             const bool has = row < g.rows;
             const int token = has ? (g.row0 + row) / a.H : 0;
             float m = kNegInf, l = 0.0f;
-            uint32_t n = n0;
-            for (int t = g.t0; t < g.t1; ++t, ++n) {
-                if (n % L::kGroups != group) continue;
+            const uint32_t end = n0 + (g.t1 - g.t0), skip = (group - n0) % L::kGroups;  // this group's first tile
+            int t = g.t0 + skip;
+            for (uint32_t n = n0 + skip; n < end; n += L::kGroups, t += L::kGroups) {
                 const bool later = t - L::kGroups >= g.t0;  // not this group's first of the segment
                 const int j0 = t * kTile + half * 32;
                 const bool whole = sees_whole(a, g, t * kTile);
@@ -640,9 +641,9 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) bar_arrive(smem_addr(&bar.p_full[n & 1]));
             }
-            some = more((n - 1) % L::kGroups == group);
+            some = more((end - 1) % L::kGroups == group);
             // This group's last tile; none where the segment's one tile was the other's.
-            const uint32_t last = (n - 1) % L::kGroups == group ? n - 1 : n - 2;
+            const uint32_t last = (end - 1) % L::kGroups == group ? end - 1 : end - 2;
             const bool any = static_cast<int>(last - n0) >= 0;
             if (any) waited(smem_addr(&bar.pv_done[last & 1]), last >> 1 & 1);
             fence_after_sync();
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
             // Before this thread's next vote, after which its group may set it again.
             if (tid % kGroup == 0) sh.odd[group] = 0;
             if (tid == 0) sh.fail[seg % kAhead] = 0;
-            n0 = n;
+            n0 = end;
         }
         if (!ok && lane == 0) atomicOr(a.err, static_cast<uint32_t>(SPEC_DATA_STALL));
     }
