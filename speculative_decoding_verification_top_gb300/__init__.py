@@ -1056,6 +1056,8 @@ def latent_attn(q, cache, page_table, lens, scale, mask=None, out=None, lse=None
         _lies(out, "out", q.dtype, (B, N, H, C), device)
     if lse is True:
         lse = _made(stream, torch.empty, (B, N, H), dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
     elif lse is not None:
         _lies(lse, "lse", torch.float32, (B, N, H), device)
     if workspace is None:
