@@ -38,11 +38,11 @@
 // What bounds it.  C = 512: shared memory, which delivers 128 bytes a cycle.  A tile of
 // 64 positions and rows takes 112 KB for S, 96 KB for O, 82 KB that loads and weights
 // write: 2270 cycles, where the products alone take 36 x 34.5 + 16 x 50; a tile is
-// measured at 2400, and a segment's beginning and end at some 20000 (55 tiles).
-// 64 x 6 tokens of 32 heads over up to 8200 positions, 181 us (0.48 of the measured
-// product rate); 16 trees of 85 nodes, 16 heads, 7001 positions, 290 us (0.46); one
+// measured at 2350, and a segment's beginning and end at some 15000 (55 tiles).
+// 64 x 6 tokens of 32 heads over up to 8200 positions, 176 us (0.49 of the measured
+// product rate); 16 trees of 85 nodes, 16 heads, 7001 positions, 276 us (0.49); one
 // token each of 64 sequences, 16 heads, 91 us (0.74 of the copy rate).  C = 128: the
-// chain of a softmax group, 2000 cycles a tile of its own: 82 us of 25 (one group: 128).
+// chain of a softmax group, 1800 cycles a tile of its own: 75 us of 25 (one group: 128).
 // Not taken: a cluster's CTAs loading a tile once for all of them (chains 312 us: a slot
 // is free only when the last of them is done), pairs of CTAs on one product (the halves of
 // keys and values that each must hold leave no room to load ahead).
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
 // ------------------------------------------------------------------ host
 
 // What beginning a band costs, in tiles: its first queries, scores and products one
-// after the other, and its results (some 20000 cycles; of 4, 8, 12 and 18 the best).
+// after the other, and its results (of 4, 8, 12 and 18 the best).
 constexpr int start_of(int C) { return C == 512 ? 8 : 12; }
 
 // Fills the plan's sizes and carves its arrays; returns the bytes needed.
