@@ -325,3 +325,37 @@ def test_past_32_bits():
     assert err == 0
     few = types.SimpleNamespace(data=cache.data[n - 3:], descriptor=cache.descriptor)
     check(out, lse, few, table - (n - 3), q, lens, 0.06)
+
+
+def test_two_graphs_and_two_streams():
+    """Two captured calls that share a workspace, replayed in turn; two streams with a workspace each, at once."""
+    rng = np.random.default_rng(9)
+    made_ = []
+    for C, lens in ((512, [900, 40, 333]), (128, [70, 1500, 8])):
+        cache, table, q, _ = make(rng, 3, 4, 32, C, 32, lens)
+        made_.append((q, cache, dev(table), dev(np.array(lens, np.int32))))
+    want = [sv.latent_attn(q, c, t, n, 0.06) for q, c, t, n in made_]
+    size = max(sv.spec_latent_workspace_size(3, 4, 32, C) for C in (512, 128))
+    ws = sv.new_workspace(size, DEV)
+    graphs, outs = [], []
+    for q, c, t, n in made_:
+        out = torch.empty(q.shape[:3] + (c.descriptor.C,), dtype=q.dtype, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sv.latent_attn(q, c, t, n, 0.06, out=out, workspace=ws)
+        graphs.append(g)
+        outs.append(out)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
+    assert sv.last_error(ws) == 0
+    sides = [torch.cuda.Stream() for _ in made_]
+    spaces = [sv.new_workspace(size, DEV) for _ in made_]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (q, c, t, n), out, s, w in zip(made_, outs, sides, spaces):
+            sv.latent_attn(q, c, t, n, 0.06, out=out, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for out, w, o in zip(outs, want, spaces):
+        assert torch.equal(out, w) and sv.last_error(o) == 0

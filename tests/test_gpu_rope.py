@@ -295,3 +295,37 @@ def test_append_past_32_bits(e4m3):
         got.append((q, *sv.kv_read(cache, table, zero, 100)))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_a_step_captured():
+    """Rotated queries and keys and the attention that reads both, in one captured graph: each waits for the one ahead."""
+    B, N, H, Hkv, D, page = 3, 5, 8, 2, 64, 16
+    g = torch.Generator(DEV)
+    g.manual_seed(3)
+    cache = sv.new_cache(40, Hkv, page, D, DEV)
+    table = torch.arange(39, dtype=torch.int32, device=DEV).view(B, 13)
+    freqs = sv.rope_freqs(D)
+    held = torch.tensor([100, 7, 64], dtype=torch.int32, device=DEV)
+    lens = held + N
+    x = [torch.randn((B, N, h, D), generator=g, device=DEV).bfloat16() for h in (H, Hkv, Hkv)]
+    old = torch.randn((B, 120, Hkv, D), generator=g, device=DEV).bfloat16()
+    sv.kv_append(cache, table, held - held, old, old)
+
+    def step(q, k, v):
+        q = sv.kv_append_rope(cache, table, held, k, v, freqs, q=q)
+        return sv.attn_tree(q, cache, table, lens)
+
+    step(*x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*x)
+    for _ in range(5):
+        for t in x:
+            t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        pos = held[:, None] + torch.arange(N, dtype=torch.int32, device=DEV)
+        sv.kv_append(cache, table, held, sv.rope(x[1], freqs, pos), x[2])
+        assert torch.equal(got, sv.attn_tree(sv.rope(x[0], freqs, pos), cache, table, lens))
