@@ -53,7 +53,7 @@ struct Shared {
     Key mine[SPEC_MAX_TOP];              // this slice's so far, sorted
     Key cand[kCap];
     Key best[kWarps];
-    uint16_t top[kChunk];                // the chunk's vectors' maxima (up_bits)
+    alignas(16) uint16_t top[kThreads][kVecs];  // the chunk's vectors' maxima (up_bits), a thread's side by side
     uint16_t queue[kQueue];
     float group[kGroups];
     Part warp[kWarps];
@@ -228,21 +228,34 @@ __device__ __forceinline__ void take_first(Shared &sh, const Slice<T> &slice, in
         const float from = ties ? above(bar) : bar;
         if (most >= from) {
 #pragma unroll 1
-            for (int i = 0; i < count; ++i) {
-                if (!(of_bits(sh.top[i * kThreads + tid]) >= from)) continue;
-                const uint32_t n = atomicAdd(&sh.n_queue, 1);
-                if (n < kQueue) sh.queue[n] = static_cast<uint16_t>(i * kThreads + tid);
+            for (int i = 0; i < count; i += 8) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(&sh.top[tid][i]);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint32_t hits = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    hits |= (__uint_as_float(w[k] << 16) >= from ? 1u : 0u) << 2 * k |
+                            (__uint_as_float(w[k] & 0xffff0000u) >= from ? 2u : 0u) << 2 * k;
+                for (hits &= first_bits(count - i); hits; hits &= hits - 1) {
+                    const uint32_t n = atomicAdd(&sh.n_queue, 1);
+                    if (n < kQueue) sh.queue[n] = static_cast<uint16_t>((i + __ffs(hits) - 1) * kThreads + tid);
+                }
             }
         }
         __syncthreads();
         const int vecs = static_cast<int>(sh.n_queue);
         if (vecs <= kQueue) {
+            constexpr int E = Elem<T>::kPerVec;  // a thread an element
 #pragma unroll 1
-            for (int i = tid; i < vecs; i += kThreads)
-                slice.from(v + sh.queue[i], from, least, [&](Key k) {
-                    const uint32_t n = atomicAdd(&sh.n, 1);
-                    if (n < kCap) sh.cand[n] = k;
-                });
+            for (int i = tid; i < vecs * E; i += kThreads) {
+                const int x = slice.at(v + sh.queue[i / E]) + i % E;
+                if (x < 0 || x >= slice.end) continue;
+                const float f = to_f32(slice.row[x]);
+                const Key k = key_of(f, x);
+                if (!(f >= from) || k <= least) continue;
+                const uint32_t n = atomicAdd(&sh.n, 1);
+                if (n < kCap) sh.cand[n] = k;
+            }
         }
         __syncthreads();
         fits = vecs <= kQueue && static_cast<int>(sh.n) <= (ties ? kCap - kTies : kCap);
@@ -251,7 +264,7 @@ __device__ __forceinline__ void take_first(Shared &sh, const Slice<T> &slice, in
         const uint32_t equal = okey<float>(bar);
 #pragma unroll 1
         for (int i = 0; i < count && static_cast<int>(sh.n) < top; ++i) {  // sh.n as the last barrier left it
-            const bool near = of_bits(sh.top[i * kThreads + tid]) >= bar;
+            const bool near = of_bits(sh.top[tid][i]) >= bar;
             bool some = false;
             if (near)
                 slice.from(v + i * kThreads + tid, bar, least, [&](Key k) { some |= static_cast<uint32_t>(k >> 32) == equal; });
@@ -289,7 +302,7 @@ __device__ __forceinline__ void take_first(Shared &sh, const Slice<T> &slice, in
         Key best = old < last ? old : 0;
 #pragma unroll 1
         for (int i = 0; i < count; ++i) {
-            if (!(of_bits(sh.top[i * kThreads + tid]) >= bar)) continue;
+            if (!(of_bits(sh.top[tid][i]) >= bar)) continue;
             slice.from(v + i * kThreads + tid, bar, 0, [&](Key y) {
                 if (y < last) best = max_key(best, y);
             });
@@ -399,7 +412,12 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
             for (int i = 0; i < kBatch; ++i) {
                 tops[i] = batch_max1<T>(q[i]);
                 top = max_nan(top, tops[i]);
-                if (SOME) sh.top[(count + i) * kThreads + tid] = up_bits(tops[i]);
+            }
+            if (SOME) {
+                static_assert(kBatch == 4, "a batch's maxima are one store");
+                *reinterpret_cast<uint2 *>(&sh.top[tid][count]) =
+                    make_uint2(up_bits(tops[0]) | static_cast<uint32_t>(up_bits(tops[1])) << 16,
+                               up_bits(tops[2]) | static_cast<uint32_t>(up_bits(tops[3])) << 16);
             }
             odd |= !(top < INFINITY);
             most = fmaxf(most, top);
