@@ -14,12 +14,13 @@
 // a bar on: the top-th of what was seen before or, in the first chunk, the top-th
 // largest of 64 groups' maxima (at least `top` elements reach it, and few more do).
 // The slices' sums and lists meet in the first CTA's shared memory.
-// Bound by what is issued (14 instructions an element of 8-element vectors, all told)
-// and, where rows are few, by the chain load, sums, bar, candidates, cluster.
-// Measured: 64 x 6 entries (224 emitted) of 151936 bf16 logits, 20 alternatives,
-// 31 to 38 us (68 MB, 2 TB/s); one row of 32000, 8 us on the GPU.  Held in registers
+// Bound by what is issued for the sums (21 of 30 us; some 10 instructions an element)
+// and by the chain bar, candidates, order, cluster after them.
+// Measured: 64 x 6 entries (228 emitted) of 151936 bf16 logits, 20 alternatives, 30 us
+// (69 MB, 2.3 TB/s), fp32 44 us (3.2); without alternatives 21.  Held in registers
 // instead, a slice cut into chunks of 2048 vectors took 120 us, and of 2560 in three
-// CTAs a multiprocessor 70: each chunk's selection is a chain of barriers.
+// CTAs a multiprocessor 70: each chunk's selection is a chain of barriers.  A thread's
+// maxima looked through one by one cost 9000 of 45000 cycles.
 
 #include "logprobs.cuh"
 #include "util.cuh"
@@ -365,8 +366,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
     const int head = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     const int vecs = (head + a.V + E - 1) / E, per = (vecs + size - 1) / size;
     const int v0 = min(vecs, rank * per), v1 = min(vecs, v0 + per);
-    const float lt = to_f32(row[token]), c = a.c;
-    const Emitted emitted = {token, lt, lt == kNegInf ? kNegInf : below(lt)};
+    const float c = a.c;
     float m = kNegInf;
     F2 z = pair_of(0.0f, 0.0f), s = z;
     const F2 c2 = pair_of(c, c);
@@ -375,6 +375,25 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
     uint32_t before = 0;
     bool odd = false;
     const Slice<T> slice = {row, head, a.V, min(a.V, v1 * E - head)};
+    uint4 next[kBatch];
+    auto batch = [&](int from, uint4 (&q)[kBatch]) {  // vectors from + i kThreads + tid
+        if (from >= inner0 && min(v1, from + kBatch * kThreads) <= inner1) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                q[i] = neg_inf_vec<T>();
+                if (from + i * kThreads + tid < v1) q[i] = ld_stream(row + slice.at(from + i * kThreads + tid));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int x = from + i * kThreads + tid;
+                q[i] = x < v1 ? load_vec(row, slice.at(x), a.V) : neg_inf_vec<T>();
+            }
+        }
+    };
+    batch(v0, next);  // on its way while the token's own logit is fetched
+    const float lt = to_f32(row[token]);
+    const Emitted emitted = {token, lt, lt == kNegInf ? kNegInf : below(lt)};
     if (SOME) {
         if (tid == 0) sh.n_mine = 0;
         __syncthreads();
@@ -383,30 +402,14 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
     for (int v = v0; v < v1; v += kChunk) {
         float most = kNegInf;  // of the chunk
         int count = 0;
-        auto batch = [&](int from, uint4 (&q)[kBatch]) {  // vectors from + i kThreads + tid
-            if (from >= inner0 && min(v1, from + kBatch * kThreads) <= inner1) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    q[i] = neg_inf_vec<T>();
-                    if (from + i * kThreads + tid < v1) q[i] = ld_stream(row + slice.at(from + i * kThreads + tid));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int x = from + i * kThreads + tid;
-                    q[i] = x < v1 ? load_vec(row, slice.at(x), a.V) : neg_inf_vec<T>();
-                }
-            }
-        };
         const int until = min(v1, v + kChunk);
-        uint4 q[kBatch], next[kBatch];
-        batch(v, next);
+        uint4 q[kBatch];
 #pragma unroll 1
         for (; v + count * kThreads < until; count += kBatch) {
             const int first = v + count * kThreads + tid;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) q[i] = next[i];
-            if (v + (count + kBatch) * kThreads < until) batch(v + (count + kBatch) * kThreads, next);
+            if (v + (count + kBatch) * kThreads < v1) batch(v + (count + kBatch) * kThreads, next);
             float tops[kBatch], top = kNegInf;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -522,7 +525,8 @@ int launch_size(const LogprobArgs &a, cudaStream_t st) {
 
 int launch_logprobs(LogprobArgs &a, int dtype, cudaStream_t st) {
     // As many CTAs a row as are resident at once: fewer leave multiprocessors idle, more
-    // go through the chain in turns (384 rows of 151936: 36 us with 2, 46 with 1, 43 with 4).
+    // go through the chain in turns (384 rows of 151936, before the last two steps: 36 us with
+    // 2, 46 with 1, 43 with 4).
     const int E = dtype == SPEC_F32 ? 4 : 8;
     const long long entries = static_cast<long long>(a.B) * a.M;
     a.cluster = 1;
