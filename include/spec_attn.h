@@ -288,7 +288,9 @@ int spec_latent_workspace_size(int B, int N, int H, int C, size_t *bytes);
  *   lse_ih = ln sum_seen e^s_ij
  * seen as in spec_attn_tree: the context always, new token j where
  * mask[b][i][j] != 0, or j <= i without a mask.  A token that sees nothing gets
- * zeros and lse -inf; an unseen position adds nothing whatever it holds.
+ * zeros and lse -inf; an unseen position adds nothing whatever it holds.  A latent
+ * element that is not finite and seen is NaN in the result (its score is not finite
+ * either), whatever else the row sees.
  * Scores, sums and accumulators are fp32, the softmax weights are rounded to
  * bf16 for the product with the latents.  Calls with the same inputs give the
  * same bits.

@@ -96,6 +96,7 @@ struct Layout {
 constexpr int kRotary = 64;  // rotary elements of a row
 constexpr int kBoxes = 4;    // pages of a tile, at most
 constexpr int kGroup = 128;  // threads of a softmax group
+constexpr float kLowest = -FLT_MAX;
 
 // Hardware barriers: of a group's votes and rows (the next one of either is the
 // second group's), and of all groups.
@@ -287,10 +288,9 @@ __device__ __forceinline__ bool clean_tile(uint8_t *slots, uint32_t slot0, int h
     return odd;
 }
 
-// What clean_tile took from element d of row `row`'s result: the elements that are
-// not finite of the positions it sees in the segment's cleaned tiles.
-__device__ __noinline__ float odd_values(const LatentArgs &a, const Segment g, int row, int d) {
-    float y = 0.0f;
+// Is element d of some position that row `row` sees in the segment's cleaned tiles
+// not finite?
+__device__ __forceinline__ bool odd_seen(const LatentArgs &a, const Segment &g, int row, int d) {
     const int n = (g.row0 + row) / a.H, first = g.len - a.N;
     for (int t = g.t0; t < g.t1; ++t) {
         if (sees_whole(a, g, t * kTile)) continue;
@@ -301,23 +301,20 @@ __device__ __noinline__ float odd_values(const LatentArgs &a, const Segment g, i
             if (page < 0 || page >= a.c.num_pages) continue;
             const long long at = (static_cast<long long>(page) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
             const float x = __bfloat162float(a.c.data[at * (a.c.C + a.c.R) + d]);
-            if (!isfinite(x)) y += x;
+            if (!isfinite(x)) return true;
         }
     }
-    return y;
+    return false;
 }
-
-// An element times its row's factor; 0 where the row sees nothing.
-__device__ __forceinline__ float scaled(float y, float factor) { return factor == 0.0f ? 0.0f : y * factor; }
 
 __device__ __forceinline__ void scale_rows(float (&o)[32], const float *factor) {
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
         const float4 f = *reinterpret_cast<const float4 *>(factor + k);
-        o[k] = scaled(o[k], f.x);
-        o[k + 1] = scaled(o[k + 1], f.y);
-        o[k + 2] = scaled(o[k + 2], f.z);
-        o[k + 3] = scaled(o[k + 3], f.w);
+        o[k] *= f.x;
+        o[k + 1] *= f.y;
+        o[k + 2] *= f.z;
+        o[k + 3] *= f.w;
     }
 }
 
@@ -330,6 +327,20 @@ __device__ __forceinline__ void write_rows(T *out, const float (&o)[32], int lef
 #pragma unroll
     for (int k = 0; k < 32; ++k)
         if (k < left) put(out + k * C, o[k]);
+}
+
+// What clean_tile took from the rows' results, row 0 at `out`: a latent element that
+// is not finite is part of the position's key too, so that the score is NaN or +inf,
+// and the row NaN anyway, or -inf, and 0 times the element is NaN.  A thread marks the
+// elements that it wrote: of groups in turn half the rows, of every fourth 32 elements.
+template <int C, typename T>
+__device__ __forceinline__ void mark_odd(const LatentArgs &a, const Segment g, T *out) {
+    const int tid = threadIdx.x;
+    for (int c = tid / kGroup; c < C / 64; c += Layout<C>::kGroups) {
+        const int d = c / 2 * 128 + tid % kGroup;
+        for (int row = c % 2 * 32; row < min(g.rows, c % 2 * 32 + 32); ++row)
+            if (odd_seen(a, g, row, d)) put(out + row * C + d, NAN);
+    }
 }
 
 template <int C>
@@ -577,6 +588,9 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) bar_arrive(smem_addr(&bar.s_empty[n & 1]));
+                // A row that sees any position has a maximum above -inf, so that one whose
+                // scores are all -inf is told from one that sees nothing: its sum is 0, its
+                // accumulators 0, or NaN, and 0 / 0 its result.
                 float top[2] = {kNegInf, kNegInf};
                 if (whole) {
 #pragma unroll
@@ -584,14 +598,14 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
                         top[0] = max3(top[0], v[c], v[c + 1]);
                         top[1] = max3(top[1], v[c + 2], v[c + 3]);
                     }
-                    top[0] = fmaxf(top[0], top[1]) * mul;
+                    top[0] = fmaxf(fmaxf(top[0], top[1]) * mul, kLowest);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
                         const float y = v[c] * mul;
                         if (seen >> c & 1u) top[c & 1] = fmaxf(top[c & 1], y);
                     }
-                    top[0] = fmaxf(top[0], top[1]);
+                    top[0] = fmaxf(fmaxf(top[0], top[1]), seen ? kLowest : kNegInf);
                 }
                 const float most = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], 16));
                 const bool up = most > m + kSlack;
@@ -668,7 +682,7 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
             const bool alone = g.t0 == 0 && g.t1 == g.tiles;
             const int part = 2 * static_cast<int>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
             if (half == 0) {
-                const float whole = !alone ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float whole = !alone ? 1.0f : most == kNegInf && !failed ? 0.0f : 1.0f / sum;
                 sh.row[group][row] = whole * ex2(m - ref);
                 const long long at = static_cast<long long>(g.b) * a.N * a.H + g.row0 + row;
                 if (group == 0 && alone && a.lse && has) a.lse[at] = sum == 0.0f ? kNegInf : (most + log2f(sum)) / kLog2e;
@@ -700,17 +714,12 @@ __global__ void __launch_bounds__(Layout<C>::kThreads, 1)
                     write_rows<C>(a.out + (first + r0) * C + d, o, g.rows - r0);
                 else
                     write_rows<C>(p.o + (first + r0) * C + d, o, g.rows - r0);
-                if (odd) {  // not finite: they decide an element whatever its finite part
-                    for (int k = 0; k < min(32, g.rows - r0); ++k) {
-                        const float y = odd_values(a, g, r0 + k, d);
-                        const long long at = (first + r0 + k) * C + d;
-                        if (y == 0.0f) continue;
-                        if (alone)
-                            a.out[at] = __float2bfloat16_rn(__bfloat162float(a.out[at]) + y);
-                        else
-                            p.o[at] += y;
-                    }
-                }
+            }
+            if (odd) {
+                if (alone)
+                    mark_odd<C>(a, g, a.out + first * C);
+                else
+                    mark_odd<C>(a, g, p.o + first * C);
             }
             fence_before_sync();
             meet<L::kSoftmax>(kAllBarrier);
@@ -740,7 +749,7 @@ struct Running {
     __device__ void add(float2 ml, const float4 (&y)[C / 128]) {
         if (isnan(ml.y)) l = NAN;
         const float top = fmaxf(m, ml.x);
-        if (top == kNegInf) return;
+        if (top == kNegInf) return;  // nothing seen: the part's accumulators are 0
         const float keep = ex2(m - top), f = ml.x == kNegInf ? 0.0f : ex2(ml.x - top);
         m = top;
         l = fmaf(f, ml.y, l * keep);
@@ -820,7 +829,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
         for (int w = 1; w < kJoinWarps; ++w) x.add(ml[w], part[w][lane]);
     }
     const long long at = static_cast<long long>(h.b) * p.rows + h.row0 + row;
-    const float inv = x.l == 0.0f ? 0.0f : 1.0f / x.l;  // nothing seen: every accumulator is 0
+    const float inv = x.m == kNegInf && !isnan(x.l) ? 0.0f : 1.0f / x.l;  // nothing seen: 0
 #pragma unroll
     for (int k = 0; k < kV; ++k)
         *reinterpret_cast<uint2 *>(a.out + at * C + k * 128 + first) =

@@ -359,3 +359,42 @@ def test_two_graphs_and_two_streams():
     torch.cuda.synchronize()
     for out, w, o in zip(outs, want, spaces):
         assert torch.equal(out, w) and sv.last_error(o) == 0
+
+
+ONE, SPLIT, MANY = [40], [2560], [134] * 304  # one tile; a tile a share, joined; whole units, two a share
+
+
+@pytest.mark.parametrize("C", [128, 256, 512])
+@pytest.mark.parametrize("lens,where", [
+    (ONE, [36]), (ONE, [5, 39]), (SPLIT, [200]), (SPLIT, range(192, 256)), (SPLIT, [2557]), (SPLIT, [3, 2554]),
+    (MANY, [10]), (MANY, range(64)), (MANY, range(128)), (MANY, [131]), ([6], range(6)), ([70], range(70))])
+def test_infinite_latents(C, lens, where):
+    """Seen infinite elements whose score is -inf: their weight is 0 and 0 * inf makes the element NaN, wherever the
+    position lies; the row's others are as without the position, and a row without another is NaN."""
+    rng = np.random.default_rng([C, len(lens), lens[0], len(where)])
+    N, H, marks = 6, 8, (0, len(lens) - 4 if len(lens) > 4 else 0)
+    cache, table, q, _ = make(rng, len(lens), N, H, C, 32, lens)
+    at = [7, C - 3]
+    x = q[..., at].float().abs() + 0.25
+    for sign, scale in ((1.0, 0.07), (-1.0, 0.07), (1.0, -0.07)):
+        q[..., at] = (-x if sign * scale > 0 else x).to(q.dtype)
+        for b in marks:
+            for i, j in enumerate(where):
+                cache.data[int(table[b, j // 32]), j % 32, at[i % 2]] = sign * float("inf")
+        out, lse, err = call(q, cache, table, lens, scale)
+        assert err == 0
+        for b in {*marks, len(lens) // 2}:
+            K, j = host(cache.data[torch.from_numpy(table[b]).to(DEV).long()]).reshape(-1, C + 64)[:lens[b]], np.arange(lens[b])
+            odd, seen = ~np.isfinite(K), seen_by(N, lens[b], None)
+            finite = ~odd.any(-1)
+            assert finite.all() == (b not in marks)
+            want, wl, spread, size = ref.latent(host(q[b]), np.where(odd, 0.0, K), C, seen & finite, scale)
+            for i in range(N):
+                nan = odd[j[seen[i]], :C].any(0) | (not (seen[i] & finite).any())
+                got, gl = host(out[b, i]), host(lse[b, i])
+                assert np.array_equal(np.isnan(got), np.broadcast_to(nan, got.shape))
+                assert np.array_equal(np.isneginf(gl), np.isneginf(wl[i]))
+                some, ds = np.isfinite(wl[i]), size[i] * (C + 72) * 2.0 ** -24  # as in check()
+                assert np.all(np.abs(gl - wl[i])[some] <= (2 * ds + 2.0 ** -12 + np.abs(wl[i]) * 2.0 ** -22)[some])
+                bound = spread[i] * (HALF_BF16 + 4 * ds[:, None] + 2.0 ** -11) + np.abs(want[i]) * HALF_BF16
+                assert np.all((np.abs(got - want[i]) <= bound + 1e-30)[:, ~nan])
