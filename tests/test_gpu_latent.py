@@ -398,3 +398,22 @@ def test_infinite_latents(C, lens, where):
                 assert np.all(np.abs(gl - wl[i])[some] <= (2 * ds + 2.0 ** -12 + np.abs(wl[i]) * 2.0 ** -22)[some])
                 bound = spread[i] * (HALF_BF16 + 4 * ds[:, None] + 2.0 ** -11) + np.abs(want[i]) * HALF_BF16
                 assert np.all((np.abs(got - want[i]) <= bound + 1e-30)[:, ~nan])
+
+
+@pytest.mark.parametrize("C", [128, 256, 512])
+@pytest.mark.parametrize("N,H,lens,tree", [
+    (40, 4, [1, 5, 39, 40, 17], False), (40, 4, [1, 5, 39, 40, 17], True), (130, 3, [70, 129, 1, 64, 65], False),
+    (130, 3, [70, 129, 1, 64, 65], True), (6, 16, [1, 2, 5] * 70, False)])
+def test_shorter_than_the_new_tokens(C, N, H, lens, tree):
+    """Caches that hold the last new tokens only: the first tokens see nothing, beside rows of the unit that do."""
+    rng = np.random.default_rng([C, N, len(lens), tree])
+    mask = trees(rng, len(lens), N) if tree else None
+    cache, table, q, m = make(rng, len(lens), N, H, C, 16, lens, mask)
+    out, lse, err = call(q, cache, table, lens, 0.07, m)
+    assert err == 0
+    if not tree:
+        for b, n in enumerate(lens):
+            assert not out[b, :N - n].any() and bool(torch.isneginf(lse[b, :N - n]).all())
+            assert bool(torch.isfinite(lse[b, N - n:]).all())
+    few = slice(0, 5)
+    check(out[few], lse[few], cache, table[few], q[few], lens[few], 0.07, None if mask is None else mask[few])
