@@ -178,9 +178,10 @@ int spec_attn_shared(const spec_kv_cache *cache, const int32_t *shared_table, in
  *   (u, v) -> amplitude (u cos - v sin, v cos + u sin)
  * SPEC_ROPE_HALF: pair i is elements (i, i + rot / 2) of the part;
  * SPEC_ROPE_INTERLEAVED: (2 i, 2 i + 1).  The head's other elements stay.
- * Angles are held as fractions of a turn in 64-bit fixed point: a frequency is
- * 2^64 theta_i / (2 pi), its product with p modulo 2^64 is exact, so that a far
- * position costs no digits.  Positions are any int32.
+ * Angles are held as fractions of a turn in 64-bit fixed point: a frequency is the
+ * integer nearest to 2^64 theta_i / (2 pi), its product with p modulo 2^64 is exact,
+ * so that the angle is at most 2^-65 |p| of a turn off (2^-34 at the farthest
+ * position, less than fp32 holds).  Positions are any int32.
  */
 enum { SPEC_ROPE_HALF = 0, SPEC_ROPE_INTERLEAVED = 1 };
 

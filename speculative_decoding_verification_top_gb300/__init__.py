@@ -46,7 +46,7 @@ SOURCES = [os.path.join(CSRC, f)
 HEADERS = [os.path.join(CSRC, f) for f in ("common.cuh", "stream.cuh", "draw.cuh", "attn.cuh",
                                              "attn_plan.cuh", "tensor.cuh", "checks.cuh",
                                              "kvrows.cuh", "target.cuh", "logprobs.cuh", "util.cuh",
-                                             "latent_plan.cuh")]
+                                             "latent_plan.cuh", "wide.h")]
 INCLUDE = os.path.join(_ROOT, "include")
 HEADER = os.path.join(INCLUDE, "spec_verify.h")
 ATTN_HEADER = os.path.join(INCLUDE, "spec_attn.h")

@@ -3,6 +3,7 @@
 
 #include "checks.cuh"
 #include "target.cuh"
+#include "wide.h"
 
 namespace specv {
 namespace {
@@ -66,15 +67,18 @@ SPEC_EXPORT int spec_rope_freqs(int rot, double base, int scaling, double factor
         a = std::fmax(0.0, std::floor(at(high)));
         b = std::fmin(rot - 1.0, std::ceil(at(low)));
     }
-    for (int i = 0; i < rot / 2; ++i) {
-        double theta = std::pow(base, -2.0 * i / rot);
-        double w = scaling == SPEC_ROPE_PLAIN ? 1.0 : 0.0;
-        if (scaling == SPEC_ROPE_TURNS) w = (original * theta / (2.0 * pi) - low) / (high - low);
-        if (scaling == SPEC_ROPE_INDEX) w = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - a) / std::fmax(b - a, 1e-3)));
-        w = std::fmin(1.0, std::fmax(0.0, w));
-        if (scaling != SPEC_ROPE_PLAIN) theta *= w + (1.0 - w) / factor;
+    // In two doubles: a frequency has up to 62 bits, and what it is off by grows with
+    // the position.
+    const Wide one = wide(1.0), per_turn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+    const Wide step = one / root(base, rot / 2);
+    Wide plain = one;  // base^(-2 i / rot)
+    for (int i = 0; i < rot / 2; ++i, plain = plain * step) {
+        Wide theta = plain, w = wide(0.0);
+        if (scaling == SPEC_ROPE_TURNS) w = share(wide(original) * theta * per_turn - wide(low), wide(high) - wide(low));
+        if (scaling == SPEC_ROPE_INDEX) w = one - share(wide(i - a), wide(std::fmax(b - a, 1e-3)));
+        if (scaling != SPEC_ROPE_PLAIN) theta = theta * (w + (one - w) / wide(factor));
         // theta <= 1: under a sixth of a turn, so the product is below 2^62
-        freqs[i] = static_cast<uint64_t>(std::nearbyint(theta / (2.0 * pi) * 0x1p64));
+        freqs[i] = nearest(theta * per_turn * wide(0x1p64));
     }
     return SPEC_OK;
 }

@@ -1,6 +1,8 @@
 """Refusals of the rotary, latent and log-probability entries on the CPU: turned
 down on the host before any CUDA call; and the frequencies, which are host work."""
 import ctypes
+import decimal
+import math
 
 import numpy as np
 import pytest
@@ -216,6 +218,39 @@ def test_frequencies(rot, base, scaling, args):
     # fixed point is off by half a step, 2^-65 of a turn
     assert np.allclose(np.array(got[:], np.float64) / 2.0 ** 64 * (2 * np.pi), want, rtol=2.0 ** -48,
                        atol=2 * np.pi * 2.0 ** -65)
+
+
+PI = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+@pytest.mark.parametrize("rot,base,scaling,args", [
+    (64, 10000.0, "plain", (1.0, 0, 0.0, 0.0)), (128, 5e5, "plain", (1.0, 0, 0.0, 0.0)), (16, 1.5, "plain", (1.0, 0, 0.0, 0.0)),
+    (1024, 1e30, "plain", (1.0, 0, 0.0, 0.0)), (1024, 1 + 2.0 ** -40, "plain", (1.0, 0, 0.0, 0.0)),
+    (128, 5e5, "linear", (3.7, 0, 0.0, 0.0)), (128, 5e5, "turns", (8.0, 8192, 1.0, 4.0)),
+    (64, 10000.0, "turns", (40.0, 4096, 0.1, 31.9)), (64, 1e30, "turns", (40.0, 1e30, 1e-301, 1e-300)),
+    (64, 1e30, "turns", (2.0, 1.0, 1e-20, 1.0)), (64, 3.0, "turns", (40.0, 7e29, 1e-300, 1e30)), (64, 10000.0, "index", (40.0, 4096, 1.0, 32.0)),
+    (1024, 1e6, "index", (4.3, 32768, 1.0, 32.0))])
+def test_frequencies_to_the_last_bit(rot, base, scaling, args):
+    """The nearest integers to 2^64 theta / (2 pi): a frequency's error grows with the position."""
+    got = (ctypes.c_uint64 * (rot // 2))()
+    sv.spec_rope_freqs(rot, base, sv.SCALINGS[scaling], *args, ctypes.addressof(got))
+    factor, original, low, high = args
+    D = decimal.Decimal
+    with decimal.localcontext() as c:
+        c.prec = 70
+        for i in range(rot // 2):
+            theta, w = (D(base).ln() * -2 * i / rot).exp(), D(0)
+            if scaling == "turns":
+                w = (D(original) * theta / (2 * PI) - D(low)) / (D(high) - D(low))
+            elif scaling == "index":
+                at = [rot * math.log(original / (t * 2 * math.pi)) / (2 * math.log(base)) for t in (high, low)]
+                a, b = max(0, math.floor(at[0])), min(rot - 1, math.ceil(at[1]))
+                w = 1 - min(D(1), max(D(0), (i - a) / D(max(b - a, 1))))
+            w = min(D(1), max(D(0), w))
+            if scaling != "plain":
+                theta *= w + (1 - w) / D(factor)
+            # half a step, and what two doubles are off by after a thousand operations: 2^-94 of less than 2^62
+            assert abs(got[i] - theta / (2 * PI) * 2 ** 64) <= D("0.5") + D(2) ** -32
 
 
 def test_frequency_refusals():
