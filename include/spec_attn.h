@@ -275,7 +275,7 @@ int spec_latent_append(const spec_latent_cache *cache, const int32_t *page_table
                        int dtype, spec_stream_t stream);
 
 /* Workspace bytes of spec_latent_attn for B sequences of N new tokens and H
- * heads (any cache lengths). */
+ * heads (any cache lengths; its sizes, its limits). */
 int spec_latent_workspace_size(int B, int N, int H, int C, size_t *bytes);
 
 /*
@@ -299,7 +299,7 @@ int spec_latent_workspace_size(int B, int N, int H, int C, size_t *bytes);
  *   q            [B, N, H, C + R] bf16, device, 16-byte aligned, tokens at
  *                q_stride elements (0: H * (C + R); a multiple of 8)
  *   mask         [B, N, N] uint8, device, or NULL (a chain)
- *   1 <= N <= SPEC_MAX_TREE_NODES, 1 <= H <= 1024; scale finite
+ *   1 <= N <= SPEC_MAX_TREE_NODES, 1 <= H <= 1024, B * N * H <= 2^30; scale finite
  *   out          [B, N, H, C] bf16, device, contiguous, 16-byte aligned
  *   out_lse      [B, N, H] fp32, device, or NULL
  *   workspace    >= spec_latent_workspace_size(...) bytes, as for spec_attn_tree

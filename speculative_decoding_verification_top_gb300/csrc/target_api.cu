@@ -10,6 +10,7 @@ namespace {
 
 constexpr int kMaxHead = 1024;  // elements of a head that spec_rope takes
 constexpr int kRotary = 64;     // rotary elements of a latent cache's row
+constexpr int kMaxRows = 1 << 30;  // query rows of a latent attention: what a 32-bit number counts with room
 
 bool rot_ok(int rot, int D) { return rot >= 16 && rot % 16 == 0 && rot <= D; }
 
@@ -43,7 +44,7 @@ int latent_view(const spec_latent_cache *cache, LatentView *c) {
 
 bool latent_sizes_ok(int B, int N, int H, int C) {
     return B >= 0 && N >= 1 && N <= SPEC_MAX_TREE_NODES && H >= 1 && H <= 1024 && (C == 128 || C == 256 || C == 512) &&
-           static_cast<long long>(B) * N * H <= INT_MAX / 1024;
+           static_cast<long long>(B) * N * H <= kMaxRows;
 }
 
 }  // namespace

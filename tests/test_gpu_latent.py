@@ -417,3 +417,21 @@ def test_shorter_than_the_new_tokens(C, N, H, lens, tree):
             assert bool(torch.isfinite(lse[b, N - n:]).all())
     few = slice(0, 5)
     check(out[few], lse[few], cache, table[few], q[few], lens[few], 0.07, None if mask is None else mask[few])
+
+
+@pytest.mark.parametrize("B,N,H", [(129, 128, 128), (2200000, 1, 1)])
+def test_many_rows(B, N, H):
+    """More than 2^21 query rows: long trees of many heads, and many short sequences, the last ones among them."""
+    rng = np.random.default_rng([B, N, H])
+    cache, _, _, _ = make(rng, 1, 1, 1, 128, 16, [16 * 40])
+    # sequences share their pages: each starts at one of 16 of them
+    table = ((np.arange(B)[:, None] * 7 + np.arange(16 if N > 1 else 1)) % 40).astype(np.int32)
+    lens = np.minimum(N + np.arange(B) % 90, 16 * table.shape[1]).astype(np.int32)
+    if N == 1:
+        lens = (np.arange(B) % 17).astype(np.int32)
+    q = torch.randn((B, N, H, 192), dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    out, lse, err = call(q, cache, table, lens, 0.07)
+    assert err == 0
+    few = [0, 1, B // 2, B - 2, B - 1]
+    check(out[few], lse[few], cache, table[few], q[few], lens[few], 0.07, some=range(0, H, 31))
+    assert not out[lens == 0].any()

@@ -173,6 +173,17 @@ def test_latent_attention():
     assert attn(B=2, ws=P + 4, ws_bytes=1 << 40) == -6
 
 
+def test_latent_rows():
+    """As many query rows as the header allows, and one more."""
+    for B, N, H in ((128, 128, 128), (1 << 10, 1 << 10, 1 << 10), (1 << 30, 1, 1), (1 << 20, 4, 256)):
+        assert sv.spec_latent_workspace_size(B, N, H, 512) > 0
+        assert attn(B=B, N=N, H=H, ws=None) == -7
+    for B, N, H in (((1 << 10) + 1, 1 << 10, 1 << 10), ((1 << 30) + 1, 1, 1), ((1 << 31) - 1, 1024, 1024)):
+        with pytest.raises(sv.SpecVerifyError):
+            sv.spec_latent_workspace_size(B, N, H, 512)
+        assert attn(B=B, N=N, H=H, ws=None) == -2
+
+
 def test_latent_workspace():
     assert 0 < sv.spec_latent_workspace_size(1, 1, 16, 512) <= sv.spec_latent_workspace_size(64, 6, 32, 512)
     for args in [(-1, 1, 4, 512), (1, 0, 4, 512), (1, 1, 0, 512), (1, 1, 4, 96), (1, 1025, 4, 512)]:
