@@ -496,6 +496,13 @@ def _launch(device, stream):
     return c._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
+def _room(workspace, device):
+    """A given workspace holds the bytes that it counts: not one of expanded elements."""
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on cuda:%d, got strides %s on %s"
+                         % (device, workspace.stride(), workspace.device))
+
+
 def new_workspace(nbytes, device):
     """A zero-filled workspace tensor (zeroing is the required first-use init)."""
     torch = _torch()
@@ -696,8 +703,8 @@ def logprobs(target, tokens, rows=None, temperature=1.0, top=0, entropy=True, ra
     out = _made(stream, _new_logprobs, B, M, top, entropy, rank, target.device)
     if workspace is None:
         workspace = _made(stream, new_workspace, spec_verify_logprobs_workspace_size(), target.device)
-    elif workspace.get_device() != device:
-        raise ValueError("the workspace must be on cuda:%d" % device)
+    else:
+        _room(workspace, device)
     spec_verify_logprobs(target.data_ptr(), tokens.data_ptr(), _ptr(rows), B, N, M, V, temperature, top,
                          _dtype_code(target), out.logprob.data_ptr(), _ptr(out.entropy), _ptr(out.rank),
                          _ptr(out.top_ids), _ptr(out.top_logprobs), workspace.data_ptr(),
@@ -1062,8 +1069,8 @@ def latent_attn(q, cache, page_table, lens, scale, mask=None, out=None, lse=None
         _lies(lse, "lse", torch.float32, (B, N, H), device)
     if workspace is None:
         workspace = _made(stream, new_workspace, spec_latent_workspace_size(B, N, H, C), q.device)
-    elif workspace.get_device() != device:
-        raise ValueError("the workspace must be on cuda:%d" % device)
+    else:
+        _room(workspace, device)
     spec_latent_attn(d, page_table.data_ptr(), width, lens.data_ptr(), q.data_ptr(), step, _ptr(mask), B,
                      N, H, scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
                      handle)

@@ -125,6 +125,16 @@ def test_tensors_of_two_devices_are_refused(calls):
     assert not calls
 
 
+def test_workspaces_that_hold_less_than_they_count_are_refused(calls):
+    """The kernels would write past an expanded workspace's one element."""
+    for ws in (OnGpu(torch.zeros(1, dtype=torch.uint8).expand(64)), OnGpu(torch.zeros(128, dtype=torch.uint8)[::2])):
+        with pytest.raises(ValueError, match="workspace"):
+            sv.latent_attn(made(2, 3, 4, 192), latent_cache(), ints(2, 1), ints(2), 1.0, out=made(2, 3, 4, 128), workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            sv.logprobs(made(2, 3, 50), ints(2, 3), workspace=ws)
+    assert not calls
+
+
 def test_strides_and_counts(calls):
     """Parts of one projection come with its stride; rows set the entries' count."""
     wide = torch.zeros((2, 3, 4 * 192 + 192), dtype=torch.bfloat16)
