@@ -214,7 +214,7 @@ int spec_rope_freqs(int rot, double base, int scaling, double factor, double ori
  *                (across sequences too) at x_stride / out_stride elements (0: H * D;
  *                at least that, a multiple of 8), a token's heads contiguous.
  *                out may be x, with the same stride (then only the turned part is
- *                written); otherwise they do not overlap
+ *                written); otherwise they do not overlap (SPEC_ERR_SHAPE)
  *   freqs        [rot / 2], device, 16-byte aligned
  *   pos          [B, N] int32, device
  *   D, rot, first  multiples of 16: 16 <= D <= 1024, first + rot <= D
@@ -237,7 +237,8 @@ int spec_rope(const void *x, int64_t x_stride, void *out, int64_t out_stride, co
  *   pos          [B, N] int32, device, or NULL
  *   freqs, rot, amplitude, layout  as for spec_rope; rot <= D
  *   q, out_q     [B, N, Hq, D] dtype, device, as x and out of spec_rope, or both
- *                NULL; with `rows` NULL only (SPEC_ERR_PARAM)
+ *                NULL; with `rows` NULL only (SPEC_ERR_PARAM).  out_q does not
+ *                overlap k or v
  * Other arguments as for spec_kv_append.
  */
 int spec_kv_append_rope(const spec_kv_cache *cache, const int32_t *page_table, int table_width,

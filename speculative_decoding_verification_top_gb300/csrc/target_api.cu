@@ -14,6 +14,21 @@ constexpr int kMaxRows = 1 << 30;  // query rows of a latent attention: what a 3
 
 bool rot_ok(int rot, int D) { return rot >= 16 && rot % 16 == 0 && rot <= D; }
 
+// Do `count` tokens from x on, each `size` elements of `bytes` and `stride` apart, share
+// no element with those from y on?  Parts of one projection, of one stride, lie
+// between each other.
+bool apart(const void *x, long long x_stride, long long x_size, const void *y, long long y_stride, long long y_size,
+           long long count, int bytes) {
+    const long long from_x = static_cast<long long>(reinterpret_cast<uintptr_t>(x)),
+                    from_y = static_cast<long long>(reinterpret_cast<uintptr_t>(y));
+    const long long to_x = from_x + ((count - 1) * x_stride + x_size) * bytes,
+                    to_y = from_y + ((count - 1) * y_stride + y_size) * bytes;
+    if (to_x <= from_y || to_y <= from_x) return true;
+    if (x_stride != y_stride) return false;
+    const long long period = x_stride * bytes, at = ((from_y - from_x) % period + period) % period;
+    return at >= x_size * bytes && at + y_size * bytes <= period;
+}
+
 // The turn's arguments; `first` + rot within the head is the caller's check.
 int turn_of(const uint64_t *freqs, int rot, float amplitude, int layout, Turn *t) {
     if (layout != SPEC_ROPE_HALF && layout != SPEC_ROPE_INTERLEAVED) return SPEC_ERR_MODE;
@@ -99,6 +114,8 @@ SPEC_EXPORT int spec_rope(const void *x, int64_t x_stride, void *out, int64_t ou
     if (B == 0 || N == 0) return SPEC_OK;
     if (!x || !out || !freqs || !pos) return SPEC_ERR_NULL;
     if (!aligned(x, 16) || !aligned(out, 16) || !aligned(freqs, 16) || !aligned(pos, 4)) return SPEC_ERR_ALIGN;
+    const long long size = static_cast<long long>(H) * D, count = static_cast<long long>(B) * N;
+    if (x != out && !apart(x, x_stride, size, out, out_stride, size, count, dtype == SPEC_F32 ? 4 : 2)) return SPEC_ERR_SHAPE;
     a.x = x;
     a.out = out;
     a.x_stride = x_stride;
@@ -139,6 +156,15 @@ SPEC_EXPORT int spec_kv_append_rope(const spec_kv_cache *cache, const int32_t *p
     if (!aligned(page_table, 4) || !aligned(starts, 4) || !aligned(k, 16) || !aligned(v, 16) || !aligned(rows, 4) ||
         !aligned(pos, 4) || !aligned(freqs, 16) || !aligned(q, 16) || !aligned(out_q, 16))
         return SPEC_ERR_ALIGN;
+    if (queries) {
+        const long long size = static_cast<long long>(Hq) * c.D, kv = static_cast<long long>(c.Hkv) * c.D;
+        const long long count = static_cast<long long>(B) * N;
+        const int bytes = dtype == SPEC_F32 ? 4 : 2;
+        if ((q != out_q && !apart(q, q_stride, size, out_q, out_q_stride, size, count, bytes)) ||
+            !apart(k, token_stride, kv, out_q, out_q_stride, size, count, bytes) ||
+            !apart(v, token_stride, kv, out_q, out_q_stride, size, count, bytes))
+            return SPEC_ERR_SHAPE;
+    }
     a.a.table = page_table;
     a.a.width = table_width;
     a.a.starts = starts;

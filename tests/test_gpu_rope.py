@@ -329,3 +329,31 @@ def test_a_step_captured():
         pos = held[:, None] + torch.arange(N, dtype=torch.int32, device=DEV)
         sv.kv_append(cache, table, held, sv.rope(x[1], freqs, pos), x[2])
         assert torch.equal(got, sv.attn_tree(sv.rope(x[0], freqs, pos), cache, table, lens))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_outputs_beside_inputs(dtype):
+    """Outputs between the parts of one projection, and in place; outputs over what is still read are refused."""
+    rng = np.random.default_rng(12)
+    B, N, Hq, Hkv, D = 3, 5, 6, 2, 64
+    freqs, table, starts = sv.rope_freqs(D), dev(np.arange(6, dtype=np.int32).reshape(3, 2)), dev(np.array([0, 3, 9], np.int32))
+    wide = dev(rng.normal(size=(B, N, 2 * Hq + 2 * Hkv, D)), dtype)
+    q, spare, k, v = wide.split((Hq, Hq, Hkv, Hkv), 2)
+    pos = (starts[:, None] + torch.arange(N, device=DEV)).int()
+    want = sv.rope(q.contiguous(), freqs, pos)
+    assert torch.equal(sv.rope(q, freqs, pos, out=spare), want) and torch.equal(spare, want)
+    spare.zero_()
+    caches = [sv.new_cache(6, Hkv, 16, D, DEV) for _ in range(2)]
+    sv.kv_append_rope(caches[0], table, starts, k.contiguous(), v.contiguous(), freqs)
+    assert torch.equal(sv.kv_append_rope(caches[1], table, starts, k, v, freqs, q=q, out_q=spare), want)
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+    before = wide.clone()
+    for bad in (wide[:, :, 1:Hq + 1], wide[:, :, Hq - 1:2 * Hq - 1]):
+        with pytest.raises(sv.SpecVerifyError):
+            sv.rope(q, freqs, pos, out=bad)
+        with pytest.raises(sv.SpecVerifyError):
+            sv.kv_append_rope(caches[1], table, starts, k, v, freqs, q=q, out_q=bad)
+    with pytest.raises(sv.SpecVerifyError):
+        sv.kv_append_rope(caches[1], table, starts, k, v, freqs, q=q, out_q=wide[:, :, Hq + 1:2 * Hq + 1])
+    assert torch.equal(wide, before)
+    assert sv.rope(q, freqs, pos, out=q) is q and torch.equal(q, want)

@@ -134,6 +134,22 @@ def test_append():
     assert append(B=2, width=0, table=None) == 0
 
 
+def test_overlapping_outputs():
+    """An output that shares elements with what other threads still read."""
+    n = 6 * 512 * 2  # bytes of the default call's six packed tokens
+    for out in (P + 16, P + 1024, P + n - 16, P - n + 16):
+        assert rope(B=2, out=out) == -2
+    assert rope(B=2, out=P + n - 16, dtype=0) == -2      # fp32: twice as long
+    assert rope(B=2, xs=1024, os=1024, out=P + 1008) == -2   # a token's stride is 2048 bytes, its elements 1024
+    assert rope(B=2, xs=1024, os=1024, out=P + 1040) == -2
+    assert rope(B=2, xs=1024, os=1040, out=P + 1024) == -2   # strides that differ
+    # tokens of 4 heads of 64 between others' 4: out_q over the keys, the values, beside them, over the queries
+    far = 1 << 20
+    a = dict(B=2, q=far, out_q=4 * far, qs=512, os=512, k=2 * far, v=3 * far, stride=512, Hq=4)
+    for out_q, os in ((2 * far + 16, 512), (3 * far + 240, 512), (3 * far - 496, 512), (far + 16, 512), (2 * far + 512, 520)):
+        assert append(kv(D=64, dtype=1), **{**a, "out_q": out_q, "os": os}) == -2
+
+
 def test_latent_append():
     assert put() == 0
     assert put(latent(C=192)) == -2
