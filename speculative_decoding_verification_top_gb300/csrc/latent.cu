@@ -35,17 +35,20 @@
 // unit that one share holds whole is written out at once, the others' parts (m, l,
 // O) are joined in the line's order: results do not depend on timing.
 //
-// What bounds it.  C = 512: shared memory, which delivers 128 bytes a cycle.  A tile of
-// 64 positions and rows takes 112 KB for S, 96 KB for O, 82 KB that loads and weights
-// write: 2270 cycles, where the products alone take 36 x 34.5 + 16 x 50; a tile is
-// measured at 2350, and a segment's beginning and end at some 15000 (55 tiles).
-// 64 x 6 tokens of 32 heads over up to 8200 positions, 176 us (0.49 of the measured
-// product rate); 16 trees of 85 nodes, 16 heads, 7001 positions, 276 us (0.49); one
-// token each of 64 sequences, 16 heads, 91 us (0.74 of the copy rate).  C = 128: the
-// chain of a softmax group, 1800 cycles a tile of its own: 75 us of 25 (one group: 128).
+// What bounds it.  The products of 64 query rows: 36 x 34.5 + 16 x 50 = 2040 cycles a
+// tile for C = 512, 1090 for 256, 614 for 128 (64 x 64 and 128 x 64 of depth 16, both
+// near what shared memory delivers).  Calls of two lengths take 1.06 to 1.13, 0.63 and
+// 0.43 us a tile, 2050 to 2190, 1220 and 840 cycles, and 27, 23 and 16 us beside the
+// tiles: 2.3 segments a CTA with their beginnings and ends, and the launch.  Every
+// operand's bytes at 128 a cycle, 112 + 96 KiB for S and O and 80 that loads and weights
+// write (C = 512), would be 2304 (1408, 832): some are read less often than that.
+// For C = 128 a softmax group's own chain is as long, 1680 cycles for every second tile.
+// 64 x 6 tokens of 32 heads over up to 8200 positions, 174 to 178 us (0.49 of the measured
+// product rate); 16 trees of 85 nodes, 16 heads, 7001 positions, 272 to 277 us (0.49); one
+// token each of 64 sequences, 16 heads, 89 us (0.75 of the copy rate).  The chains with
+// C = 256 104 us (0.44), 128 72 us (0.35; one group: 128).
 // Not taken: a cluster's CTAs loading a tile once for all of them (chains 312 us: a slot
-// is free only when the last of them is done), pairs of CTAs on one product (the halves of
-// keys and values that each must hold leave no room to load ahead).
+// is free only when the last of them is done).  Not built: pairs of CTAs on one product.
 
 #include "latent_plan.cuh"
 

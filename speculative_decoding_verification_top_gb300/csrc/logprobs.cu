@@ -14,10 +14,11 @@
 // a bar on: the top-th of what was seen before or, in the first chunk, the top-th
 // largest of 64 groups' maxima (at least `top` elements reach it, and few more do).
 // The slices' sums and lists meet in the first CTA's shared memory.
-// Bound by what is issued for the sums (21 of 30 us; some 10 instructions an element)
-// and by the chain bar, candidates, order, cluster after them.
-// Measured: 64 x 6 entries (228 emitted) of 151936 bf16 logits, 20 alternatives, 30 us
-// (69 MB, 2.3 TB/s), fp32 44 us (3.2); without alternatives 21.  Held in registers
+// Bound by what is issued for the sums (21 of 25 to 28 us; some 10 instructions an
+// element) and by the chain bar, candidates, order, cluster after them.
+// Measured: 64 x 6 entries (228 emitted) of 151936 bf16 logits, 20 alternatives, 25 to
+// 28 us (69 MB, 2.5 to 2.8 TB/s), fp32 39 to 45 us (3.1 to 3.6); without alternatives
+// 21.  Held in registers
 // instead, a slice cut into chunks of 2048 vectors took 120 us, and of 2560 in three
 // CTAs a multiprocessor 70: each chunk's selection is a chain of barriers.  A thread's
 // maxima looked through one by one cost 9000 of 45000 cycles.
@@ -525,8 +526,8 @@ int launch_size(const LogprobArgs &a, cudaStream_t st) {
 
 int launch_logprobs(LogprobArgs &a, int dtype, cudaStream_t st) {
     // As many CTAs a row as are resident at once: fewer leave multiprocessors idle, more
-    // go through the chain in turns (384 rows of 151936, before the last two steps: 36 us with
-    // 2, 46 with 1, 43 with 4).
+    // go through the chain in turns (384 rows of 151936, 20 alternatives: 25 to 28 us
+    // with 2, 37 with 1, 34 with 4, 53 with 8).
     const int E = dtype == SPEC_F32 ? 4 : 8;
     const long long entries = static_cast<long long>(a.B) * a.M;
     a.cluster = 1;

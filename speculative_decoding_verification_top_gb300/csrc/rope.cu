@@ -17,8 +17,9 @@
 // where 121 are needed).
 // Measured: 8 x 4099 tokens of 16 fp32 heads of 128, 79 us (6.8 TB/s, the copy rate);
 // their keys, values and queries, 32/8 bf16 heads, into a bf16 cache, 121 us (6.6);
-// 16 x 6001 latent rows of 512 + 64, 39 us (5.6).  Calls of a few hundred tokens take
-// 4 to 6 us on the GPU and are bound by the way there.
+// 16 x 6001 latent rows of 512 + 64, 39 us (5.6); the keys, values and queries into an
+// e4m3 cache, 139 us (5.3).  Calls of a few hundred tokens take 4.4 to 6.1 us on the GPU
+// (cold, timed alone) and are bound by the way there.
 
 #include "kvrows.cuh"
 #include "target.cuh"
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
 }
 
 // Heads a thread: four where that leaves every multiprocessor full, else one (64 x 6
-// tokens of 32 heads: 5.2 us; with four, a fifth of the multiprocessors idle).
+// tokens of 32 heads: 5.5 us; with four, a fifth of the multiprocessors idle).
 constexpr long long kFull = 152ll * 2048;
 
 unsigned blocks_for(long long threads) { return static_cast<unsigned>((threads + kThreads - 1) / kThreads); }
