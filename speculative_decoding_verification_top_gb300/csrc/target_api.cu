@@ -19,13 +19,13 @@ bool rot_ok(int rot, int D) { return rot >= 16 && rot % 16 == 0 && rot <= D; }
 // between each other.
 bool apart(const void *x, long long x_stride, long long x_size, const void *y, long long y_stride, long long y_size,
            long long count, int bytes) {
-    const long long from_x = static_cast<long long>(reinterpret_cast<uintptr_t>(x)),
-                    from_y = static_cast<long long>(reinterpret_cast<uintptr_t>(y));
-    const long long to_x = from_x + ((count - 1) * x_stride + x_size) * bytes,
-                    to_y = from_y + ((count - 1) * y_stride + y_size) * bytes;
+    using Address = __int128;  // the largest strides and counts pass 64 bits
+    const Address from_x = reinterpret_cast<uintptr_t>(x), from_y = reinterpret_cast<uintptr_t>(y), tokens = count;
+    const Address to_x = from_x + ((tokens - 1) * x_stride + x_size) * bytes,
+                  to_y = from_y + ((tokens - 1) * y_stride + y_size) * bytes;
     if (to_x <= from_y || to_y <= from_x) return true;
     if (x_stride != y_stride) return false;
-    const long long period = x_stride * bytes, at = ((from_y - from_x) % period + period) % period;
+    const Address period = Address(x_stride) * bytes, at = ((from_y - from_x) % period + period) % period;
     return at >= x_size * bytes && at + y_size * bytes <= period;
 }
 

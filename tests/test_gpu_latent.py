@@ -395,7 +395,8 @@ def test_infinite_latents(C, lens, where):
                 assert np.array_equal(np.isnan(got), np.broadcast_to(nan, got.shape))
                 assert np.array_equal(np.isneginf(gl), np.isneginf(wl[i]))
                 some, ds = np.isfinite(wl[i]), size[i] * (C + 72) * 2.0 ** -24  # as in check()
-                assert np.all(np.abs(gl - wl[i])[some] <= (2 * ds + 2.0 ** -12 + np.abs(wl[i]) * 2.0 ** -22)[some])
+                off, bound = np.abs(gl[some] - wl[i][some]), np.abs(wl[i][some]) * 2.0 ** -22
+                assert np.all(off <= 2 * ds[some] + 2.0 ** -12 + bound)
                 bound = spread[i] * (HALF_BF16 + 4 * ds[:, None] + 2.0 ** -11) + np.abs(want[i]) * HALF_BF16
                 assert np.all((np.abs(got - want[i]) <= bound + 1e-30)[:, ~nan])
 

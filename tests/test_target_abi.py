@@ -137,12 +137,13 @@ def test_append():
 def test_overlapping_outputs():
     """An output that shares elements with what other threads still read."""
     n = 6 * 512 * 2  # bytes of the default call's six packed tokens
-    for out in (P + 16, P + 1024, P + n - 16, P - n + 16):
-        assert rope(B=2, out=out) == -2
+    for d in (16, 1024, n - 16, 16 - n):
+        assert rope(B=2, x=4 * P, out=4 * P + d) == -2
     assert rope(B=2, out=P + n - 16, dtype=0) == -2      # fp32: twice as long
     assert rope(B=2, xs=1024, os=1024, out=P + 1008) == -2   # a token's stride is 2048 bytes, its elements 1024
     assert rope(B=2, xs=1024, os=1024, out=P + 1040) == -2
     assert rope(B=2, xs=1024, os=1040, out=P + 1024) == -2   # strides that differ
+    assert rope(B=1 << 15, N=1 << 15, H=1, D=16, rot=16, xs=1 << 40, os=1 << 40, out=P + 16) == -2  # past 64 bits
     # tokens of 4 heads of 64 between others' 4: out_q over the keys, the values, beside them, over the queries
     far = 1 << 20
     a = dict(B=2, q=far, out_q=4 * far, qs=512, os=512, k=2 * far, v=3 * far, stride=512, Hq=4)
